@@ -11,7 +11,10 @@
  *   - both in one launch per layer (decode_step_paged);
  *   - a host-tiled variant that keeps (m, l, acc) in global memory while KV
  *     tiles are streamed in from pinned host memory, and a zero-copy variant
- *     that reads a history held in pinned host memory directly.
+ *     that reads a history held in pinned host memory directly;
+ *   - drafted-tree decoding: a prologue whose rotary positions are given on
+ *     several axes, attention of a tree of drafted tokens over the cache, and
+ *     the move of the accepted path's rows behind the prefix.
  *
  * Sources (page title, section):
  *   "From Qwen3 math to CUDA kernels: a 0.6B inference runtime"
@@ -79,6 +82,7 @@ enum pgqa_status {
 #define PGQA_DEVERR_BAD_PAGE 1u     /* block-table entry outside [0, num_pages) */
 #define PGQA_DEVERR_BAD_CONTEXT 2u  /* context length < 0 (or < 1 for the prologue) or too long */
 #define PGQA_DEVERR_WAIT_TIMEOUT 4u /* a bounded wait (an asynchronous copy) ran out */
+#define PGQA_DEVERR_BAD_PATH 8u     /* an accepted path that is no increasing list of drafted tokens */
 
 /* Message of the calling thread's last failing call ("" if none). */
 const char *pgqa_last_error(void);
@@ -482,6 +486,120 @@ int decode_attn_paged_static(const pgqa_bf16 *q, const pgqa_bf16 *k_cache,
                              int page_size, int max_pages, int num_pages, float scale,
                              int num_partitions, float *out_f32, pgqa_bf16 *out_bf16,
                              cudaStream_t stream);
+
+/*
+ * Drafted-tree decoding (no counterpart on the pages; the multi-query decode
+ * above with a tree in place of a chain). A verification step carries up to M
+ * drafted tokens per sequence, listed parents first; the tree's branches are
+ * alternatives for the same positions. context_lens[b] = T_b counts sequence
+ * b's n_b drafted tokens (draft_lens[b], or M where draft_lens is NULL): its
+ * prefix is the first T_b - n_b slots of the cache, and drafted token i
+ * occupies slot T_b - n_b + i until the step is committed. A step is
+ * qk_norm_rope_append_axes, decode_attn_paged_tree (per layer), then
+ * kv_cache_commit_path once for all layers.
+ *
+ * qk_norm_rope_append_axes -- qk_norm_rope_append_multi with the rotary
+ * positions given, on one to four axes (time, height and width of image or
+ * video patches; a drafted token's depth): frequency pair r of token i turns
+ * by positions[b][i][axis_of_pair[r]] * theta^(-2r/D).
+ *   q [B][M][Hq][D], k, v [B][M][Hkv][D], q_out [B][M][Hq][D] bf16, M >= 1
+ *                  (no upper limit but B * M <= 2^30: prompts too)
+ *   positions      [B][M][n_axes] int32, any values (equal on all axes for
+ *                  text); they are independent of the slots
+ *   axis_of_pair   HOST array of D/2 = 64 bytes below n_axes, read during the
+ *                  call: the axis of each pair (r, r + D/2), in sections or
+ *                  interleaved
+ *   new_lens       [B] int32, nullable: n_b in [0, M], the tokens of sequence
+ *                  b that exist (NULL: M). Token i < n_b is written to slot
+ *                  T_b - n_b + i; rows of tokens i >= n_b are neither read
+ *                  nor written.
+ *   The rest as for qk_norm_rope_append. Arithmetic in fp32; the angle is
+ *   reduced modulo a turn in 64-bit fixed point, so it stays accurate at
+ *   large positions (below 1e-6 rad up to 2^31). A sequence with n_b outside
+ *   [0, M], T_b < n_b or T_b > max_pages * page_size is skipped
+ *   (PGQA_DEVERR_BAD_CONTEXT); K and V rows of a page outside the pool are
+ *   skipped (PGQA_DEVERR_BAD_PAGE). Results do not depend on M or B.
+ */
+int qk_norm_rope_append_axes(const pgqa_bf16 *q, const pgqa_bf16 *k, const pgqa_bf16 *v,
+                             const pgqa_bf16 *gamma_q, const pgqa_bf16 *gamma_k, const int32_t *positions,
+                             int n_axes, const uint8_t *axis_of_pair, const int32_t *context_lens,
+                             const int32_t *new_lens, const int32_t *block_table, pgqa_bf16 *k_cache,
+                             pgqa_bf16 *v_cache, pgqa_bf16 *q_out, int B, int M, int Hq, int Hkv, int D,
+                             int page_size, int max_pages, int num_pages, float rope_theta, float eps,
+                             cudaStream_t stream);
+
+/*
+ * decode_attn_paged_tree -- attention of a tree of drafted tokens over the
+ * paged cache. Query head h of drafted token i sees the whole prefix and the
+ * drafted tokens j whose bit is set in its mask:
+ *   x_j = scale * <q_ih, K_j>
+ *   x_j = softcap * tanh(x_j / softcap)           if softcap > 0
+ *   x_j = x_j + slopes[h] * (pos_j - pos_i)       if slopes
+ *   out_ih = sum_j softmax(x)_j V_j over the keys it sees; 0 if there is none
+ * with pos_j = j for prefix keys and the drafted tokens' given positions. M =
+ * 1 with bit 0 set is single-token decoding with those score options. A key
+ * that a query does not see does not reach it, whatever its K and V rows hold
+ * (infinities and NaN too), and slots past T_b are not read as numbers.
+ *   q            [B][M][Hq][D] bf16 (the prologue's q_out), 1 <= M <= 64
+ *   tree_mask    [B][M] uint64, 8-byte aligned: bit j of entry (b, i) lets
+ *                drafted token i see drafted token j (its ancestors and itself
+ *                in a tree; any bits are allowed, those >= n_b are ignored)
+ *   positions    [B][M] int32, nullable unless slopes is given: pos_i
+ *   draft_lens   [B] int32, nullable: n_b in [0, M]; output rows of tokens
+ *                i >= n_b are left as they were
+ *   slopes       [Hq] float, nullable, any sign
+ *   softcap      0 (none) or a positive finite number
+ *   out_f32, out_bf16  [B][M][Hq][D], at least one non-NULL
+ *   workspace    device scratch of ws_bytes >= decode_attn_tree_workspace_size
+ *                (of the current device); no initial value needed. Calls whose
+ *                work may overlap on the GPU must not share one.
+ * Every input is read after the previous kernel in the stream completes. A
+ * sequence with n_b outside [0, M], T_b < n_b or T_b > max_pages * page_size
+ * produces zeros in all its M rows (PGQA_DEVERR_BAD_CONTEXT); keys of a page
+ * outside the pool are skipped (PGQA_DEVERR_BAD_PAGE). Scores, softmax sums
+ * and outputs are accumulated in fp32; the weights enter the product with V
+ * as a bf16 hi + lo pair, as in decode_attn_paged. For given arguments on a
+ * given device the results are reproducible bit for bit.
+ */
+size_t decode_attn_tree_workspace_size(int B, int M, int Hq, int Hkv, int D, int page_size, int max_pages);
+int decode_attn_paged_tree(const pgqa_bf16 *q, const pgqa_bf16 *k_cache, const pgqa_bf16 *v_cache,
+                           const int32_t *block_table, const int32_t *context_lens, const uint64_t *tree_mask,
+                           const int32_t *positions, const int32_t *draft_lens, const float *slopes, int B,
+                           int M, int Hq, int Hkv, int D, int page_size, int max_pages, int num_pages,
+                           float scale, float softcap, float *out_f32, pgqa_bf16 *out_bf16, void *workspace,
+                           size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * kv_cache_commit_path -- keep the accepted path of a drafted tree: for i <
+ * path_lens[b] the K and V rows of slot T_b - n_b + path[b][i] move to slot
+ * T_b - n_b + i, in every KV head of every layer, in one launch, and
+ * context_lens_out[b] = T_b - n_b + path_lens[b] is the sequence's length
+ * afterwards. Rows are moved bit for bit (they were rotated at the positions
+ * that they keep); rows behind the new length hold no defined values until
+ * they are written again.
+ *   k_caches, v_caches, block_tables  HOST arrays of n_layers device pointers
+ *                (1 <= n_layers <= PGQA_MAX_COMMIT_LAYERS), read during the
+ *                call: each layer's bf16 caches and its [B][max_pages] table
+ *                (layers may share one table; two layers may not share both
+ *                a cache and a table)
+ *   path         [B][A] int32, 1 <= A <= M: drafted tokens, strictly
+ *                increasing in the first path_lens[b] entries; the others are
+ *                ignored
+ *   path_lens    [B] int32 in [0, A]
+ *   draft_lens   [B] int32, nullable as above
+ *   context_lens_out [B] int32, no overlap with the other index arrays
+ * A path that is out of range or not increasing counts as empty
+ * (PGQA_DEVERR_BAD_PATH: nothing of the sequence moves, its new length is T_b
+ * - n_b); an invalid n_b or T_b moves nothing and leaves the length T_b
+ * (PGQA_DEVERR_BAD_CONTEXT); rows of a page outside the pool stay
+ * (PGQA_DEVERR_BAD_PAGE).
+ */
+#define PGQA_MAX_COMMIT_LAYERS 128
+int kv_cache_commit_path(pgqa_bf16 *const *k_caches, pgqa_bf16 *const *v_caches,
+                         const int32_t *const *block_tables, int n_layers, const int32_t *context_lens,
+                         const int32_t *draft_lens, const int32_t *path, const int32_t *path_lens,
+                         int32_t *context_lens_out, int B, int M, int A, int Hkv, int D, int page_size,
+                         int max_pages, int num_pages, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

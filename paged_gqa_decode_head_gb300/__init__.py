@@ -6,6 +6,7 @@ does not load the library: the first call of a binding function does, and it
 raises if the library is missing (there is no CPU fallback).
 """
 from .binding import (  # noqa: F401
+    CacheLayers,
     PgqaError,
     attn_host_direct,
     attn_host_direct_partition_count,
@@ -21,15 +22,19 @@ from .binding import (  # noqa: F401
     decode_attn_paged_int8,
     decode_attn_paged_multi,
     decode_attn_paged_static,
+    decode_attn_paged_tree,
+    decode_attn_tree_workspace_size,
     decode_step_paged,
     decode_step_paged_int8,
     decode_step_paged_multi,
     decode_attn_partition_count,
     decode_attn_workspace_size,
     device_error_flags,
+    kv_cache_commit_path,
     library_path,
     load_library,
     qk_norm_rope_append,
+    qk_norm_rope_append_axes,
     qk_norm_rope_append_int8,
     qk_norm_rope_append_multi,
 )

@@ -47,6 +47,10 @@ EXPORTED = (
     "attn_host_direct_workspace_size",
     "attn_host_direct",
     "decode_attn_paged_static",
+    "qk_norm_rope_append_axes",
+    "decode_attn_tree_workspace_size",
+    "decode_attn_paged_tree",
+    "kv_cache_commit_path",
 )
 
 STATUS_NAMES = {
@@ -61,6 +65,7 @@ STATUS_NAMES = {
 DEVERR_BAD_PAGE = 1
 DEVERR_BAD_CONTEXT = 2
 DEVERR_WAIT_TIMEOUT = 4
+DEVERR_BAD_PATH = 8
 
 
 class PgqaError(RuntimeError):
@@ -138,6 +143,14 @@ def load_library(path: str | None = None):
         lib.pgqa_selftest_wait_timeout.restype = I
         lib.decode_attn_paged_static.argtypes = [P] * 5 + [I] * 7 + [F, I, P, P, P]
         lib.decode_attn_paged_static.restype = I
+        lib.qk_norm_rope_append_axes.argtypes = [P] * 6 + [I, P] + [P] * 6 + [I] * 8 + [F, F, P]
+        lib.qk_norm_rope_append_axes.restype = I
+        lib.decode_attn_tree_workspace_size.argtypes = [I] * 7
+        lib.decode_attn_tree_workspace_size.restype = S
+        lib.decode_attn_paged_tree.argtypes = [P] * 9 + [I] * 8 + [F, F, P, P, P, S, P]
+        lib.decode_attn_paged_tree.restype = I
+        lib.kv_cache_commit_path.argtypes = [P, P, P, I] + [P] * 5 + [I] * 8 + [P]
+        lib.kv_cache_commit_path.restype = I
         _lib = lib
         return lib
 
@@ -513,3 +526,134 @@ def decode_attn_paged_static(q, k_cache, v_cache, block_table, context_lens, sca
         _dev(out_f32, torch.float32, "out_f32", nullable=True), _dev(out_bf16, bf, "out_bf16", nullable=True),
         _stream(stream))
     _check("decode_attn_paged_static", st)
+
+
+# ---------------------------------------------------------------- drafted-tree decoding
+def _shape(t, shape, name):
+    """Refuse a tensor (None passes) whose shape is not `shape`."""
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+
+
+def _on_one_device(**tensors):
+    """Refuse tensors that lie on different devices, or not on the current one
+    (the kernels run there)."""
+    here = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != here:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
+
+
+def qk_norm_rope_append_axes(q, k, v, gamma_q, gamma_k, positions, context_lens, block_table, k_cache, v_cache, q_out,
+                             axis_of_pair, rope_theta: float, eps: float = 1e-6, new_lens=None, stream=None) -> None:
+    """Prologue with given rotary positions on 1 to 4 axes: q [B, M, Hq, D], k/v [B, M, Hkv, D], positions
+    int32 [B, M, n_axes]. axis_of_pair: 64 axis numbers, one per frequency pair (for sections of s_0, s_1, ...
+    pairs: [0] * s_0 + [1] * s_1 + ...). new_lens int32 [B]: how many of a sequence's M tokens exist."""
+    lib = load_library()
+    bf, i32 = torch.bfloat16, torch.int32
+    B, M, Hq, D = q.shape
+    Hkv = k.shape[2]
+    num_pages, _, P, _ = k_cache.shape
+    n_axes = positions.shape[-1]
+    _shape(k, (B, M, Hkv, D), "k"), _shape(v, (B, M, Hkv, D), "v"), _shape(q_out, q.shape, "q_out")
+    _shape(gamma_q, (D,), "gamma_q"), _shape(gamma_k, (D,), "gamma_k")
+    _shape(positions, (B, M, n_axes), "positions"), _shape(context_lens, (B,), "context_lens")
+    _shape(new_lens, (B,), "new_lens"), _shape(block_table, (B, block_table.shape[-1]), "block_table")
+    _shape(k_cache, (num_pages, Hkv, P, D), "k_cache"), _shape(v_cache, (num_pages, Hkv, P, D), "v_cache")
+    axes = bytes(bytearray(axis_of_pair))
+    if len(axes) != 64:
+        raise ValueError(f"axis_of_pair must hold 64 axis numbers, got {len(axes)}")
+    _on_one_device(q=q, k=k, v=v, gamma_q=gamma_q, gamma_k=gamma_k, positions=positions, context_lens=context_lens,
+                   block_table=block_table, k_cache=k_cache, v_cache=v_cache, q_out=q_out, new_lens=new_lens)
+    st = lib.qk_norm_rope_append_axes(
+        _dev(q, bf, "q"), _dev(k, bf, "k"), _dev(v, bf, "v"), _dev(gamma_q, bf, "gamma_q"),
+        _dev(gamma_k, bf, "gamma_k"), _dev(positions, i32, "positions"), n_axes, axes,
+        _dev(context_lens, i32, "context_lens"), _dev(new_lens, i32, "new_lens", nullable=True),
+        _dev(block_table, i32, "block_table"), _dev(k_cache, bf, "k_cache"), _dev(v_cache, bf, "v_cache"),
+        _dev(q_out, bf, "q_out"), B, M, Hq, Hkv, D, P, block_table.shape[1], num_pages, float(rope_theta),
+        float(eps), _stream(stream))
+    _check("qk_norm_rope_append_axes", st)
+
+
+def decode_attn_tree_workspace_size(B: int, M: int, Hq: int, Hkv: int, D: int, page_size: int, max_pages: int) -> int:
+    return int(load_library().decode_attn_tree_workspace_size(B, M, Hq, Hkv, D, page_size, max_pages))
+
+
+def decode_attn_paged_tree(q, k_cache, v_cache, block_table, context_lens, tree_mask, scale: float, positions=None,
+                           draft_lens=None, slopes=None, softcap: float = 0.0, out_f32=None, out_bf16=None,
+                           workspace=None, stream=None) -> None:
+    """Attention of a tree of M drafted tokens per sequence: q and outputs [B, M, Hq, D]; tree_mask int64
+    [B, M] (bit j of entry i: token i sees drafted token j); positions int32 [B, M] and slopes float32 [Hq]
+    for the distance bias; draft_lens int32 [B] where a sequence has fewer than M tokens."""
+    lib = load_library()
+    bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    B, M, Hq, D = q.shape
+    num_pages, Hkv, P, _ = k_cache.shape
+    _shape(k_cache, (num_pages, Hkv, P, D), "k_cache"), _shape(v_cache, k_cache.shape, "v_cache")
+    _shape(block_table, (B, block_table.shape[-1]), "block_table"), _shape(context_lens, (B,), "context_lens")
+    _shape(tree_mask, (B, M), "tree_mask"), _shape(positions, (B, M), "positions")
+    _shape(draft_lens, (B,), "draft_lens"), _shape(slopes, (Hq,), "slopes")
+    _shape(out_f32, q.shape, "out_f32"), _shape(out_bf16, q.shape, "out_bf16")
+    _on_one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, context_lens=context_lens,
+                   tree_mask=tree_mask, positions=positions, draft_lens=draft_lens, slopes=slopes, out_f32=out_f32,
+                   out_bf16=out_bf16, workspace=workspace)
+    ws_ptr = _dev(workspace, torch.uint8, "workspace", nullable=True)
+    ws_bytes = workspace.numel() if workspace is not None else 0
+    st = lib.decode_attn_paged_tree(
+        _dev(q, bf, "q"), _dev(k_cache, bf, "k_cache"), _dev(v_cache, bf, "v_cache"),
+        _dev(block_table, i32, "block_table"), _dev(context_lens, i32, "context_lens"),
+        _dev(tree_mask, torch.int64, "tree_mask"), _dev(positions, i32, "positions", nullable=True),
+        _dev(draft_lens, i32, "draft_lens", nullable=True), _dev(slopes, f32, "slopes", nullable=True), B, M, Hq, Hkv,
+        D, P, block_table.shape[1], num_pages, float(scale), float(softcap), _dev(out_f32, f32, "out_f32", nullable=True),
+        _dev(out_bf16, bf, "out_bf16", nullable=True), ws_ptr, ws_bytes, _stream(stream))
+    _check("decode_attn_paged_tree", st)
+
+
+class CacheLayers:
+    """The paged caches and block tables of a model's layers, as kv_cache_commit_path takes them. Checked
+    once here; the object keeps the tensors alive. All layers have the same shapes; they may share a table."""
+
+    def __init__(self, k_caches, v_caches, block_tables):
+        n = len(k_caches)
+        if n < 1 or len(v_caches) != n or len(block_tables) != n:
+            raise ValueError("CacheLayers needs the same number (at least 1) of K caches, V caches and block tables")
+        bf, i32 = torch.bfloat16, torch.int32
+        self.num_pages, self.Hkv, self.page_size, self.D = k_caches[0].shape
+        self.B, self.max_pages = block_tables[0].shape
+        self.device = k_caches[0].device
+        for i in range(n):
+            _shape(k_caches[i], k_caches[0].shape, f"k_caches[{i}]")
+            _shape(v_caches[i], k_caches[0].shape, f"v_caches[{i}]")
+            _shape(block_tables[i], block_tables[0].shape, f"block_tables[{i}]")
+            if not k_caches[i].device == v_caches[i].device == block_tables[i].device == self.device:
+                raise ValueError(f"layer {i} is not on {self.device}")
+        array = ctypes.c_void_p * n
+        self.k_ptrs = array(*[_dev(t, bf, "k_cache") for t in k_caches])
+        self.v_ptrs = array(*[_dev(t, bf, "v_cache") for t in v_caches])
+        self.table_ptrs = array(*[_dev(t, i32, "block_table") for t in block_tables])
+        self.tensors = (list(k_caches), list(v_caches), list(block_tables))
+
+    def __len__(self) -> int:
+        return len(self.k_ptrs)
+
+
+def kv_cache_commit_path(layers: CacheLayers, context_lens, path, path_lens, context_lens_out, M: int, draft_lens=None,
+                         stream=None) -> None:
+    """Keep the accepted path of a drafted tree: slot prefix + path[b, i] moves to slot prefix + i in every
+    layer's K and V cache, and context_lens_out[b] = prefix + path_lens[b]. path int32 [B, A]; M is the
+    number of drafted tokens per sequence that context_lens counts (draft_lens int32 [B] where it varies)."""
+    lib = load_library()
+    i32 = torch.int32
+    B, A = path.shape
+    if B != layers.B:
+        raise ValueError(f"path has {B} sequences, the layers' block tables {layers.B}")
+    _shape(context_lens, (B,), "context_lens"), _shape(path_lens, (B,), "path_lens")
+    _shape(context_lens_out, (B,), "context_lens_out"), _shape(draft_lens, (B,), "draft_lens")
+    _on_one_device(caches=layers.tensors[0][0], context_lens=context_lens, path=path, path_lens=path_lens,
+                   context_lens_out=context_lens_out, draft_lens=draft_lens)
+    st = lib.kv_cache_commit_path(
+        layers.k_ptrs, layers.v_ptrs, layers.table_ptrs, len(layers), _dev(context_lens, i32, "context_lens"),
+        _dev(draft_lens, i32, "draft_lens", nullable=True), _dev(path, i32, "path"), _dev(path_lens, i32, "path_lens"),
+        _dev(context_lens_out, i32, "context_lens_out"), B, int(M), A, layers.Hkv, layers.D, layers.page_size,
+        layers.max_pages, layers.num_pages, _stream(stream))
+    _check("kv_cache_commit_path", st)

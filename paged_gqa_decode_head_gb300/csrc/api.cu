@@ -115,14 +115,20 @@ int pgqa_device_error(unsigned *flags_out, int clear)
     cudaError_t err = cudaDeviceSynchronize();
     if (err != cudaSuccess)
         return cuda_fail(err, "pgqa_device_error");
-    unsigned a = 0, b = 0, c = 0;
+    unsigned a = 0, b = 0, c = 0, d = 0, e = 0, f = 0;
     if ((err = pgqa::read_flags_prologue(&a, clear != 0)) != cudaSuccess)
         return cuda_fail(err, "pgqa_device_error");
     if ((err = pgqa::read_flags_decode(&b, clear != 0)) != cudaSuccess)
         return cuda_fail(err, "pgqa_device_error");
     if ((err = pgqa::read_flags_int8(&c, clear != 0)) != cudaSuccess)
         return cuda_fail(err, "pgqa_device_error");
-    *flags_out = a | b | c;
+    if ((err = pgqa::read_flags_rope_axes(&d, clear != 0)) != cudaSuccess)
+        return cuda_fail(err, "pgqa_device_error");
+    if ((err = pgqa::read_flags_tree_attn(&e, clear != 0)) != cudaSuccess)
+        return cuda_fail(err, "pgqa_device_error");
+    if ((err = pgqa::read_flags_commit_path(&f, clear != 0)) != cudaSuccess)
+        return cuda_fail(err, "pgqa_device_error");
+    *flags_out = a | b | c | d | e | f;
     return ok();
 }
 
@@ -874,6 +880,164 @@ int decode_step_paged_int8(const pgqa_bf16 *q, const pgqa_bf16 *k, const pgqa_bf
                           v_scale, block_table, context_lens, q_out, B, Hq, Hkv, D, page_size, max_pages,
                           num_pages, rope_theta, eps, scale, num_partitions, out_f32, out_bf16, workspace,
                           ws_bytes, stream);
+}
+
+// ---------------------------------------------------------------- drafted-tree decoding
+
+int qk_norm_rope_append_axes(const pgqa_bf16 *q, const pgqa_bf16 *k, const pgqa_bf16 *v,
+                             const pgqa_bf16 *gamma_q, const pgqa_bf16 *gamma_k, const int32_t *positions,
+                             int n_axes, const uint8_t *axis_of_pair, const int32_t *context_lens,
+                             const int32_t *new_lens, const int32_t *block_table, pgqa_bf16 *k_cache,
+                             pgqa_bf16 *v_cache, pgqa_bf16 *q_out, int B, int M, int Hq, int Hkv, int D,
+                             int page_size, int max_pages, int num_pages, float rope_theta, float eps,
+                             cudaStream_t stream)
+{
+    const char *fn = "qk_norm_rope_append_axes";
+    if (int st = check_heads(fn, B, Hq, Hkv, D))
+        return st;
+    if (int st = check_pages(fn, page_size, max_pages, num_pages))
+        return st;
+    if (!(rope_theta > 0.f) || !std::isfinite(rope_theta) || !(eps >= 0.f) || !std::isfinite(eps))
+        return fail(PGQA_ERR_INVALID_ARG, "%s: rope_theta must be > 0 and eps >= 0", fn);
+    if (M < 1)
+        return fail(PGQA_ERR_INVALID_ARG, "%s: M = %d new tokens per sequence, need >= 1", fn, M);
+    if (static_cast<long long>(B) * M > (1LL << 30))
+        return fail(PGQA_ERR_UNSUPPORTED, "%s: B * M exceeds 2^30 tokens", fn);
+    if (n_axes < 1 || n_axes > 4)
+        return fail(PGQA_ERR_UNSUPPORTED, "%s: n_axes = %d outside [1, 4]", fn, n_axes);
+    if (!axis_of_pair)
+        return fail(PGQA_ERR_INVALID_ARG, "%s: axis_of_pair is NULL", fn);
+    for (int r = 0; r < pgqa::kHeadDimHost / 2; ++r)
+        if (axis_of_pair[r] >= n_axes)
+            return fail(PGQA_ERR_INVALID_ARG, "%s: axis_of_pair[%d] = %d, need an axis below %d", fn, r,
+                        axis_of_pair[r], n_axes);
+    if (B == 0)
+        return ok();
+    if (!q || !k || !v || !gamma_q || !gamma_k || !positions || !context_lens || !block_table || !k_cache ||
+        !v_cache || !q_out)
+        return fail(PGQA_ERR_INVALID_ARG, "%s: a required pointer is NULL", fn);
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(gamma_q) || !aligned16(gamma_k) ||
+        !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(q_out) || !aligned4(positions) ||
+        !aligned4(context_lens) || !aligned4(block_table) || !aligned4(new_lens))
+        return fail(PGQA_ERR_MISALIGNED, "%s: tensors need 16-byte and index arrays 4-byte alignment", fn);
+    pgqa::RopeAxesArgs a{q, k, v, gamma_q, gamma_k, positions, n_axes, axis_of_pair, context_lens, new_lens,
+                         block_table, k_cache, v_cache, q_out, B, M, Hq, Hkv, page_size, max_pages, num_pages,
+                         static_cast<double>(rope_theta), eps};
+    cudaError_t err = pgqa::launch_rope_axes(a, stream);
+    if (err != cudaSuccess)
+        return cuda_fail(err, fn);
+    return ok();
+}
+
+size_t decode_attn_tree_workspace_size(int B, int M, int Hq, int Hkv, int D, int page_size, int max_pages)
+{
+    (void)D;
+    if (B < 0 || M < 1 || M > 64 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Hq / Hkv > pgqa::kMaxGroupHost ||
+        page_size <= 0 || max_pages < 0)
+        return 0;
+    return pgqa::tree_attn_workspace_bytes(B, M, Hq, Hkv, page_size, max_pages, sm_count_current_device());
+}
+
+int decode_attn_paged_tree(const pgqa_bf16 *q, const pgqa_bf16 *k_cache, const pgqa_bf16 *v_cache,
+                           const int32_t *block_table, const int32_t *context_lens, const uint64_t *tree_mask,
+                           const int32_t *positions, const int32_t *draft_lens, const float *slopes, int B,
+                           int M, int Hq, int Hkv, int D, int page_size, int max_pages, int num_pages,
+                           float scale, float softcap, float *out_f32, pgqa_bf16 *out_bf16, void *workspace,
+                           size_t ws_bytes, cudaStream_t stream)
+{
+    const char *fn = "decode_attn_paged_tree";
+    if (int st = check_heads(fn, B, Hq, Hkv, D))
+        return st;
+    if (int st = check_pages(fn, page_size, max_pages, num_pages))
+        return st;
+    if (M < 1 || M > 64)
+        return fail(PGQA_ERR_INVALID_ARG, "%s: M = %d drafted tokens per sequence outside [1, 64]", fn, M);
+    if (!std::isfinite(scale))
+        return fail(PGQA_ERR_INVALID_ARG, "%s: scale is not finite", fn);
+    if (!(softcap >= 0.f) || !std::isfinite(softcap))
+        return fail(PGQA_ERR_INVALID_ARG, "%s: softcap must be 0 or a positive finite number", fn);
+    if (static_cast<long long>(num_pages) * Hkv * page_size > 0x7FFFFFFFLL)
+        return fail(PGQA_ERR_UNSUPPORTED, "%s: num_pages * Hkv * page_size exceeds 2^31 - 1 rows", fn);
+    if (B == 0)
+        return ok();
+    if (!q || !k_cache || !v_cache || !block_table || !context_lens || !tree_mask)
+        return fail(PGQA_ERR_INVALID_ARG, "%s: a required pointer is NULL", fn);
+    if (num_pages == 0)
+        return fail(PGQA_ERR_INVALID_ARG, "%s: the page pool is empty", fn);
+    if (slopes && !positions)
+        return fail(PGQA_ERR_INVALID_ARG, "%s: slopes need positions", fn);
+    if (!out_f32 && !out_bf16)
+        return fail(PGQA_ERR_INVALID_ARG, "%s: out_f32 and out_bf16 are both NULL", fn);
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out_f32) ||
+        !aligned16(out_bf16) || !aligned16(workspace))
+        return fail(PGQA_ERR_MISALIGNED, "%s: tensors need 16-byte alignment", fn);
+    if ((reinterpret_cast<uintptr_t>(tree_mask) & 7u) || !aligned4(block_table) || !aligned4(context_lens) ||
+        !aligned4(positions) || !aligned4(draft_lens) || !aligned4(slopes))
+        return fail(PGQA_ERR_MISALIGNED, "%s: tree_mask needs 8-byte, the other index arrays 4-byte alignment", fn);
+    pgqa::TreeAttnArgs a{q, k_cache, v_cache, block_table, context_lens, tree_mask, positions, draft_lens,
+                         slopes, B, M, Hq, Hkv, page_size, max_pages, num_pages, scale, softcap, out_f32,
+                         out_bf16, workspace, sm_count_current_device()};
+    const size_t need = pgqa::tree_attn_workspace_bytes(B, M, Hq, Hkv, page_size, max_pages, a.sm_count);
+    if (need > 0 && (!workspace || ws_bytes < need))
+        return fail(PGQA_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, got %zu", fn, need,
+                    workspace ? ws_bytes : static_cast<size_t>(0));
+    cudaError_t err = pgqa::launch_tree_attn(a, stream);
+    if (err != cudaSuccess)
+        return cuda_fail(err, fn);
+    return ok();
+}
+
+int kv_cache_commit_path(pgqa_bf16 *const *k_caches, pgqa_bf16 *const *v_caches,
+                         const int32_t *const *block_tables, int n_layers, const int32_t *context_lens,
+                         const int32_t *draft_lens, const int32_t *path, const int32_t *path_lens,
+                         int32_t *context_lens_out, int B, int M, int A, int Hkv, int D, int page_size,
+                         int max_pages, int num_pages, cudaStream_t stream)
+{
+    const char *fn = "kv_cache_commit_path";
+    if (int st = check_heads(fn, B, Hkv, Hkv, D))
+        return st;
+    if (Hkv > 65535)
+        return fail(PGQA_ERR_UNSUPPORTED, "%s: Hkv = %d exceeds 65535", fn, Hkv);
+    if (int st = check_pages(fn, page_size, max_pages, num_pages))
+        return st;
+    if (M < 1 || M > 64)
+        return fail(PGQA_ERR_INVALID_ARG, "%s: M = %d drafted tokens per sequence outside [1, 64]", fn, M);
+    if (A < 1 || A > M)
+        return fail(PGQA_ERR_INVALID_ARG, "%s: paths of A = %d entries, need 1 <= A <= M = %d", fn, A, M);
+    if (n_layers < 1 || n_layers > PGQA_MAX_COMMIT_LAYERS)
+        return fail(PGQA_ERR_UNSUPPORTED, "%s: n_layers = %d outside [1, %d]", fn, n_layers,
+                    PGQA_MAX_COMMIT_LAYERS);
+    if (!k_caches || !v_caches || !block_tables)
+        return fail(PGQA_ERR_INVALID_ARG, "%s: a required pointer is NULL", fn);
+    if (B == 0)
+        return ok();
+    if (!context_lens || !path || !path_lens || !context_lens_out)
+        return fail(PGQA_ERR_INVALID_ARG, "%s: a required pointer is NULL", fn);
+    if (!aligned4(context_lens) || !aligned4(draft_lens) || !aligned4(path) || !aligned4(path_lens) ||
+        !aligned4(context_lens_out))
+        return fail(PGQA_ERR_MISALIGNED, "%s: index arrays need 4-byte alignment", fn);
+    for (int l = 0; l < n_layers; ++l) {
+        if (!k_caches[l] || !v_caches[l] || !block_tables[l])
+            return fail(PGQA_ERR_INVALID_ARG, "%s: a pointer of layer %d is NULL", fn, l);
+        if (!aligned16(k_caches[l]) || !aligned16(v_caches[l]) || !aligned4(block_tables[l]))
+            return fail(PGQA_ERR_MISALIGNED, "%s: layer %d: caches need 16-byte, the table 4-byte alignment", fn, l);
+        for (int e = 0; e < l; ++e)
+            if (block_tables[e] == block_tables[l] && (k_caches[e] == k_caches[l] || v_caches[e] == v_caches[l]))
+                return fail(PGQA_ERR_INVALID_ARG, "%s: layers %d and %d share a cache and its table", fn, e, l);
+    }
+    const auto overlap = [&](const int32_t *p, long long n) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(context_lens_out);
+        return p && x < y + 4ull * B && y < x + 4ull * n;
+    };
+    if (overlap(context_lens, B) || overlap(draft_lens, B) || overlap(path_lens, B) ||
+        overlap(path, static_cast<long long>(B) * A))
+        return fail(PGQA_ERR_INVALID_ARG, "%s: context_lens_out overlaps another index array", fn);
+    pgqa::CommitPathArgs a{k_caches, v_caches, block_tables, n_layers, context_lens, draft_lens, path, path_lens,
+                           context_lens_out, B, M, A, Hkv, page_size, max_pages, num_pages};
+    cudaError_t err = pgqa::launch_commit_path(a, stream);
+    if (err != cudaSuccess)
+        return cuda_fail(err, fn);
+    return ok();
 }
 
 } // extern "C"

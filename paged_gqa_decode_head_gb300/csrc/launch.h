@@ -130,6 +130,49 @@ cudaError_t launch_decode_int8(const DecodeInt8Args &a, cudaStream_t stream);
 size_t decode_int8_workspace_bytes(int B, int Hkv, int Hq, int num_partitions);
 cudaError_t read_flags_int8(unsigned *flags, bool clear);
 
+// Drafted-tree decoding (rope_axes.cu, tree_attn.cu, commit_path.cu).
+struct RopeAxesArgs {
+    const pgqa_bf16 *q, *k, *v, *gamma_q, *gamma_k;
+    const int32_t *positions; // [B][M][n_axes]
+    int n_axes;
+    const uint8_t *axis_of_pair; // host, 64 entries
+    const int32_t *context_lens, *new_lens, *block_table;
+    pgqa_bf16 *k_cache, *v_cache, *q_out;
+    int B, M, Hq, Hkv, page_size, max_pages, num_pages;
+    double rope_theta;
+    float eps;
+};
+cudaError_t launch_rope_axes(const RopeAxesArgs &a, cudaStream_t stream);
+cudaError_t read_flags_rope_axes(unsigned *flags, bool clear);
+
+struct TreeAttnArgs {
+    const pgqa_bf16 *q, *k_cache, *v_cache;
+    const int32_t *block_table, *context_lens;
+    const uint64_t *tree_mask;
+    const int32_t *positions, *draft_lens; // nullable
+    const float *slopes;                   // nullable
+    int B, M, Hq, Hkv, page_size, max_pages, num_pages;
+    float scale, softcap;
+    float *out_f32;      // nullable
+    pgqa_bf16 *out_bf16; // nullable
+    void *ws;
+    int sm_count;
+};
+size_t tree_attn_workspace_bytes(int B, int M, int Hq, int Hkv, int page_size, int max_pages, int sm_count);
+cudaError_t launch_tree_attn(const TreeAttnArgs &a, cudaStream_t stream);
+cudaError_t read_flags_tree_attn(unsigned *flags, bool clear);
+
+struct CommitPathArgs {
+    pgqa_bf16 *const *k_caches, *const *v_caches; // host arrays of n_layers
+    const int32_t *const *block_tables;
+    int n_layers;
+    const int32_t *context_lens, *draft_lens, *path, *path_lens;
+    int32_t *context_lens_out;
+    int B, M, A, Hkv, page_size, max_pages, num_pages;
+};
+cudaError_t launch_commit_path(const CommitPathArgs &a, cudaStream_t stream);
+cudaError_t read_flags_commit_path(unsigned *flags, bool clear);
+
 // Launch `kernel` on `stream` with programmatic stream serialisation: it may
 // start while the previous kernel in the stream is still running, and must
 // call griddepcontrol.wait before touching anything that kernel produces.

@@ -1,0 +1,206 @@
+// rope_axes.cu -- qk_norm_rope_append_axes: per-head Q/K RMSNorm, rotary
+// positions with several axes, and the paged K/V append of M tokens per
+// sequence (drafted trees, image and video patches, prompts).
+//
+// For token i with positions p_0 .. p_(A-1) and pair r (dims r and r + 64):
+//   xhat = x * gamma / sqrt(mean(x^2) + eps)
+//   phi_r = p_(axis(r)) * theta^(-2r/128)
+//   (a, b) -> (a cos phi - b sin phi, b cos phi + a sin phi)
+// The angle is taken modulo one turn in 64-bit fixed point: w_r = frac(omega_r
+// / 2 pi) * 2^64, and the low 64 bits of p * w_r are the fraction of a turn,
+// exactly for that w_r and any int32 p. This GPU's fp64 rate is a small
+// fraction of its integer rate; one 64-bit integer product replaces the fp64
+// product and reduction.
+//
+// Bound: memory, (2 Hq + 4 Hkv) * 256 bytes a token read and written once. The
+// single-token prologue (prologue.cu) recomputes the angles for every head; at
+// prompt lengths that would cost more than the copy, so here a block owns one
+// token, forms its 64 rotations once in shared memory, and its 16 groups of 8
+// lanes walk the token's Hq + 2 Hkv rows with 16-byte loads and stores (lane s
+// of a group holds dims 8s .. 8s+7 and 64 + 8s .. 64 + 8s + 7, so a pair's two
+// halves are in one lane).
+#include "common.cuh"
+#include "launch.h"
+
+#include <cmath>
+
+namespace pgqa {
+namespace {
+
+__device__ unsigned g_flags_rope_axes;
+
+constexpr int kPairs = kHeadDim / 2;
+constexpr int kRopeThreads = 128;
+constexpr int kRowLanes = 8;                               // lanes that hold one head row
+constexpr int kRowsPerPass = kRopeThreads / kRowLanes;     // head rows a block handles at once
+
+struct RopeAxesParams {
+    uint64_t turn[kPairs];  // frac(omega_r / 2 pi) * 2^64
+    uint64_t axis_bits[2];  // axis of pair r: two bits at 2 (r % 32) of word r / 32
+    const uint16_t *q, *k, *v, *gamma_q, *gamma_k;
+    const int32_t *positions, *context_lens, *new_lens, *block_table;
+    uint16_t *k_cache, *v_cache, *q_out;
+    int M, Hq, Hkv, n_axes, log2_page, max_pages, num_pages;
+    float eps;
+};
+
+// x -> the row's element j of lo (dims 8s + j) or hi (64 + 8s + j)
+__device__ __forceinline__ uint4 pack8(const float *f)
+{
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+}
+
+__global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(const __grid_constant__ RopeAxesParams p)
+{
+    // Everything this kernel reads may come from the kernel before it, and
+    // what it writes may still be read there: wait before touching memory.
+    allow_dependent_launch();
+    grid_dependency_wait();
+    const int tid = threadIdx.x;
+    const int tok = blockIdx.x; // b * M + i
+    const int b = tok / p.M, i = tok - b * p.M;
+    const int n = p.new_lens ? p.new_lens[b] : p.M;
+    const int T = p.context_lens[b];
+    if (n < 0 || n > p.M || T < n || T > (p.max_pages << p.log2_page)) {
+        if (i == 0 && tid == 0)
+            atomicOr(&g_flags_rope_axes, PGQA_DEVERR_BAD_CONTEXT);
+        return;
+    }
+    if (i >= n)
+        return;
+    const int slot = T - n + i;
+    const int phys = p.block_table[static_cast<size_t>(b) * p.max_pages + (slot >> p.log2_page)];
+    const bool page_ok = phys >= 0 && phys < p.num_pages;
+    if (!page_ok && tid == 0)
+        atomicOr(&g_flags_rope_axes, PGQA_DEVERR_BAD_PAGE);
+
+    const int lane8 = tid & (kRowLanes - 1), row0 = tid / kRowLanes;
+    const int rows = p.Hq + 2 * p.Hkv; // Q heads, K heads, V heads
+    const size_t P = size_t{1} << p.log2_page;
+    const size_t cell = static_cast<size_t>(phys) * p.Hkv * P + (slot & (P - 1)); // + head * P: the cache row
+    const auto load = [&](int row, uint4 &lo, uint4 &hi) {
+        const uint16_t *src;
+        if (row < p.Hq)
+            src = p.q + (static_cast<size_t>(tok) * p.Hq + row) * kHeadDim;
+        else if (row < p.Hq + p.Hkv)
+            src = p.k + (static_cast<size_t>(tok) * p.Hkv + row - p.Hq) * kHeadDim;
+        else
+            src = p.v + (static_cast<size_t>(tok) * p.Hkv + row - p.Hq - p.Hkv) * kHeadDim;
+        lo = *reinterpret_cast<const uint4 *>(src + 8 * lane8);
+        hi = *reinterpret_cast<const uint4 *>(src + kPairs + 8 * lane8);
+    };
+    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+    if (row0 < rows)
+        load(row0, lo, hi);
+
+    __shared__ __align__(16) float rot_cos[kPairs], rot_sin[kPairs];
+    if (tid < kPairs) {
+        const int axis = static_cast<int>(p.axis_bits[tid >> 5] >> (2 * (tid & 31))) & 3;
+        const int pos = p.positions[static_cast<size_t>(tok) * p.n_axes + axis];
+        const uint64_t frac = static_cast<uint64_t>(static_cast<int64_t>(pos)) * p.turn[tid];
+        // the upper 32 bits as a signed part of a turn, in half turns
+        const float half_turns = static_cast<float>(static_cast<int32_t>(frac >> 32)) * 0x1p-31f;
+        sincospif(half_turns, &rot_sin[tid], &rot_cos[tid]);
+    }
+    __syncthreads();
+    float cs[8], sn[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        cs[j] = rot_cos[8 * lane8 + j];
+        sn[j] = rot_sin[8 * lane8 + j];
+    }
+
+    for (int base = 0; base < rows; base += kRowsPerPass) {
+        const int row = base + row0;
+        uint4 next_lo = make_uint4(0, 0, 0, 0), next_hi = next_lo;
+        if (row + kRowsPerPass < rows)
+            load(row + kRowsPerPass, next_lo, next_hi);
+        const bool is_q = row < p.Hq, is_v = row >= p.Hq + p.Hkv;
+        float a[8], c[8];
+        unpack8(lo, a);
+        unpack8(hi, c);
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            ss = fmaf(a[j], a[j], fmaf(c[j], c[j], ss));
+#pragma unroll
+        for (int off = kRowLanes / 2; off > 0; off >>= 1)
+            ss += __shfl_xor_sync(0xFFFFFFFFu, ss, off);
+        if (row < rows && (is_q || page_ok)) {
+            uint4 out_lo = lo, out_hi = hi; // V rows go through bit for bit
+            if (!is_v) {
+                const float inv_rms = rsqrtf(fmaf(ss, 1.0f / kHeadDim, p.eps));
+                const uint16_t *gamma = is_q ? p.gamma_q : p.gamma_k;
+                float ga[8], gc[8];
+                unpack8(*reinterpret_cast<const uint4 *>(gamma + 8 * lane8), ga);
+                unpack8(*reinterpret_cast<const uint4 *>(gamma + kPairs + 8 * lane8), gc);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float x = a[j] * inv_rms * ga[j], y = c[j] * inv_rms * gc[j];
+                    a[j] = fmaf(x, cs[j], -(y * sn[j]));
+                    c[j] = fmaf(y, cs[j], x * sn[j]);
+                }
+                out_lo = pack8(a);
+                out_hi = pack8(c);
+            }
+            uint16_t *dst;
+            if (is_q)
+                dst = p.q_out + (static_cast<size_t>(tok) * p.Hq + row) * kHeadDim;
+            else if (!is_v)
+                dst = p.k_cache + (cell + (row - p.Hq) * P) * kHeadDim;
+            else
+                dst = p.v_cache + (cell + (row - p.Hq - p.Hkv) * P) * kHeadDim;
+            *reinterpret_cast<uint4 *>(dst + 8 * lane8) = out_lo;
+            *reinterpret_cast<uint4 *>(dst + kPairs + 8 * lane8) = out_hi;
+        }
+        lo = next_lo;
+        hi = next_hi;
+    }
+}
+
+} // namespace
+
+cudaError_t launch_rope_axes(const RopeAxesArgs &a, cudaStream_t stream)
+{
+    RopeAxesParams p{};
+    for (int r = 0; r < kPairs; ++r) {
+        const double turns = std::pow(a.rope_theta, -2.0 * r / kHeadDim) / 6.283185307179586476925;
+        p.turn[r] = static_cast<uint64_t>(std::ldexp(turns - std::floor(turns), 64));
+        p.axis_bits[r >> 5] |= static_cast<uint64_t>(a.axis_of_pair[r] & 3) << (2 * (r & 31));
+    }
+    p.q = a.q;
+    p.k = a.k;
+    p.v = a.v;
+    p.gamma_q = a.gamma_q;
+    p.gamma_k = a.gamma_k;
+    p.positions = a.positions;
+    p.context_lens = a.context_lens;
+    p.new_lens = a.new_lens;
+    p.block_table = a.block_table;
+    p.k_cache = a.k_cache;
+    p.v_cache = a.v_cache;
+    p.q_out = a.q_out;
+    p.M = a.M;
+    p.Hq = a.Hq;
+    p.Hkv = a.Hkv;
+    p.n_axes = a.n_axes;
+    p.log2_page = __builtin_ctz(static_cast<unsigned>(a.page_size));
+    p.max_pages = a.max_pages;
+    p.num_pages = a.num_pages;
+    p.eps = a.eps;
+    return launch_pdl(rope_axes_kernel, dim3(static_cast<unsigned>(a.B) * static_cast<unsigned>(a.M)),
+                      dim3(kRopeThreads), 0, stream, p);
+}
+
+cudaError_t read_flags_rope_axes(unsigned *flags, bool clear)
+{
+    cudaError_t err = cudaMemcpyFromSymbol(flags, g_flags_rope_axes, sizeof(unsigned));
+    if (err == cudaSuccess && clear) {
+        const unsigned zero = 0;
+        err = cudaMemcpyToSymbol(g_flags_rope_axes, &zero, sizeof(unsigned));
+    }
+    return err;
+}
+
+} // namespace pgqa
