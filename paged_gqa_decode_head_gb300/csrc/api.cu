@@ -958,6 +958,10 @@ int decode_attn_paged_tree(const pgqa_bf16 *q, const pgqa_bf16 *k_cache, const p
         return fail(PGQA_ERR_INVALID_ARG, "%s: softcap must be 0 or a positive finite number", fn);
     if (static_cast<long long>(num_pages) * Hkv * page_size > 0x7FFFFFFFLL)
         return fail(PGQA_ERR_UNSUPPORTED, "%s: num_pages * Hkv * page_size exceeds 2^31 - 1 rows", fn);
+    if (Hkv > 65535)
+        return fail(PGQA_ERR_UNSUPPORTED, "%s: Hkv = %d exceeds 65535", fn, Hkv);
+    if ((static_cast<long long>(max_pages) * page_size / 128 + 1) * Hkv > 0x7FFFFFFFLL / (B > 0 ? B : 1))
+        return fail(PGQA_ERR_UNSUPPORTED, "%s: B * Hkv * max_pages * page_size exceeds 2^31 tiles of 128 keys", fn);
     if (B == 0)
         return ok();
     if (!q || !k_cache || !v_cache || !block_table || !context_lens || !tree_mask)

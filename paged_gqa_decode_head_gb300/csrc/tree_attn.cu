@@ -1,16 +1,68 @@
 // tree_attn.cu -- decode_attn_paged_tree: attention of a tree of drafted
 // tokens over the paged cache, with an optional tanh cap and distance bias.
 //
-// One warp per query row (sequence, drafted token, head) walks the keys with
-// an online softmax; lane l holds dims 4l .. 4l+3. Every row reads the cache
-// by itself.
+// Mathematics. For the R = M * g query rows (drafted token, head) that share a
+// KV head: x = scale Q K^T, capped and biased; softmax over the keys that the
+// row sees (the prefix, and the drafted tokens of its mask); O = P V. Computed
+// over tiles of 128 keys with a running reference m and sum l per row (online
+// softmax in base 2): p = 2^(y - m), l += p, O += p V; when a row's scores rise
+// more than 8 above m, m moves up and l and O are scaled (2^8 is far inside
+// fp32's range, so most tiles need no rescale).
+//
+// Bound. The cache is read once: 512 bytes per (key, KV head) against 4 * 128 * R
+// flops. Up to R of about 200 the memory bounds it, above that the tensor cores.
+// mma.sync cannot follow the memory from R = 32 on; tcgen05 with M = 128 rows can,
+// even with rows to spare.
+//
+// Work split. The tiles of all sequences and KV heads are numbered in one row
+// (sequence, head, tile) and each CTA takes an equal run of them, whatever the
+// lengths: no partition size, no waves, ragged batches balance by themselves.
+// A run that covers a (sequence, head) from its first to its last tile writes
+// the output; the pieces of the others go to the workspace (at most two per
+// CTA) and merge_kernel joins them, in order, in the same stream.
+//
+// CTA: one per SM, 12 warps around a ring of five 32 KB shared-memory slots
+// (K and V tiles in consumption order), Q, and all of tensor memory (S/P of
+// two streams, O of two streams, 128 columns each):
+//   warp 8   requests Q, K and V tiles by TMA, one lane per page of a tile;
+//   warp 9   issues the tcgen05 products S = Q K^T (both operands from shared
+//            memory) and O += P V (P from tensor memory);
+//   warps 0-3 and 4-7  one softmax warpgroup per stream: a thread owns a row,
+//            reads its 128 scores from tensor memory and writes P over them.
+// Two streams keep the tensor core and the softmax busy at once. With up to
+// 128 rows the streams take alternate key tiles of the same rows and are joined
+// at the end of a run; with more, they are two row tiles over the same keys.
+//
+// Rounding: P enters its product as a bf16 pair hi + lo (16 significant bits,
+// so that fp32 outputs keep their meaning); S, O, m and l are fp32.
 #include "common.cuh"
 #include "launch.h"
+#include "tcgen05.cuh"
+#include "tensor_map.h"
+
+#include <atomic>
+#include <cfloat>
+#include <cmath>
 
 namespace pgqa {
 namespace {
 
 __device__ unsigned g_flags_tree;
+
+constexpr int kTileKeys = 128;
+constexpr int kTileRows = 128;
+constexpr int kTileBytes = kTileKeys * kRowBytes; // 32 KB of K or V
+constexpr int kSlots = 5;
+constexpr int kValidRing = 8;      // units whose page masks are kept (the ring holds at most 4 ahead)
+constexpr int kSoftmaxThreads = 256;
+constexpr int kTreeThreads = 384; // three warpgroups (the last two warps idle)
+constexpr int kProducerWarp = 8, kMmaWarp = 9;
+constexpr float kRescaleLog2 = 8.f; // rise of a row's scores that moves its reference
+constexpr int kMergeThreads = 256;
+
+// TMEM columns: S (fp32, 128 columns; P hi in its first 64, P lo in the other
+// 64) and O of stream s.
+constexpr uint32_t kColS = 0, kColO = 256;
 
 struct TreeParams {
     const uint16_t *q, *k, *v;
@@ -18,98 +70,989 @@ struct TreeParams {
     const uint64_t *tree_mask;
     const int32_t *positions, *draft_lens;
     const float *slopes;
-    int M, Hq, Hkv, log2_page, max_pages, num_pages;
-    float scale, softcap;
+    int B, M, Hq, Hkv, log2_page, max_pages, num_pages;
+    int g;             // query heads per KV head
+    int tile_tokens;   // drafted tokens per row tile (g * tile_tokens <= 128 rows)
+    int row_tiles;     // ceil(M / tile_tokens)
+    int row_groups;    // CTAs that share a run of tiles: one per pair of row tiles
+    int rec_rows;      // rows of a partial record
+    int ctas;          // grid size / row_groups
+    float c;           // plain scores: y = |scale| log2 e * x (the sign is in the MMA descriptor)
+    float cap_in, cap_out; // capped: y = cap_out tanh(x cap_in / (2 log2 e))
+    uint32_t negate_q;     // scale < 0
     float *out_f32;
     uint16_t *out_bf16;
+    int32_t *unit_base;     // [B + 1] first tile number of each sequence, total
+    float *rec_m, *rec_l;   // [2 * grid][rec_rows]
+    float *rec_acc;         // [2 * grid][rec_rows][128]
 };
 
-__device__ __forceinline__ float4 load4(const uint16_t *row)
+struct __align__(1024) TreeSmem {
+    unsigned char slots[kSlots][kTileBytes];
+    unsigned char q[2][kTileRows * kRowBytes];
+    // barriers
+    uint64_t full[kSlots], empty[kSlots];
+    uint64_t q_full[2], q_empty[2];
+    uint64_t s_full[2], p_ready[2];
+    uint64_t seg_done, ml_ready, epi_done, drain;
+    uint64_t bad_rows;  // drafted tokens of the segment whose V row is not finite
+    uint32_t valid[kValidRing]; // pages inside the pool, a bit per 16 keys of a tile
+    uint32_t tmem_base;
+    int start_b, start_h, start_tile, units; // this CTA's run
+    int scan[kTreeThreads / 32];
+    float2 ml[2][kTileRows]; // (m, l) of both streams
+};
+constexpr int kTreeSmem = sizeof(TreeSmem);
+static_assert(kTreeSmem <= 232448, "one CTA's shared memory");
+
+__device__ __forceinline__ float ex2(float x)
 {
-    const uint2 u = reinterpret_cast<const uint2 *>(row)[threadIdx.x & 31];
-    return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-__global__ void __launch_bounds__(32) tree_rows_kernel(const TreeParams p)
+// A bounded wait by a whole warp, with one answer for all its lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity)
+{
+    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity));
+}
+
+// Sequence b's length and drafted tokens; false if they make no sense.
+__device__ __forceinline__ bool sequence(const TreeParams &p, int b, int &T, int &n)
+{
+    T = p.context_lens[b];
+    n = p.draft_lens ? p.draft_lens[b] : p.M;
+    return n >= 0 && n <= p.M && T >= n && T <= (p.max_pages << p.log2_page);
+}
+__device__ __forceinline__ int tiles_of(const TreeParams &p, int b, int &T, int &n)
+{
+    return sequence(p, b, T, n) && n > 0 ? (T - 1) / kTileKeys + 1 : 0;
+}
+
+// Walks a CTA's run of tiles, segment by segment (the tiles of one (sequence,
+// KV head)).
+struct Segments {
+    int b, h, tile, left;      // next tile, tiles left in the run
+    int T, n, tiles;           // sequence b
+    int seg_tile0, seg_tile1;  // current segment
+    __device__ Segments(const TreeParams &p, const TreeSmem &s)
+        : b(s.start_b), h(s.start_h), tile(s.start_tile), left(s.units)
+    {
+        tiles = left > 0 ? tiles_of(p, b, T, n) : 0;
+    }
+    __device__ bool next(const TreeParams &p)
+    {
+        if (left <= 0)
+            return false;
+        if (tile >= tiles) {
+            tile = 0;
+            if (++h == p.Hkv) {
+                h = 0;
+                do {
+                    if (++b >= p.B)
+                        return false;
+                    tiles = tiles_of(p, b, T, n);
+                } while (tiles == 0);
+            }
+        }
+        seg_tile0 = tile;
+        seg_tile1 = min(tiles, tile + left);
+        left -= seg_tile1 - tile;
+        tile = seg_tile1;
+        return true;
+    }
+};
+
+// The same, tile by tile.
+struct Units {
+    Segments seg;
+    int t, index; // current tile, segments begun before this one
+    __device__ Units(const TreeParams &p, const TreeSmem &s) : seg(p, s), t(-1), index(-1) { advance(p); }
+    __device__ void advance(const TreeParams &p)
+    {
+        if (index >= 0 && ++t < seg.seg_tile1)
+            return;
+        if (seg.next(p)) {
+            ++index;
+            t = seg.seg_tile0;
+        }
+    }
+    __device__ bool first() const { return t == seg.seg_tile0; }
+    __device__ bool last() const { return t == seg.seg_tile1 - 1; }
+};
+
+// Position in the ring of unit u's K and V tile, of N units. Two row tiles
+// (pair): K0 V0 K1 V1 ...; one row tile, whose scores run two tiles ahead of
+// its products with V: K0 K1 V0 K2 V1 K3 ...
+__device__ __forceinline__ int ring_k(bool pair, int u) { return pair ? 2 * u : (u < 2 ? u : 2 * u - 1); }
+__device__ __forceinline__ int ring_v(bool pair, int u, int N)
+{
+    return pair ? 2 * u + 1 : (u == N - 1 ? 2 * N - 1 : 2 * u + 2);
+}
+
+// ---------------------------------------------------------------- producer
+__device__ bool produce(const TreeParams &p, TreeSmem &s, const CUtensorMap *mq, const CUtensorMap *mk,
+                        const CUtensorMap *mv, int rg, bool pair)
+{
+    const int lane = threadIdx.x & 31;
+    const int P = 1 << p.log2_page;
+    const int box_keys = min(P, kTileKeys);
+    const int boxes = kTileKeys / box_keys; // pages of a tile
+    const int outside = static_cast<int>((static_cast<long long>(p.num_pages) * p.Hkv << p.log2_page) >> 3);
+    // K and V are read once per row group: with one group nothing reads them again
+    const uint64_t policy = l2_evict_first_policy();
+    int put = 0;
+    bool ok = true;
+    const auto load_tile = [&](const CUtensorMap *map, int group) {
+        const int slot = put % kSlots;
+        ok = ok && warp_wait(&s.empty[slot], ((put / kSlots) & 1) ^ 1);
+        if (!ok)
+            return;
+        if (lane == 0)
+            mbar_arrive_expect_tx(&s.full[slot], kTileBytes);
+        __syncwarp();
+        if (lane < boxes)
+            tma_load_4d(s.slots[slot] + lane * box_keys * kRowBytes, map, 0, 0, 0, group, &s.full[slot], policy);
+        ++put;
+    };
+    const int ahead = pair ? 1 : 2; // tiles of K requested before the V of the first of them
+    int group1 = 0, group2 = 0;     // this lane's page of the last tile and of the one before
+    Segments seg(p, s);
+    int unit = 0;
+    for (int index = 0; ok && seg.next(p); ++index) {
+        const int32_t *table = p.block_table + static_cast<size_t>(seg.b) * p.max_pages;
+        const auto entry = [&](int tile) {
+            const int key = tile * kTileKeys + lane * box_keys;
+            return lane < boxes && key < seg.T ? table[key >> p.log2_page] : 0;
+        };
+        int phys_next = entry(seg.seg_tile0);
+        for (int tile = seg.seg_tile0; ok && tile < seg.seg_tile1; ++tile, ++unit) {
+            const int phys = phys_next;
+            if (tile + 1 < seg.seg_tile1)
+                phys_next = entry(tile + 1);
+            const int key = tile * kTileKeys + lane * box_keys;
+            const bool needed = lane < boxes && key < seg.T;
+            const bool in_pool = phys >= 0 && phys < p.num_pages;
+            const int group = needed && in_pool
+                                  ? static_cast<int>((((static_cast<long long>(phys) * p.Hkv + seg.h) << p.log2_page) +
+                                                      (key & (P - 1))) >>
+                                                     3)
+                                  : outside; // a box outside the tensor arrives as zeros
+            if (needed && !in_pool)
+                atomicOr(&g_flags_tree, PGQA_DEVERR_BAD_PAGE);
+            uint32_t valid = __ballot_sync(0xFFFFFFFFu, !needed || in_pool);
+            if (unit >= ahead)
+                load_tile(mv, ahead == 1 ? group1 : group2);
+            if (tile == seg.seg_tile0 && ok) {
+                // Q: one buffer per segment in turn, or both for two row tiles
+                const int buf = pair ? 0 : index & 1;
+                ok = warp_wait(&s.q_empty[buf], ((pair ? index : index >> 1) & 1) ^ 1);
+                if (ok && lane == 0) {
+                    const int bytes = p.tile_tokens * p.g * 128; // one 64-column half of a row tile
+                    mbar_arrive_expect_tx(&s.q_full[buf], (pair ? 4 : 2) * bytes);
+                    for (int i = 0; i < (pair ? 2 : 1); ++i)
+                        for (int half = 0; half < 2; ++half)
+                            tma_load_3d_default(s.q[buf + i] + half * (kTileRows * 128), mq, 64 * half, seg.h * p.g,
+                                                seg.b * p.M + (2 * rg + i) * p.tile_tokens, &s.q_full[buf]);
+                }
+            }
+            if (lane == 0) {
+                uint32_t by16 = 0; // a bit per 16 keys
+                for (int i = 0; i < 8; ++i)
+                    by16 |= ((valid >> (i * 16 / box_keys)) & 1u) << i;
+                s.valid[unit % kValidRing] = by16;
+            }
+            load_tile(mk, group);
+            group2 = group1;
+            group1 = group;
+        }
+    }
+    if (ok && !pair && unit > 1)
+        load_tile(mv, group2);
+    if (ok && unit > 0)
+        load_tile(mv, group1);
+    if (!ok) // wait, with a limit, for what is still on its way into shared memory
+        for (int i = max(0, put - kSlots); i < put; ++i)
+            (void)warp_wait(&s.full[i % kSlots], (i / kSlots) & 1);
+    return ok;
+}
+
+// ---------------------------------------------------------------- matrix products
+// Before a V tile that holds the end of the sequence or drafted tokens enters
+// a product: rows past T become zeros (their weights are zeros, and 0 * NaN is
+// not), and elements of drafted tokens that are not finite become zeros and are
+// noted, so that they reach only the rows that see them (at the end).
+__device__ uint64_t settle_v_tile(unsigned char *v, int key0, int T, int n, int box_keys)
+{
+    const int lane = threadIdx.x & 31;
+    const int sub = lane >> 4, part = lane & 15; // two rows at a time, 16 bytes per lane
+    const auto at = [&](int row) { // the row's eighth-of-a-half `part` (order within the row does not matter)
+        return v + (row >> 3) * 2048 + (part >> 3) * 1024 + (row & 7) * 128 + (part & 7) * 16;
+    };
+    uint64_t bad = 0;
+    const int end = T - key0;                                     // rows that exist
+    const int loaded = min(kTileKeys, (end + box_keys - 1) / box_keys * box_keys);
+    const int first = max(0, end - n);
+    for (int row = first + sub; row < min(end, kTileKeys); row += 2) {
+        uint4 *x = reinterpret_cast<uint4 *>(at(row));
+        uint32_t w[4] = {x->x, x->y, x->z, x->w};
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if ((w[i] & 0x7F80u) == 0x7F80u)
+                w[i] &= 0xFFFF0000u, any = true;
+            if ((w[i] & 0x7F800000u) == 0x7F800000u)
+                w[i] &= 0x0000FFFFu, any = true;
+        }
+        if (any) {
+            *x = make_uint4(w[0], w[1], w[2], w[3]);
+            bad |= 1ull << (row - (end - n));
+        }
+    }
+    for (int row = end + sub; row < loaded; row += 2)
+        *reinterpret_cast<uint4 *>(at(row)) = make_uint4(0, 0, 0, 0);
+    const uint32_t lo = __reduce_or_sync(0xFFFFFFFFu, static_cast<uint32_t>(bad));
+    const uint32_t hi = __reduce_or_sync(0xFFFFFFFFu, static_cast<uint32_t>(bad >> 32));
+    fence_proxy_async_smem();
+    __syncwarp();
+    return static_cast<uint64_t>(hi) << 32 | lo;
+}
+
+__device__ bool multiply(const TreeParams &p, TreeSmem &s, bool pair)
+{
+    const int lane = threadIdx.x & 31;
+    const int N = s.units;                  // tiles
+    const int steps = pair ? 2 * N : N;     // (tile, stream)
+    const uint32_t tmem = s.tmem_base;
+    const uint32_t idesc_s = tc_idesc_bf16(kTileKeys, p.negate_q != 0, false);
+    const uint32_t idesc_o = tc_idesc_bf16(kHeadDim, false, true);
+    const int box_keys = min(1 << p.log2_page, kTileKeys);
+    Units su(p, s), pu(p, s); // of the next score product and of the next product with V
+    uint64_t bad = 0;
+    bool ok = true;
+
+    // S of step n: Q rows 128 x 128, K tile rows are the N dimension
+    const auto scores = [&](int n) {
+        const int stream = n & 1, unit = pair ? n >> 1 : n;
+        const bool new_tile = !pair || stream == 0;
+        const int buf = pair ? 0 : su.index & 1;
+        const int k_at = ring_k(pair, unit);
+        if (su.first() && new_tile)
+            ok = ok && warp_wait(&s.q_full[buf], (pair ? su.index : su.index >> 1) & 1);
+        if (new_tile)
+            ok = ok && warp_wait(&s.full[k_at % kSlots], (k_at / kSlots) & 1);
+        if (!ok)
+            return;
+        tc_fence_after();
+        if (lane == 0) {
+            const uint32_t qa = smem_addr(s.q[pair ? stream : buf]);
+            const uint32_t ka = smem_addr(s.slots[k_at % kSlots]);
+#pragma unroll
+            for (int k = 0; k < kHeadDim / 16; ++k) {
+                const int half = k >> 2, off = (k & 3) * 32;
+                tc_mma_ss(tmem + kColS + stream * 128, tc_smem_desc(qa + half * (kTileRows * 128) + off, 16, 1024),
+                          tc_smem_desc(ka + half * 1024 + off, 16, 2048), idesc_s, k > 0);
+            }
+            if (!pair || stream == 1) {
+                tc_commit(&s.empty[k_at % kSlots]);
+                if (su.last())
+                    tc_commit(&s.q_empty[buf]);
+            }
+            tc_commit(&s.s_full[stream]);
+            mbar_arrive(&s.s_full[stream]); // orders the page mask's write before its readers
+        }
+        __syncwarp();
+        if (!pair || stream == 1)
+            su.advance(p);
+    };
+    // O += P V of step n; P hi in the first 64 columns of S's place, P lo in the others
+    const auto values = [&](int n) {
+        const int stream = n & 1, unit = pair ? n >> 1 : n;
+        const bool new_tile = !pair || stream == 0;
+        const int v_at = ring_v(pair, unit, N);
+        unsigned char *v = s.slots[v_at % kSlots];
+        if (new_tile) {
+            ok = ok && warp_wait(&s.full[v_at % kSlots], (v_at / kSlots) & 1);
+            if (!ok)
+                return;
+            if (pu.first())
+                bad = 0;
+            const int key0 = pu.t * kTileKeys;
+            if (key0 + kTileKeys > pu.seg.T - pu.seg.n)
+                bad |= settle_v_tile(v, key0, pu.seg.T, pu.seg.n, box_keys);
+        }
+        ok = ok && warp_wait(&s.p_ready[stream], (n >> 1) & 1);
+        if (!ok)
+            return;
+        tc_fence_after();
+        if (lane == 0) {
+            const uint32_t va = smem_addr(v);
+            const uint32_t o = tmem + kColO + stream * 128;
+            // the first product of a stream in a segment overwrites O
+            const uint32_t keep = pair ? !pu.first() : pu.t - pu.seg.seg_tile0 >= 2;
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+                for (int k = 0; k < kTileKeys / 16; ++k)
+                    tc_mma_ts(o, tmem + kColS + stream * 128 + part * 64 + k * 8,
+                              tc_smem_desc(va + k * 4096, 1024, 2048), idesc_o, keep || part > 0 || k > 0);
+            if (!pair || stream == 1) {
+                tc_commit(&s.empty[v_at % kSlots]);
+                if (pu.last()) {
+                    s.bad_rows = bad;
+                    tc_commit(&s.seg_done);
+                    mbar_arrive(&s.seg_done); // orders bad_rows before its readers
+                }
+            }
+        }
+        __syncwarp();
+        if (!pair || stream == 1)
+            pu.advance(p);
+    };
+    for (int n = 0; n < min(2, steps) && ok; ++n)
+        scores(n);
+    for (int n = 0; n < steps && ok; ++n) {
+        values(n);
+        if (n + 2 < steps && ok)
+            scores(n + 2);
+    }
+    if (!ok) { // wait, with a limit, for the products in flight
+        if (lane == 0)
+            tc_commit(&s.drain);
+        (void)warp_wait(&s.drain, 0);
+    }
+    return ok;
+}
+
+// ---------------------------------------------------------------- softmax
+// Bits of the keys key0 + 32 w .. + 31 that a row sees, w = 0 .. 3: the prefix,
+// then the drafted tokens of its mask, without pages outside the pool.
+__device__ __forceinline__ uint32_t visible_word(int w, int prefix_keys, uint64_t mask, uint32_t valid)
+{
+    const int below = prefix_keys - 32 * w; // prefix keys from this word's first on
+    uint32_t bits = below >= 32 ? 0xFFFFFFFFu : (below > 0 ? (1u << below) - 1u : 0u);
+    if (below < 32) {
+        // drafted token j sits at bit below + j of the word
+        const uint64_t drafted = below >= 0 ? mask << below : (below > -64 ? mask >> -below : 0ull);
+        bits |= static_cast<uint32_t>(drafted);
+    }
+    const uint32_t v = valid >> (2 * w);
+    return bits & (((v & 1u) ? 0xFFFFu : 0u) | ((v & 2u) ? 0xFFFF0000u : 0u));
+}
+
+template <int kScore> // bit 0: tanh cap, bit 1: distance bias
+__device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int cta)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int stream = warp >> 2;
+    const int row = (warp & 3) * 32 + lane; // of the row tile
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tmem_s = s.tmem_base + lanes + kColS + stream * 128;
+    const int row_tile = 2 * rg + (pair ? stream : 0);
+    const int token = row_tile * p.tile_tokens + row / p.g;
+    const bool real = row < p.tile_tokens * p.g && token < p.M;
+    const bool warp_works = __any_sync(0xFFFFFFFFu, real);
+    const float c = kScore ? 1.f : p.c;
+
+    Segments seg(p, s);
+    int step = 0; // the run's next step, of either stream
+    bool ok = true;
+    for (int index = 0; ok && seg.next(p); ++index) {
+        const int prefix = seg.T - seg.n;
+        const int head = seg.h * p.g + row % p.g;
+        uint64_t mask = 0;
+        float slope = 0.f;
+        int pos = 0;
+        const bool live = real && token < seg.n;
+        if (live) {
+            mask = p.tree_mask[static_cast<size_t>(seg.b) * p.M + token];
+            if (seg.n < 64)
+                mask &= (1ull << seg.n) - 1ull;
+            if constexpr ((kScore & 2) != 0) {
+                slope = p.slopes[head] * kLog2e;
+                pos = p.positions[static_cast<size_t>(seg.b) * p.M + token];
+            }
+        }
+        const int seg_steps = (seg.seg_tile1 - seg.seg_tile0) * (pair ? 2 : 1);
+        float m = -INFINITY; // the reference, in units of 1 / c
+        float l = 0.f;
+        bool fresh = true; // O holds nothing of this segment yet
+        for (int n = step + ((step ^ stream) & 1); ok && n < step + seg_steps; n += 2) {
+            const int tile = seg.seg_tile0 + ((n - step) >> (pair ? 1 : 0));
+            const int unit = pair ? n >> 1 : n;
+            ok = warp_wait(&s.s_full[stream], (n >> 1) & 1);
+            if (!ok)
+                break;
+            tc_fence_after();
+            if (warp_works) {
+                float x[kTileKeys];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    tmem_ld32(x + 32 * i, tmem_s + 32 * i);
+                const int key0 = tile * kTileKeys;
+                const uint32_t valid = s.valid[unit % kValidRing];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    tmem_wait_ld32(x + 32 * i);
+                const bool tail = key0 + kTileKeys > prefix;
+                if constexpr (kScore != 0) {
+                    const float far0 = static_cast<float>(static_cast<long long>(key0) - pos);
+#pragma unroll
+                    for (int j = 0; j < kTileKeys; ++j) {
+                        float y;
+                        if constexpr ((kScore & 1) != 0) // cap tanh(u) = cap - 2 cap / (1 + e^2u)
+                            y = fmaf(-2.f * p.cap_out, rcp(1.f + ex2(x[j] * p.cap_in)), p.cap_out);
+                        else
+                            y = x[j] * p.c;
+                        if constexpr ((kScore & 2) != 0) {
+                            float far = far0 + static_cast<float>(j);
+                            if (tail && key0 + j >= prefix) // a drafted token's own position
+                                far = static_cast<float>(
+                                    static_cast<long long>(
+                                        p.positions[static_cast<size_t>(seg.b) * p.M + min(key0 + j - prefix, p.M - 1)]) -
+                                    pos);
+                            y = fmaf(slope, far, y);
+                        }
+                        x[j] = y;
+                    }
+                }
+                if (tail || valid != 0xFFu) {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t bits = visible_word(w, prefix - key0, mask, valid);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            x[32 * w + j] = (bits >> j) & 1u ? x[32 * w + j] : -INFINITY;
+                    }
+                }
+                float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                for (int j = 4; j < kTileKeys; ++j)
+                    top[j & 3] = fmaxf(top[j & 3], x[j]);
+                const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                // move the reference where the row has none yet, or its scores left its range
+                const bool move = fresh ? true : (m == -INFINITY ? high > -INFINITY : (high - m) * c > kRescaleLog2);
+                if (__any_sync(0xFFFFFFFFu, move)) {
+                    const float before = m;
+                    if (move)
+                        m = high;
+                    if (!fresh) {
+                        const float f = !move ? 1.f : (before == -INFINITY ? 0.f : ex2((before - m) * c));
+                        l *= f;
+                        const uint32_t o = s.tmem_base + lanes + kColO + stream * 128;
+#pragma unroll 1
+                        for (int i = 0; i < 4; ++i) {
+                            float acc[32];
+                            tmem_ld32(acc, o + 32 * i);
+                            tmem_wait_ld32(acc);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                acc[j] *= f;
+                            tmem_st32(o + 32 * i, acc);
+                        }
+                    }
+                }
+                float ref = m == -INFINITY ? 0.f : m * c;
+                if constexpr (kScore == 0) {
+                    // x c - m c loses |m c| 2^-24 of the exponent: where that
+                    // matters, subtract before the product
+                    const bool large = fabsf(ref) > 65536.f;
+                    if (__any_sync(0xFFFFFFFFu, large)) {
+                        const float shift = large ? m : 0.f;
+#pragma unroll
+                        for (int j = 0; j < kTileKeys; ++j)
+                            x[j] -= shift;
+                        ref = large ? 0.f : ref;
+                    }
+                }
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float a = ex2(fmaf(x[32 * i + 2 * j], c, -ref));
+                        const float b = ex2(fmaf(x[32 * i + 2 * j + 1], c, -ref));
+                        sum[j & 3] += a + b;
+                        hi[j] = pack_bf16x2(a, b);
+                        lo[j] = pack_bf16x2(a - bf16_lo(hi[j]), b - bf16_hi(hi[j]));
+                    }
+                    tmem_st16(tmem_s + 16 * i, hi);
+                    tmem_st16(tmem_s + 64 + 16 * i, lo);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_wait_st();
+            }
+            fresh = false;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&s.p_ready[stream]);
+        }
+        step += seg_steps;
+        if (!ok)
+            break;
+
+        // ---- the end of the segment: O of the last product, joined and written
+        float w_own = 1.f, w_other = 0.f, top = m == -INFINITY ? -INFINITY : m * c;
+        if (!pair) {
+            // both streams hold part of every row: exchange (m, l)
+            s.ml[stream][row] = make_float2(top, l);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&s.ml_ready);
+            ok = warp_wait(&s.ml_ready, index & 1);
+            if (!ok)
+                break;
+            const float2 other = s.ml[stream ^ 1][row];
+            const float own_top = top;
+            top = fmaxf(own_top, other.x);
+            w_own = l == 0.f ? 0.f : ex2(own_top - top);
+            w_other = other.y == 0.f ? 0.f : ex2(other.x - top);
+            l = (l == 0.f ? 0.f : l * w_own) + (other.y == 0.f ? 0.f : other.y * w_other);
+        } else if (l == 0.f) {
+            w_own = 0.f;
+        }
+        ok = warp_wait(&s.seg_done, index & 1);
+        if (!ok)
+            break;
+        tc_fence_after();
+        const uint64_t bad = s.bad_rows & mask;
+        const bool whole = seg.seg_tile0 == 0 && seg.seg_tile1 == seg.tiles;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const size_t out_row = (static_cast<size_t>(seg.b) * p.M + token) * p.Hq + head;
+        const size_t rec = static_cast<size_t>(2 * cta + (seg.seg_tile0 > 0 ? 0 : 1)) * p.rec_rows +
+                           (pair ? stream * kTileRows : 0) + row;
+        const int halves = pair ? 2 : 1;
+        for (int i = 0; i < halves; ++i) {
+            const int col = pair ? 64 * i : 64 * stream;
+            float o[64];
+            if (warp_works) {
+                const uint32_t base = s.tmem_base + lanes + kColO + col;
+                tmem_ld32(o, base + stream * 128);
+                tmem_ld32(o + 32, base + stream * 128 + 32);
+                if (!pair) {
+                    float o2[64];
+                    tmem_ld32(o2, base + (stream ^ 1) * 128);
+                    tmem_ld32(o2 + 32, base + (stream ^ 1) * 128 + 32);
+                    tmem_wait_ld32(o), tmem_wait_ld32(o + 32), tmem_wait_ld32(o2), tmem_wait_ld32(o2 + 32);
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) { // a stream without a visible key may hold anything
+                        const float a = w_own == 0.f ? 0.f : o[j] * w_own;
+                        o[j] = w_other == 0.f ? a : fmaf(o2[j], w_other, a);
+                    }
+                } else {
+                    tmem_wait_ld32(o), tmem_wait_ld32(o + 32);
+                    if (w_own == 0.f) {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j)
+                            o[j] = 0.f;
+                    }
+                }
+            }
+            if (i == halves - 1) {
+                tc_fence_before();
+                if (!pair) {
+                    // neither stream's O may be overwritten before both warpgroups have it
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&s.epi_done);
+                    ok = warp_wait(&s.epi_done, index & 1);
+                }
+            }
+            if (live && ok) {
+                if (bad) {
+                    // V elements left out of the products because they are not finite
+                    for (uint64_t rest = bad; rest; rest &= rest - 1) {
+                        const int slot = prefix + __ffsll(static_cast<long long>(rest)) - 1;
+                        const int tile = slot / kTileKeys;
+                        if (tile < seg.seg_tile0 || tile >= seg.seg_tile1)
+                            continue;
+                        const int phys = p.block_table[static_cast<size_t>(seg.b) * p.max_pages + (slot >> p.log2_page)];
+                        if (phys < 0 || phys >= p.num_pages)
+                            continue;
+                        const uint16_t *v =
+                            p.v + ((((static_cast<size_t>(phys) * p.Hkv + seg.h) << p.log2_page) +
+                                    (slot & ((1 << p.log2_page) - 1))) *
+                                       kHeadDim +
+                                   col);
+#pragma unroll
+                        for (int j = 0; j < 64; ++j)
+                            if ((v[j] & 0x7F80u) == 0x7F80u)
+                                o[j] += __uint_as_float(static_cast<uint32_t>(v[j]) << 16);
+                    }
+                }
+                if (whole) {
+#pragma unroll
+                    for (int j = 0; j < 64; ++j)
+                        o[j] *= inv;
+                    if (p.out_f32) {
+                        float4 *dst = reinterpret_cast<float4 *>(p.out_f32 + out_row * kHeadDim + col);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    }
+                    if (p.out_bf16) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(p.out_bf16 + out_row * kHeadDim + col);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            dst[j] = make_uint4(pack_bf16x2(o[8 * j], o[8 * j + 1]), pack_bf16x2(o[8 * j + 2], o[8 * j + 3]),
+                                                pack_bf16x2(o[8 * j + 4], o[8 * j + 5]),
+                                                pack_bf16x2(o[8 * j + 6], o[8 * j + 7]));
+                    }
+                } else {
+                    float4 *dst = reinterpret_cast<float4 *>(p.rec_acc + rec * kHeadDim + col);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    if (col == 0) {
+                        p.rec_m[rec] = top;
+                        p.rec_l[rec] = l;
+                    }
+                }
+            }
+        }
+    }
+    return ok;
+}
+
+template <int kScore>
+__global__ void __launch_bounds__(kTreeThreads, 1)
+    tree_attn_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ TreeParams p)
+{
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    TreeSmem &s = *reinterpret_cast<TreeSmem *>(smem_raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rg = blockIdx.x % p.row_groups, cta = blockIdx.x / p.row_groups;
+    const bool pair = 2 * rg + 1 < p.row_tiles;
+    allow_dependent_launch();
+    if (tid == 0) {
+        prefetch_tensormap(&mq), prefetch_tensormap(&mk), prefetch_tensormap(&mv);
+        for (int i = 0; i < kSlots; ++i)
+            mbar_init(&s.full[i], 1), mbar_init(&s.empty[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.q_full[i], 1), mbar_init(&s.q_empty[i], 1);
+            mbar_init(&s.s_full[i], 2);  // the products' completion, and the issuing thread
+            mbar_init(&s.p_ready[i], 4); // one arrival per warp of the stream
+        }
+        mbar_init(&s.seg_done, 2);
+        mbar_init(&s.ml_ready, kSoftmaxThreads / 32);
+        mbar_init(&s.epi_done, kSoftmaxThreads / 32);
+        mbar_init(&s.drain, 1);
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp)
+        tmem_alloc_all(&s.tmem_base);
+
+    // Everything read from here on may come from the kernel before this one.
+    grid_dependency_wait();
+    // This CTA's run of tiles: thread t sums the tiles of sequences [t per, (t + 1) per).
+    const int per = (p.B + kTreeThreads - 1) / kTreeThreads;
+    const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+    int mine = 0, T, n;
+    for (int b = b0; b < b1; ++b)
+        mine += tiles_of(p, b, T, n) * p.Hkv;
+    int before = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, before, off);
+        if (lane >= off)
+            before += v;
+    }
+    if (lane == 31)
+        s.scan[warp] = before;
+    before -= mine;
+    __syncthreads();
+    int total = 0;
+    for (int w = 0; w < kTreeThreads / 32; ++w) {
+        if (w < warp)
+            before += s.scan[w];
+        total += s.scan[w];
+    }
+    // with fewer tiles than CTAs the first `total` take one each: every CTA
+    // between a (sequence, head)'s first and last then holds a piece of it
+    const int ctas = min(p.ctas, max(total, 1));
+    const int u0 = static_cast<int>(static_cast<long long>(total) * min(cta, ctas) / ctas);
+    const int u1 = static_cast<int>(static_cast<long long>(total) * min(cta + 1, ctas) / ctas);
+    if (tid == 0)
+        s.units = u1 - u0;
+    if (mine > 0 && u0 >= before && u0 < before + mine) {
+        int b = b0, at = before;
+        for (int t; at + (t = tiles_of(p, b, T, n) * p.Hkv) <= u0; ++b)
+            at += t;
+        const int tiles = tiles_of(p, b, T, n);
+        s.start_b = b;
+        s.start_h = (u0 - at) / tiles;
+        s.start_tile = (u0 - at) % tiles;
+    }
+    if (blockIdx.x == 0) { // for the merge
+        int at = before;
+        for (int b = b0; b < b1; ++b) {
+            p.unit_base[b] = at;
+            at += tiles_of(p, b, T, n) * p.Hkv;
+        }
+        if (tid == 0)
+            p.unit_base[p.B] = total;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+
+    // Registers move from the third warpgroup to the softmax, whose threads
+    // hold 128 scores: 256 * 208 + 128 * 72 <= 384 * 168 as launched.
+    bool ok = true;
+    if (warp >= kProducerWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == kProducerWarp && s.units > 0)
+            ok = produce(p, s, &mq, &mk, &mv, rg, pair);
+        else if (warp == kMmaWarp && s.units > 0)
+            ok = multiply(p, s, pair);
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        if (s.units > 0)
+            ok = soften<kScore>(p, s, rg, pair, blockIdx.x);
+    }
+    if (!ok && lane == 0)
+        atomicOr(&g_flags_tree, PGQA_DEVERR_WAIT_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp)
+        tmem_free_all(s.tmem_base);
+}
+
+// Joins the pieces of every (sequence, KV head) that several CTAs worked on,
+// one warp per query row, pieces in the order of their keys:
+//   top = max m_k, out = sum acc_k 2^(m_k - top) / sum l_k 2^(m_k - top).
+// Rows of sequences whose lengths make no sense become zeros here.
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeParams p)
 {
     allow_dependent_launch();
     grid_dependency_wait();
-    const int lane = threadIdx.x;
-    const int h = blockIdx.x % p.Hq, i = blockIdx.x / p.Hq, b = blockIdx.y;
-    const int T = p.context_lens[b], n = p.draft_lens ? p.draft_lens[b] : p.M;
-    const bool valid = n >= 0 && n <= p.M && T >= n && T <= (p.max_pages << p.log2_page);
-    if (valid && i >= n)
+    const int lane = threadIdx.x & 31;
+    const int r = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
+    const int h = blockIdx.y, b = blockIdx.z;
+    if (r >= p.M * p.g)
         return;
-    const size_t row = (static_cast<size_t>(b) * p.M + i) * p.Hq + h;
+    const int token = r / p.g;
+    const size_t out_row = (static_cast<size_t>(b) * p.M + token) * p.Hq + h * p.g + r % p.g;
+    int T, n;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float m = -INFINITY, l = 0.f;
-    if (valid) {
-        const float4 q = load4(p.q + row * kHeadDim);
-        const int prefix = T - n;
-        const uint64_t mask = p.tree_mask[static_cast<size_t>(b) * p.M + i];
-        const int kvh = h / (p.Hq / p.Hkv);
-        const int pos_i = p.positions ? p.positions[static_cast<size_t>(b) * p.M + i] : 0;
-        for (int j = 0; j < T; ++j) {
-            if (j >= prefix && !(mask >> (j - prefix) & 1))
-                continue;
-            const int phys = p.block_table[static_cast<size_t>(b) * p.max_pages + (j >> p.log2_page)];
-            if (phys < 0 || phys >= p.num_pages) {
-                if (lane == 0)
-                    atomicOr(&g_flags_tree, PGQA_DEVERR_BAD_PAGE);
-                continue;
-            }
-            const size_t cell =
-                (((static_cast<size_t>(phys) * p.Hkv + kvh) << p.log2_page) + (j & ((1 << p.log2_page) - 1))) * kHeadDim;
-            const float4 k = load4(p.k + cell);
-            float x = q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
+    if (sequence(p, b, T, n)) {
+        if (token >= n)
+            return;
+        const int tiles = (T - 1) / kTileKeys + 1;
+        const long long u0 = p.unit_base[b] + h * tiles, u1 = u0 + tiles - 1, total = p.unit_base[p.B];
+        // the CTA of tile u: the c with floor(total c / ctas) <= u < floor(total (c + 1) / ctas)
+        const long long ctas = total < p.ctas ? total : p.ctas;
+        const int c0 = static_cast<int>(((u0 + 1) * ctas - 1) / total);
+        const int c1 = static_cast<int>(((u1 + 1) * ctas - 1) / total);
+        if (c0 == c1)
+            return;
+        const int row_tile = token / p.tile_tokens, rg = row_tile >> 1;
+        const int rec_row = (row_tile & 1) * kTileRows + r - row_tile * p.tile_tokens * p.g;
+        // piece k is CTA c0 + k's: its last segment for the first piece, its first for the others
+        const auto record = [&](int k) {
+            return (static_cast<size_t>(c0 + k) * p.row_groups + rg) * 2 * p.rec_rows + (k == 0 ? p.rec_rows : 0) + rec_row;
+        };
+        const int pieces = c1 - c0 + 1;
+        float top = -INFINITY;
+        for (int k = lane; k < pieces; k += 32)
+            if (p.rec_l[record(k)] != 0.f)
+                top = fmaxf(top, p.rec_m[record(k)]);
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1)
-                x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
-            x *= p.scale;
-            if (p.softcap > 0.f)
-                x = p.softcap * tanhf(x / p.softcap);
-            if (p.slopes) {
-                const int pos_j = j < prefix ? j : p.positions[static_cast<size_t>(b) * p.M + j - prefix];
-                x = fmaf(p.slopes[h], static_cast<float>(pos_j - pos_i), x);
+        for (int off = 16; off > 0; off >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+        float l = 0.f;
+        for (int first = 0; first < pieces; first += 32) {
+            float w = 0.f, piece_l = 0.f;
+            if (first + lane < pieces) {
+                piece_l = p.rec_l[record(first + lane)];
+                w = piece_l == 0.f ? 0.f : ex2(p.rec_m[record(first + lane)] - top);
             }
-            const float m_new = fmaxf(m, x);
-            const float ref = m_new == -INFINITY ? 0.f : m_new;
-            const float keep = exp2f((m - ref) * kLog2e), w = exp2f((x - ref) * kLog2e);
-            const float4 v = load4(p.v + cell);
-            acc.x = fmaf(w, v.x, acc.x * keep);
-            acc.y = fmaf(w, v.y, acc.y * keep);
-            acc.z = fmaf(w, v.z, acc.z * keep);
-            acc.w = fmaf(w, v.w, acc.w * keep);
-            l = fmaf(l, keep, w);
-            m = m_new;
+            const int count = min(32, pieces - first);
+#pragma unroll 4
+            for (int k = 0; k < count; ++k) {
+                const float wk = __shfl_sync(0xFFFFFFFFu, w, k), lk = __shfl_sync(0xFFFFFFFFu, piece_l, k);
+                const float4 v = reinterpret_cast<const float4 *>(p.rec_acc + record(first + k) * kHeadDim)[lane];
+                if (lk != 0.f) {
+                    l = fmaf(lk, wk, l);
+                    acc.x = fmaf(v.x, wk, acc.x);
+                    acc.y = fmaf(v.y, wk, acc.y);
+                    acc.z = fmaf(v.z, wk, acc.z);
+                    acc.w = fmaf(v.w, wk, acc.w);
+                }
+            }
         }
-    } else if (i == 0 && h == 0 && lane == 0) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    } else if (r == 0 && h == 0 && lane == 0) {
         atomicOr(&g_flags_tree, PGQA_DEVERR_BAD_CONTEXT);
     }
-    const float inv = l != 0.f ? 1.f / l : 0.f;
-    const float4 r = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     if (p.out_f32)
-        reinterpret_cast<float4 *>(p.out_f32 + row * kHeadDim)[lane] = r;
+        reinterpret_cast<float4 *>(p.out_f32 + out_row * kHeadDim)[lane] = acc;
     if (p.out_bf16)
-        reinterpret_cast<uint2 *>(p.out_bf16 + row * kHeadDim)[lane] =
-            make_uint2(pack_bf16x2(r.x, r.y), pack_bf16x2(r.z, r.w));
+        reinterpret_cast<uint2 *>(p.out_bf16 + out_row * kHeadDim)[lane] =
+            make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+}
+
+// How a call's rows and CTAs are laid out; from sizes alone, so that the
+// workspace query and the launch agree.
+struct Layout {
+    int tile_tokens, row_tiles, row_groups, rec_rows, ctas;
+    size_t base_bytes, stat_bytes, acc_bytes;
+};
+
+size_t align256(size_t x) { return (x + 255) & ~size_t{255}; }
+
+Layout layout(int B, int M, int Hq, int Hkv, int page_size, int max_pages, int sm_count)
+{
+    Layout y{};
+    const int g = Hq / Hkv;
+    y.tile_tokens = M < kTileRows / g ? M : kTileRows / g;
+    y.row_tiles = (M + y.tile_tokens - 1) / y.tile_tokens;
+    y.row_groups = (y.row_tiles + 1) / 2;
+    y.rec_rows = y.row_tiles > 1 ? 2 * kTileRows : y.tile_tokens * g;
+    const long long tiles = (static_cast<long long>(max_pages) * page_size + kTileKeys - 1) / kTileKeys;
+    const long long units = tiles * B * Hkv;
+    const int ctas = sm_count / y.row_groups;
+    y.ctas = static_cast<int>(units < ctas ? units : ctas);
+    if (y.ctas < 1)
+        y.ctas = 1;
+    const size_t records = static_cast<size_t>(2) * y.ctas * y.row_groups;
+    y.base_bytes = align256((static_cast<size_t>(B) + 1) * sizeof(int32_t));
+    y.stat_bytes = align256(records * y.rec_rows * sizeof(float));
+    y.acc_bytes = records * y.rec_rows * kHeadDim * sizeof(float);
+    return y;
+}
+
+CUresult encode_cache(EncodeTiledFn fn, CUtensorMap *map, const void *base, long long rows, int page_size)
+{
+    // [row group of 8][half][row][64 columns]: a box is a page's (or half a
+    // page's) rows as 1 KB swizzle atoms, two per 8 rows
+    const int box_groups = (page_size < kTileKeys ? page_size : kTileKeys) / 8;
+    const cuuint64_t dims[4] = {64u, 8u, 2u, static_cast<cuuint64_t>(rows / 8)};
+    const cuuint64_t strides[3] = {kRowBytes, 128u, 8u * kRowBytes};
+    const cuuint32_t box[4] = {64u, 8u, 2u, static_cast<cuuint32_t>(box_groups)};
+    const cuuint32_t elem[4] = {1u, 1u, 1u, 1u};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, elem,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+CUresult encode_query(EncodeTiledFn fn, CUtensorMap *map, const void *base, int tokens, int Hq, int g, int tile_tokens)
+{
+    const cuuint64_t dims[3] = {kHeadDim, static_cast<cuuint64_t>(Hq), static_cast<cuuint64_t>(tokens)};
+    const cuuint64_t strides[2] = {kRowBytes, static_cast<cuuint64_t>(Hq) * kRowBytes};
+    const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(g), static_cast<cuuint32_t>(tile_tokens)};
+    const cuuint32_t elem[3] = {1u, 1u, 1u};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, elem,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+constexpr int kMaxDevices = 64;
+
+template <int kScore>
+cudaError_t launch_score(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const TreeParams &p,
+                         cudaStream_t stream)
+{
+    static std::atomic<bool> configured[kMaxDevices];
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess)
+        return err;
+    if (dev >= kMaxDevices || !configured[dev].load(std::memory_order_acquire)) {
+        err = cudaFuncSetAttribute(tree_attn_kernel<kScore>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTreeSmem);
+        if (err != cudaSuccess)
+            return err;
+        if (dev < kMaxDevices)
+            configured[dev].store(true, std::memory_order_release);
+    }
+    return launch_pdl(tree_attn_kernel<kScore>, dim3(static_cast<unsigned>(p.ctas * p.row_groups)), dim3(kTreeThreads),
+                      kTreeSmem, stream, mq, mk, mv, p);
 }
 
 } // namespace
 
 size_t tree_attn_workspace_bytes(int B, int M, int Hq, int Hkv, int page_size, int max_pages, int sm_count)
 {
-    (void)B, (void)M, (void)Hq, (void)Hkv, (void)page_size, (void)max_pages, (void)sm_count;
-    return 0;
+    if (B == 0)
+        return 0;
+    const Layout y = layout(B, M, Hq, Hkv, page_size, max_pages, sm_count);
+    return y.base_bytes + 2 * y.stat_bytes + y.acc_bytes;
 }
 
 cudaError_t launch_tree_attn(const TreeAttnArgs &a, cudaStream_t stream)
 {
-    const TreeParams p{a.q, a.k_cache, a.v_cache, a.block_table, a.context_lens, a.tree_mask, a.positions,
-                       a.draft_lens, a.slopes, a.M, a.Hq, a.Hkv, __builtin_ctz(static_cast<unsigned>(a.page_size)),
-                       a.max_pages, a.num_pages, a.scale, a.softcap, a.out_f32, a.out_bf16};
-    return launch_pdl(tree_rows_kernel, dim3(static_cast<unsigned>(a.M * a.Hq), static_cast<unsigned>(a.B)), dim3(32),
-                      0, stream, p);
+    const EncodeTiledFn fn = tensor_map_encoder();
+    if (!fn)
+        return cudaErrorNotSupported;
+    const Layout y = layout(a.B, a.M, a.Hq, a.Hkv, a.page_size, a.max_pages, a.sm_count);
+    TreeParams p{};
+    p.q = a.q;
+    p.k = a.k_cache;
+    p.v = a.v_cache;
+    p.block_table = a.block_table;
+    p.context_lens = a.context_lens;
+    p.tree_mask = a.tree_mask;
+    p.positions = a.positions;
+    p.draft_lens = a.draft_lens;
+    p.slopes = a.slopes;
+    p.B = a.B;
+    p.M = a.M;
+    p.Hq = a.Hq;
+    p.Hkv = a.Hkv;
+    p.log2_page = __builtin_ctz(static_cast<unsigned>(a.page_size));
+    p.max_pages = a.max_pages;
+    p.num_pages = a.num_pages;
+    p.g = a.Hq / a.Hkv;
+    p.tile_tokens = y.tile_tokens;
+    p.row_tiles = y.row_tiles;
+    p.row_groups = y.row_groups;
+    p.rec_rows = y.rec_rows;
+    p.ctas = y.ctas;
+    p.negate_q = a.scale < 0.f;
+    // A scale of 0 gives every key the same weight; the smallest positive
+    // factor does the same and keeps -inf * c, the score of a hidden key, -inf.
+    p.c = std::fmax(std::fabs(a.scale) * kLog2e, FLT_MIN);
+    if (a.softcap > 0.f) {
+        p.cap_in = std::fmin(2.f * std::fabs(a.scale) / a.softcap * kLog2e, FLT_MAX);
+        p.cap_out = a.softcap * kLog2e;
+    }
+    p.out_f32 = a.out_f32;
+    p.out_bf16 = a.out_bf16;
+    unsigned char *ws = static_cast<unsigned char *>(a.ws);
+    p.unit_base = reinterpret_cast<int32_t *>(ws);
+    p.rec_m = reinterpret_cast<float *>(ws + y.base_bytes);
+    p.rec_l = reinterpret_cast<float *>(ws + y.base_bytes + y.stat_bytes);
+    p.rec_acc = reinterpret_cast<float *>(ws + y.base_bytes + 2 * y.stat_bytes);
+    CUtensorMap mq, mk, mv;
+    const long long rows = static_cast<long long>(a.num_pages) * a.Hkv * a.page_size;
+    if (encode_query(fn, &mq, a.q, a.B * a.M, a.Hq, p.g, y.tile_tokens) != CUDA_SUCCESS ||
+        encode_cache(fn, &mk, a.k_cache, rows, a.page_size) != CUDA_SUCCESS ||
+        encode_cache(fn, &mv, a.v_cache, rows, a.page_size) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    cudaError_t err;
+    switch ((a.softcap > 0.f ? 1 : 0) | (a.slopes ? 2 : 0)) {
+    case 0: err = launch_score<0>(mq, mk, mv, p, stream); break;
+    case 1: err = launch_score<1>(mq, mk, mv, p, stream); break;
+    case 2: err = launch_score<2>(mq, mk, mv, p, stream); break;
+    default: err = launch_score<3>(mq, mk, mv, p, stream); break;
+    }
+    if (err != cudaSuccess)
+        return err;
+    const dim3 grid(static_cast<unsigned>((a.M * p.g + kMergeThreads / 32 - 1) / (kMergeThreads / 32)),
+                    static_cast<unsigned>(a.Hkv), static_cast<unsigned>(a.B));
+    return launch_pdl(tree_merge_kernel, grid, dim3(kMergeThreads), 0, stream, p);
 }
 
 cudaError_t read_flags_tree_attn(unsigned *flags, bool clear)
