@@ -36,20 +36,45 @@ __device__ __forceinline__ void tc_commit(uint64_t *bar)
                  : "memory");
 }
 
+// One lane of a converged warp (the same one every time).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes != 0;
+}
+
+// A value that is the same in every lane, marked as such for the compiler: the
+// products' operands are uniform registers.
+__device__ __forceinline__ uint32_t warp_uniform(uint32_t x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
+
+// Shared-memory operand descriptor, 128-byte swizzle. Low word: start address
+// and leading byte offset, high word: stride byte offset (all in units of 16
+// bytes), version 1 (bit 46), swizzle code 2 (bits 61-63).
+__device__ __forceinline__ uint32_t tc_desc_low(uint32_t addr, uint32_t lead_bytes)
+{
+    return (addr >> 4) | lead_bytes >> 4 << 16;
+}
+__host__ __device__ constexpr uint32_t tc_desc_high(uint32_t stride_bytes) { return stride_bytes >> 4 | 1u << 14 | 2u << 29; }
+
 // d (TMEM) (+)= A B, bf16 operands, fp32 accumulators. A and B by shared-memory
 // descriptor (ss) or A in TMEM (ts). accumulate = 0 overwrites d.
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t a_low, uint32_t a_high, uint32_t b_low, uint32_t b_high,
+                                          uint32_t idesc, uint32_t accumulate)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+                 "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+                 "r"(a_low), "r"(a_high), "r"(b_low), "r"(b_high), "r"(idesc), "r"(accumulate)
                  : "memory");
 }
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b_low, uint32_t b_high, uint32_t idesc,
+                                          uint32_t accumulate)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-                 "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+                 "mov.b64 b, {%2, %3};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+                 "r"(a), "r"(b_low), "r"(b_high), "r"(idesc), "r"(accumulate)
                  : "memory");
 }
 
@@ -60,15 +85,6 @@ __host__ __device__ constexpr uint32_t tc_idesc_bf16(uint32_t n, bool negate_a, 
 {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((negate_a ? 1u : 0u) << 13) | ((b_mn_major ? 1u : 0u) << 16) |
            ((n >> 3) << 17) | ((128u >> 4) << 24);
-}
-
-// Shared-memory operand descriptor, 128-byte swizzle: start address, leading
-// and stride byte offsets (all in units of 16 bytes), version 1 (bit 46),
-// swizzle code 2 (bits 61-63).
-__device__ __forceinline__ uint64_t tc_smem_desc(uint32_t addr, uint32_t lead_bytes, uint32_t stride_bytes)
-{
-    return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | static_cast<uint64_t>(lead_bytes >> 4) << 16 |
-           static_cast<uint64_t>(stride_bytes >> 4) << 32 | 1ull << 46 | 2ull << 61;
 }
 
 // Tiled TMA load of a box of a 4-D or 3-D tensor map, default L2 policy for 3-D.

@@ -25,8 +25,8 @@
 // (K and V tiles in consumption order), Q, and all of tensor memory (S/P of
 // two streams, O of two streams, 128 columns each):
 //   warp 8   requests Q, K and V tiles by TMA, one lane per page of a tile;
-//   warp 9   issues the tcgen05 products S = Q K^T (both operands from shared
-//            memory) and O += P V (P from tensor memory);
+//   warps 9 and 10  issue the tcgen05 products of one stream each: S = Q K^T
+//            (both operands from shared memory), O += P V (P from tensor memory);
 //   warps 0-3 and 4-7  one softmax warpgroup per stream: a thread owns a row,
 //            reads its 128 scores from tensor memory and writes P over them.
 // Two streams keep the tensor core and the softmax busy at once. With up to
@@ -55,13 +55,12 @@ constexpr int kTileBytes = kTileKeys * kRowBytes; // 32 KB of K or V
 constexpr int kSlots = 5;
 constexpr int kValidRing = 8;      // units whose page masks are kept (the ring holds at most 4 ahead)
 constexpr int kSoftmaxThreads = 256;
-constexpr int kTreeThreads = 384; // three warpgroups (the last two warps idle)
-constexpr int kProducerWarp = 8, kMmaWarp = 9;
+constexpr int kTreeThreads = 384; // three warpgroups (the last warp idles)
+constexpr int kProducerWarp = 8, kMmaWarp = 9; // and kMmaWarp + 1
 constexpr float kRescaleLog2 = 8.f; // rise of a row's scores that moves its reference
 constexpr int kMergeThreads = 256;
 
-// TMEM columns: S (fp32, 128 columns; P hi in its first 64, P lo in the other
-// 64) and O of stream s.
+// TMEM columns of stream s's S (fp32, 128 columns, P over it) and O, + 128 s.
 constexpr uint32_t kColS = 0, kColO = 256;
 
 struct TreeParams {
@@ -91,11 +90,15 @@ struct __align__(1024) TreeSmem {
     unsigned char slots[kSlots][kTileBytes];
     unsigned char q[2][kTileRows * kRowBytes];
     // barriers
-    uint64_t full[kSlots], empty[kSlots];
+    // a slot's loads complete on the barrier of the stream that reads them (the
+    // first one's where both do), so that each stream sees every phase it waits for
+    uint64_t full[2][kSlots], empty[kSlots];
     uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[2], p_ready[2];
-    uint64_t seg_done, ml_ready, epi_done, drain;
-    uint64_t bad_rows;  // drafted tokens of the segment whose V row is not finite
+    uint64_t s_full[2], p_half[2], p_ready[2];
+    uint64_t seg_done, ml_ready, epi_done, drain[2];
+    // drafted tokens of a stream's tiles of a segment whose V row is not finite
+    // (with two row tiles a stream may be two segments ahead of the other's readers)
+    uint64_t bad_rows[4][2];
     uint32_t valid[kValidRing]; // pages inside the pool, a bit per 16 keys of a tile
     uint32_t tmem_base;
     int start_b, start_h, start_tile, units; // this CTA's run
@@ -170,22 +173,39 @@ struct Segments {
     }
 };
 
-// The same, tile by tile.
-struct Units {
+// The steps of one stream in a CTA's run. A step is a (tile, stream); with one
+// row tile the streams take alternate tiles of the whole run, with two (pair)
+// each takes every tile.
+struct Steps {
     Segments seg;
-    int t, index; // current tile, segments begun before this one
-    __device__ Units(const TreeParams &p, const TreeSmem &s) : seg(p, s), t(-1), index(-1) { advance(p); }
+    int stream, index; // segments begun before this one
+    int begin, end;    // the segment's steps, of either stream
+    int n;             // the current step
+    bool pair, any;
+    __device__ Steps(const TreeParams &p, const TreeSmem &s, int stream, bool pair)
+        : seg(p, s), stream(stream), index(-1), begin(0), end(0), n(0), pair(pair), any(true)
+    {
+        advance(p);
+    }
     __device__ void advance(const TreeParams &p)
     {
-        if (index >= 0 && ++t < seg.seg_tile1)
-            return;
-        if (seg.next(p)) {
+        n += 2;
+        while (any && n >= end) {
+            any = seg.next(p);
+            if (!any)
+                break;
             ++index;
-            t = seg.seg_tile0;
+            begin = end;
+            end = begin + (seg.seg_tile1 - seg.seg_tile0) * (pair ? 2 : 1);
+            n = begin + ((begin ^ stream) & 1);
         }
     }
-    __device__ bool first() const { return t == seg.seg_tile0; }
-    __device__ bool last() const { return t == seg.seg_tile1 - 1; }
+    __device__ int unit() const { return pair ? n >> 1 : n; }
+    __device__ int tile() const { return seg.seg_tile0 + ((n - begin) >> (pair ? 1 : 0)); }
+    __device__ bool first() const { return n < begin + 2; }
+    __device__ bool last() const { return n + 2 >= end; }
+    // the segment has a single step: its stream signals for the other one too
+    __device__ bool alone() const { return end - begin == 1; }
 };
 
 // Position in the ring of unit u's K and V tile, of N units. Two row tiles
@@ -209,17 +229,22 @@ __device__ bool produce(const TreeParams &p, TreeSmem &s, const CUtensorMap *mq,
     // K and V are read once per row group: with one group nothing reads them again
     const uint64_t policy = l2_evict_first_policy();
     int put = 0;
+    uint32_t issued = 0, phases = 0; // per barrier (stream, slot): used, parity of its last load
     bool ok = true;
-    const auto load_tile = [&](const CUtensorMap *map, int group) {
+    const auto load_tile = [&](const CUtensorMap *map, int group, int reader) {
         const int slot = put % kSlots;
         ok = ok && warp_wait(&s.empty[slot], ((put / kSlots) & 1) ^ 1);
         if (!ok)
             return;
+        uint64_t *full = &s.full[reader][slot];
         if (lane == 0)
-            mbar_arrive_expect_tx(&s.full[slot], kTileBytes);
+            mbar_arrive_expect_tx(full, kTileBytes);
         __syncwarp();
         if (lane < boxes)
-            tma_load_4d(s.slots[slot] + lane * box_keys * kRowBytes, map, 0, 0, 0, group, &s.full[slot], policy);
+            tma_load_4d(s.slots[slot] + lane * box_keys * kRowBytes, map, 0, 0, 0, group, full, policy);
+        const uint32_t bit = 1u << (reader * kSlots + slot);
+        phases = issued & bit ? phases ^ bit : phases;
+        issued |= bit;
         ++put;
     };
     const int ahead = pair ? 1 : 2; // tiles of K requested before the V of the first of them
@@ -249,7 +274,7 @@ __device__ bool produce(const TreeParams &p, TreeSmem &s, const CUtensorMap *mq,
                 atomicOr(&g_flags_tree, PGQA_DEVERR_BAD_PAGE);
             uint32_t valid = __ballot_sync(0xFFFFFFFFu, !needed || in_pool);
             if (unit >= ahead)
-                load_tile(mv, ahead == 1 ? group1 : group2);
+                load_tile(mv, pair ? group1 : group2, pair ? 0 : unit & 1);
             if (tile == seg.seg_tile0 && ok) {
                 // Q: one buffer per segment in turn, or both for two row tiles
                 const int buf = pair ? 0 : index & 1;
@@ -269,18 +294,19 @@ __device__ bool produce(const TreeParams &p, TreeSmem &s, const CUtensorMap *mq,
                     by16 |= ((valid >> (i * 16 / box_keys)) & 1u) << i;
                 s.valid[unit % kValidRing] = by16;
             }
-            load_tile(mk, group);
+            load_tile(mk, group, pair ? 0 : unit & 1);
             group2 = group1;
             group1 = group;
         }
     }
     if (ok && !pair && unit > 1)
-        load_tile(mv, group2);
+        load_tile(mv, group2, unit & 1);
     if (ok && unit > 0)
-        load_tile(mv, group1);
-    if (!ok) // wait, with a limit, for what is still on its way into shared memory
-        for (int i = max(0, put - kSlots); i < put; ++i)
-            (void)warp_wait(&s.full[i % kSlots], (i / kSlots) & 1);
+        load_tile(mv, group1, pair ? 0 : (unit - 1) & 1);
+    // nothing may still be on its way into shared memory when the CTA ends
+    for (int i = 0; i < 2 * kSlots; ++i)
+        if (issued >> i & 1u)
+            ok = warp_wait(&s.full[i / kSlots][i % kSlots], phases >> i & 1u) && ok;
     return ok;
 }
 
@@ -325,129 +351,173 @@ __device__ uint64_t settle_v_tile(unsigned char *v, int key0, int T, int n, int 
     return static_cast<uint64_t>(hi) << 32 | lo;
 }
 
-__device__ bool multiply(const TreeParams &p, TreeSmem &s, bool pair)
+// One warp per stream, so that one's waits lie under the other's products.
+__device__ bool multiply(const TreeParams &p, TreeSmem &s, bool pair, int stream)
 {
-    const int lane = threadIdx.x & 31;
-    const int N = s.units;                  // tiles
-    const int steps = pair ? 2 * N : N;     // (tile, stream)
-    const uint32_t tmem = s.tmem_base;
+    const int N = s.units; // tiles
+    const bool leader = elect_one(); // issues every product and commit
+    const uint32_t tmem_s = warp_uniform(s.tmem_base + kColS + stream * 128);
     const uint32_t idesc_s = tc_idesc_bf16(kTileKeys, p.negate_q != 0, false);
     const uint32_t idesc_o = tc_idesc_bf16(kHeadDim, false, true);
     const int box_keys = min(1 << p.log2_page, kTileKeys);
-    Units su(p, s), pu(p, s); // of the next score product and of the next product with V
     uint64_t bad = 0;
+    uint64_t *full = s.full[pair ? 0 : stream];
+    uint32_t phases = 0; // of `full`, a bit per slot
     bool ok = true;
-
-    // S of step n: Q rows 128 x 128, K tile rows are the N dimension
-    const auto scores = [&](int n) {
-        const int stream = n & 1, unit = pair ? n >> 1 : n;
-        const bool new_tile = !pair || stream == 0;
-        const int buf = pair ? 0 : su.index & 1;
-        const int k_at = ring_k(pair, unit);
-        if (su.first() && new_tile)
-            ok = ok && warp_wait(&s.q_full[buf], (pair ? su.index : su.index >> 1) & 1);
-        if (new_tile)
-            ok = ok && warp_wait(&s.full[k_at % kSlots], (k_at / kSlots) & 1);
-        if (!ok)
-            return;
-        tc_fence_after();
-        if (lane == 0) {
-            const uint32_t qa = smem_addr(s.q[pair ? stream : buf]);
-            const uint32_t ka = smem_addr(s.slots[k_at % kSlots]);
-#pragma unroll
-            for (int k = 0; k < kHeadDim / 16; ++k) {
-                const int half = k >> 2, off = (k & 3) * 32;
-                tc_mma_ss(tmem + kColS + stream * 128, tc_smem_desc(qa + half * (kTileRows * 128) + off, 16, 1024),
-                          tc_smem_desc(ka + half * 1024 + off, 16, 2048), idesc_s, k > 0);
-            }
-            if (!pair || stream == 1) {
-                tc_commit(&s.empty[k_at % kSlots]);
-                if (su.last())
-                    tc_commit(&s.q_empty[buf]);
-            }
-            tc_commit(&s.s_full[stream]);
-            mbar_arrive(&s.s_full[stream]); // orders the page mask's write before its readers
-        }
-        __syncwarp();
-        if (!pair || stream == 1)
-            su.advance(p);
+    const auto landed = [&](int slot) {
+        const bool yes = warp_wait(&full[slot], phases >> slot & 1u);
+        phases ^= 1u << slot;
+        return yes;
     };
-    // O += P V of step n; P hi in the first 64 columns of S's place, P lo in the others
-    const auto values = [&](int n) {
-        const int stream = n & 1, unit = pair ? n >> 1 : n;
-        const bool new_tile = !pair || stream == 0;
-        const int v_at = ring_v(pair, unit, N);
-        unsigned char *v = s.slots[v_at % kSlots];
-        if (new_tile) {
-            ok = ok && warp_wait(&s.full[v_at % kSlots], (v_at / kSlots) & 1);
+
+    Steps su(p, s, stream, pair), pu(p, s, stream, pair); // of the next score product and of the next product with V
+    // the first round issues only the first scores
+    for (bool started = false; ok && (pu.any || !started); started = true) {
+        if (started) { // O += P V; P lies in S's place, for each 32 keys 16 columns hi and 16 lo
+            const int n = pu.n;
+            const int slot = ring_v(pair, pu.unit(), N) % kSlots;
+            unsigned char *v = s.slots[slot];
+            ok = landed(slot);
             if (!ok)
-                return;
+                break;
             if (pu.first())
                 bad = 0;
-            const int key0 = pu.t * kTileKeys;
-            if (key0 + kTileKeys > pu.seg.T - pu.seg.n)
+            const int key0 = pu.tile() * kTileKeys;
+            if (key0 + kTileKeys > pu.seg.T - pu.seg.n) // of two streams on one tile both do this: the same zeros
                 bad |= settle_v_tile(v, key0, pu.seg.T, pu.seg.n, box_keys);
-        }
-        ok = ok && warp_wait(&s.p_ready[stream], (n >> 1) & 1);
-        if (!ok)
-            return;
-        tc_fence_after();
-        if (lane == 0) {
-            const uint32_t va = smem_addr(v);
-            const uint32_t o = tmem + kColO + stream * 128;
-            // the first product of a stream in a segment overwrites O
-            const uint32_t keep = pair ? !pu.first() : pu.t - pu.seg.seg_tile0 >= 2;
+            const uint32_t va = warp_uniform(tc_desc_low(smem_addr(v), 1024));
+            const uint32_t keep = warp_uniform(!pu.first()); // a segment's first product overwrites O
 #pragma unroll
-            for (int part = 0; part < 2; ++part)
+            for (int half = 0; half < 2; ++half) { // 64 keys each
+                ok = ok && warp_wait(half == 0 ? &s.p_half[stream] : &s.p_ready[stream], (n >> 1) & 1);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                if (leader) {
 #pragma unroll
-                for (int k = 0; k < kTileKeys / 16; ++k)
-                    tc_mma_ts(o, tmem + kColS + stream * 128 + part * 64 + k * 8,
-                              tc_smem_desc(va + k * 4096, 1024, 2048), idesc_o, keep || part > 0 || k > 0);
-            if (!pair || stream == 1) {
-                tc_commit(&s.empty[v_at % kSlots]);
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int part = 0; part < 2; ++part) // 16 keys: hi, then lo
+                            tc_mma_ts(tmem_s + (kColO - kColS), tmem_s + half * 64 + (k >> 1) * 32 + part * 16 + (k & 1) * 8,
+                                      va + (half * 4 + k) * (4096 / 16), tc_desc_high(2048), idesc_o,
+                                      half > 0 || part > 0 || k > 0 ? 1u : keep);
+                }
+            }
+            if (!ok)
+                break;
+            if (leader) {
+                tc_commit(&s.empty[slot]);
                 if (pu.last()) {
-                    s.bad_rows = bad;
+                    s.bad_rows[pu.index & 3][stream] = bad;
                     tc_commit(&s.seg_done);
+                    if (pu.alone()) {
+                        s.bad_rows[pu.index & 3][stream ^ 1] = 0;
+                        tc_commit(&s.seg_done);
+                        mbar_arrive(&s.seg_done);
+                    }
                     mbar_arrive(&s.seg_done); // orders bad_rows before its readers
                 }
             }
-        }
-        __syncwarp();
-        if (!pair || stream == 1)
+            __syncwarp();
             pu.advance(p);
-    };
-    for (int n = 0; n < min(2, steps) && ok; ++n)
-        scores(n);
-    for (int n = 0; n < steps && ok; ++n) {
-        values(n);
-        if (n + 2 < steps && ok)
-            scores(n + 2);
+        }
+        if (su.any) { // S = Q K^T over the place of the P that was just used
+            const int slot = ring_k(pair, su.unit()) % kSlots;
+            const int buf = pair ? 0 : su.index & 1;
+            // K first: once it is there, the buffer's earlier Q was there too
+            // (a stream may have had no step in that segment), and the parity
+            // of q_full means this segment's Q
+            ok = landed(slot);
+            if (su.first())
+                ok = ok && warp_wait(&s.q_full[buf], (pair ? su.index : su.index >> 1) & 1);
+            if (!ok)
+                break;
+            tc_fence_after();
+            const uint32_t qa = warp_uniform(tc_desc_low(smem_addr(s.q[pair ? stream : buf]), 16));
+            const uint32_t ka = warp_uniform(tc_desc_low(smem_addr(s.slots[slot]), 16));
+            if (leader) {
+#pragma unroll
+                for (int k = 0; k < kHeadDim / 16; ++k) {
+                    const int half = k >> 2, off = (k & 3) * 2; // 64 columns each; 32 bytes a step
+                    tc_mma_ss(tmem_s, qa + half * (kTileRows * 128 / 16) + off, tc_desc_high(1024),
+                              ka + half * (1024 / 16) + off, tc_desc_high(2048), idesc_s, k > 0);
+                }
+                tc_commit(&s.s_full[stream]);
+                mbar_arrive(&s.s_full[stream]); // orders the page mask's write before its readers
+                tc_commit(&s.empty[slot]);
+                if (su.last()) {
+                    tc_commit(&s.q_empty[buf]);
+                    if (su.alone())
+                        tc_commit(&s.q_empty[buf]);
+                }
+            }
+            __syncwarp();
+            su.advance(p);
+        }
     }
-    if (!ok) { // wait, with a limit, for the products in flight
-        if (lane == 0)
-            tc_commit(&s.drain);
-        (void)warp_wait(&s.drain, 0);
-    }
-    return ok;
+    // no product may still be running when the CTA ends
+    if (leader)
+        tc_commit(&s.drain[stream]);
+    return warp_wait(&s.drain[stream], 0) && ok;
 }
 
 // ---------------------------------------------------------------- softmax
-// Bits of the keys key0 + 32 w .. + 31 that a row sees, w = 0 .. 3: the prefix,
-// then the drafted tokens of its mask, without pages outside the pool.
-__device__ __forceinline__ uint32_t visible_word(int w, int prefix_keys, uint64_t mask, uint32_t valid)
+// Bits of the 32 keys of which the first `below` lie in the prefix (any
+// integer; drafted token j is key below + j) that a row sees: the prefix, the
+// drafted tokens of its mask, without pages outside the pool (two bits of
+// `valid`, 16 keys each).
+__device__ __forceinline__ uint32_t visible_word(int below, uint64_t mask, uint32_t valid)
 {
-    const int below = prefix_keys - 32 * w; // prefix keys from this word's first on
     uint32_t bits = below >= 32 ? 0xFFFFFFFFu : (below > 0 ? (1u << below) - 1u : 0u);
-    if (below < 32) {
-        // drafted token j sits at bit below + j of the word
-        const uint64_t drafted = below >= 0 ? mask << below : (below > -64 ? mask >> -below : 0ull);
-        bits |= static_cast<uint32_t>(drafted);
-    }
-    const uint32_t v = valid >> (2 * w);
-    return bits & (((v & 1u) ? 0xFFFFu : 0u) | ((v & 2u) ? 0xFFFF0000u : 0u));
+    if (below < 32)
+        bits |= static_cast<uint32_t>(below >= 0 ? mask << below : (below > -64 ? mask >> -below : 0ull));
+    return bits & (((valid & 1u) ? 0xFFFFu : 0u) | ((valid & 2u) ? 0xFFFF0000u : 0u));
 }
 
-template <int kScore> // bit 0: tanh cap, bit 1: distance bias
+// 32 scores of a row from key `key` on, transformed (kScore bit 0: tanh cap,
+// bit 1: distance bias) and, if `masked`, hidden keys set to -inf; returns the
+// largest. far0: distance of the first key if it lies in the prefix; pos_lo and
+// pos_hi: this lane's drafted tokens' positions (lane, lane + 32).
+template <int kScore>
+__device__ __forceinline__ float prepare_scores(const TreeParams &p, float *x, int key, float slope, float far0, int pos,
+                                                int prefix, int n, int pos_lo, int pos_hi, bool masked, uint64_t mask,
+                                                uint32_t valid)
+{
+    if constexpr (kScore != 0) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            float y;
+            if constexpr ((kScore & 1) != 0) // c tanh(u) = c - 2 c / (1 + e^2u)
+                y = fmaf(-2.f * p.cap_out, rcp(1.f + ex2(x[j] * p.cap_in)), p.cap_out);
+            else
+                y = x[j] * p.c;
+            if constexpr ((kScore & 2) != 0) {
+                // keys of the prefix; drafted tokens have positions of their own
+                float far = far0 + static_cast<float>(j);
+                if (masked && key + j >= prefix && key + j - prefix < n) {
+                    const int d = key + j - prefix;
+                    const int kpos = __shfl_sync(0xFFFFFFFFu, d < 32 ? pos_lo : pos_hi, d & 31);
+                    far = static_cast<float>(static_cast<long long>(kpos) - pos);
+                }
+                y = fmaf(slope, far, y);
+            }
+            x[j] = y;
+        }
+    }
+    if (masked) {
+        const uint32_t bits = visible_word(prefix - key, mask, valid);
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            x[j] = (bits >> j) & 1u ? x[j] : -INFINITY;
+    }
+    float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+    for (int j = 4; j < 32; ++j)
+        top[j & 3] = fmaxf(top[j & 3], x[j]);
+    return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+}
+
+template <int kScore>
 __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int cta)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -469,7 +539,7 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
         const int head = seg.h * p.g + row % p.g;
         uint64_t mask = 0;
         float slope = 0.f;
-        int pos = 0;
+        int pos = 0, pos_lo = 0, pos_hi = 0;
         const bool live = real && token < seg.n;
         if (live) {
             mask = p.tree_mask[static_cast<size_t>(seg.b) * p.M + token];
@@ -479,6 +549,11 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
                 slope = p.slopes[head] * kLog2e;
                 pos = p.positions[static_cast<size_t>(seg.b) * p.M + token];
             }
+        }
+        if constexpr ((kScore & 2) != 0) {
+            const int32_t *at = p.positions + static_cast<size_t>(seg.b) * p.M;
+            pos_lo = lane < seg.n ? at[lane] : 0;
+            pos_hi = lane + 32 < seg.n ? at[lane + 32] : 0;
         }
         const int seg_steps = (seg.seg_tile1 - seg.seg_tile0) * (pair ? 2 : 1);
         float m = -INFINITY; // the reference, in units of 1 / c
@@ -492,51 +567,45 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
                 break;
             tc_fence_after();
             if (warp_works) {
-                float x[kTileKeys];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    tmem_ld32(x + 32 * i, tmem_s + 32 * i);
                 const int key0 = tile * kTileKeys;
                 const uint32_t valid = s.valid[unit % kValidRing];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    tmem_wait_ld32(x + 32 * i);
                 const bool tail = key0 + kTileKeys > prefix;
-                if constexpr (kScore != 0) {
+                float high = -INFINITY;
+                if (kScore == 0 && !tail && valid == 0xFFu) {
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float x[2][32];
+                        tmem_ld32(x[0], tmem_s + 64 * i);
+                        tmem_ld32(x[1], tmem_s + 64 * i + 32);
+                        tmem_wait_ld32(x[0]);
+                        tmem_wait_ld32(x[1]);
+#pragma unroll
+                        for (int j = 0; j < 64; ++j)
+                            top[j & 3] = fmaxf(top[j & 3], x[j >> 5][j & 31]);
+                    }
+                    high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                } else {
+                    // scores are transformed and hidden keys marked in place
                     const float far0 = static_cast<float>(static_cast<long long>(key0) - pos);
+                    float x[2][32];
+                    tmem_ld32(x[0], tmem_s);
+#pragma unroll 1
+                    for (int i = 0; i < 4; i += 2) {
 #pragma unroll
-                    for (int j = 0; j < kTileKeys; ++j) {
-                        float y;
-                        if constexpr ((kScore & 1) != 0) // cap tanh(u) = cap - 2 cap / (1 + e^2u)
-                            y = fmaf(-2.f * p.cap_out, rcp(1.f + ex2(x[j] * p.cap_in)), p.cap_out);
-                        else
-                            y = x[j] * p.c;
-                        if constexpr ((kScore & 2) != 0) {
-                            float far = far0 + static_cast<float>(j);
-                            if (tail && key0 + j >= prefix) // a drafted token's own position
-                                far = static_cast<float>(
-                                    static_cast<long long>(
-                                        p.positions[static_cast<size_t>(seg.b) * p.M + min(key0 + j - prefix, p.M - 1)]) -
-                                    pos);
-                            y = fmaf(slope, far, y);
+                        for (int k = 0; k < 2; ++k) {
+                            tmem_wait_ld32(x[k]);
+                            tmem_ld32(x[k ^ 1], tmem_s + 32 * ((i + k + 1) & 3));
+                            const float y = prepare_scores<kScore>(p, x[k], key0 + 32 * (i + k), slope,
+                                                                   far0 + 32 * (i + k), pos, prefix, seg.n, pos_lo, pos_hi,
+                                                                   tail || valid != 0xFFu, mask, valid >> (2 * (i + k)));
+                            tmem_st32(tmem_s + 32 * (i + k), x[k]);
+                            high = fmaxf(high, y);
                         }
-                        x[j] = y;
                     }
+                    tmem_wait_ld32(x[0]); // the last prefetch, of no use
+                    tmem_wait_st();
                 }
-                if (tail || valid != 0xFFu) {
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const uint32_t bits = visible_word(w, prefix - key0, mask, valid);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            x[32 * w + j] = (bits >> j) & 1u ? x[32 * w + j] : -INFINITY;
-                    }
-                }
-                float top[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-                for (int j = 4; j < kTileKeys; ++j)
-                    top[j & 3] = fmaxf(top[j & 3], x[j]);
-                const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                 // move the reference where the row has none yet, or its scores left its range
                 const bool move = fresh ? true : (m == -INFINITY ? high > -INFINITY : (high - m) * c > kRescaleLog2);
                 if (__any_sync(0xFFFFFFFFu, move)) {
@@ -559,36 +628,51 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
                         }
                     }
                 }
-                float ref = m == -INFINITY ? 0.f : m * c;
-                if constexpr (kScore == 0) {
-                    // x c - m c loses |m c| 2^-24 of the exponent: where that
-                    // matters, subtract before the product
-                    const bool large = fabsf(ref) > 65536.f;
-                    if (__any_sync(0xFFFFFFFFu, large)) {
-                        const float shift = large ? m : 0.f;
-#pragma unroll
-                        for (int j = 0; j < kTileKeys; ++j)
-                            x[j] -= shift;
-                        ref = large ? 0.f : ref;
-                    }
-                }
+                // p = 2^(x c - m c). For scores so large that the rounding of m c
+                // matters the difference is taken before the product.
+                const float ref = m == -INFINITY ? 0.f : m * c;
+                const bool large = kScore == 0 && fabsf(ref) > 65536.f;
+                const float shift = large ? m : 0.f, neg_ref = large ? 0.f : -ref;
+                const bool any_large = __any_sync(0xFFFFFFFFu, large);
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                float x[2][32];
+                tmem_ld32(x[0], tmem_s);
+#pragma unroll 1
+                for (int i = 0; i < 4; i += 2) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t hi[16], lo[16];
+                    for (int k = 0; k < 2; ++k) {
+                        tmem_wait_ld32(x[k]);
+                        tmem_ld32(x[k ^ 1], tmem_s + 32 * ((i + k + 1) & 3));
+                        if (any_large) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float a = ex2(fmaf(x[32 * i + 2 * j], c, -ref));
-                        const float b = ex2(fmaf(x[32 * i + 2 * j + 1], c, -ref));
-                        sum[j & 3] += a + b;
-                        hi[j] = pack_bf16x2(a, b);
-                        lo[j] = pack_bf16x2(a - bf16_lo(hi[j]), b - bf16_hi(hi[j]));
+                            for (int j = 0; j < 32; ++j)
+                                x[k][j] -= shift;
+                        }
+                        uint32_t hi[16], lo[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float a = ex2(fmaf(x[k][2 * j], c, neg_ref));
+                            const float b = ex2(fmaf(x[k][2 * j + 1], c, neg_ref));
+                            sum[j & 3] += a + b;
+                            hi[j] = pack_bf16x2(a, b);
+                            lo[j] = pack_bf16x2(a - bf16_lo(hi[j]), b - bf16_hi(hi[j]));
+                        }
+                        tmem_st16(tmem_s + 32 * (i + k), hi);
+                        tmem_st16(tmem_s + 32 * (i + k) + 16, lo);
                     }
-                    tmem_st16(tmem_s + 16 * i, hi);
-                    tmem_st16(tmem_s + 64 + 16 * i, lo);
+                    if (i == 0) { // half of P: its product can start
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(&s.p_half[stream]);
+                    }
                 }
+                tmem_wait_ld32(x[0]); // the last prefetch, of no use
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 tmem_wait_st();
+            } else if (lane == 0) {
+                mbar_arrive(&s.p_half[stream]);
             }
             fresh = false;
             tc_fence_before();
@@ -624,7 +708,7 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
         if (!ok)
             break;
         tc_fence_after();
-        const uint64_t bad = s.bad_rows & mask;
+        const uint64_t bad = (s.bad_rows[index & 3][0] | s.bad_rows[index & 3][1]) & mask;
         const bool whole = seg.seg_tile0 == 0 && seg.seg_tile1 == seg.tiles;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const size_t out_row = (static_cast<size_t>(seg.b) * p.M + token) * p.Hq + head;
@@ -737,16 +821,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     if (tid == 0) {
         prefetch_tensormap(&mq), prefetch_tensormap(&mk), prefetch_tensormap(&mv);
         for (int i = 0; i < kSlots; ++i)
-            mbar_init(&s.full[i], 1), mbar_init(&s.empty[i], 1);
+            mbar_init(&s.full[0][i], 1), mbar_init(&s.full[1][i], 1),
+                mbar_init(&s.empty[i], pair ? 2 : 1); // the streams that read a slot
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&s.q_full[i], 1), mbar_init(&s.q_empty[i], 1);
+            mbar_init(&s.q_full[i], 1), mbar_init(&s.q_empty[i], 2);
+            mbar_init(&s.drain[i], 1);
             mbar_init(&s.s_full[i], 2);  // the products' completion, and the issuing thread
-            mbar_init(&s.p_ready[i], 4); // one arrival per warp of the stream
+            mbar_init(&s.p_half[i], 4); // one arrival per warp of the stream
+            mbar_init(&s.p_ready[i], 4);
         }
-        mbar_init(&s.seg_done, 2);
+        mbar_init(&s.seg_done, 4); // per stream: the products' completion, and the issuing thread
         mbar_init(&s.ml_ready, kSoftmaxThreads / 32);
         mbar_init(&s.epi_done, kSoftmaxThreads / 32);
-        mbar_init(&s.drain, 1);
         fence_mbar_init();
     }
     if (warp == kMmaWarp)
@@ -813,8 +899,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == kProducerWarp && s.units > 0)
             ok = produce(p, s, &mq, &mk, &mv, rg, pair);
-        else if (warp == kMmaWarp && s.units > 0)
-            ok = multiply(p, s, pair);
+        else if (warp <= kMmaWarp + 1 && s.units > 0)
+            ok = multiply(p, s, pair, warp - kMmaWarp);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         if (s.units > 0)
