@@ -155,4 +155,38 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *u)
                  : "memory");
 }
 
+// Two fp32 operations in one instruction (packed pairs).
+struct f32x2 {
+    uint64_t bits;
+    __device__ __forceinline__ f32x2(float lo, float hi)
+    {
+        asm("mov.b64 %0, {%1, %2};" : "=l"(bits) : "f"(lo), "f"(hi));
+    }
+    __device__ __forceinline__ void get(float &lo, float &hi) const
+    {
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(bits));
+    }
+};
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c)
+{
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c.bits) : "l"(a.bits), "l"(b.bits));
+    return c;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b)
+{
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a.bits) : "l"(b.bits));
+    return a;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b)
+{
+    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a.bits) : "l"(b.bits));
+    return a;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 } // namespace pgqa

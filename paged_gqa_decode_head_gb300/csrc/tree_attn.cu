@@ -484,25 +484,36 @@ __device__ __forceinline__ float prepare_scores(const TreeParams &p, float *x, i
                                                 uint32_t valid)
 {
     if constexpr (kScore != 0) {
+        const bool drafted = masked && key + 32 > prefix && key < prefix + n;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            float y;
-            if constexpr ((kScore & 1) != 0) // c tanh(u) = c - 2 c / (1 + e^2u)
-                y = fmaf(-2.f * p.cap_out, rcp(1.f + ex2(x[j] * p.cap_in)), p.cap_out);
-            else
-                y = x[j] * p.c;
-            if constexpr ((kScore & 2) != 0) {
-                // keys of the prefix; drafted tokens have positions of their own
-                float far = far0 + static_cast<float>(j);
-                if (masked && key + j >= prefix && key + j - prefix < n) {
-                    const int d = key + j - prefix;
-                    const int kpos = __shfl_sync(0xFFFFFFFFu, d < 32 ? pos_lo : pos_hi, d & 31);
-                    far = static_cast<float>(static_cast<long long>(kpos) - pos);
-                }
-                y = fmaf(slope, far, y);
+        for (int j = 0; j < 32; j += 2) {
+            f32x2 y(x[j], x[j + 1]);
+            if constexpr ((kScore & 1) != 0) { // c tanh(u) = c - 2 c / (1 + e^2u)
+                float a, b;
+                mul2(y, f32x2(p.cap_in, p.cap_in)).get(a, b);
+                add2(f32x2(ex2(a), ex2(b)), f32x2(1.f, 1.f)).get(a, b);
+                y = fma2(f32x2(rcp(a), rcp(b)), f32x2(-2.f * p.cap_out, -2.f * p.cap_out), f32x2(p.cap_out, p.cap_out));
+            } else {
+                y = mul2(y, f32x2(p.c, p.c));
             }
-            x[j] = y;
+            if constexpr ((kScore & 2) != 0)
+                if (!drafted)
+                    y = fma2(f32x2(slope, slope), add2(f32x2(far0, far0), f32x2(j, j + 1)), y);
+            y.get(x[j], x[j + 1]);
         }
+        if constexpr ((kScore & 2) != 0)
+            if (drafted) { // drafted tokens have positions of their own
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const int d = key + j - prefix;
+                    float far = far0 + static_cast<float>(j);
+                    if (d >= 0 && d < n) {
+                        const int kpos = __shfl_sync(0xFFFFFFFFu, d < 32 ? pos_lo : pos_hi, d & 31);
+                        far = static_cast<float>(static_cast<long long>(kpos) - pos);
+                    }
+                    x[j] = fmaf(slope, far, x[j]);
+                }
+            }
     }
     if (masked) {
         const uint32_t bits = visible_word(prefix - key, mask, valid);
@@ -510,11 +521,11 @@ __device__ __forceinline__ float prepare_scores(const TreeParams &p, float *x, i
         for (int j = 0; j < 32; ++j)
             x[j] = (bits >> j) & 1u ? x[j] : -INFINITY;
     }
-    float top[4] = {x[0], x[1], x[2], x[3]};
+    float top[2] = {x[0], x[1]};
 #pragma unroll
-    for (int j = 4; j < 32; ++j)
-        top[j & 3] = fmaxf(top[j & 3], x[j]);
-    return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+    for (int j = 2; j < 32; j += 2)
+        top[j >> 1 & 1] = max3(top[j >> 1 & 1], x[j], x[j + 1]);
+    return fmaxf(top[0], top[1]);
 }
 
 template <int kScore>
@@ -563,6 +574,10 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
             const int tile = seg.seg_tile0 + ((n - step) >> (pair ? 1 : 0));
             const int unit = pair ? n >> 1 : n;
             ok = warp_wait(&s.s_full[stream], (n >> 1) & 1);
+            // The streams take turns: one starts its softmax when the other has
+            // half of P, so that one's products run under the other's softmax.
+            if (n > 0)
+                ok = ok && warp_wait(&s.p_half[stream ^ 1], ((n - 1) >> 1) & 1);
             if (!ok)
                 break;
             tc_fence_after();
@@ -581,8 +596,8 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
                         tmem_wait_ld32(x[0]);
                         tmem_wait_ld32(x[1]);
 #pragma unroll
-                        for (int j = 0; j < 64; ++j)
-                            top[j & 3] = fmaxf(top[j & 3], x[j >> 5][j & 31]);
+                        for (int j = 0; j < 64; j += 2)
+                            top[j >> 1 & 3] = max3(top[j >> 1 & 3], x[j >> 5][j & 31], x[j >> 5][(j & 31) + 1]);
                     }
                     high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                 } else {
@@ -634,7 +649,7 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
                 const bool large = kScore == 0 && fabsf(ref) > 65536.f;
                 const float shift = large ? m : 0.f, neg_ref = large ? 0.f : -ref;
                 const bool any_large = __any_sync(0xFFFFFFFFu, large);
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                f32x2 sum[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
                 float x[2][32];
                 tmem_ld32(x[0], tmem_s);
 #pragma unroll 1
@@ -651,11 +666,19 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
                         uint32_t hi[16], lo[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
-                            const float a = ex2(fmaf(x[k][2 * j], c, neg_ref));
-                            const float b = ex2(fmaf(x[k][2 * j + 1], c, neg_ref));
-                            sum[j & 3] += a + b;
-                            hi[j] = pack_bf16x2(a, b);
-                            lo[j] = pack_bf16x2(a - bf16_lo(hi[j]), b - bf16_hi(hi[j]));
+                            float a, b;
+                            fma2(f32x2(x[k][2 * j], x[k][2 * j + 1]), f32x2(c, c), f32x2(neg_ref, neg_ref)).get(a, b);
+                            a = ex2(a), b = ex2(b);
+                            const f32x2 w(a, b);
+                            sum[j & 1] = add2(sum[j & 1], w);
+                            // hi: the upper 16 bits as they are; lo: the exact rest, rounded
+                            const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+                            hi[j] = __byte_perm(ua, ub, 0x7632);
+                            float ra, rb;
+                            add2(w, f32x2(__uint_as_float((ua & 0xFFFF0000u) ^ 0x80000000u),
+                                          __uint_as_float((ub & 0xFFFF0000u) ^ 0x80000000u)))
+                                .get(ra, rb);
+                            lo[j] = pack_bf16x2(ra, rb);
                         }
                         tmem_st16(tmem_s + 32 * (i + k), hi);
                         tmem_st16(tmem_s + 32 * (i + k) + 16, lo);
@@ -669,7 +692,9 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
                     }
                 }
                 tmem_wait_ld32(x[0]); // the last prefetch, of no use
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                float even, odd;
+                add2(sum[0], sum[1]).get(even, odd);
+                l += even + odd;
                 tmem_wait_st();
             } else if (lane == 0) {
                 mbar_arrive(&s.p_half[stream]);
