@@ -150,6 +150,14 @@ __device__ __forceinline__ uint64_t l2_evict_first_policy()
     return pol;
 }
 
+// The default L2 policy, for loads that name one.
+__device__ __forceinline__ uint64_t l2_evict_normal_policy()
+{
+    uint64_t pol;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+    return pol;
+}
+
 // Bulk (non-tensor) TMA copy global -> this CTA's shared memory, completing
 // `bytes` of transaction count on `bar`. Both addresses 16-byte aligned,
 // bytes a multiple of 16.

@@ -101,7 +101,7 @@ struct __align__(1024) TreeSmem {
     uint64_t bad_rows[4][2];
     uint32_t valid[kValidRing]; // pages inside the pool, a bit per 16 keys of a tile
     uint32_t tmem_base;
-    int start_b, start_h, start_tile, units; // this CTA's run
+    int start_b, start_h, start_tile, start_T, start_n, units; // this CTA's run
     int scan[kTreeThreads / 32];
     float2 ml[2][kTileRows]; // (m, l) of both streams
 };
@@ -139,16 +139,34 @@ __device__ __forceinline__ int tiles_of(const TreeParams &p, int b, int &T, int 
     return sequence(p, b, T, n) && n > 0 ? (T - 1) / kTileKeys + 1 : 0;
 }
 
+// CTA c's run of the `total` tiles: [first, first + result). Equal parts, the
+// first total % ctas CTAs one more; with fewer tiles than CTAs the first take
+// one each, so every CTA between a (sequence, head)'s first and last has a
+// piece of it.
+__device__ __forceinline__ int run_of(const TreeParams &p, int total, int c, int &first)
+{
+    const int part = total / p.ctas, more = total - part * p.ctas;
+    first = c * part + min(c, more);
+    return part + (c < more ? 1 : 0);
+}
+// The CTA whose run holds tile u.
+__device__ __forceinline__ int cta_of(const TreeParams &p, int total, int u)
+{
+    const int part = total / p.ctas, more = total - part * p.ctas;
+    const int head = more * (part + 1); // tiles of the CTAs with one more
+    return u < head ? u / (part + 1) : more + (u - head) / part;
+}
+
 // Walks a CTA's run of tiles, segment by segment (the tiles of one (sequence,
 // KV head)).
 struct Segments {
     int b, h, tile, left;      // next tile, tiles left in the run
     int T, n, tiles;           // sequence b
     int seg_tile0, seg_tile1;  // current segment
-    __device__ Segments(const TreeParams &p, const TreeSmem &s)
-        : b(s.start_b), h(s.start_h), tile(s.start_tile), left(s.units)
+    __device__ explicit Segments(const TreeSmem &s)
+        : b(s.start_b), h(s.start_h), tile(s.start_tile), left(s.units), T(s.start_T), n(s.start_n),
+          tiles((s.start_T - 1) / kTileKeys + 1)
     {
-        tiles = left > 0 ? tiles_of(p, b, T, n) : 0;
     }
     __device__ bool next(const TreeParams &p)
     {
@@ -183,7 +201,7 @@ struct Steps {
     int n;             // the current step
     bool pair, any;
     __device__ Steps(const TreeParams &p, const TreeSmem &s, int stream, bool pair)
-        : seg(p, s), stream(stream), index(-1), begin(0), end(0), n(0), pair(pair), any(true)
+        : seg(s), stream(stream), index(-1), begin(0), end(0), n(0), pair(pair), any(true)
     {
         advance(p);
     }
@@ -226,8 +244,9 @@ __device__ bool produce(const TreeParams &p, TreeSmem &s, const CUtensorMap *mq,
     const int box_keys = min(P, kTileKeys);
     const int boxes = kTileKeys / box_keys; // pages of a tile
     const int outside = static_cast<int>((static_cast<long long>(p.num_pages) * p.Hkv << p.log2_page) >> 3);
-    // K and V are read once per row group: with one group nothing reads them again
-    const uint64_t policy = l2_evict_first_policy();
+    // one row group reads K and V once; of several, running side by side, the
+    // first leaves them in L2 for the others
+    const uint64_t policy = p.row_groups == 1 ? l2_evict_first_policy() : l2_evict_normal_policy();
     int put = 0;
     uint32_t issued = 0, phases = 0; // per barrier (stream, slot): used, parity of its last load
     bool ok = true;
@@ -249,7 +268,7 @@ __device__ bool produce(const TreeParams &p, TreeSmem &s, const CUtensorMap *mq,
     };
     const int ahead = pair ? 1 : 2; // tiles of K requested before the V of the first of them
     int group1 = 0, group2 = 0;     // this lane's page of the last tile and of the one before
-    Segments seg(p, s);
+    Segments seg(s);
     int unit = 0;
     for (int index = 0; ok && seg.next(p); ++index) {
         const int32_t *table = p.block_table + static_cast<size_t>(seg.b) * p.max_pages;
@@ -373,7 +392,7 @@ __device__ bool multiply(const TreeParams &p, TreeSmem &s, bool pair, int stream
     Steps su(p, s, stream, pair), pu(p, s, stream, pair); // of the next score product and of the next product with V
     // the first round issues only the first scores
     for (bool started = false; ok && (pu.any || !started); started = true) {
-        if (started) { // O += P V; P lies in S's place, for each 32 keys 16 columns hi and 16 lo
+        if (started) { // O += P V; P lies in S's place, for each 16 keys 8 columns hi and 8 lo
             const int n = pu.n;
             const int slot = ring_v(pair, pu.unit(), N) % kSlots;
             unsigned char *v = s.slots[slot];
@@ -398,7 +417,7 @@ __device__ bool multiply(const TreeParams &p, TreeSmem &s, bool pair, int stream
                     for (int k = 0; k < 4; ++k)
 #pragma unroll
                         for (int part = 0; part < 2; ++part) // 16 keys: hi, then lo
-                            tc_mma_ts(tmem_s + (kColO - kColS), tmem_s + half * 64 + (k >> 1) * 32 + part * 16 + (k & 1) * 8,
+                            tc_mma_ts(tmem_s + (kColO - kColS), tmem_s + half * 64 + k * 16 + part * 8,
                                       va + (half * 4 + k) * (4096 / 16), tc_desc_high(2048), idesc_o,
                                       half > 0 || part > 0 || k > 0 ? 1u : keep);
                 }
@@ -474,58 +493,57 @@ __device__ __forceinline__ uint32_t visible_word(int below, uint64_t mask, uint3
     return bits & (((valid & 1u) ? 0xFFFFu : 0u) | ((valid & 2u) ? 0xFFFF0000u : 0u));
 }
 
-// 32 scores of a row from key `key` on, transformed (kScore bit 0: tanh cap,
-// bit 1: distance bias) and, if `masked`, hidden keys set to -inf; returns the
-// largest. far0: distance of the first key if it lies in the prefix; pos_lo and
-// pos_hi: this lane's drafted tokens' positions (lane, lane + 32).
-template <int kScore>
-__device__ __forceinline__ float prepare_scores(const TreeParams &p, float *x, int key, float slope, float far0, int pos,
-                                                int prefix, int n, int pos_lo, int pos_hi, bool masked, uint64_t mask,
-                                                uint32_t valid)
+// a - b as a float for any two int32 (by halves: the difference of 64-bit
+// integers would go through this GPU's slow 64-bit conversion).
+__device__ __forceinline__ float distance(int a, int b)
 {
-    if constexpr (kScore != 0) {
-        const bool drafted = masked && key + 32 > prefix && key < prefix + n;
+    return fmaf(2.f, static_cast<float>((a >> 1) - (b >> 1)), static_cast<float>((a & 1) - (b & 1)));
+}
+
+// 16 scores of a row, capped (kScore bit 0) or scaled, in base 2; with `linear`
+// (bit 1) the bias of keys whose positions are their slots, far0 the first
+// one's distance.
+template <int kScore>
+__device__ __forceinline__ void prepare_scores(const TreeParams &p, float *x, float slope, float far0)
+{
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-            f32x2 y(x[j], x[j + 1]);
-            if constexpr ((kScore & 1) != 0) { // c tanh(u) = c - 2 c / (1 + e^2u)
-                float a, b;
-                mul2(y, f32x2(p.cap_in, p.cap_in)).get(a, b);
-                add2(f32x2(ex2(a), ex2(b)), f32x2(1.f, 1.f)).get(a, b);
-                y = fma2(f32x2(rcp(a), rcp(b)), f32x2(-2.f * p.cap_out, -2.f * p.cap_out), f32x2(p.cap_out, p.cap_out));
-            } else {
-                y = mul2(y, f32x2(p.c, p.c));
-            }
-            if constexpr ((kScore & 2) != 0)
-                if (!drafted)
-                    y = fma2(f32x2(slope, slope), add2(f32x2(far0, far0), f32x2(j, j + 1)), y);
-            y.get(x[j], x[j + 1]);
+    for (int j = 0; j < 16; j += 2) {
+        f32x2 y(x[j], x[j + 1]);
+        if constexpr ((kScore & 1) != 0) { // c tanh(u) = c - 2 c / (1 + e^2u)
+            float a, b;
+            mul2(y, f32x2(p.cap_in, p.cap_in)).get(a, b);
+            add2(f32x2(ex2(a), ex2(b)), f32x2(1.f, 1.f)).get(a, b);
+            y = fma2(f32x2(rcp(a), rcp(b)), f32x2(-2.f * p.cap_out, -2.f * p.cap_out), f32x2(p.cap_out, p.cap_out));
+        } else {
+            y = mul2(y, f32x2(p.c, p.c));
         }
         if constexpr ((kScore & 2) != 0)
-            if (drafted) { // drafted tokens have positions of their own
+            y = fma2(f32x2(slope, slope), add2(f32x2(far0, far0), f32x2(j, j + 1)), y);
+        y.get(x[j], x[j + 1]);
+    }
+}
+
+// Lane q of each group of four gets the others' fourth q: o[4 i + j] of lane q
+// becomes o[4 q + j] of lane i.
+__device__ __forceinline__ void transpose4(float *o)
+{
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const int d = key + j - prefix;
-                    float far = far0 + static_cast<float>(j);
-                    if (d >= 0 && d < n) {
-                        const int kpos = __shfl_sync(0xFFFFFFFFu, d < 32 ? pos_lo : pos_hi, d & 31);
-                        far = static_cast<float>(static_cast<long long>(kpos) - pos);
-                    }
-                    x[j] = fmaf(slope, far, x[j]);
+    for (int bit = 1; bit < 4; bit <<= 1) {
+        const bool odd = lane & bit;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (!(k & bit)) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? o[4 * k + j] : o[4 * (k | bit) + j], bit);
+                    if (odd)
+                        o[4 * k + j] = got;
+                    else
+                        o[4 * (k | bit) + j] = got;
                 }
             }
     }
-    if (masked) {
-        const uint32_t bits = visible_word(prefix - key, mask, valid);
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            x[j] = (bits >> j) & 1u ? x[j] : -INFINITY;
-    }
-    float top[2] = {x[0], x[1]};
-#pragma unroll
-    for (int j = 2; j < 32; j += 2)
-        top[j >> 1 & 1] = max3(top[j >> 1 & 1], x[j], x[j + 1]);
-    return fmaxf(top[0], top[1]);
 }
 
 template <int kScore>
@@ -542,7 +560,7 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
     const bool warp_works = __any_sync(0xFFFFFFFFu, real);
     const float c = kScore ? 1.f : p.c;
 
-    Segments seg(p, s);
+    Segments seg(s);
     int step = 0; // the run's next step, of either stream
     bool ok = true;
     for (int index = 0; ok && seg.next(p); ++index) {
@@ -585,41 +603,70 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
                 const int key0 = tile * kTileKeys;
                 const uint32_t valid = s.valid[unit % kValidRing];
                 const bool tail = key0 + kTileKeys > prefix;
+                const bool fix = tail || valid != 0xFFu;
                 float high = -INFINITY;
-                if (kScore == 0 && !tail && valid == 0xFFu) {
-                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                if constexpr (kScore != 0) { // scores are transformed in place
+                    float far = distance(key0, pos);
+                    float y[2][16];
+                    tmem_ld16(y[0], tmem_s);
+#pragma unroll 1
+                    for (int i = 0; i < 8; i += 2) {
 #pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            tmem_wait_ld16(y[k]);
+                            tmem_ld16(y[k ^ 1], tmem_s + 16 * ((i + k + 1) & 7));
+                            // keys from the prefix's end on get their bias below
+                            prepare_scores<kScore>(p, y[k], 16 * (i + k + 1) <= prefix - key0 ? slope : 0.f, far);
+                            far += 16.f;
+                            tmem_st16(tmem_s + 16 * (i + k), y[k]);
+#pragma unroll
+                            for (int j = 0; j < 16; j += 2)
+                                high = max3(high, y[k][j], y[k][j + 1]);
+                        }
+                    }
+                    tmem_wait_ld16(y[0]); // the last prefetch, of no use
+                    tmem_wait_st();
+                }
+                if (fix) { // hidden keys become -inf; drafted tokens' bias goes by their own positions
+                    const int whole_chunks = max(0, prefix - key0) >> 4; // of 16 keys, in the prefix
+#pragma unroll 1
+                    for (int i = valid != 0xFFu ? 0 : 2 * whole_chunks; i < 16; ++i) {
+                        float y[8];
+                        const int key = key0 + 8 * i;
+                        const uint32_t bits = visible_word(prefix - key, mask, valid >> (i >> 1));
+                        tmem_ld8(y, tmem_s + 8 * i);
+                        tmem_wait_ld8(y);
+                        const float line = i >= 2 * whole_chunks ? slope : 0.f;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            if constexpr ((kScore & 2) != 0) {
+                                const int d = key + j - prefix;
+                                const int drafted = __shfl_sync(0xFFFFFFFFu, d < 32 ? pos_lo : pos_hi, d & 31);
+                                y[j] = fmaf(line, distance(d < 0 ? key + j : drafted, pos), y[j]);
+                            }
+                            y[j] = (bits >> j) & 1u ? y[j] : -INFINITY;
+                        }
+                        tmem_st8(tmem_s + 8 * i, y);
+                    }
+                    tmem_wait_st();
+                }
+                if (kScore == 0 || fix) {
+                    high = -INFINITY;
+                    float x[2][32];
+#pragma unroll 1
                     for (int i = 0; i < 2; ++i) {
-                        float x[2][32];
                         tmem_ld32(x[0], tmem_s + 64 * i);
                         tmem_ld32(x[1], tmem_s + 64 * i + 32);
                         tmem_wait_ld32(x[0]);
                         tmem_wait_ld32(x[1]);
+                        float tops[2] = {x[0][0], x[1][0]};
 #pragma unroll
-                        for (int j = 0; j < 64; j += 2)
-                            top[j >> 1 & 3] = max3(top[j >> 1 & 3], x[j >> 5][j & 31], x[j >> 5][(j & 31) + 1]);
-                    }
-                    high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                } else {
-                    // scores are transformed and hidden keys marked in place
-                    const float far0 = static_cast<float>(static_cast<long long>(key0) - pos);
-                    float x[2][32];
-                    tmem_ld32(x[0], tmem_s);
-#pragma unroll 1
-                    for (int i = 0; i < 4; i += 2) {
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            tmem_wait_ld32(x[k]);
-                            tmem_ld32(x[k ^ 1], tmem_s + 32 * ((i + k + 1) & 3));
-                            const float y = prepare_scores<kScore>(p, x[k], key0 + 32 * (i + k), slope,
-                                                                   far0 + 32 * (i + k), pos, prefix, seg.n, pos_lo, pos_hi,
-                                                                   tail || valid != 0xFFu, mask, valid >> (2 * (i + k)));
-                            tmem_st32(tmem_s + 32 * (i + k), x[k]);
-                            high = fmaxf(high, y);
+                        for (int j = 1; j < 31; j += 2) {
+                            tops[0] = max3(tops[0], x[0][j], x[0][j + 1]);
+                            tops[1] = max3(tops[1], x[1][j], x[1][j + 1]);
                         }
+                        high = max3(high, fmaxf(tops[0], x[0][31]), fmaxf(tops[1], x[1][31]));
                     }
-                    tmem_wait_ld32(x[0]); // the last prefetch, of no use
-                    tmem_wait_st();
                 }
                 // move the reference where the row has none yet, or its scores left its range
                 const bool move = fresh ? true : (m == -INFINITY ? high > -INFINITY : (high - m) * c > kRescaleLog2);
@@ -632,14 +679,14 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
                         l *= f;
                         const uint32_t o = s.tmem_base + lanes + kColO + stream * 128;
 #pragma unroll 1
-                        for (int i = 0; i < 4; ++i) {
-                            float acc[32];
-                            tmem_ld32(acc, o + 32 * i);
-                            tmem_wait_ld32(acc);
+                        for (int i = 0; i < 8; ++i) {
+                            float acc[16];
+                            tmem_ld16(acc, o + 16 * i);
+                            tmem_wait_ld16(acc);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
+                            for (int j = 0; j < 16; ++j)
                                 acc[j] *= f;
-                            tmem_st32(o + 32 * i, acc);
+                            tmem_st16(o + 16 * i, acc);
                         }
                     }
                 }
@@ -649,41 +696,40 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
                 const bool large = kScore == 0 && fabsf(ref) > 65536.f;
                 const float shift = large ? m : 0.f, neg_ref = large ? 0.f : -ref;
                 const bool any_large = __any_sync(0xFFFFFFFFu, large);
-                f32x2 sum[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
-                float x[2][32];
-                tmem_ld32(x[0], tmem_s);
+                f32x2 sum(0.f, 0.f);
+                float x[2][16];
+                tmem_ld16(x[0], tmem_s);
 #pragma unroll 1
-                for (int i = 0; i < 4; i += 2) {
+                for (int i = 0; i < 8; i += 2) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        tmem_wait_ld32(x[k]);
-                        tmem_ld32(x[k ^ 1], tmem_s + 32 * ((i + k + 1) & 3));
+                        tmem_wait_ld16(x[k]);
+                        tmem_ld16(x[k ^ 1], tmem_s + 16 * ((i + k + 1) & 7));
                         if (any_large) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
+                            for (int j = 0; j < 16; ++j)
                                 x[k][j] -= shift;
                         }
-                        uint32_t hi[16], lo[16];
+                        float w[16]; // 8 columns hi, 8 columns lo
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
+                        for (int j = 0; j < 8; ++j) {
                             float a, b;
                             fma2(f32x2(x[k][2 * j], x[k][2 * j + 1]), f32x2(c, c), f32x2(neg_ref, neg_ref)).get(a, b);
                             a = ex2(a), b = ex2(b);
-                            const f32x2 w(a, b);
-                            sum[j & 1] = add2(sum[j & 1], w);
+                            const f32x2 ab(a, b);
+                            sum = add2(sum, ab);
                             // hi: the upper 16 bits as they are; lo: the exact rest, rounded
                             const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-                            hi[j] = __byte_perm(ua, ub, 0x7632);
+                            w[j] = __uint_as_float(__byte_perm(ua, ub, 0x7632));
                             float ra, rb;
-                            add2(w, f32x2(__uint_as_float((ua & 0xFFFF0000u) ^ 0x80000000u),
-                                          __uint_as_float((ub & 0xFFFF0000u) ^ 0x80000000u)))
+                            add2(ab, f32x2(__uint_as_float((ua & 0xFFFF0000u) ^ 0x80000000u),
+                                           __uint_as_float((ub & 0xFFFF0000u) ^ 0x80000000u)))
                                 .get(ra, rb);
-                            lo[j] = pack_bf16x2(ra, rb);
+                            w[8 + j] = __uint_as_float(pack_bf16x2(ra, rb));
                         }
-                        tmem_st16(tmem_s + 32 * (i + k), hi);
-                        tmem_st16(tmem_s + 32 * (i + k) + 16, lo);
+                        tmem_st16(tmem_s + 16 * (i + k), w);
                     }
-                    if (i == 0) { // half of P: its product can start
+                    if (i == 2) { // half of P: its product can start
                         tmem_wait_st();
                         tc_fence_before();
                         __syncwarp();
@@ -691,9 +737,9 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
                             mbar_arrive(&s.p_half[stream]);
                     }
                 }
-                tmem_wait_ld32(x[0]); // the last prefetch, of no use
                 float even, odd;
-                add2(sum[0], sum[1]).get(even, odd);
+                tmem_wait_ld16(x[0]); // the last prefetch, of no use
+                sum.get(even, odd);
                 l += even + odd;
                 tmem_wait_st();
             } else if (lane == 0) {
@@ -736,97 +782,89 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
         const uint64_t bad = (s.bad_rows[index & 3][0] | s.bad_rows[index & 3][1]) & mask;
         const bool whole = seg.seg_tile0 == 0 && seg.seg_tile1 == seg.tiles;
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const size_t out_row = (static_cast<size_t>(seg.b) * p.M + token) * p.Hq + head;
+        const uint32_t out_row = (static_cast<uint32_t>(seg.b) * p.M + token) * p.Hq + head;
+        const uint32_t live_rows = __ballot_sync(0xFFFFFFFFu, live);
         const size_t rec = static_cast<size_t>(2 * cta + (seg.seg_tile0 > 0 ? 0 : 1)) * p.rec_rows +
-                           (pair ? stream * kTileRows : 0) + row;
-        const int halves = pair ? 2 : 1;
-        for (int i = 0; i < halves; ++i) {
-            const int col = pair ? 64 * i : 64 * stream;
-            float o[64];
-            if (warp_works) {
-                const uint32_t base = s.tmem_base + lanes + kColO + col;
-                tmem_ld32(o, base + stream * 128);
-                tmem_ld32(o + 32, base + stream * 128 + 32);
+                           (pair ? stream * kTileRows : 0) + (warp & 3) * 32; // this warp's first row
+        // 16 columns at a time: all 128 of the stream's row tile, or 64 of the joined streams
+        const int col0 = pair ? 0 : 64 * stream, columns = pair ? 128 : 64;
+        const uint32_t tmem_o = s.tmem_base + lanes + kColO;
+        if (warp_works) {
+#pragma unroll 1
+            for (int col = col0; col < col0 + columns; col += 16) {
+                float o[16];
+                tmem_ld16(o, tmem_o + stream * 128 + col);
                 if (!pair) {
-                    float o2[64];
-                    tmem_ld32(o2, base + (stream ^ 1) * 128);
-                    tmem_ld32(o2 + 32, base + (stream ^ 1) * 128 + 32);
-                    tmem_wait_ld32(o), tmem_wait_ld32(o + 32), tmem_wait_ld32(o2), tmem_wait_ld32(o2 + 32);
+                    float o2[16];
+                    tmem_ld16(o2, tmem_o + (stream ^ 1) * 128 + col);
+                    tmem_wait_ld16(o), tmem_wait_ld16(o2);
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) { // a stream without a visible key may hold anything
+                    for (int j = 0; j < 16; ++j) { // a stream without a visible key may hold anything
                         const float a = w_own == 0.f ? 0.f : o[j] * w_own;
                         o[j] = w_other == 0.f ? a : fmaf(o2[j], w_other, a);
                     }
                 } else {
-                    tmem_wait_ld32(o), tmem_wait_ld32(o + 32);
-                    if (w_own == 0.f) {
+                    tmem_wait_ld16(o);
 #pragma unroll
-                        for (int j = 0; j < 64; ++j)
-                            o[j] = 0.f;
-                    }
+                    for (int j = 0; j < 16; ++j)
+                        o[j] = w_own == 0.f ? 0.f : o[j];
                 }
-            }
-            if (i == halves - 1) {
-                tc_fence_before();
-                if (!pair) {
-                    // neither stream's O may be overwritten before both warpgroups have it
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(&s.epi_done);
-                    ok = warp_wait(&s.epi_done, index & 1);
-                }
-            }
-            if (live && ok) {
-                if (bad) {
+                if (live) {
                     // V elements left out of the products because they are not finite
                     for (uint64_t rest = bad; rest; rest &= rest - 1) {
                         const int slot = prefix + __ffsll(static_cast<long long>(rest)) - 1;
                         const int tile = slot / kTileKeys;
-                        if (tile < seg.seg_tile0 || tile >= seg.seg_tile1)
-                            continue;
                         const int phys = p.block_table[static_cast<size_t>(seg.b) * p.max_pages + (slot >> p.log2_page)];
-                        if (phys < 0 || phys >= p.num_pages)
+                        if (tile < seg.seg_tile0 || tile >= seg.seg_tile1 || phys < 0 || phys >= p.num_pages)
                             continue;
-                        const uint16_t *v =
-                            p.v + ((((static_cast<size_t>(phys) * p.Hkv + seg.h) << p.log2_page) +
-                                    (slot & ((1 << p.log2_page) - 1))) *
-                                       kHeadDim +
-                                   col);
+                        const uint16_t *v = p.v + ((((static_cast<size_t>(phys) * p.Hkv + seg.h) << p.log2_page) +
+                                                    (slot & ((1 << p.log2_page) - 1))) *
+                                                       kHeadDim +
+                                                   col);
 #pragma unroll
-                        for (int j = 0; j < 64; ++j)
+                        for (int j = 0; j < 16; ++j)
                             if ((v[j] & 0x7F80u) == 0x7F80u)
                                 o[j] += __uint_as_float(static_cast<uint32_t>(v[j]) << 16);
                     }
                 }
                 if (whole) {
 #pragma unroll
-                    for (int j = 0; j < 64; ++j)
-                        o[j] *= inv;
-                    if (p.out_f32) {
-                        float4 *dst = reinterpret_cast<float4 *>(p.out_f32 + out_row * kHeadDim + col);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-                    }
-                    if (p.out_bf16) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(p.out_bf16 + out_row * kHeadDim + col);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            dst[j] = make_uint4(pack_bf16x2(o[8 * j], o[8 * j + 1]), pack_bf16x2(o[8 * j + 2], o[8 * j + 3]),
-                                                pack_bf16x2(o[8 * j + 4], o[8 * j + 5]),
-                                                pack_bf16x2(o[8 * j + 6], o[8 * j + 7]));
-                    }
-                } else {
-                    float4 *dst = reinterpret_cast<float4 *>(p.rec_acc + rec * kHeadDim + col);
-#pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-                    if (col == 0) {
-                        p.rec_m[rec] = top;
-                        p.rec_l[rec] = l;
+                        o[j] *= inv;
+                }
+                // 4 x 4 transpose in groups of four lanes: lane q gets columns
+                // 4q .. 4q+3 of the group's rows, and a store covers 64 bytes
+                // of each of 8 rows instead of 16 bytes of each of 32
+                transpose4(o);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int from = (lane & ~3) + i;
+                    const uint32_t row_i = __shfl_sync(0xFFFFFFFFu, out_row, from);
+                    if (live_rows >> from & 1u) {
+                        const int c = col + 4 * (lane & 3);
+                        const float4 v = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        if (!whole)
+                            *reinterpret_cast<float4 *>(p.rec_acc + (rec + from) * kHeadDim + c) = v;
+                        if (whole && p.out_f32)
+                            *reinterpret_cast<float4 *>(p.out_f32 + static_cast<size_t>(row_i) * kHeadDim + c) = v;
+                        if (whole && p.out_bf16)
+                            *reinterpret_cast<uint2 *>(p.out_bf16 + static_cast<size_t>(row_i) * kHeadDim + c) =
+                                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
                     }
                 }
+                __syncwarp();
             }
+            if (live && !whole && (pair || stream == 0)) {
+                p.rec_m[rec + lane] = top;
+                p.rec_l[rec + lane] = l;
+            }
+        }
+        if (!pair) { // neither stream's O may be overwritten before both warpgroups have it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&s.epi_done);
+            ok = warp_wait(&s.epi_done, index & 1);
         }
     }
     return ok;
@@ -883,32 +921,37 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     before -= mine;
     __syncthreads();
     int total = 0;
+#pragma unroll
     for (int w = 0; w < kTreeThreads / 32; ++w) {
         if (w < warp)
             before += s.scan[w];
         total += s.scan[w];
     }
-    // with fewer tiles than CTAs the first `total` take one each: every CTA
-    // between a (sequence, head)'s first and last then holds a piece of it
-    const int ctas = min(p.ctas, max(total, 1));
-    const int u0 = static_cast<int>(static_cast<long long>(total) * min(cta, ctas) / ctas);
-    const int u1 = static_cast<int>(static_cast<long long>(total) * min(cta + 1, ctas) / ctas);
+    int u0;
+    const int units = run_of(p, total, cta, u0);
     if (tid == 0)
-        s.units = u1 - u0;
+        s.units = units;
     if (mine > 0 && u0 >= before && u0 < before + mine) {
-        int b = b0, at = before;
-        for (int t; at + (t = tiles_of(p, b, T, n) * p.Hkv) <= u0; ++b)
-            at += t;
-        const int tiles = tiles_of(p, b, T, n);
+        int b = b0, at = before, tiles = mine / p.Hkv; // of one head of sequence b
+        if (per > 1)
+            for (; at + (tiles = tiles_of(p, b, T, n)) * p.Hkv <= u0; ++b)
+                at += tiles * p.Hkv;
         s.start_b = b;
         s.start_h = (u0 - at) / tiles;
-        s.start_tile = (u0 - at) % tiles;
+        s.start_tile = u0 - at - s.start_h * tiles;
+        s.start_T = T;
+        s.start_n = n;
     }
     if (blockIdx.x == 0) { // for the merge
-        int at = before;
-        for (int b = b0; b < b1; ++b) {
-            p.unit_base[b] = at;
-            at += tiles_of(p, b, T, n) * p.Hkv;
+        if (per == 1) {
+            if (b0 < b1)
+                p.unit_base[b0] = before;
+        } else {
+            int at = before;
+            for (int b = b0; b < b1; ++b) {
+                p.unit_base[b] = at;
+                at += tiles_of(p, b, T, n) * p.Hkv;
+            }
         }
         if (tid == 0)
             p.unit_base[p.B] = total;
@@ -940,34 +983,38 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         tmem_free_all(s.tmem_base);
 }
 
-// Joins the pieces of every (sequence, KV head) that several CTAs worked on,
-// one warp per query row, pieces in the order of their keys:
+// Joins the pieces of every (sequence, KV head) that several CTAs worked on:
 //   top = max m_k, out = sum acc_k 2^(m_k - top) / sum l_k 2^(m_k - top).
-// Rows of sequences whose lengths make no sense become zeros here.
+// A row belongs to a group of four warps; warp w takes pieces w, w + 4, .. in
+// order (each with all its loads in flight at once), and the four sums are
+// added in order. What bounds it is latency: two trips to memory after the
+// lengths. Rows of sequences whose lengths make no sense become zeros here.
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeParams p)
 {
     allow_dependent_launch();
     grid_dependency_wait();
-    const int lane = threadIdx.x & 31;
-    const int r = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
+    __shared__ float4 sums[kMergeThreads];
+    __shared__ float sum_l[kMergeThreads / 32];
+    constexpr int kRows = kMergeThreads / 128;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp & 3;
+    const int r = blockIdx.x * kRows + (warp >> 2);
     const int h = blockIdx.y, b = blockIdx.z;
-    if (r >= p.M * p.g)
-        return;
     const int token = r / p.g;
-    const size_t out_row = (static_cast<size_t>(b) * p.M + token) * p.Hq + h * p.g + r % p.g;
     int T, n;
+    const int base = p.unit_base[b], total = p.unit_base[p.B];
+    const bool good = sequence(p, b, T, n);
+    const int tiles = (T - 1) / kTileKeys + 1;
+    int c0 = 0, c1 = 0;
+    if (good && n > 0) {
+        c0 = cta_of(p, total, base + h * tiles);
+        c1 = cta_of(p, total, base + (h + 1) * tiles - 1);
+    }
+    if (good && c0 == c1) // nothing to join (the same for the whole block)
+        return;
+    const bool live = r < p.M * p.g && (!good || token < n);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (sequence(p, b, T, n)) {
-        if (token >= n)
-            return;
-        const int tiles = (T - 1) / kTileKeys + 1;
-        const long long u0 = p.unit_base[b] + h * tiles, u1 = u0 + tiles - 1, total = p.unit_base[p.B];
-        // the CTA of tile u: the c with floor(total c / ctas) <= u < floor(total (c + 1) / ctas)
-        const long long ctas = total < p.ctas ? total : p.ctas;
-        const int c0 = static_cast<int>(((u0 + 1) * ctas - 1) / total);
-        const int c1 = static_cast<int>(((u1 + 1) * ctas - 1) / total);
-        if (c0 == c1)
-            return;
+    float l = 0.f;
+    if (good && live) {
         const int row_tile = token / p.tile_tokens, rg = row_tile >> 1;
         const int rec_row = (row_tile & 1) * kTileRows + r - row_tile * p.tile_tokens * p.g;
         // piece k is CTA c0 + k's: its last segment for the first piece, its first for the others
@@ -975,39 +1022,59 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
             return (static_cast<size_t>(c0 + k) * p.row_groups + rg) * 2 * p.rec_rows + (k == 0 ? p.rec_rows : 0) + rec_row;
         };
         const int pieces = c1 - c0 + 1;
-        float top = -INFINITY;
-        for (int k = lane; k < pieces; k += 32)
-            if (p.rec_l[record(k)] != 0.f)
-                top = fmaxf(top, p.rec_m[record(k)]);
+        constexpr int kFlight = 8; // this warp's pieces in flight
+        for (int first = 0; first < pieces; first += 32) { // (one round for up to 32 pieces)
+            float4 v[kFlight];
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
-        float l = 0.f;
-        for (int first = 0; first < pieces; first += 32) {
-            float w = 0.f, piece_l = 0.f;
-            if (first + lane < pieces) {
-                piece_l = p.rec_l[record(first + lane)];
-                w = piece_l == 0.f ? 0.f : ex2(p.rec_m[record(first + lane)] - top);
+            for (int i = 0; i < kFlight; ++i) {
+                const int k = first + 4 * i + part;
+                if (k < pieces)
+                    v[i] = reinterpret_cast<const float4 *>(p.rec_acc + record(k) * kHeadDim)[lane];
             }
-            const int count = min(32, pieces - first);
-#pragma unroll 4
-            for (int k = 0; k < count; ++k) {
-                const float wk = __shfl_sync(0xFFFFFFFFu, w, k), lk = __shfl_sync(0xFFFFFFFFu, piece_l, k);
-                const float4 v = reinterpret_cast<const float4 *>(p.rec_acc + record(first + k) * kHeadDim)[lane];
-                if (lk != 0.f) {
-                    l = fmaf(lk, wk, l);
-                    acc.x = fmaf(v.x, wk, acc.x);
-                    acc.y = fmaf(v.y, wk, acc.y);
-                    acc.z = fmaf(v.z, wk, acc.z);
-                    acc.w = fmaf(v.w, wk, acc.w);
+            // the reference over all pieces, the same in all four warps
+            float top = -INFINITY;
+            for (int k = lane; k < pieces; k += 32) {
+                const float m = p.rec_m[record(k)], piece_l = p.rec_l[record(k)];
+                top = piece_l == 0.f ? top : fmaxf(top, m);
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+            const int mine = first + 4 * lane + part; // lane i holds piece i of this warp
+            float w = 0.f, piece_l = 0.f;
+            if (lane < kFlight && mine < pieces) {
+                piece_l = p.rec_l[record(mine)];
+                w = piece_l == 0.f ? 0.f : ex2(p.rec_m[record(mine)] - top);
+            }
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) {
+                const float wi = __shfl_sync(0xFFFFFFFFu, w, i), li = __shfl_sync(0xFFFFFFFFu, piece_l, i);
+                if (li != 0.f) { // a piece without a visible key counts for nothing
+                    l = fmaf(li, wi, l);
+                    acc.x = fmaf(v[i].x, wi, acc.x);
+                    acc.y = fmaf(v[i].y, wi, acc.y);
+                    acc.z = fmaf(v[i].z, wi, acc.z);
+                    acc.w = fmaf(v[i].w, wi, acc.w);
                 }
             }
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    } else if (r == 0 && h == 0 && lane == 0) {
-        atomicOr(&g_flags_tree, PGQA_DEVERR_BAD_CONTEXT);
     }
+    if (!good && r == 0 && h == 0 && threadIdx.x == 0)
+        atomicOr(&g_flags_tree, PGQA_DEVERR_BAD_CONTEXT);
+    sums[threadIdx.x] = acc;
+    if (lane == 0)
+        sum_l[warp] = l;
+    __syncthreads();
+    if (!live || part != 0)
+        return;
+    for (int i = 1; i < 4; ++i) {
+        const float4 v = sums[threadIdx.x + 32 * i];
+        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+        l += sum_l[warp + i];
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    const size_t out_row = (static_cast<size_t>(b) * p.M + token) * p.Hq + h * p.g + r % p.g;
     if (p.out_f32)
         reinterpret_cast<float4 *>(p.out_f32 + out_row * kHeadDim)[lane] = acc;
     if (p.out_bf16)
@@ -1161,7 +1228,7 @@ cudaError_t launch_tree_attn(const TreeAttnArgs &a, cudaStream_t stream)
     }
     if (err != cudaSuccess)
         return err;
-    const dim3 grid(static_cast<unsigned>((a.M * p.g + kMergeThreads / 32 - 1) / (kMergeThreads / 32)),
+    const dim3 grid(static_cast<unsigned>((a.M * p.g + kMergeThreads / 128 - 1) / (kMergeThreads / 128)),
                     static_cast<unsigned>(a.Hkv), static_cast<unsigned>(a.B));
     return launch_pdl(tree_merge_kernel, grid, dim3(kMergeThreads), 0, stream, p);
 }
