@@ -175,6 +175,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const float *r)
                  : "memory");
 }
 
+__device__ __forceinline__ float lds_f32(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.volatile.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 // Two fp32 operations in one instruction (packed pairs).
 struct f32x2 {
     uint64_t bits;

@@ -103,6 +103,7 @@ struct __align__(1024) TreeSmem {
     uint32_t tmem_base;
     int start_b, start_h, start_tile, start_T, start_n, units; // this CTA's run
     int scan[kTreeThreads / 32];
+    float zero;
     float2 ml[2][kTileRows]; // (m, l) of both streams
 };
 constexpr int kTreeSmem = sizeof(TreeSmem);
@@ -604,7 +605,6 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
                 const uint32_t valid = s.valid[unit % kValidRing];
                 const bool tail = key0 + kTileKeys > prefix;
                 const bool fix = tail || valid != 0xFFu;
-                float high = -INFINITY;
                 if constexpr (kScore != 0) { // scores are transformed in place
                     float far = distance(key0, pos);
                     float y[2][16];
@@ -619,9 +619,6 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
                             prepare_scores<kScore>(p, y[k], 16 * (i + k + 1) <= prefix - key0 ? slope : 0.f, far);
                             far += 16.f;
                             tmem_st16(tmem_s + 16 * (i + k), y[k]);
-#pragma unroll
-                            for (int j = 0; j < 16; j += 2)
-                                high = max3(high, y[k][j], y[k][j + 1]);
                         }
                     }
                     tmem_wait_ld16(y[0]); // the last prefetch, of no use
@@ -650,24 +647,18 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
                     }
                     tmem_wait_st();
                 }
-                if (kScore == 0 || fix) {
-                    high = -INFINITY;
-                    float x[2][32];
-#pragma unroll 1
-                    for (int i = 0; i < 2; ++i) {
-                        tmem_ld32(x[0], tmem_s + 64 * i);
-                        tmem_ld32(x[1], tmem_s + 64 * i + 32);
-                        tmem_wait_ld32(x[0]);
-                        tmem_wait_ld32(x[1]);
-                        float tops[2] = {x[0][0], x[1][0]};
+                float x[kTileKeys];
 #pragma unroll
-                        for (int j = 1; j < 31; j += 2) {
-                            tops[0] = max3(tops[0], x[0][j], x[0][j + 1]);
-                            tops[1] = max3(tops[1], x[1][j], x[1][j + 1]);
-                        }
-                        high = max3(high, fmaxf(tops[0], x[0][31]), fmaxf(tops[1], x[1][31]));
-                    }
-                }
+                for (int i = 0; i < 8; ++i)
+                    tmem_ld16(x + 16 * i, tmem_s + 16 * i);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    tmem_wait_ld16(x + 16 * i);
+                float tops[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                for (int j = 4; j < kTileKeys; j += 2)
+                    tops[j >> 1 & 3] = max3(tops[j >> 1 & 3], x[j], x[j + 1]);
+                const float high = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                 // move the reference where the row has none yet, or its scores left its range
                 const bool move = fresh ? true : (m == -INFINITY ? high > -INFINITY : (high - m) * c > kRescaleLog2);
                 if (__any_sync(0xFFFFFFFFu, move)) {
@@ -696,49 +687,45 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
                 const bool large = kScore == 0 && fabsf(ref) > 65536.f;
                 const float shift = large ? m : 0.f, neg_ref = large ? 0.f : -ref;
                 const bool any_large = __any_sync(0xFFFFFFFFu, large);
+                if (any_large) {
+#pragma unroll
+                    for (int j = 0; j < kTileKeys; ++j)
+                        x[j] -= shift;
+                }
                 f32x2 sum(0.f, 0.f);
-                float x[2][16];
-                tmem_ld16(x[0], tmem_s);
-#pragma unroll 1
-                for (int i = 0; i < 8; i += 2) {
+                float offset = neg_ref;
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        tmem_wait_ld16(x[k]);
-                        tmem_ld16(x[k ^ 1], tmem_s + 16 * ((i + k + 1) & 7));
-                        if (any_large) {
+                for (int i = 0; i < 8; ++i) {
+                    float w[16]; // 8 columns hi, 8 columns lo
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                x[k][j] -= shift;
-                        }
-                        float w[16]; // 8 columns hi, 8 columns lo
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            float a, b;
-                            fma2(f32x2(x[k][2 * j], x[k][2 * j + 1]), f32x2(c, c), f32x2(neg_ref, neg_ref)).get(a, b);
-                            a = ex2(a), b = ex2(b);
-                            const f32x2 ab(a, b);
-                            sum = add2(sum, ab);
-                            // hi: the upper 16 bits as they are; lo: the exact rest, rounded
-                            const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-                            w[j] = __uint_as_float(__byte_perm(ua, ub, 0x7632));
-                            float ra, rb;
-                            add2(ab, f32x2(__uint_as_float((ua & 0xFFFF0000u) ^ 0x80000000u),
-                                           __uint_as_float((ub & 0xFFFF0000u) ^ 0x80000000u)))
-                                .get(ra, rb);
-                            w[8 + j] = __uint_as_float(pack_bf16x2(ra, rb));
-                        }
-                        tmem_st16(tmem_s + 16 * (i + k), w);
+                    for (int j = 0; j < 8; ++j) {
+                        float a, b;
+                        fma2(f32x2(x[16 * i + 2 * j], x[16 * i + 2 * j + 1]), f32x2(c, c), f32x2(offset, offset)).get(a, b);
+                        a = ex2(a), b = ex2(b);
+                        const f32x2 ab(a, b);
+                        sum = add2(sum, ab);
+                        // hi: the upper 16 bits as they are; lo: the exact rest, rounded
+                        const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+                        w[j] = __uint_as_float(__byte_perm(ua, ub, 0x7632));
+                        float ra, rb;
+                        add2(ab, f32x2(__uint_as_float((ua & 0xFFFF0000u) ^ 0x80000000u),
+                                       __uint_as_float((ub & 0xFFFF0000u) ^ 0x80000000u)))
+                            .get(ra, rb);
+                        w[8 + j] = __uint_as_float(pack_bf16x2(ra, rb));
                     }
-                    if (i == 2) { // half of P: its product can start
+                    tmem_st16(tmem_s + 16 * i, w);
+                    if (i == 3) { // half of P: its product can start
                         tmem_wait_st();
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0)
                             mbar_arrive(&s.p_half[stream]);
+                        // a zero read after the arrival: the second half's work
+                        // depends on it and so stays behind it
+                        offset += lds_f32(smem_addr(&s.zero));
                     }
                 }
                 float even, odd;
-                tmem_wait_ld16(x[0]); // the last prefetch, of no use
                 sum.get(even, odd);
                 l += even + odd;
                 tmem_wait_st();
@@ -930,7 +917,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     int u0;
     const int units = run_of(p, total, cta, u0);
     if (tid == 0)
-        s.units = units;
+        s.units = units, s.zero = 0.f;
     if (mine > 0 && u0 >= before && u0 < before + mine) {
         int b = b0, at = before, tiles = mine / p.Hkv; // of one head of sequence b
         if (per > 1)
@@ -961,7 +948,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     tc_fence_after();
 
     // Registers move from the third warpgroup to the softmax, whose threads
-    // hold 128 scores: 256 * 208 + 128 * 72 <= 384 * 168 as launched.
+    // hold 128 scores: 256 * 216 + 128 * 72 = 384 * 168 as launched.
     bool ok = true;
     if (warp >= kProducerWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -970,7 +957,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         else if (warp <= kMmaWarp + 1 && s.units > 0)
             ok = multiply(p, s, pair, warp - kMmaWarp);
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         if (s.units > 0)
             ok = soften<kScore>(p, s, rg, pair, blockIdx.x);
     }
