@@ -529,19 +529,25 @@ def decode_attn_paged_static(q, k_cache, v_cache, block_table, context_lens, sca
 
 
 # ---------------------------------------------------------------- drafted-tree decoding
-def _shape(t, shape, name):
-    """Refuse a tensor (None passes) whose shape is not `shape`."""
-    if t is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+# These calls take many small tensors and are short on the GPU, so a tensor is
+# checked in one expression and its faults are spelled out only when it fails.
+def _arg(t, dtype, shape, name, device):
+    """The address of a contiguous tensor of this dtype and shape on the current device (its index)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device
+            and t.is_contiguous()):
+        _dev(t, dtype, name)
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
+    return t.data_ptr()
 
 
-def _on_one_device(**tensors):
-    """Refuse tensors that lie on different devices, or not on the current one
-    (the kernels run there)."""
-    here = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != here:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
+def _opt(t, dtype, shape, name, device):
+    return None if t is None else _arg(t, dtype, shape, name, device)
+
+
+def _raw_stream(stream, device):
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
 def qk_norm_rope_append_axes(q, k, v, gamma_q, gamma_k, positions, context_lens, block_table, k_cache, v_cache, q_out,
@@ -550,29 +556,24 @@ def qk_norm_rope_append_axes(q, k, v, gamma_q, gamma_k, positions, context_lens,
     int32 [B, M, n_axes]. axis_of_pair: 64 axis numbers, one per frequency pair (for sections of s_0, s_1, ...
     pairs: [0] * s_0 + [1] * s_1 + ...). new_lens int32 [B]: how many of a sequence's M tokens exist."""
     lib = load_library()
-    bf, i32 = torch.bfloat16, torch.int32
+    bf, i32, here = torch.bfloat16, torch.int32, torch.cuda.current_device()
     B, M, Hq, D = q.shape
-    Hkv = k.shape[2]
-    num_pages, _, P, _ = k_cache.shape
-    n_axes = positions.shape[-1]
-    _shape(k, (B, M, Hkv, D), "k"), _shape(v, (B, M, Hkv, D), "v"), _shape(q_out, q.shape, "q_out")
-    _shape(gamma_q, (D,), "gamma_q"), _shape(gamma_k, (D,), "gamma_k")
-    _shape(positions, (B, M, n_axes), "positions"), _shape(context_lens, (B,), "context_lens")
-    _shape(new_lens, (B,), "new_lens"), _shape(block_table, (B, block_table.shape[-1]), "block_table")
-    _shape(k_cache, (num_pages, Hkv, P, D), "k_cache"), _shape(v_cache, (num_pages, Hkv, P, D), "v_cache")
-    axes = bytes(bytearray(axis_of_pair))
+    num_pages, Hkv, P, _ = k_cache.shape
+    max_pages, n_axes = block_table.shape[-1], positions.shape[-1]
+    axes = bytes(axis_of_pair)
     if len(axes) != 64:
         raise ValueError(f"axis_of_pair must hold 64 axis numbers, got {len(axes)}")
-    _on_one_device(q=q, k=k, v=v, gamma_q=gamma_q, gamma_k=gamma_k, positions=positions, context_lens=context_lens,
-                   block_table=block_table, k_cache=k_cache, v_cache=v_cache, q_out=q_out, new_lens=new_lens)
+    new, cache = (B, M, Hkv, D), (num_pages, Hkv, P, D)
     st = lib.qk_norm_rope_append_axes(
-        _dev(q, bf, "q"), _dev(k, bf, "k"), _dev(v, bf, "v"), _dev(gamma_q, bf, "gamma_q"),
-        _dev(gamma_k, bf, "gamma_k"), _dev(positions, i32, "positions"), n_axes, axes,
-        _dev(context_lens, i32, "context_lens"), _dev(new_lens, i32, "new_lens", nullable=True),
-        _dev(block_table, i32, "block_table"), _dev(k_cache, bf, "k_cache"), _dev(v_cache, bf, "v_cache"),
-        _dev(q_out, bf, "q_out"), B, M, Hq, Hkv, D, P, block_table.shape[1], num_pages, float(rope_theta),
-        float(eps), _stream(stream))
-    _check("qk_norm_rope_append_axes", st)
+        _arg(q, bf, q.shape, "q", here), _arg(k, bf, new, "k", here), _arg(v, bf, new, "v", here),
+        _arg(gamma_q, bf, (D,), "gamma_q", here), _arg(gamma_k, bf, (D,), "gamma_k", here),
+        _arg(positions, i32, (B, M, n_axes), "positions", here), n_axes, axes,
+        _arg(context_lens, i32, (B,), "context_lens", here), _opt(new_lens, i32, (B,), "new_lens", here),
+        _arg(block_table, i32, (B, max_pages), "block_table", here), _arg(k_cache, bf, cache, "k_cache", here),
+        _arg(v_cache, bf, cache, "v_cache", here), _arg(q_out, bf, q.shape, "q_out", here), B, M, Hq, Hkv, D, P,
+        max_pages, num_pages, float(rope_theta), float(eps), _raw_stream(stream, here))
+    if st:
+        _check("qk_norm_rope_append_axes", st)
 
 
 def decode_attn_tree_workspace_size(B: int, M: int, Hq: int, Hkv: int, D: int, page_size: int, max_pages: int) -> int:
@@ -586,27 +587,21 @@ def decode_attn_paged_tree(q, k_cache, v_cache, block_table, context_lens, tree_
     [B, M] (bit j of entry i: token i sees drafted token j); positions int32 [B, M] and slopes float32 [Hq]
     for the distance bias; draft_lens int32 [B] where a sequence has fewer than M tokens."""
     lib = load_library()
-    bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    bf, i32, f32, here = torch.bfloat16, torch.int32, torch.float32, torch.cuda.current_device()
     B, M, Hq, D = q.shape
-    num_pages, Hkv, P, _ = k_cache.shape
-    _shape(k_cache, (num_pages, Hkv, P, D), "k_cache"), _shape(v_cache, k_cache.shape, "v_cache")
-    _shape(block_table, (B, block_table.shape[-1]), "block_table"), _shape(context_lens, (B,), "context_lens")
-    _shape(tree_mask, (B, M), "tree_mask"), _shape(positions, (B, M), "positions")
-    _shape(draft_lens, (B,), "draft_lens"), _shape(slopes, (Hq,), "slopes")
-    _shape(out_f32, q.shape, "out_f32"), _shape(out_bf16, q.shape, "out_bf16")
-    _on_one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, context_lens=context_lens,
-                   tree_mask=tree_mask, positions=positions, draft_lens=draft_lens, slopes=slopes, out_f32=out_f32,
-                   out_bf16=out_bf16, workspace=workspace)
-    ws_ptr = _dev(workspace, torch.uint8, "workspace", nullable=True)
+    num_pages, Hkv, P, _ = cache = k_cache.shape
+    max_pages = block_table.shape[-1]
     ws_bytes = workspace.numel() if workspace is not None else 0
     st = lib.decode_attn_paged_tree(
-        _dev(q, bf, "q"), _dev(k_cache, bf, "k_cache"), _dev(v_cache, bf, "v_cache"),
-        _dev(block_table, i32, "block_table"), _dev(context_lens, i32, "context_lens"),
-        _dev(tree_mask, torch.int64, "tree_mask"), _dev(positions, i32, "positions", nullable=True),
-        _dev(draft_lens, i32, "draft_lens", nullable=True), _dev(slopes, f32, "slopes", nullable=True), B, M, Hq, Hkv,
-        D, P, block_table.shape[1], num_pages, float(scale), float(softcap), _dev(out_f32, f32, "out_f32", nullable=True),
-        _dev(out_bf16, bf, "out_bf16", nullable=True), ws_ptr, ws_bytes, _stream(stream))
-    _check("decode_attn_paged_tree", st)
+        _arg(q, bf, q.shape, "q", here), _arg(k_cache, bf, (num_pages, Hkv, P, D), "k_cache", here),
+        _arg(v_cache, bf, cache, "v_cache", here), _arg(block_table, i32, (B, max_pages), "block_table", here),
+        _arg(context_lens, i32, (B,), "context_lens", here), _arg(tree_mask, torch.int64, (B, M), "tree_mask", here),
+        _opt(positions, i32, (B, M), "positions", here), _opt(draft_lens, i32, (B,), "draft_lens", here),
+        _opt(slopes, f32, (Hq,), "slopes", here), B, M, Hq, Hkv, D, P, max_pages, num_pages, float(scale), float(softcap),
+        _opt(out_f32, f32, q.shape, "out_f32", here), _opt(out_bf16, bf, q.shape, "out_bf16", here),
+        _opt(workspace, torch.uint8, (ws_bytes,), "workspace", here), ws_bytes, _raw_stream(stream, here))
+    if st:
+        _check("decode_attn_paged_tree", st)
 
 
 class CacheLayers:
@@ -621,16 +616,11 @@ class CacheLayers:
         self.num_pages, self.Hkv, self.page_size, self.D = k_caches[0].shape
         self.B, self.max_pages = block_tables[0].shape
         self.device = k_caches[0].device
-        for i in range(n):
-            _shape(k_caches[i], k_caches[0].shape, f"k_caches[{i}]")
-            _shape(v_caches[i], k_caches[0].shape, f"v_caches[{i}]")
-            _shape(block_tables[i], block_tables[0].shape, f"block_tables[{i}]")
-            if not k_caches[i].device == v_caches[i].device == block_tables[i].device == self.device:
-                raise ValueError(f"layer {i} is not on {self.device}")
-        array = ctypes.c_void_p * n
-        self.k_ptrs = array(*[_dev(t, bf, "k_cache") for t in k_caches])
-        self.v_ptrs = array(*[_dev(t, bf, "v_cache") for t in v_caches])
-        self.table_ptrs = array(*[_dev(t, i32, "block_table") for t in block_tables])
+        array, here = ctypes.c_void_p * n, self.device.index
+        cache, table = k_caches[0].shape, block_tables[0].shape
+        self.k_ptrs = array(*[_arg(t, bf, cache, f"k_caches[{i}]", here) for i, t in enumerate(k_caches)])
+        self.v_ptrs = array(*[_arg(t, bf, cache, f"v_caches[{i}]", here) for i, t in enumerate(v_caches)])
+        self.table_ptrs = array(*[_arg(t, i32, table, f"block_tables[{i}]", here) for i, t in enumerate(block_tables)])
         self.tensors = (list(k_caches), list(v_caches), list(block_tables))
 
     def __len__(self) -> int:
@@ -643,17 +633,16 @@ def kv_cache_commit_path(layers: CacheLayers, context_lens, path, path_lens, con
     layer's K and V cache, and context_lens_out[b] = prefix + path_lens[b]. path int32 [B, A]; M is the
     number of drafted tokens per sequence that context_lens counts (draft_lens int32 [B] where it varies)."""
     lib = load_library()
-    i32 = torch.int32
+    i32, here = torch.int32, torch.cuda.current_device()
     B, A = path.shape
     if B != layers.B:
         raise ValueError(f"path has {B} sequences, the layers' block tables {layers.B}")
-    _shape(context_lens, (B,), "context_lens"), _shape(path_lens, (B,), "path_lens")
-    _shape(context_lens_out, (B,), "context_lens_out"), _shape(draft_lens, (B,), "draft_lens")
-    _on_one_device(caches=layers.tensors[0][0], context_lens=context_lens, path=path, path_lens=path_lens,
-                   context_lens_out=context_lens_out, draft_lens=draft_lens)
+    if layers.device.index != here:
+        raise ValueError(f"the layers are on {layers.device}, the current device is cuda:{here}")
     st = lib.kv_cache_commit_path(
-        layers.k_ptrs, layers.v_ptrs, layers.table_ptrs, len(layers), _dev(context_lens, i32, "context_lens"),
-        _dev(draft_lens, i32, "draft_lens", nullable=True), _dev(path, i32, "path"), _dev(path_lens, i32, "path_lens"),
-        _dev(context_lens_out, i32, "context_lens_out"), B, int(M), A, layers.Hkv, layers.D, layers.page_size,
-        layers.max_pages, layers.num_pages, _stream(stream))
-    _check("kv_cache_commit_path", st)
+        layers.k_ptrs, layers.v_ptrs, layers.table_ptrs, len(layers), _arg(context_lens, i32, (B,), "context_lens", here),
+        _opt(draft_lens, i32, (B,), "draft_lens", here), _arg(path, i32, (B, A), "path", here),
+        _arg(path_lens, i32, (B,), "path_lens", here), _arg(context_lens_out, i32, (B,), "context_lens_out", here), B, M,
+        A, layers.Hkv, layers.D, layers.page_size, layers.max_pages, layers.num_pages, _raw_stream(stream, here))
+    if st:
+        _check("kv_cache_commit_path", st)

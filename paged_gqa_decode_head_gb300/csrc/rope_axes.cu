@@ -163,10 +163,20 @@ __global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(const __grid_co
 
 cudaError_t launch_rope_axes(const RopeAxesArgs &a, cudaStream_t stream)
 {
+    // 64 powers cost more than a launch, and a model has one theta: the thread
+    // keeps the table of the last one.
+    static thread_local double table_theta = 0.0; // no valid theta
+    static thread_local uint64_t table[kPairs];
+    if (table_theta != a.rope_theta) {
+        for (int r = 0; r < kPairs; ++r) {
+            const double turns = std::pow(a.rope_theta, -2.0 * r / kHeadDim) / 6.283185307179586476925;
+            table[r] = static_cast<uint64_t>(std::ldexp(turns - std::floor(turns), 64));
+        }
+        table_theta = a.rope_theta;
+    }
     RopeAxesParams p{};
     for (int r = 0; r < kPairs; ++r) {
-        const double turns = std::pow(a.rope_theta, -2.0 * r / kHeadDim) / 6.283185307179586476925;
-        p.turn[r] = static_cast<uint64_t>(std::ldexp(turns - std::floor(turns), 64));
+        p.turn[r] = table[r];
         p.axis_bits[r >> 5] |= static_cast<uint64_t>(a.axis_of_pair[r] & 3) << (2 * (r & 31));
     }
     p.q = a.q;

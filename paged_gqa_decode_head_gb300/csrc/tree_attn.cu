@@ -95,6 +95,7 @@ struct __align__(1024) TreeSmem {
     uint64_t full[2][kSlots], empty[kSlots];
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], p_half[2], p_ready[2];
+    uint64_t round_done[2]; // a stream's products of a step, and its next scores, are issued
     uint64_t seg_done, ml_ready, epi_done, drain[2];
     // drafted tokens of a stream's tiles of a segment whose V row is not finite
     // (with two row tiles a stream may be two segments ahead of the other's readers)
@@ -206,9 +207,14 @@ struct Steps {
     {
         advance(p);
     }
-    __device__ void advance(const TreeParams &p)
+    __device__ __forceinline__ void advance(const TreeParams &p)
     {
         n += 2;
+        if (n >= end)
+            enter(p);
+    }
+    __device__ __forceinline__ void enter(const TreeParams &p)
+    {
         while (any && n >= end) {
             any = seg.next(p);
             if (!any)
@@ -226,15 +232,6 @@ struct Steps {
     // the segment has a single step: its stream signals for the other one too
     __device__ bool alone() const { return end - begin == 1; }
 };
-
-// Position in the ring of unit u's K and V tile, of N units. Two row tiles
-// (pair): K0 V0 K1 V1 ...; one row tile, whose scores run two tiles ahead of
-// its products with V: K0 K1 V0 K2 V1 K3 ...
-__device__ __forceinline__ int ring_k(bool pair, int u) { return pair ? 2 * u : (u < 2 ? u : 2 * u - 1); }
-__device__ __forceinline__ int ring_v(bool pair, int u, int N)
-{
-    return pair ? 2 * u + 1 : (u == N - 1 ? 2 * N - 1 : 2 * u + 2);
-}
 
 // ---------------------------------------------------------------- producer
 __device__ bool produce(const TreeParams &p, TreeSmem &s, const CUtensorMap *mq, const CUtensorMap *mk,
@@ -384,6 +381,14 @@ __device__ bool multiply(const TreeParams &p, TreeSmem &s, bool pair, int stream
     uint64_t *full = s.full[pair ? 0 : stream];
     uint32_t phases = 0; // of `full`, a bit per slot
     bool ok = true;
+    // Order of the tiles in the ring. Two row tiles (pair): K0 V0 K1 V1 ...; one
+    // row tile, whose scores run two tiles ahead of its products with V: K0 K1
+    // V0 K2 V1 K3 ... K(N-1) V(N-2) V(N-1).
+    int k_slot = pair ? 0 : stream, v_slot = pair ? 1 : 2 + 2 * stream;
+    const auto move_on = [&](int &slot, int tiles) {
+        slot += tiles;
+        slot -= slot >= kSlots ? kSlots : 0;
+    };
     const auto landed = [&](int slot) {
         const bool yes = warp_wait(&full[slot], phases >> slot & 1u);
         phases ^= 1u << slot;
@@ -391,11 +396,26 @@ __device__ bool multiply(const TreeParams &p, TreeSmem &s, bool pair, int stream
     };
 
     Steps su(p, s, stream, pair), pu(p, s, stream, pair); // of the next score product and of the next product with V
+    // Every operand of a round is waited for before its first product where
+    // possible, so that the products follow each other without a gap.
+    bool k_there = false;
+    const auto wait_for_scores = [&] {
+        // K first: once it is there, the buffer's earlier Q was there too (a
+        // stream may have had no step in that segment), and the parity of
+        // q_full means this segment's Q
+        ok = ok && landed(k_slot);
+        if (su.first())
+            ok = ok && warp_wait(&s.q_full[pair ? 0 : su.index & 1], (pair ? su.index : su.index >> 1) & 1);
+        k_there = true;
+    };
     // the first round issues only the first scores
     for (bool started = false; ok && (pu.any || !started); started = true) {
         if (started) { // O += P V; P lies in S's place, for each 16 keys 8 columns hi and 8 lo
             const int n = pu.n;
-            const int slot = ring_v(pair, pu.unit(), N) % kSlots;
+            int slot = v_slot;
+            if (!pair && n == N - 1) // the last tile has no K between V and the V before
+                move_on(slot, kSlots - 1);
+            move_on(v_slot, pair ? 2 : 4);
             unsigned char *v = s.slots[slot];
             ok = landed(slot);
             if (!ok)
@@ -405,6 +425,12 @@ __device__ bool multiply(const TreeParams &p, TreeSmem &s, bool pair, int stream
             const int key0 = pu.tile() * kTileKeys;
             if (key0 + kTileKeys > pu.seg.T - pu.seg.n) // of two streams on one tile both do this: the same zeros
                 bad |= settle_v_tile(v, key0, pu.seg.T, pu.seg.n, box_keys);
+            if (su.any && !su.first())
+                wait_for_scores();
+            // The streams' products alternate: a stream's next scores go before
+            // the other's products with V, so that its softmax can start.
+            if (n > 0)
+                ok = ok && warp_wait(&s.round_done[stream ^ 1], ((n - 1) >> 1) & 1);
             const uint32_t va = warp_uniform(tc_desc_low(smem_addr(v), 1024));
             const uint32_t keep = warp_uniform(!pu.first()); // a segment's first product overwrites O
 #pragma unroll
@@ -415,12 +441,10 @@ __device__ bool multiply(const TreeParams &p, TreeSmem &s, bool pair, int stream
                 tc_fence_after();
                 if (leader) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int part = 0; part < 2; ++part) // 16 keys: hi, then lo
-                            tc_mma_ts(tmem_s + (kColO - kColS), tmem_s + half * 64 + k * 16 + part * 8,
-                                      va + (half * 4 + k) * (4096 / 16), tc_desc_high(2048), idesc_o,
-                                      half > 0 || part > 0 || k > 0 ? 1u : keep);
+                    for (int k = 0; k < 8; ++k) // 16 keys: hi, then lo
+                        tc_mma_ts(tmem_s + (kColO - kColS), tmem_s + half * 64 + k * 8,
+                                  va + (half * 4 + (k >> 1)) * (4096 / 16), tc_desc_high(2048), idesc_o,
+                                  half > 0 || k > 0 ? 1u : keep);
                 }
             }
             if (!ok)
@@ -438,21 +462,16 @@ __device__ bool multiply(const TreeParams &p, TreeSmem &s, bool pair, int stream
                     mbar_arrive(&s.seg_done); // orders bad_rows before its readers
                 }
             }
-            __syncwarp();
-            pu.advance(p);
         }
         if (su.any) { // S = Q K^T over the place of the P that was just used
-            const int slot = ring_k(pair, su.unit()) % kSlots;
-            const int buf = pair ? 0 : su.index & 1;
-            // K first: once it is there, the buffer's earlier Q was there too
-            // (a stream may have had no step in that segment), and the parity
-            // of q_full means this segment's Q
-            ok = landed(slot);
-            if (su.first())
-                ok = ok && warp_wait(&s.q_full[buf], (pair ? su.index : su.index >> 1) & 1);
+            if (!k_there)
+                wait_for_scores();
+            k_there = false;
             if (!ok)
                 break;
             tc_fence_after();
+            const int slot = k_slot;
+            const int buf = pair ? 0 : su.index & 1;
             const uint32_t qa = warp_uniform(tc_desc_low(smem_addr(s.q[pair ? stream : buf]), 16));
             const uint32_t ka = warp_uniform(tc_desc_low(smem_addr(s.slots[slot]), 16));
             if (leader) {
@@ -464,6 +483,8 @@ __device__ bool multiply(const TreeParams &p, TreeSmem &s, bool pair, int stream
                 }
                 tc_commit(&s.s_full[stream]);
                 mbar_arrive(&s.s_full[stream]); // orders the page mask's write before its readers
+                if (started)
+                    mbar_arrive(&s.round_done[stream]);
                 tc_commit(&s.empty[slot]);
                 if (su.last()) {
                     tc_commit(&s.q_empty[buf]);
@@ -472,8 +493,14 @@ __device__ bool multiply(const TreeParams &p, TreeSmem &s, bool pair, int stream
                 }
             }
             __syncwarp();
+            move_on(k_slot, pair ? 2 : (su.n == 0 ? 3 : 4));
             su.advance(p);
+        } else if (started && leader) {
+            mbar_arrive(&s.round_done[stream]);
         }
+        __syncwarp();
+        if (started)
+            pu.advance(p);
     }
     // no product may still be running when the CTA ends
     if (leader)
@@ -593,10 +620,6 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
             const int tile = seg.seg_tile0 + ((n - step) >> (pair ? 1 : 0));
             const int unit = pair ? n >> 1 : n;
             ok = warp_wait(&s.s_full[stream], (n >> 1) & 1);
-            // The streams take turns: one starts its softmax when the other has
-            // half of P, so that one's products run under the other's softmax.
-            if (n > 0)
-                ok = ok && warp_wait(&s.p_half[stream ^ 1], ((n - 1) >> 1) & 1);
             if (!ok)
                 break;
             tc_fence_after();
@@ -877,6 +900,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             mbar_init(&s.q_full[i], 1), mbar_init(&s.q_empty[i], 2);
             mbar_init(&s.drain[i], 1);
             mbar_init(&s.s_full[i], 2);  // the products' completion, and the issuing thread
+            mbar_init(&s.round_done[i], 1);
             mbar_init(&s.p_half[i], 4); // one arrival per warp of the stream
             mbar_init(&s.p_ready[i], 4);
         }
