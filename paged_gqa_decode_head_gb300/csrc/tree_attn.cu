@@ -123,10 +123,20 @@ __device__ __forceinline__ float rcp(float x)
     return y;
 }
 
-// A bounded wait by a whole warp, with one answer for all its lanes.
+// A bounded wait by a whole warp, with one answer for all its lanes. The limit
+// is counted in SM clocks (some 200 ms): reading %globaltimer between two tries
+// takes about as long as a tile's scores.
+constexpr long long kWaitLimitClocks = 400ll * 1000 * 1000;
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity)
 {
-    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity));
+    bool there = mbar_try_wait(bar, parity);
+    if (!there) {
+        const long long start = clock64();
+        do
+            there = mbar_try_wait(bar, parity);
+        while (!there && clock64() - start < kWaitLimitClocks);
+    }
+    return __all_sync(0xFFFFFFFFu, there);
 }
 
 // Sequence b's length and drafted tokens; false if they make no sense.
@@ -528,14 +538,14 @@ __device__ __forceinline__ float distance(int a, int b)
     return fmaf(2.f, static_cast<float>((a >> 1) - (b >> 1)), static_cast<float>((a & 1) - (b & 1)));
 }
 
-// 16 scores of a row, capped (kScore bit 0) or scaled, in base 2; with `linear`
-// (bit 1) the bias of keys whose positions are their slots, far0 the first
-// one's distance.
-template <int kScore>
+// N scores of a row, capped (kScore bit 0) or scaled, in base 2, with the bias
+// (bit 1) of keys whose positions are their slots; far0: the first one's
+// distance.
+template <int kScore, int N>
 __device__ __forceinline__ void prepare_scores(const TreeParams &p, float *x, float slope, float far0)
 {
 #pragma unroll
-    for (int j = 0; j < 16; j += 2) {
+    for (int j = 0; j < N; j += 2) {
         f32x2 y(x[j], x[j + 1]);
         if constexpr ((kScore & 1) != 0) { // c tanh(u) = c - 2 c / (1 + e^2u)
             float a, b;
@@ -588,30 +598,41 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
     const bool warp_works = __any_sync(0xFFFFFFFFu, real);
     const float c = kScore ? 1.f : p.c;
 
-    Segments seg(s);
-    int step = 0; // the run's next step, of either stream
-    bool ok = true;
-    for (int index = 0; ok && seg.next(p); ++index) {
-        const int prefix = seg.T - seg.n;
-        const int head = seg.h * p.g + row % p.g;
-        uint64_t mask = 0;
-        float slope = 0.f;
-        int pos = 0, pos_lo = 0, pos_hi = 0;
-        const bool live = real && token < seg.n;
-        if (live) {
-            mask = p.tree_mask[static_cast<size_t>(seg.b) * p.M + token];
-            if (seg.n < 64)
-                mask &= (1ull << seg.n) - 1ull;
+    // What a row brings into a segment; the next segment's is fetched while this
+    // one's last products run.
+    struct Row {
+        uint64_t mask;
+        float slope;
+        int pos, pos_lo, pos_hi; // its position; this lane's drafted tokens' (lane, lane + 32)
+        bool live;
+    };
+    const auto fetch_row = [&](const Segments &of) {
+        Row r{0, 0.f, 0, 0, 0, real && token < of.n};
+        if (r.live) {
+            r.mask = p.tree_mask[static_cast<size_t>(of.b) * p.M + token];
             if constexpr ((kScore & 2) != 0) {
-                slope = p.slopes[head] * kLog2e;
-                pos = p.positions[static_cast<size_t>(seg.b) * p.M + token];
+                r.slope = p.slopes[of.h * p.g + row % p.g] * kLog2e;
+                r.pos = p.positions[static_cast<size_t>(of.b) * p.M + token];
             }
         }
         if constexpr ((kScore & 2) != 0) {
-            const int32_t *at = p.positions + static_cast<size_t>(seg.b) * p.M;
-            pos_lo = lane < seg.n ? at[lane] : 0;
-            pos_hi = lane + 32 < seg.n ? at[lane + 32] : 0;
+            const int32_t *at = p.positions + static_cast<size_t>(of.b) * p.M;
+            r.pos_lo = lane < of.n ? at[lane] : 0;
+            r.pos_hi = lane + 32 < of.n ? at[lane + 32] : 0;
         }
+        return r;
+    };
+    Segments seg(s);
+    bool more = seg.next(p);
+    Row next_row = fetch_row(seg);
+    int step = 0; // the run's next step, of either stream
+    bool ok = true;
+    for (int index = 0; ok && more; ++index) {
+        const int prefix = seg.T - seg.n;
+        const bool live = next_row.live;
+        const uint64_t mask = seg.n < 64 ? next_row.mask & ((1ull << seg.n) - 1ull) : next_row.mask;
+        const float slope = next_row.slope;
+        const int pos = next_row.pos, pos_lo = next_row.pos_lo, pos_hi = next_row.pos_hi;
         const int seg_steps = (seg.seg_tile1 - seg.seg_tile0) * (pair ? 2 : 1);
         float m = -INFINITY; // the reference, in units of 1 / c
         float l = 0.f;
@@ -628,48 +649,30 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
                 const uint32_t valid = s.valid[unit % kValidRing];
                 const bool tail = key0 + kTileKeys > prefix;
                 const bool fix = tail || valid != 0xFFu;
-                if constexpr (kScore != 0) { // scores are transformed in place
-                    float far = distance(key0, pos);
-                    float y[2][16];
-                    tmem_ld16(y[0], tmem_s);
+                // Biased scores of a tile with drafted tokens, whose positions are
+                // their own: once per segment, in tensor memory, 16 keys at a time.
+                const bool drafted = (kScore & 2) != 0 && tail;
+                if constexpr ((kScore & 2) != 0)
+                    if (drafted) {
 #pragma unroll 1
-                    for (int i = 0; i < 8; i += 2) {
+                        for (int key = key0; key < key0 + kTileKeys; key += 16) {
+                            float y[16];
+                            tmem_ld16(y, tmem_s + (key - key0));
+                            tmem_wait_ld16(y);
+                            const bool own = key + 16 > prefix && key < seg.T;
+                            prepare_scores<kScore, 16>(p, y, own ? 0.f : slope, distance(key, pos));
+                            if (own) {
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            tmem_wait_ld16(y[k]);
-                            tmem_ld16(y[k ^ 1], tmem_s + 16 * ((i + k + 1) & 7));
-                            // keys from the prefix's end on get their bias below
-                            prepare_scores<kScore>(p, y[k], 16 * (i + k + 1) <= prefix - key0 ? slope : 0.f, far);
-                            far += 16.f;
-                            tmem_st16(tmem_s + 16 * (i + k), y[k]);
-                        }
-                    }
-                    tmem_wait_ld16(y[0]); // the last prefetch, of no use
-                    tmem_wait_st();
-                }
-                if (fix) { // hidden keys become -inf; drafted tokens' bias goes by their own positions
-                    const int whole_chunks = max(0, prefix - key0) >> 4; // of 16 keys, in the prefix
-#pragma unroll 1
-                    for (int i = valid != 0xFFu ? 0 : 2 * whole_chunks; i < 16; ++i) {
-                        float y[8];
-                        const int key = key0 + 8 * i;
-                        const uint32_t bits = visible_word(prefix - key, mask, valid >> (i >> 1));
-                        tmem_ld8(y, tmem_s + 8 * i);
-                        tmem_wait_ld8(y);
-                        const float line = i >= 2 * whole_chunks ? slope : 0.f;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            if constexpr ((kScore & 2) != 0) {
-                                const int d = key + j - prefix;
-                                const int drafted = __shfl_sync(0xFFFFFFFFu, d < 32 ? pos_lo : pos_hi, d & 31);
-                                y[j] = fmaf(line, distance(d < 0 ? key + j : drafted, pos), y[j]);
+                                for (int j = 0; j < 16; ++j) {
+                                    const int d = key + j - prefix;
+                                    const int at = __shfl_sync(0xFFFFFFFFu, d < 32 ? pos_lo : pos_hi, d & 31);
+                                    y[j] = fmaf(slope, distance(d < 0 ? key + j : at, pos), y[j]);
+                                }
                             }
-                            y[j] = (bits >> j) & 1u ? y[j] : -INFINITY;
+                            tmem_st16(tmem_s + (key - key0), y);
                         }
-                        tmem_st8(tmem_s + 8 * i, y);
+                        tmem_wait_st();
                     }
-                    tmem_wait_st();
-                }
                 float x[kTileKeys];
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
@@ -677,6 +680,18 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     tmem_wait_ld16(x + 16 * i);
+                if constexpr (kScore != 0)
+                    if (!drafted)
+                        prepare_scores<kScore, kTileKeys>(p, x, slope, distance(key0, pos));
+                if (fix) { // hidden keys
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t bits = visible_word(prefix - key0 - 32 * w, mask, valid >> (2 * w));
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            x[32 * w + j] = (bits >> j) & 1u ? x[32 * w + j] : -INFINITY;
+                    }
+                }
                 float tops[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
                 for (int j = 4; j < kTileKeys; j += 2)
@@ -765,6 +780,11 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
         if (!ok)
             break;
 
+        Segments following = seg;
+        more = following.next(p);
+        if (more)
+            next_row = fetch_row(following);
+
         // ---- the end of the segment: O of the last product, joined and written
         float w_own = 1.f, w_other = 0.f, top = m == -INFINITY ? -INFINITY : m * c;
         if (!pair) {
@@ -792,7 +812,7 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
         const uint64_t bad = (s.bad_rows[index & 3][0] | s.bad_rows[index & 3][1]) & mask;
         const bool whole = seg.seg_tile0 == 0 && seg.seg_tile1 == seg.tiles;
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const uint32_t out_row = (static_cast<uint32_t>(seg.b) * p.M + token) * p.Hq + head;
+        const uint32_t out_row = (static_cast<uint32_t>(seg.b) * p.M + token) * p.Hq + seg.h * p.g + row % p.g;
         const uint32_t live_rows = __ballot_sync(0xFFFFFFFFu, live);
         const size_t rec = static_cast<size_t>(2 * cta + (seg.seg_tile0 > 0 ? 0 : 1)) * p.rec_rows +
                            (pair ? stream * kTileRows : 0) + (warp & 3) * 32; // this warp's first row
@@ -876,6 +896,7 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
                 mbar_arrive(&s.epi_done);
             ok = warp_wait(&s.epi_done, index & 1);
         }
+        seg = following;
     }
     return ok;
 }
