@@ -1039,7 +1039,8 @@ int kv_cache_commit_path(pgqa_bf16 *const *k_caches, pgqa_bf16 *const *v_caches,
         overlap(path, static_cast<long long>(B) * A))
         return fail(PGQA_ERR_INVALID_ARG, "%s: context_lens_out overlaps another index array", fn);
     pgqa::CommitPathArgs a{k_caches, v_caches, block_tables, n_layers, context_lens, draft_lens, path, path_lens,
-                           context_lens_out, B, M, A, Hkv, page_size, max_pages, num_pages};
+                           context_lens_out, B, M, A, Hkv, page_size, max_pages, num_pages,
+                           sm_count_current_device()};
     cudaError_t err = pgqa::launch_commit_path(a, stream);
     if (err != cudaSuccess)
         return cuda_fail(err, fn);

@@ -169,6 +169,7 @@ struct CommitPathArgs {
     const int32_t *context_lens, *draft_lens, *path, *path_lens;
     int32_t *context_lens_out;
     int B, M, A, Hkv, page_size, max_pages, num_pages;
+    int sm_count;
 };
 cudaError_t launch_commit_path(const CommitPathArgs &a, cudaStream_t stream);
 cudaError_t read_flags_commit_path(unsigned *flags, bool clear);

@@ -12,13 +12,17 @@
 // fraction of its integer rate; one 64-bit integer product replaces the fp64
 // product and reduction.
 //
-// Bound: memory, (2 Hq + 4 Hkv) * 256 bytes a token read and written once. The
+// Bound: memory, (2 Hq + 4 Hkv) * 256 bytes a token, read and written once. The
 // single-token prologue (prologue.cu) recomputes the angles for every head; at
 // prompt lengths that would cost more than the copy, so here a block owns one
-// token, forms its 64 rotations once in shared memory, and its 16 groups of 8
-// lanes walk the token's Hq + 2 Hkv rows with 16-byte loads and stores (lane s
-// of a group holds dims 8s .. 8s+7 and 64 + 8s .. 64 + 8s + 7, so a pair's two
-// halves are in one lane).
+// or two tokens of a sequence, forms their rotations once in shared memory, and
+// its 16 groups of 8 lanes walk the tokens' Hq + 2 Hkv rows with 16-byte loads
+// and stores, two rows of a group on their way at a time (lane s of a group
+// holds dims 8s .. 8s+7 and 64 + 8s .. 64 + 8s + 7, so a pair's two halves are in
+// one lane). Measured (32 query, 8 KV heads): 32768 tokens 120 us, 6.69 TB/s, 99 %
+// of the measured copy bandwidth; ragged halves of that 71 us, 6.35 TB/s; 4095
+// tokens of 16 + 8 heads 14.5 us, 4.6 TB/s (its 2 waves of blocks start and end
+// unevenly); 16 tokens 3.1 us, a launch and three trips to memory.
 #include "common.cuh"
 #include "launch.h"
 
@@ -33,6 +37,7 @@ constexpr int kPairs = kHeadDim / 2;
 constexpr int kRopeThreads = 128;
 constexpr int kRowLanes = 8;                               // lanes that hold one head row
 constexpr int kRowsPerPass = kRopeThreads / kRowLanes;     // head rows a block handles at once
+constexpr int kInFlight = 2;                               // rows a group of lanes has on their way
 
 struct RopeAxesParams {
     uint64_t turn[kPairs];  // frac(omega_r / 2 pi) * 2^64
@@ -41,6 +46,7 @@ struct RopeAxesParams {
     const int32_t *positions, *context_lens, *new_lens, *block_table;
     uint16_t *k_cache, *v_cache, *q_out;
     int M, Hq, Hkv, n_axes, log2_page, max_pages, num_pages;
+    int blocks_per_seq;
     float eps;
 };
 
@@ -51,6 +57,8 @@ __device__ __forceinline__ uint4 pack8(const float *f)
                       pack_bf16x2(f[6], f[7]));
 }
 
+// kTokens consecutive tokens of one sequence per block.
+template <int kTokens>
 __global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(const __grid_constant__ RopeAxesParams p)
 {
     // Everything this kernel reads may come from the kernel before it, and
@@ -58,104 +66,128 @@ __global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(const __grid_co
     allow_dependent_launch();
     grid_dependency_wait();
     const int tid = threadIdx.x;
-    const int tok = blockIdx.x; // b * M + i
-    const int b = tok / p.M, i = tok - b * p.M;
+    const int b = blockIdx.x / p.blocks_per_seq, i0 = (blockIdx.x - b * p.blocks_per_seq) * kTokens;
     const int n = p.new_lens ? p.new_lens[b] : p.M;
     const int T = p.context_lens[b];
     if (n < 0 || n > p.M || T < n || T > (p.max_pages << p.log2_page)) {
-        if (i == 0 && tid == 0)
+        if (i0 == 0 && tid == 0)
             atomicOr(&g_flags_rope_axes, PGQA_DEVERR_BAD_CONTEXT);
         return;
     }
-    if (i >= n)
+    const int live = min(n - i0, kTokens);
+    if (live <= 0)
         return;
-    const int slot = T - n + i;
-    const int phys = p.block_table[static_cast<size_t>(b) * p.max_pages + (slot >> p.log2_page)];
-    const bool page_ok = phys >= 0 && phys < p.num_pages;
-    if (!page_ok && tid == 0)
-        atomicOr(&g_flags_rope_axes, PGQA_DEVERR_BAD_PAGE);
-
-    const int lane8 = tid & (kRowLanes - 1), row0 = tid / kRowLanes;
-    const int rows = p.Hq + 2 * p.Hkv; // Q heads, K heads, V heads
+    const size_t tok0 = static_cast<size_t>(b) * p.M + i0;
+    const int lane8 = tid & (kRowLanes - 1);
+    const int rows = p.Hq + 2 * p.Hkv; // of a token: Q heads, K heads, V heads
     const size_t P = size_t{1} << p.log2_page;
-    const size_t cell = static_cast<size_t>(phys) * p.Hkv * P + (slot & (P - 1)); // + head * P: the cache row
-    const auto load = [&](int row, uint4 &lo, uint4 &hi) {
+
+    // The block's rows, token by token; this thread's group takes every 16th.
+    struct At {
+        int t, row;
+    };
+    const auto step = [&](At &at) {
+        at.row += kRowsPerPass;
+        while (at.row >= rows)
+            at.row -= rows, ++at.t;
+    };
+    const auto load = [&](const At &at, uint4 &lo, uint4 &hi) {
+        const size_t tok = tok0 + at.t;
         const uint16_t *src;
-        if (row < p.Hq)
-            src = p.q + (static_cast<size_t>(tok) * p.Hq + row) * kHeadDim;
-        else if (row < p.Hq + p.Hkv)
-            src = p.k + (static_cast<size_t>(tok) * p.Hkv + row - p.Hq) * kHeadDim;
+        if (at.row < p.Hq)
+            src = p.q + (tok * p.Hq + at.row) * kHeadDim;
+        else if (at.row < p.Hq + p.Hkv)
+            src = p.k + (tok * p.Hkv + at.row - p.Hq) * kHeadDim;
         else
-            src = p.v + (static_cast<size_t>(tok) * p.Hkv + row - p.Hq - p.Hkv) * kHeadDim;
+            src = p.v + (tok * p.Hkv + at.row - p.Hq - p.Hkv) * kHeadDim;
         lo = *reinterpret_cast<const uint4 *>(src + 8 * lane8);
         hi = *reinterpret_cast<const uint4 *>(src + kPairs + 8 * lane8);
     };
-    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-    if (row0 < rows)
-        load(row0, lo, hi);
+    At at{0, tid / kRowLanes};
+    while (at.row >= rows)
+        at.row -= rows, ++at.t;
+    At ahead = at;
+    uint4 lo[kInFlight], hi[kInFlight];
+#pragma unroll
+    for (int k = 0; k < kInFlight; ++k) {
+        if (ahead.t < live)
+            load(ahead, lo[k], hi[k]);
+        step(ahead);
+    }
 
-    __shared__ __align__(16) float rot_cos[kPairs], rot_sin[kPairs];
-    if (tid < kPairs) {
-        const int axis = static_cast<int>(p.axis_bits[tid >> 5] >> (2 * (tid & 31))) & 3;
-        const int pos = p.positions[static_cast<size_t>(tok) * p.n_axes + axis];
-        const uint64_t frac = static_cast<uint64_t>(static_cast<int64_t>(pos)) * p.turn[tid];
+    __shared__ __align__(16) float rot_cos[kTokens][kPairs], rot_sin[kTokens][kPairs];
+    __shared__ long long cells[kTokens]; // cache row of the token's slot in KV head 0, -1: page outside the pool
+    for (int r = tid; r < live * kPairs; r += kRopeThreads) {
+        const int t = r / kPairs, pair = r % kPairs;
+        const int axis = static_cast<int>(p.axis_bits[pair >> 5] >> (2 * (pair & 31))) & 3;
+        const int pos = p.positions[(tok0 + t) * p.n_axes + axis];
+        const uint64_t frac = static_cast<uint64_t>(static_cast<int64_t>(pos)) * p.turn[pair];
         // the upper 32 bits as a signed part of a turn, in half turns
         const float half_turns = static_cast<float>(static_cast<int32_t>(frac >> 32)) * 0x1p-31f;
-        sincospif(half_turns, &rot_sin[tid], &rot_cos[tid]);
+        sincospif(half_turns, &rot_sin[t][pair], &rot_cos[t][pair]);
+    }
+    if (tid < live) {
+        const int slot = T - n + i0 + tid;
+        const int phys = p.block_table[static_cast<size_t>(b) * p.max_pages + (slot >> p.log2_page)];
+        const bool in_pool = phys >= 0 && phys < p.num_pages;
+        cells[tid] = in_pool ? static_cast<long long>(phys) * p.Hkv * P + (slot & (P - 1)) : -1;
+        if (!in_pool)
+            atomicOr(&g_flags_rope_axes, PGQA_DEVERR_BAD_PAGE);
     }
     __syncthreads();
-    float cs[8], sn[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        cs[j] = rot_cos[8 * lane8 + j];
-        sn[j] = rot_sin[8 * lane8 + j];
-    }
 
-    for (int base = 0; base < rows; base += kRowsPerPass) {
-        const int row = base + row0;
-        uint4 next_lo = make_uint4(0, 0, 0, 0), next_hi = next_lo;
-        if (row + kRowsPerPass < rows)
-            load(row + kRowsPerPass, next_lo, next_hi);
-        const bool is_q = row < p.Hq, is_v = row >= p.Hq + p.Hkv;
-        float a[8], c[8];
-        unpack8(lo, a);
-        unpack8(hi, c);
-        float ss = 0.f;
+    const int passes = (live * rows + kRowsPerPass - 1) / kRowsPerPass;
+    for (int pass = 0; pass < passes; pass += kInFlight) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            ss = fmaf(a[j], a[j], fmaf(c[j], c[j], ss));
+        for (int k = 0; k < kInFlight; ++k) {
+            const bool here = at.t < live; // (a row group may be past the last row)
+            const bool is_q = at.row < p.Hq, is_v = at.row >= p.Hq + p.Hkv;
+            const int t = here ? at.t : 0;
+            const uint4 in_lo = lo[k], in_hi = hi[k];
+            float a[8], c[8];
+            unpack8(in_lo, a);
+            unpack8(in_hi, c);
+            float ss = 0.f;
 #pragma unroll
-        for (int off = kRowLanes / 2; off > 0; off >>= 1)
-            ss += __shfl_xor_sync(0xFFFFFFFFu, ss, off);
-        if (row < rows && (is_q || page_ok)) {
-            uint4 out_lo = lo, out_hi = hi; // V rows go through bit for bit
-            if (!is_v) {
-                const float inv_rms = rsqrtf(fmaf(ss, 1.0f / kHeadDim, p.eps));
-                const uint16_t *gamma = is_q ? p.gamma_q : p.gamma_k;
-                float ga[8], gc[8];
-                unpack8(*reinterpret_cast<const uint4 *>(gamma + 8 * lane8), ga);
-                unpack8(*reinterpret_cast<const uint4 *>(gamma + kPairs + 8 * lane8), gc);
+            for (int j = 0; j < 8; ++j)
+                ss = fmaf(a[j], a[j], fmaf(c[j], c[j], ss));
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float x = a[j] * inv_rms * ga[j], y = c[j] * inv_rms * gc[j];
-                    a[j] = fmaf(x, cs[j], -(y * sn[j]));
-                    c[j] = fmaf(y, cs[j], x * sn[j]);
+            for (int off = kRowLanes / 2; off > 0; off >>= 1)
+                ss += __shfl_xor_sync(0xFFFFFFFFu, ss, off);
+            if (ahead.t < live)
+                load(ahead, lo[k], hi[k]);
+            step(ahead);
+            const long long cell = cells[t];
+            if (here && (is_q || cell >= 0)) {
+                uint4 out_lo = in_lo, out_hi = in_hi; // V rows go through bit for bit
+                if (!is_v) {
+                    const float inv_rms = rsqrtf(fmaf(ss, 1.0f / kHeadDim, p.eps));
+                    const uint16_t *gamma = is_q ? p.gamma_q : p.gamma_k;
+                    float ga[8], gc[8];
+                    unpack8(*reinterpret_cast<const uint4 *>(gamma + 8 * lane8), ga);
+                    unpack8(*reinterpret_cast<const uint4 *>(gamma + kPairs + 8 * lane8), gc);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float cs = rot_cos[t][8 * lane8 + j], sn = rot_sin[t][8 * lane8 + j];
+                        const float x = a[j] * inv_rms * ga[j], y = c[j] * inv_rms * gc[j];
+                        a[j] = fmaf(x, cs, -(y * sn));
+                        c[j] = fmaf(y, cs, x * sn);
+                    }
+                    out_lo = pack8(a);
+                    out_hi = pack8(c);
                 }
-                out_lo = pack8(a);
-                out_hi = pack8(c);
+                uint16_t *dst;
+                if (is_q)
+                    dst = p.q_out + ((tok0 + t) * p.Hq + at.row) * kHeadDim;
+                else if (!is_v)
+                    dst = p.k_cache + (cell + (at.row - p.Hq) * P) * kHeadDim;
+                else
+                    dst = p.v_cache + (cell + (at.row - p.Hq - p.Hkv) * P) * kHeadDim;
+                *reinterpret_cast<uint4 *>(dst + 8 * lane8) = out_lo;
+                *reinterpret_cast<uint4 *>(dst + kPairs + 8 * lane8) = out_hi;
             }
-            uint16_t *dst;
-            if (is_q)
-                dst = p.q_out + (static_cast<size_t>(tok) * p.Hq + row) * kHeadDim;
-            else if (!is_v)
-                dst = p.k_cache + (cell + (row - p.Hq) * P) * kHeadDim;
-            else
-                dst = p.v_cache + (cell + (row - p.Hq - p.Hkv) * P) * kHeadDim;
-            *reinterpret_cast<uint4 *>(dst + 8 * lane8) = out_lo;
-            *reinterpret_cast<uint4 *>(dst + kPairs + 8 * lane8) = out_hi;
+            step(at);
         }
-        lo = next_lo;
-        hi = next_hi;
     }
 }
 
@@ -199,8 +231,14 @@ cudaError_t launch_rope_axes(const RopeAxesArgs &a, cudaStream_t stream)
     p.max_pages = a.max_pages;
     p.num_pages = a.num_pages;
     p.eps = a.eps;
-    return launch_pdl(rope_axes_kernel, dim3(static_cast<unsigned>(a.B) * static_cast<unsigned>(a.M)),
-                      dim3(kRopeThreads), 0, stream, p);
+    // Two tokens per block where that still gives every SM its fill of blocks (7
+    // of 72 registers a thread): the lengths' and tables' trips to memory are
+    // shared. 4095 tokens: 15.9 us with one, 14.5 with two, 14.4 with four; 16
+    // tokens: 3.1 us with one, 4.0 with two.
+    const bool two = static_cast<long long>(a.B) * a.M >= 2048;
+    p.blocks_per_seq = two ? (a.M + 1) / 2 : a.M;
+    const dim3 grid(static_cast<unsigned>(a.B) * static_cast<unsigned>(p.blocks_per_seq));
+    return launch_pdl(two ? rope_axes_kernel<2> : rope_axes_kernel<1>, grid, dim3(kRopeThreads), 0, stream, p);
 }
 
 cudaError_t read_flags_rope_axes(unsigned *flags, bool clear)
