@@ -515,7 +515,7 @@ int decode_attn_paged_static(const pgqa_bf16 *q, const pgqa_bf16 *k_cache,
  *                  nor written.
  *   The rest as for qk_norm_rope_append. Arithmetic in fp32; the angle is
  *   reduced modulo a turn in 64-bit fixed point, so it stays accurate at
- *   large positions (below 1e-6 rad up to 2^31). A sequence with n_b outside
+ *   large positions (below 1e-6 rad up to 2^31 for theta >= 1). A sequence with n_b outside
  *   [0, M], T_b < n_b or T_b > max_pages * page_size is skipped
  *   (PGQA_DEVERR_BAD_CONTEXT); K and V rows of a page outside the pool are
  *   skipped (PGQA_DEVERR_BAD_PAGE). Results do not depend on M or B.
@@ -549,10 +549,13 @@ int qk_norm_rope_append_axes(const pgqa_bf16 *q, const pgqa_bf16 *k, const pgqa_
  *                i >= n_b are left as they were
  *   slopes       [Hq] float, nullable, any sign
  *   softcap      0 (none) or a positive finite number
- *   out_f32, out_bf16  [B][M][Hq][D], at least one non-NULL
+ *   out_f32, out_bf16  [B][M][Hq][D], at least one non-NULL; no overlap with
+ *                the inputs
  *   workspace    device scratch of ws_bytes >= decode_attn_tree_workspace_size
  *                (of the current device); no initial value needed. Calls whose
  *                work may overlap on the GPU must not share one.
+ * Limits: max_pages * page_size <= 2^30, B * M * Hq < 2^31, and fewer than 2^31
+ * tiles of 128 keys over all sequences and KV heads (PGQA_ERR_UNSUPPORTED).
  * Every input is read after the previous kernel in the stream completes. A
  * sequence with n_b outside [0, M], T_b < n_b or T_b > max_pages * page_size
  * produces zeros in all its M rows (PGQA_DEVERR_BAD_CONTEXT); keys of a page

@@ -560,6 +560,8 @@ def qk_norm_rope_append_axes(q, k, v, gamma_q, gamma_k, positions, context_lens,
     B, M, Hq, D = q.shape
     num_pages, Hkv, P, _ = k_cache.shape
     max_pages, n_axes = block_table.shape[-1], positions.shape[-1]
+    if isinstance(axis_of_pair, int):
+        raise TypeError("axis_of_pair must be a sequence of 64 axis numbers")
     axes = bytes(axis_of_pair)
     if len(axes) != 64:
         raise ValueError(f"axis_of_pair must hold 64 axis numbers, got {len(axes)}")

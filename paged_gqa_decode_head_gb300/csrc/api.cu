@@ -962,6 +962,8 @@ int decode_attn_paged_tree(const pgqa_bf16 *q, const pgqa_bf16 *k_cache, const p
         return fail(PGQA_ERR_UNSUPPORTED, "%s: Hkv = %d exceeds 65535", fn, Hkv);
     if (static_cast<long long>(Hq) * M > 0x7FFFFFFFLL / (B > 0 ? B : 1))
         return fail(PGQA_ERR_UNSUPPORTED, "%s: B * M * Hq exceeds 2^31 - 1 rows", fn);
+    if (static_cast<long long>(max_pages) * page_size > (1LL << 30))
+        return fail(PGQA_ERR_UNSUPPORTED, "%s: max_pages * page_size exceeds 2^30 positions", fn);
     if ((static_cast<long long>(max_pages) * page_size / 128 + 1) * Hkv > 0x7FFFFFFFLL / (B > 0 ? B : 1))
         return fail(PGQA_ERR_UNSUPPORTED, "%s: B * Hkv * max_pages * page_size exceeds 2^31 tiles of 128 keys", fn);
     if (B == 0)

@@ -1238,7 +1238,7 @@ cudaError_t launch_tree_attn(const TreeAttnArgs &a, cudaStream_t stream)
     p.negate_q = a.scale < 0.f;
     // A scale of 0 gives every key the same weight; the smallest positive
     // factor does the same and keeps -inf * c, the score of a hidden key, -inf.
-    p.c = std::fmax(std::fabs(a.scale) * kLog2e, FLT_MIN);
+    p.c = std::fmin(std::fmax(std::fabs(a.scale) * kLog2e, FLT_MIN), FLT_MAX);
     if (a.softcap > 0.f) {
         p.cap_in = std::fmin(2.f * std::fabs(a.scale) / a.softcap * kLog2e, FLT_MAX);
         p.cap_out = a.softcap * kLog2e;

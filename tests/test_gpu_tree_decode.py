@@ -383,6 +383,101 @@ def test_one_long_context():
     c.check()
 
 
+@pytest.mark.parametrize("seed", range(24))
+def test_random_calls(seed):
+    """Sizes, lengths, heads, options and masks drawn together."""
+    gen = inputs.generator(1800 + seed, 7)
+    pick = lambda *x: x[int(gen.integers(0, len(x)))]  # noqa: E731
+    g, Hkv, P, M = pick(1, 2, 3, 5, 8), pick(1, 2, 3), pick(16, 32, 64, 128, 256), int(gen.integers(1, 65))
+    B = int(gen.integers(1, 9))
+    n = [int(gen.integers(0, M + 1)) for _ in range(B)]
+    ctx = [x + int(pick(0, 1, gen.integers(0, 40), gen.integers(0, 700))) for x in n]
+    slopes = [float(x) for x in gen.normal(0, 0.2, g * Hkv)] if gen.random() < 0.4 else None
+    masks = None
+    if gen.random() < 0.4:
+        masks = [[int(gen.integers(0, 2 ** 62)) << int(gen.integers(0, 3)) for _ in range(M)] for _ in range(B)]
+    Case(1800 + seed, ctx, M, Hq=g * Hkv, Hkv=Hkv, P=P, draft_lens=n, masks=masks, slopes=slopes,
+         softcap=float(pick(0.0, 0.0, 8.0)), max_pages=max(1, -(-max(ctx) // P) + int(gen.integers(0, 5)))).check()
+
+
+def test_more_sequences_than_threads():
+    """Several sequences per thread of the schedule's scan, empty ones among them."""
+    gen = inputs.generator(1830, 8)
+    n = [int(gen.integers(0, 3)) for _ in range(900)]
+    ctx = [x + (int(gen.integers(0, 300)) if x else 0) for x in n]
+    Case(1830, ctx, 2, Hq=2, Hkv=1, draft_lens=n).check()
+
+
+@pytest.mark.parametrize("g,T", [(4, 3000), (8, 2000), (5, 1500)])
+def test_wide_trees_over_many_pieces(g, T):
+    """Two and more row tiles per KV head, every head split over several CTAs."""
+    Case(1840 + g, [T], 64, Hq=g, Hkv=1).check()
+
+
+@pytest.mark.parametrize("T", [64, 200, 1000])
+def test_nonfinite_rows_with_two_row_tiles(T):
+    M = 64
+    c = Case(1850 + T, [T, T + 7], M, Hq=8, Hkv=2)
+    kv = c.kv
+    clean = kv.v_cache.copy()
+    for b in range(2):
+        s = int(kv.context_lens[b]) - M + 20
+        kv.v_cache[kv.block_table[b, s // 16], :, s % 16, 3] = 0x7F80
+    of, _ = c.run()
+    kv.v_cache = clean
+    out, bound = c.reference()
+    for b in range(2):
+        for i in range(M):
+            if c.masks[b][i] >> 20 & 1:
+                assert (of[b, i, :, 3] == np.inf).all()
+            else:
+                assert (np.abs(of[b, i] - out[b, i]) <= bound[b, i] + 2.0 ** -24 * np.abs(out[b, i])).all()
+
+
+def test_binding_refuses():
+    """Wrong dtype, shape, layout or device of a tensor: an error that names it, nothing launched."""
+    c = Case(1860, [100], 8)
+    d = c.upload()
+
+    def call(**kw):
+        a = dict(q=d["q"], kc=d["kc"], vc=d["vc"], bt=d["bt"], cl=d["cl"], mask=d["mask"], pos=d["pos"], dl=None,
+                 slopes=None, of=d["of"], ws=d["ws"])
+        a.update(kw)
+        pg.decode_attn_paged_tree(a["q"], a["kc"], a["vc"], a["bt"], a["cl"], a["mask"], SCALE, positions=a["pos"],
+                                  draft_lens=a["dl"], slopes=a["slopes"], out_f32=a["of"], workspace=a["ws"])
+
+    bad = [("q", d["q"].half(), TypeError), ("kc", d["kc"].float(), TypeError), ("vc", d["vc"][:1], ValueError),
+           ("kc", d["kc"].transpose(0, 2).contiguous().transpose(0, 2), ValueError), ("bt", d["bt"].long(), TypeError),
+           ("cl", d["cl"].cpu(), ValueError), ("cl", d["cl"].repeat(2), ValueError),
+           ("mask", d["mask"].int(), TypeError), ("mask", d["mask"][:, :4], ValueError),
+           ("pos", d["pos"].reshape(-1), ValueError), ("dl", torch.zeros(2, dtype=torch.int32, device="cuda"), ValueError),
+           ("slopes", torch.zeros(3, device="cuda"), ValueError), ("of", d["of"][..., :64], ValueError),
+           ("of", d["of"].bfloat16(), TypeError), ("ws", d["ws"].float(), TypeError)]
+    for name, value, error in bad:
+        with pytest.raises(error):
+            call(**{name: value})
+    for ws in (None, d["ws"][:16]):
+        with pytest.raises(binding.PgqaError) as e:
+            call(ws=ws)
+        assert e.value.status == -4
+    torch.cuda.synchronize()
+    assert (d["of"] == SENTINEL).all()
+    p = prologue_case(1861, [20], 4, 3, SECTIONS)
+    for axes in ([0] * 63, [3] * 64, 64, [300] * 64):
+        with pytest.raises((ValueError, TypeError, binding.PgqaError)):
+            run_prologue(dict(p, axes=axes))
+    with pytest.raises(ValueError):
+        pg.CacheLayers([d["kc"]], [d["vc"], d["vc"]], [d["bt"]])
+    with pytest.raises(ValueError):
+        pg.CacheLayers([d["kc"], d["kc"][:2]], [d["vc"], d["vc"]], [d["bt"], d["bt"]])
+    layers = pg.CacheLayers([d["kc"]], [d["vc"]], [d["bt"]])
+    one = torch.ones(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(binding.PgqaError):  # in place
+        pg.kv_cache_commit_path(layers, d["cl"], one.view(1, 1), one, d["cl"], 8)
+    with pytest.raises(ValueError):
+        pg.kv_cache_commit_path(layers, d["cl"], one.view(1, 1).repeat(2, 1), one, torch.zeros_like(one), 8)
+
+
 # ------------------------------------------------------------------ prologue
 def prologue_case(seed, ctx, M, n_axes, axes, Hq=16, Hkv=8, P=16, new_lens=None, big=False):
     gen = inputs.generator(seed, 311)

@@ -36,6 +36,8 @@ def attention(lib, **kw):
     (dict(D=64), -2), (dict(Hq=12), -2), (dict(Hq=72), -2), (dict(P=8), -2), (dict(P=48), -2), (dict(P=512), -2),
     (dict(B=-1), -1), (dict(B=65536), -2), (dict(M=0), -1), (dict(M=65), -1), (dict(scale=math.nan), -1),
     (dict(scale=math.inf), -1), (dict(cap=-1.0), -1), (dict(cap=math.nan), -1), (dict(cap=math.inf), -1),
+    (dict(P=256, max_pages=(1 << 22) + 1), -2), (dict(B=60000, P=256, max_pages=1 << 22), -2),
+    (dict(B=65535, M=64, Hq=8192, Hkv=1024), -2), (dict(Hq=70000, Hkv=70000), -2),
     (dict(max_pages=-1), -1), (dict(num_pages=-1), -1), (dict(num_pages=0), -1), (dict(num_pages=2 ** 26), -2),
     (dict(q=None), -1), (dict(k=None), -1), (dict(v=None), -1), (dict(bt=None), -1), (dict(ctx=None), -1),
     (dict(mask=None), -1), (dict(of=None), -1), (dict(slopes=BASE, pos=None), -1),
