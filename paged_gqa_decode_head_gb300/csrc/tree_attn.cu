@@ -747,13 +747,11 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
                         a = ex2(a), b = ex2(b);
                         const f32x2 ab(a, b);
                         sum = add2(sum, ab);
-                        // hi: the upper 16 bits as they are; lo: the exact rest, rounded
-                        const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-                        w[j] = __uint_as_float(__byte_perm(ua, ub, 0x7632));
+                        // hi: nearest bf16; lo: the exact rest, rounded
+                        const uint32_t hi = pack_bf16x2(a, b);
+                        w[j] = __uint_as_float(hi);
                         float ra, rb;
-                        add2(ab, f32x2(__uint_as_float((ua & 0xFFFF0000u) ^ 0x80000000u),
-                                       __uint_as_float((ub & 0xFFFF0000u) ^ 0x80000000u)))
-                            .get(ra, rb);
+                        fma2(f32x2(bf16_lo(hi), bf16_hi(hi)), f32x2(-1.f, -1.f), ab).get(ra, rb);
                         w[8 + j] = __uint_as_float(pack_bf16x2(ra, rb));
                     }
                     tmem_st16(tmem_s + 16 * i, w);
