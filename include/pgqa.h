@@ -518,7 +518,8 @@ int decode_attn_paged_static(const pgqa_bf16 *q, const pgqa_bf16 *k_cache,
  *   large positions (below 1e-6 rad up to 2^31 for theta >= 1). A sequence with n_b outside
  *   [0, M], T_b < n_b or T_b > max_pages * page_size is skipped
  *   (PGQA_DEVERR_BAD_CONTEXT); K and V rows of a page outside the pool are
- *   skipped (PGQA_DEVERR_BAD_PAGE). Results do not depend on M or B.
+ *   skipped (PGQA_DEVERR_BAD_PAGE). Results do not depend on M or B. Every
+ *   call of the library may follow directly in the stream.
  */
 int qk_norm_rope_append_axes(const pgqa_bf16 *q, const pgqa_bf16 *k, const pgqa_bf16 *v,
                              const pgqa_bf16 *gamma_q, const pgqa_bf16 *gamma_k, const int32_t *positions,
@@ -595,7 +596,8 @@ int decode_attn_paged_tree(const pgqa_bf16 *q, const pgqa_bf16 *k_cache, const p
  * (PGQA_DEVERR_BAD_PATH: nothing of the sequence moves, its new length is T_b
  * - n_b); an invalid n_b or T_b moves nothing and leaves the length T_b
  * (PGQA_DEVERR_BAD_CONTEXT); rows of a page outside the pool stay
- * (PGQA_DEVERR_BAD_PAGE).
+ * (PGQA_DEVERR_BAD_PAGE). Every call of the library may follow directly in the
+ * stream, context_lens_out as its lengths.
  */
 #define PGQA_MAX_COMMIT_LAYERS 128
 int kv_cache_commit_path(pgqa_bf16 *const *k_caches, pgqa_bf16 *const *v_caches,

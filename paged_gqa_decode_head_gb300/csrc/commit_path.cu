@@ -38,7 +38,9 @@ struct CommitParams {
 
 __global__ void __launch_bounds__(kCommitThreads) commit_path_kernel(const __grid_constant__ CommitParams p)
 {
-    allow_dependent_launch();
+    // The next kernel may read tables, lengths and cache rows before it waits for
+    // this one (the decode kernels do): no early launch of it here, and every
+    // write is performed before its thread ends.
     grid_dependency_wait();
     __shared__ long long from[kMaxDrafted], to[kMaxDrafted]; // cache rows of KV head 0, -1: page outside the pool
     const int tid = threadIdx.x;
@@ -51,6 +53,7 @@ __global__ void __launch_bounds__(kCommitThreads) commit_path_kernel(const __gri
         if (reports && tid == 0) {
             p.context_lens_out[b] = T;
             atomicOr(&g_flags_commit_path, PGQA_DEVERR_BAD_CONTEXT);
+            __threadfence();
         }
         return;
     }
@@ -81,6 +84,7 @@ __global__ void __launch_bounds__(kCommitThreads) commit_path_kernel(const __gri
         p.context_lens_out[b] = T - n + (bad ? 0 : a);
         if (bad)
             atomicOr(&g_flags_commit_path, PGQA_DEVERR_BAD_PATH);
+        __threadfence();
     }
     if (bad)
         return;
@@ -114,6 +118,7 @@ __global__ void __launch_bounds__(kCommitThreads) commit_path_kernel(const __gri
                 reinterpret_cast<uint4 *>(dst[u])[lane] = row[u];
         __syncthreads();
     }
+    __threadfence();
 }
 
 } // namespace

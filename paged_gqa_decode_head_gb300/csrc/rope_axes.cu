@@ -62,8 +62,12 @@ template <int kTokens>
 __global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(const __grid_constant__ RopeAxesParams p)
 {
     // Everything this kernel reads may come from the kernel before it, and
-    // what it writes may still be read there: wait before touching memory.
-    allow_dependent_launch();
+    // what it writes may still be read there: wait before touching memory. The
+    // next kernel may read cache rows below T - 1 before it waits for this one
+    // (the decode kernels do): it may start early only where a single token's
+    // row, T - 1, is written here.
+    if (p.M == 1)
+        allow_dependent_launch();
     grid_dependency_wait();
     const int tid = threadIdx.x;
     const int b = blockIdx.x / p.blocks_per_seq, i0 = (blockIdx.x - b * p.blocks_per_seq) * kTokens;
@@ -189,6 +193,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(const __grid_co
             step(at);
         }
     }
+    if (p.M > 1)
+        __threadfence(); // performed before the thread ends, and so before the next kernel starts
 }
 
 } // namespace

@@ -19,7 +19,7 @@
 // lengths: no partition size, no waves, ragged batches balance by themselves.
 // A run that covers a (sequence, head) from its first to its last tile writes
 // the output; the pieces of the others go to the workspace (at most two per
-// CTA) and merge_kernel joins them, in order, in the same stream.
+// CTA) and tree_merge_kernel joins them, in order, in the same stream.
 //
 // CTA: one per SM, 12 warps around a ring of five 32 KB shared-memory slots
 // (K and V tiles in consumption order), Q, and all of tensor memory (S/P of
@@ -33,8 +33,30 @@
 // 128 rows the streams take alternate key tiles of the same rows and are joined
 // at the end of a run; with more, they are two row tiles over the same keys.
 //
-// Rounding: P enters its product as a bf16 pair hi + lo (16 significant bits,
-// so that fp32 outputs keep their meaning); S, O, m and l are fp32.
+// A stream's step: S from the tensor core, 128 scores of a row in a thread's
+// registers (2000 clocks for a full tile, some 1100 instructions a warp), P in
+// two halves, the first handed over while the second is formed, then O += P V
+// and the next S in one go. The streams' products alternate (a stream's next
+// scores before the other's products with V). The tensor core's queue is a few
+// products deep, so every gap in issuing shows: operands are waited for ahead,
+// and each stream has an issuing warp of its own.
+//
+// Rounding: P enters its product as a bf16 pair hi + lo (17 significant bits, so
+// that fp32 outputs keep their meaning: 1.3e-6 from the formula, 2-norm), which
+// is half as much tensor work again; S, O, m and l are fp32.
+//
+// Measured (GB300; bf16 outputs; HBM at the measured copy bandwidth of 6.78 TB/s):
+//   B = 64, ragged to 32768, 16 drafted, g = 2: 615 us, 6.4 TB/s of K and V (94 %);
+//   B = 1, T = 131072, 16 drafted, g = 4, capped: 110 us, 4.9 TB/s (the cap's
+//     exponentials and reciprocals, and the run's start and end);
+//   B = 8, T = 16384, 64 drafted, g = 8: 345 us, 797 TFLOP/s and half as much again
+//     for lo, at some 1.3 GHz under the power limit (4000 clocks for two steps whose
+//     products take 3072);
+//   B = 1, T = 8192, g = 2: 16 drafted 20.5 us, 64 drafted 24.5 us (the lengths, the
+//     table and the first tile are three trips to memory before the first product;
+//     joining the pieces is a second kernel);
+//   B = 33, ragged to 4001, one token, g = 3, capped and biased: 109 us, 2.5 TB/s (one
+//     warp of each stream holds all rows, both on the same SM partition).
 #include "common.cuh"
 #include "launch.h"
 #include "tcgen05.cuh"
@@ -58,13 +80,13 @@ constexpr int kSoftmaxThreads = 256;
 constexpr int kTreeThreads = 384; // three warpgroups (the last warp idles)
 constexpr int kProducerWarp = 8, kMmaWarp = 9; // and kMmaWarp + 1
 constexpr float kRescaleLog2 = 8.f; // rise of a row's scores that moves its reference
-constexpr int kMergeThreads = 256;
+constexpr int kMergeThreads = 128;
 
 // TMEM columns of stream s's S (fp32, 128 columns, P over it) and O, + 128 s.
 constexpr uint32_t kColS = 0, kColO = 256;
 
 struct TreeParams {
-    const uint16_t *q, *k, *v;
+    const uint16_t *v;
     const int32_t *block_table, *context_lens;
     const uint64_t *tree_mask;
     const int32_t *positions, *draft_lens;
@@ -235,7 +257,6 @@ struct Steps {
             n = begin + ((begin ^ stream) & 1);
         }
     }
-    __device__ int unit() const { return pair ? n >> 1 : n; }
     __device__ int tile() const { return seg.seg_tile0 + ((n - begin) >> (pair ? 1 : 0)); }
     __device__ bool first() const { return n < begin + 2; }
     __device__ bool last() const { return n + 2 >= end; }
@@ -1211,8 +1232,6 @@ cudaError_t launch_tree_attn(const TreeAttnArgs &a, cudaStream_t stream)
         return cudaErrorNotSupported;
     const Layout y = layout(a.B, a.M, a.Hq, a.Hkv, a.page_size, a.max_pages, a.sm_count);
     TreeParams p{};
-    p.q = a.q;
-    p.k = a.k_cache;
     p.v = a.v_cache;
     p.block_table = a.block_table;
     p.context_lens = a.context_lens;

@@ -818,3 +818,48 @@ def test_verification_steps_match_token_by_token_decoding():
             for p, o in rows:
                 assert torch.equal(kc[p, :, o], chain_k[p, :, o]) and torch.equal(vc[p, :, o], chain_v[p, :, o])
     assert pg.device_error_flags() == 0
+
+
+def test_decode_may_follow_a_commit_or_a_prologue_directly():
+    """decode_attn_paged reads lengths and cache rows before it waits for the kernel before it: right after the
+    commit (lengths and rows written) and after a prologue of several tokens its result is that of a synchronised
+    run. Repeated, with other contents before each time."""
+    dev, Hq, Hkv, P, M = "cuda", 16, 8, 16, 40
+    gen = inputs.generator(4100, 330)
+    B, base = 6, [300, 17, 1000, 64, 5, 640]
+    kv = inputs.paged_kv(4100, [x + M for x in base], Hkv=Hkv, page_size=P, fill_unused="normal")
+    bt = to_device_i32(kv.block_table, dev)
+    cl = to_device_i32(kv.context_lens, dev)
+    paths = [sorted(int(x) for x in gen.choice(M, 9, replace=False)) for _ in range(B)]
+    path, plen = to_device_i32(np.array(paths), dev), to_device_i32(np.full(B, 9), dev)
+    q = to_device_bf16(inputs.normal_bf16(gen, (B, Hq, 128)), dev)
+    n = pg.decode_attn_workspace_size(B, Hq, Hkv, 128, P, kv.max_pages, 0)
+    ws = torch.zeros(max(16, n), dtype=torch.uint8, device=dev)
+    gq, gk = (to_device_bf16(inputs.uniform_bf16(gen, (128,), 0.5, 1.5), dev) for _ in range(2))
+    qs, ks, vs = (to_device_bf16(inputs.normal_bf16(gen, (B, M, h, 128)), dev) for h in (Hq, Hkv, Hkv))
+    pos = to_device_i32(np.array(base)[:, None, None] + np.arange(M)[None, :, None] + np.zeros((B, M, 3), int), dev)
+    q_out = torch.empty_like(qs)
+    kc, vc = to_device_bf16(kv.k_cache, dev), to_device_bf16(kv.v_cache, dev)
+    layers = pg.CacheLayers([kc], [vc], [bt])
+    lens = torch.empty(B, dtype=torch.int32, device=dev)
+    out = torch.empty((B, Hq, 128), dtype=torch.float32, device=dev)
+
+    def run(which, sync):
+        kc.copy_(to_device_bf16(kv.k_cache, dev)), vc.copy_(to_device_bf16(kv.v_cache, dev))
+        lens.fill_(1), out.fill_(SENTINEL)
+        torch.cuda.synchronize()
+        if which == "commit":
+            pg.kv_cache_commit_path(layers, cl, path, plen, lens, M)
+        else:
+            pg.qk_norm_rope_append_axes(qs, ks, vs, gq, gk, pos, cl, bt, kc, vc, q_out, SECTIONS, THETA)
+        if sync:
+            torch.cuda.synchronize()
+        pg.decode_attn_paged(q, kc, vc, bt, lens if which == "commit" else cl, SCALE, out_f32=out, workspace=ws)
+        torch.cuda.synchronize()
+        return out.cpu()
+
+    for which in ("commit", "prologue"):
+        want = run(which, True)
+        for _ in range(25):
+            assert torch.equal(run(which, False), want), which
+    assert pg.device_error_flags() == 0
