@@ -66,9 +66,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(const __grid_co
     // next kernel may read cache rows below T - 1 before it waits for this one
     // (the decode kernels do): it may start early only where a single token's
     // row, T - 1, is written here.
+    grid_dependency_wait();
     if (p.M == 1)
         allow_dependent_launch();
-    grid_dependency_wait();
     const int tid = threadIdx.x;
     const int b = blockIdx.x / p.blocks_per_seq, i0 = (blockIdx.x - b * p.blocks_per_seq) * kTokens;
     const int n = p.new_lens ? p.new_lens[b] : p.M;

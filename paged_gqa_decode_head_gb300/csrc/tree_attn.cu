@@ -935,7 +935,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rg = blockIdx.x % p.row_groups, cta = blockIdx.x / p.row_groups;
     const bool pair = 2 * rg + 1 < p.row_tiles;
-    allow_dependent_launch();
     if (tid == 0) {
         prefetch_tensormap(&mq), prefetch_tensormap(&mk), prefetch_tensormap(&mv);
         for (int i = 0; i < kSlots; ++i)
@@ -957,8 +956,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     if (warp == kMmaWarp)
         tmem_alloc_all(&s.tmem_base);
 
-    // Everything read from here on may come from the kernel before this one.
+    // Everything read from here on may come from the kernel before this one, and
+    // the next kernel may start once that one is done (it may read inputs before
+    // it waits).
     grid_dependency_wait();
+    allow_dependent_launch();
     // This CTA's run of tiles: thread t sums the tiles of sequences [t per, (t + 1) per).
     const int per = (p.B + kTreeThreads - 1) / kTreeThreads;
     const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
@@ -1047,8 +1049,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 // lengths. Rows of sequences whose lengths make no sense become zeros here.
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeParams p)
 {
-    allow_dependent_launch();
     grid_dependency_wait();
+    allow_dependent_launch();
     __shared__ float4 sums[kMergeThreads];
     __shared__ float sum_l[kMergeThreads / 32];
     constexpr int kRows = kMergeThreads / 128;
