@@ -99,7 +99,8 @@ struct TreeParams {
     int rec_rows;      // rows of a partial record
     int ctas;          // grid size / row_groups
     float c;           // plain scores: y = |scale| log2 e * x (the sign is in the MMA descriptor)
-    float cap_in, cap_out; // capped: y = cap_out tanh(x cap_in / (2 log2 e))
+    float cap_u, cap_out;  // capped: y = cap_out tanh(cap_u x)
+    float tanh_c[7];       // cap_out times the polynomial's coefficients
     uint32_t negate_q;     // scale < 0
     float *out_f32;
     uint16_t *out_bf16;
@@ -559,26 +560,74 @@ __device__ __forceinline__ float distance(int a, int b)
     return fmaf(2.f, static_cast<float>((a >> 1) - (b >> 1)), static_cast<float>((a & 1) - (b & 1)));
 }
 
+// The cap c tanh(u), u = scale x / c. For |u| <= 1 the polynomial u P(u^2), whose
+// error is relative to the value (degree 6 in u^2, fitted to tanh(u) / u on [0, 1]:
+// 5e-8; 3 units of 2^-24 evaluated in fp32), and which takes no turn of the
+// special-function unit; only scores past their cap take c - 2 c / (1 + e^2|u|),
+// whose error is relative to 2 c / (1 + e^2|u|).
+constexpr int kTanhTerms = 7;
+constexpr double kTanh[kTanhTerms] = {0.9999999502432662,   -0.33332839158678823, 0.13325204110108205,
+                                      -0.053457030406905304, 0.020289981289038105, -0.006203379388692019,
+                                      0.0010410225990803521};
+
 // N scores of a row, capped (kScore bit 0) or scaled, in base 2, with the bias
 // (bit 1) of keys whose positions are their slots; far0: the first one's
-// distance.
+// distance. Returns the largest u^2: above 1 the capped ones are not valid.
 template <int kScore, int N>
-__device__ __forceinline__ void prepare_scores(const TreeParams &p, float *x, float slope, float far0)
+__device__ __forceinline__ float prepare_scores(const TreeParams &p, float *x, float slope, float far0)
 {
+    float over = 0.f;
 #pragma unroll
     for (int j = 0; j < N; j += 2) {
         f32x2 y(x[j], x[j + 1]);
-        if constexpr ((kScore & 1) != 0) { // c tanh(u) = c - 2 c / (1 + e^2u)
-            float a, b;
-            mul2(y, f32x2(p.cap_in, p.cap_in)).get(a, b);
-            add2(f32x2(ex2(a), ex2(b)), f32x2(1.f, 1.f)).get(a, b);
-            y = fma2(f32x2(rcp(a), rcp(b)), f32x2(-2.f * p.cap_out, -2.f * p.cap_out), f32x2(p.cap_out, p.cap_out));
+        if constexpr ((kScore & 1) != 0) {
+            const f32x2 u = mul2(y, f32x2(p.cap_u, p.cap_u)), t = mul2(u, u);
+            float t0, t1;
+            t.get(t0, t1);
+            over = max3(over, t0, t1);
+            y = f32x2(p.tanh_c[kTanhTerms - 1], p.tanh_c[kTanhTerms - 1]);
+#pragma unroll
+            for (int k = kTanhTerms - 2; k >= 0; --k)
+                y = fma2(y, t, f32x2(p.tanh_c[k], p.tanh_c[k]));
+            y = mul2(u, y);
         } else {
             y = mul2(y, f32x2(p.c, p.c));
         }
         if constexpr ((kScore & 2) != 0)
             y = fma2(f32x2(slope, slope), add2(f32x2(far0, far0), f32x2(j, j + 1)), y);
         y.get(x[j], x[j + 1]);
+    }
+    return over;
+}
+
+// 16 scores of any size from key `key` on, any of them drafted tokens, whose
+// positions are their own (pos_lo and pos_hi: this lane's, lane and lane + 32).
+template <int kScore>
+__device__ __forceinline__ void prepare_any_scores(const TreeParams &p, float *x, float slope, int key, int prefix, int pos,
+                                                   int pos_lo, int pos_hi)
+{
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        float y;
+        if constexpr ((kScore & 1) != 0) {
+            const float u = x[j] * p.cap_u, size = fabsf(u);
+            y = p.tanh_c[kTanhTerms - 1];
+#pragma unroll
+            for (int k = kTanhTerms - 2; k >= 0; --k)
+                y = fmaf(y, u * u, p.tanh_c[k]);
+            y *= u;
+            const float rest = rcp(1.f + ex2(size * (2.f * kLog2e)));
+            if (size > 1.f)
+                y = copysignf(fmaf(-2.f * p.cap_out, rest, p.cap_out), u);
+        } else {
+            y = x[j] * p.c;
+        }
+        if constexpr ((kScore & 2) != 0) {
+            const int d = key + j - prefix;
+            const int drafted = __shfl_sync(0xFFFFFFFFu, d < 32 ? pos_lo : pos_hi, d & 31);
+            y = fmaf(slope, distance(d < 0 ? key + j : drafted, pos), y);
+        }
+        x[j] = y;
     }
 }
 
@@ -670,10 +719,13 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
                 const uint32_t valid = s.valid[unit % kValidRing];
                 const bool tail = key0 + kTileKeys > prefix;
                 const bool fix = tail || valid != 0xFFu;
-                // Biased scores are formed in place, 16 keys at a time: the loop's
-                // code is small enough to stay in the instruction cache (110 us
-                // for token decoding of 33 ragged sequences, 119 us unrolled in
-                // registers); only drafted tokens have positions of their own.
+                // Capped and biased scores, 16 keys at a time. Biased ones are formed
+                // in place, in a loop small enough for the instruction cache (109
+                // us for token decoding of 33 ragged sequences, 119 us unrolled in
+                // registers). What the common form does not cover (drafted tokens'
+                // own positions, scores past their cap) is left as it is and done
+                // after it.
+                uint32_t left = 0; // a bit per 16 keys
                 if constexpr ((kScore & 2) != 0) {
                     float y[2][16];
                     tmem_ld16(y[0], tmem_s);
@@ -684,31 +736,50 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
                             tmem_wait_ld16(y[k]);
                             tmem_ld16(y[k ^ 1], tmem_s + 16 * ((i + k + 1) & 7));
                             const int key = key0 + 16 * (i + k);
-                            const bool own = key + 16 > prefix && key < seg.T;
-                            prepare_scores<kScore, 16>(p, y[k], own ? 0.f : slope, distance(key, pos));
-                            if (own) {
-#pragma unroll
-                                for (int j = 0; j < 16; ++j) {
-                                    const int d = key + j - prefix;
-                                    const int at = __shfl_sync(0xFFFFFFFFu, d < 32 ? pos_lo : pos_hi, d & 31);
-                                    y[k][j] = fmaf(slope, distance(d < 0 ? key + j : at, pos), y[k][j]);
-                                }
-                            }
-                            tmem_st16(tmem_s + 16 * (i + k), y[k]);
+                            const float over = prepare_scores<kScore, 16>(p, y[k], slope, distance(key, pos));
+                            const bool rest = __any_sync(0xFFFFFFFFu, live && over > 1.f) || (key + 16 > prefix && key < seg.T);
+                            if (rest)
+                                left |= 1u << (i + k);
+                            else
+                                tmem_st16(tmem_s + 16 * (i + k), y[k]);
                         }
                     }
                     tmem_wait_ld16(y[0]); // the last prefetch, of no use
-                    tmem_wait_st();
                 }
                 float x[kTileKeys];
+                if constexpr (kScore == 1) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    tmem_ld16(x + 16 * i, tmem_s + 16 * i);
+                    for (int i = 0; i < 8; ++i)
+                        tmem_ld16(x + 16 * i, tmem_s + 16 * i);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    tmem_wait_ld16(x + 16 * i);
-                if constexpr (kScore == 1)
-                    prepare_scores<kScore, kTileKeys>(p, x, 0.f, 0.f);
+                    for (int i = 0; i < 8; ++i)
+                        tmem_wait_ld16(x + 16 * i);
+                    const float over = prepare_scores<kScore, kTileKeys>(p, x, 0.f, 0.f);
+                    left = __any_sync(0xFFFFFFFFu, live && over > 1.f) ? 0xFFu : 0u;
+                }
+                if constexpr (kScore != 0) {
+                    if (left) {
+#pragma unroll 1
+                        for (int i = 0; i < 8; ++i) {
+                            if (!(left >> i & 1u))
+                                continue;
+                            float y[16];
+                            tmem_ld16(y, tmem_s + 16 * i);
+                            tmem_wait_ld16(y);
+                            prepare_any_scores<kScore>(p, y, slope, key0 + 16 * i, prefix, pos, pos_lo, pos_hi);
+                            tmem_st16(tmem_s + 16 * i, y);
+                        }
+                    }
+                    tmem_wait_st();
+                }
+                if (kScore != 1 || left) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        tmem_ld16(x + 16 * i, tmem_s + 16 * i);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        tmem_wait_ld16(x + 16 * i);
+                }
                 if (fix) { // hidden keys
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
@@ -1259,8 +1330,10 @@ cudaError_t launch_tree_attn(const TreeAttnArgs &a, cudaStream_t stream)
     // factor does the same and keeps -inf * c, the score of a hidden key, -inf.
     p.c = std::fmin(std::fmax(std::fabs(a.scale) * kLog2e, FLT_MIN), FLT_MAX);
     if (a.softcap > 0.f) {
-        p.cap_in = std::fmin(2.f * std::fabs(a.scale) / a.softcap * kLog2e, FLT_MAX);
+        p.cap_u = std::fmin(std::fabs(a.scale) / a.softcap, FLT_MAX);
         p.cap_out = a.softcap * kLog2e;
+        for (int k = 0; k < kTanhTerms; ++k)
+            p.tanh_c[k] = static_cast<float>(kTanh[k] * a.softcap * 1.4426950408889634);
     }
     p.out_f32 = a.out_f32;
     p.out_bf16 = a.out_bf16;

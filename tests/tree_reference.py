@@ -7,8 +7,9 @@ Bound on the kernel's fp32 output. A relative error e_j of weight j moves the ou
 sum_j p_j |V_j| e_j + |out| sum_j p_j e_j. e_j collects, in units of u = 2^-24:
   - the score: 128 products summed in fp32 in any order, at most 128 u sum_d |q_d K_jd| scale, and its own
     scaling, 2 u |x_j|;
-  - the cap: tanh as 1 - 2 / (1 + e^2y) has an absolute error of at most 16 u (exp2 and reciprocal at 2 ulp
-    each, the rounding of the argument 2y <= 2 |x| / c counted with the score), times c;
+  - the cap: up to |x| = c a polynomial within 5e-8 (1 u) of tanh(y) / y, evaluated with at most 4 u more; past
+    it 1 - 2 / (1 + e^2y), where 2 / (1 + e^2y) <= 0.24 carries exp2 and reciprocal at 2 ulp each: either way
+    8 u of the capped score, the rounding of the argument counted with the score;
   - the bias: product and sum, 2 u (|bias| + |x|);
   - the exponent: argument (x_j - max) log2 e rounded twice, 4 u (|x_j| + |max|), and exp2 itself, 8 u;
   - the weight's hi + lo bf16 pair: 2^-16;
@@ -73,7 +74,7 @@ def attention(q, k_cache, v_cache, table, context_lens, masks, scale, draft_lens
                 e = 128 * U * abs(scale) * (np.abs(k) @ np.abs(qv)) + 2 * U * np.abs(x)
                 if softcap > 0:
                     x = softcap * np.tanh(x / softcap)
-                    e = e + 16 * U * softcap
+                    e = e + 8 * U * np.abs(x)
                 if slopes is not None:
                     bias = float(slopes[h]) * (kpos[idx] - float(positions[b][i]))
                     e = e + 2 * U * (np.abs(bias) + np.abs(x))
