@@ -562,8 +562,10 @@ int qk_norm_rope_append_axes(const pgqa_bf16 *q, const pgqa_bf16 *k, const pgqa_
  * produces zeros in all its M rows (PGQA_DEVERR_BAD_CONTEXT); keys of a page
  * outside the pool are skipped (PGQA_DEVERR_BAD_PAGE). Scores, softmax sums
  * and outputs are accumulated in fp32; the weights enter the product with V
- * as a bf16 hi + lo pair, as in decode_attn_paged. For given arguments on a
- * given device the results are reproducible bit for bit.
+ * as a bf16 hi + lo pair, as in decode_attn_paged. With out_f32 the sums over
+ * long contexts are formed more exactly (some 5e-6 of the result against
+ * 2e-5), so out_bf16 may then differ in a last bit from a call without it. For
+ * given arguments on a given device the results are reproducible bit for bit.
  */
 size_t decode_attn_tree_workspace_size(int B, int M, int Hq, int Hkv, int D, int page_size, int max_pages);
 int decode_attn_paged_tree(const pgqa_bf16 *q, const pgqa_bf16 *k_cache, const pgqa_bf16 *v_cache,

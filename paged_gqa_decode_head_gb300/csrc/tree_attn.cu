@@ -80,6 +80,7 @@ constexpr int kSoftmaxThreads = 256;
 constexpr int kTreeThreads = 384; // three warpgroups (the last warp idles)
 constexpr int kProducerWarp = 8, kMmaWarp = 9; // and kMmaWarp + 1
 constexpr float kRescaleLog2 = 8.f; // rise of a row's scores that moves its reference
+constexpr int kSpan = 16; // a stream's tiles between two moves of O out of the tensor core (fp32 outputs)
 constexpr int kMergeThreads = 128;
 
 // TMEM columns of stream s's S (fp32, 128 columns, P over it) and O, + 128 s.
@@ -107,6 +108,8 @@ struct TreeParams {
     int32_t *unit_base;     // [B + 1] first tile number of each sequence, total
     float *rec_m, *rec_l;   // [2 * grid][rec_rows]
     float *rec_acc;         // [2 * grid][rec_rows][128]
+    float *sums;            // [2 * grid][128][sum_rows]: O of earlier spans; null: bf16 outputs only
+    int sum_rows;           // rows of a row tile, to whole warps
 };
 
 struct __align__(1024) TreeSmem {
@@ -464,7 +467,8 @@ __device__ bool multiply(const TreeParams &p, TreeSmem &s, bool pair, int stream
             if (n > 0)
                 ok = ok && warp_wait(&s.round_done[stream ^ 1], ((n - 1) >> 1) & 1);
             const uint32_t va = warp_uniform(tc_desc_low(smem_addr(v), 1024));
-            const uint32_t keep = warp_uniform(!pu.first()); // a segment's first product overwrites O
+            // a segment's first product, and a span's, overwrites O
+            const uint32_t keep = warp_uniform(!pu.first() && !(p.sums && ((n - pu.begin) >> 1) % kSpan == 0));
 #pragma unroll
             for (int half = 0; half < 2; ++half) { // 64 keys each
                 ok = ok && warp_wait(half == 0 ? &s.p_half[stream] : &s.p_ready[stream], (n >> 1) & 1);
@@ -654,6 +658,35 @@ __device__ __forceinline__ void transpose4(float *o)
     }
 }
 
+// This thread's row of O (TMEM) and of earlier spans: v = O + f * sums. `out`
+// writes v to `sums` (which counts from `earlier` on), else to O. sums[column * stride].
+__device__ __forceinline__ void add_up(float *sums, int stride, uint32_t o, bool earlier, float f, bool out)
+{
+#pragma unroll 1
+    for (int col = 0; col < kHeadDim; col += 16) {
+        float acc[16], was[16];
+        tmem_ld16(acc, o + col);
+        if (earlier) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                was[j] = sums[static_cast<size_t>(col + j) * stride];
+        }
+        tmem_wait_ld16(acc);
+        if (earlier) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                acc[j] = fmaf(was[j], f, acc[j]);
+        }
+        if (out) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                sums[static_cast<size_t>(col + j) * stride] = acc[j];
+        } else {
+            tmem_st16(o + col, acc);
+        }
+    }
+}
+
 template <int kScore>
 __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int cta)
 {
@@ -692,6 +725,7 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
         }
         return r;
     };
+    float *sums = p.sums ? p.sums + static_cast<size_t>(2 * cta + stream) * kHeadDim * p.sum_rows + row : nullptr;
     Segments seg(s);
     bool more = seg.next(p);
     Row next_row = fetch_row(seg);
@@ -706,7 +740,9 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
         const int seg_steps = (seg.seg_tile1 - seg.seg_tile0) * (pair ? 2 : 1);
         float m = -INFINITY; // the reference, in units of 1 / c
         float l = 0.f;
-        bool fresh = true; // O holds nothing of this segment yet
+        bool fresh = true;  // nothing of this segment yet
+        bool summed = false; // `sums` holds earlier spans, relative to m_sums
+        float m_sums = 0.f;
         for (int n = step + ((step ^ stream) & 1); ok && n < step + seg_steps; n += 2) {
             const int tile = seg.seg_tile0 + ((n - step) >> (pair ? 1 : 0));
             const int unit = pair ? n >> 1 : n;
@@ -794,15 +830,28 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
                 for (int j = 4; j < kTileKeys; j += 2)
                     tops[j >> 1 & 3] = max3(tops[j >> 1 & 3], x[j], x[j + 1]);
                 const float high = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                // The tensor core rounds its accumulators towards zero at each product:
+                // over thousands of keys O loses some 2^-25 of itself a time. For fp32
+                // outputs O moves out every kSpan tiles and is added up in fp32, to
+                // nearest (4 x 131072 keys: 2.3e-5 -> 4.7e-6 of the result; bf16 outputs round
+                // far above that).
+                const bool span = p.sums && !fresh && ((n - step) >> 1) % kSpan == 0;
+                if (span) {
+                    const float f = summed && m_sums > -INFINITY ? ex2((m_sums - m) * c) : 0.f;
+                    add_up(sums, p.sum_rows, s.tmem_base + lanes + kColO + stream * 128, summed, f, true);
+                    summed = true;
+                    m_sums = m;
+                }
                 // move the reference where the row has none yet, or its scores left its range
-                const bool move = fresh ? true : (m == -INFINITY ? high > -INFINITY : (high - m) * c > kRescaleLog2);
+                const bool move =
+                    fresh || (live && (m == -INFINITY ? high > -INFINITY : (high - m) * c > kRescaleLog2));
                 if (__any_sync(0xFFFFFFFFu, move)) {
                     const float before = m;
                     if (move)
                         m = high;
-                    if (!fresh) {
-                        const float f = !move ? 1.f : (before == -INFINITY ? 0.f : ex2((before - m) * c));
-                        l *= f;
+                    const float f = !move ? 1.f : (before == -INFINITY ? 0.f : ex2((before - m) * c));
+                    l *= f;
+                    if (!fresh && !span) {
                         const uint32_t o = s.tmem_base + lanes + kColO + stream * 128;
 #pragma unroll 1
                         for (int i = 0; i < 8; ++i) {
@@ -882,6 +931,18 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
 
         // ---- the end of the segment: O of the last product, joined and written
         float w_own = 1.f, w_other = 0.f, top = m == -INFINITY ? -INFINITY : m * c;
+        if (p.sums) {
+            ok = warp_wait(&s.seg_done, index & 1);
+            if (!ok)
+                break;
+            tc_fence_after();
+            if (summed) { // (the same for the whole warpgroup)
+                const float f = m_sums > -INFINITY ? ex2((m_sums - m) * c) : 0.f;
+                add_up(sums, p.sum_rows, s.tmem_base + lanes + kColO + stream * 128, true, f, false);
+                tmem_wait_st();
+            }
+            tc_fence_before();
+        }
         if (!pair) {
             // both streams hold part of every row: exchange (m, l)
             s.ml[stream][row] = make_float2(top, l);
@@ -900,7 +961,8 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
         } else if (l == 0.f) {
             w_own = 0.f;
         }
-        ok = warp_wait(&s.seg_done, index & 1);
+        if (!p.sums)
+            ok = warp_wait(&s.seg_done, index & 1);
         if (!ok)
             break;
         tc_fence_after();
@@ -1215,7 +1277,8 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
 // workspace query and the launch agree.
 struct Layout {
     int tile_tokens, row_tiles, row_groups, rec_rows, ctas;
-    size_t base_bytes, stat_bytes, acc_bytes;
+    size_t base_bytes, stat_bytes, acc_bytes, sum_bytes;
+    int sum_rows;
 };
 
 size_t align256(size_t x) { return (x + 255) & ~size_t{255}; }
@@ -1238,6 +1301,9 @@ Layout layout(int B, int M, int Hq, int Hkv, int page_size, int max_pages, int s
     y.base_bytes = align256((static_cast<size_t>(B) + 1) * sizeof(int32_t));
     y.stat_bytes = align256(records * y.rec_rows * sizeof(float));
     y.acc_bytes = records * y.rec_rows * kHeadDim * sizeof(float);
+    // a stream passes a span only where a (sequence, head) has that many tiles
+    y.sum_rows = (y.tile_tokens * g + 31) / 32 * 32;
+    y.sum_bytes = tiles > kSpan ? records * kHeadDim * y.sum_rows * sizeof(float) : 0;
     return y;
 }
 
@@ -1295,7 +1361,7 @@ size_t tree_attn_workspace_bytes(int B, int M, int Hq, int Hkv, int page_size, i
     if (B == 0)
         return 0;
     const Layout y = layout(B, M, Hq, Hkv, page_size, max_pages, sm_count);
-    return y.base_bytes + 2 * y.stat_bytes + y.acc_bytes;
+    return y.base_bytes + 2 * y.stat_bytes + y.acc_bytes + y.sum_bytes;
 }
 
 cudaError_t launch_tree_attn(const TreeAttnArgs &a, cudaStream_t stream)
@@ -1342,6 +1408,9 @@ cudaError_t launch_tree_attn(const TreeAttnArgs &a, cudaStream_t stream)
     p.rec_m = reinterpret_cast<float *>(ws + y.base_bytes);
     p.rec_l = reinterpret_cast<float *>(ws + y.base_bytes + y.stat_bytes);
     p.rec_acc = reinterpret_cast<float *>(ws + y.base_bytes + 2 * y.stat_bytes);
+    if (a.out_f32 && y.sum_bytes)
+        p.sums = reinterpret_cast<float *>(ws + y.base_bytes + 2 * y.stat_bytes + y.acc_bytes);
+    p.sum_rows = y.sum_rows;
     CUtensorMap mq, mk, mv;
     const long long rows = static_cast<long long>(a.num_pages) * a.Hkv * a.page_size;
     if (encode_query(fn, &mq, a.q, a.B * a.M, a.Hq, p.g, y.tile_tokens) != CUDA_SUCCESS ||

@@ -408,6 +408,43 @@ def test_more_sequences_than_threads():
     Case(1830, ctx, 2, Hq=2, Hkv=1, draft_lens=n).check()
 
 
+@pytest.mark.parametrize("B,M,Hq,Hkv,T,rising", [(4, 2, 8, 8, 90000, False), (3, 40, 32, 8, 40000, False),
+                                                 (2, 3, 4, 4, 120000, True)])
+def test_long_contexts_keep_fp32_outputs(B, M, Hq, Hkv, T, rising):
+    """Many tiles per CTA and stream, one and two row tiles, scores that rise along the keys; against the formula in
+    64 bits on the GPU. The weights are within 2^-18 (hi + lo); the tensor core's accumulators lose at most one unit
+    in the last place (2^-23) at each of the 256 products of a span, half of that on average: 2^-16."""
+    P, g = 64, torch.Generator(device="cuda").manual_seed(B)
+    pages = -(-T // P)
+    rand = lambda *shape: torch.randn(*shape, generator=g, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    kc, vc = rand(B * pages, Hkv, P, 128), rand(B * pages, Hkv, P, 128)
+    q = rand(B, M, Hq, 128)
+    bt = torch.randperm(B * pages, generator=g, device="cuda").to(torch.int32).view(B, pages)
+    if rising:  # along the queries' mean direction, in steps that move the running reference now and then
+        for b in range(B):
+            d = q[b].float().view(M, Hkv, -1, 128).mean((0, 2))
+            up = torch.linspace(0, 25, pages, device="cuda")[:, None, None, None] / 11.3
+            kc[bt[b].long()] = (kc[bt[b].long()].float() + up * d[None, :, None]).bfloat16()
+    lens = [T - 1000 * b for b in range(B)]
+    of = torch.empty((B, M, Hq, 128), dtype=torch.float32, device="cuda")
+    masks = [[(1 << (i + 1)) - 1 for i in range(M)]] * B
+    pg.decode_attn_paged_tree(q, kc, vc, bt, to_device_i32(np.array(lens), "cuda"), mask_tensor(masks), SCALE,
+                              out_f32=of, workspace=workspace(B, M, Hq, Hkv, P, pages))
+    torch.cuda.synchronize()
+    for b in range(B):
+        n = lens[b]
+        k = kc[bt[b].long()].transpose(0, 1).reshape(Hkv, -1, 128)[:, :n].double()
+        v = vc[bt[b].long()].transpose(0, 1).reshape(Hkv, -1, 128)[:, :n].double()
+        seen = torch.ones(M, n, dtype=torch.bool, device="cuda")
+        seen[:, n - M:] = torch.tril(torch.ones(M, M, device="cuda")).bool()
+        for h in range(Hq):
+            x = (q[b, :, h].double() @ k[h // (Hq // Hkv)].t() * SCALE).masked_fill(~seen, -math.inf)
+            want = torch.softmax(x, -1) @ v[h // (Hq // Hkv)]
+            rel = ((of[b, :, h].double() - want).norm() / want.norm()).item()
+            assert rel <= 2.0 ** -18 + 2.0 ** -16, (b, h, rel)
+    assert pg.device_error_flags() == 0
+
+
 @pytest.mark.parametrize("g,T", [(4, 3000), (8, 2000), (5, 1500)])
 def test_wide_trees_over_many_pieces(g, T):
     """Two and more row tiles per KV head, every head split over several CTAs."""
