@@ -46,16 +46,16 @@
 // is half as much tensor work again; S, O, m and l are fp32.
 //
 // Measured (GB300; bf16 outputs; HBM at the measured copy bandwidth of 6.78 TB/s):
-//   B = 64, ragged to 32768, 16 drafted, g = 2: 615 us, 6.4 TB/s of K and V (94 %);
-//   B = 1, T = 131072, 16 drafted, g = 4, capped: 110 us, 4.9 TB/s (the cap's
-//     exponentials and reciprocals, and the run's start and end);
-//   B = 8, T = 16384, 64 drafted, g = 8: 345 us, 797 TFLOP/s and half as much again
-//     for lo, at some 1.3 GHz under the power limit (4000 clocks for two steps whose
-//     products take 3072);
-//   B = 1, T = 8192, g = 2: 16 drafted 20.5 us, 64 drafted 24.5 us (the lengths, the
+//   B = 64, ragged to 32768, 16 drafted, g = 2: 597 us, 6.6 TB/s of K and V (97 %);
+//   B = 1, T = 131072, 16 drafted, g = 4, capped: 114 us, 4.7 TB/s (the cap's
+//     polynomial, and the run's start and end);
+//   B = 8, T = 16384, 64 drafted, g = 8: 279 us, 986 TFLOP/s and half as much again
+//     for lo, under the power limit (4000 clocks for two steps whose products take
+//     3072);
+//   B = 1, T = 8192, g = 2: 16 drafted 20.9 us, 64 drafted 25.1 us (the lengths, the
 //     table and the first tile are three trips to memory before the first product;
 //     joining the pieces is a second kernel);
-//   B = 33, ragged to 4001, one token, g = 3, capped and biased: 109 us, 2.5 TB/s (one
+//   B = 33, ragged to 4001, one token, g = 3, capped and biased: 118 us, 2.3 TB/s (one
 //     warp of each stream holds all rows, both on the same SM partition).
 #include "common.cuh"
 #include "launch.h"
@@ -1176,19 +1176,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 
 // Joins the pieces of every (sequence, KV head) that several CTAs worked on:
 //   top = max m_k, out = sum acc_k 2^(m_k - top) / sum l_k 2^(m_k - top).
-// A row belongs to a group of four warps; warp w takes pieces w, w + 4, .. in
-// order (each with all its loads in flight at once), and the four sums are
-// added in order. What bounds it is latency: two trips to memory after the
-// lengths. Rows of sequences whose lengths make no sense become zeros here.
+// A row belongs to kParts warps; warp w takes pieces w, w + kParts, .. in order
+// (each with all its loads in flight at once), and the sums are added in order.
+// What bounds it is latency: two trips to memory after the lengths. Rows of
+// sequences whose lengths make no sense become zeros here.
+template <int kParts>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeParams p)
 {
     grid_dependency_wait();
     allow_dependent_launch();
     __shared__ float4 sums[kMergeThreads];
     __shared__ float sum_l[kMergeThreads / 32];
-    constexpr int kRows = kMergeThreads / 128;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp & 3;
-    const int r = blockIdx.x * kRows + (warp >> 2);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % kParts;
+    const int r = blockIdx.x * (kMergeThreads / 32 / kParts) + warp / kParts;
     const int h = blockIdx.y, b = blockIdx.z;
     const int token = r / p.g;
     int T, n;
@@ -1214,15 +1214,15 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
         };
         const int pieces = c1 - c0 + 1;
         constexpr int kFlight = 8; // this warp's pieces in flight
-        for (int first = 0; first < pieces; first += 32) { // (one round for up to 32 pieces)
+        for (int first = 0; first < pieces; first += kFlight * kParts) {
             float4 v[kFlight];
 #pragma unroll
             for (int i = 0; i < kFlight; ++i) {
-                const int k = first + 4 * i + part;
+                const int k = first + kParts * i + part;
                 if (k < pieces)
                     v[i] = reinterpret_cast<const float4 *>(p.rec_acc + record(k) * kHeadDim)[lane];
             }
-            // the reference over all pieces, the same in all four warps
+            // the reference over all pieces, the same in all of the row's warps
             float top = -INFINITY;
             for (int k = lane; k < pieces; k += 32) {
                 const float m = p.rec_m[record(k)], piece_l = p.rec_l[record(k)];
@@ -1231,7 +1231,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1)
                 top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
-            const int mine = first + 4 * lane + part; // lane i holds piece i of this warp
+            const int mine = first + kParts * lane + part; // lane i holds piece i of this warp
             float w = 0.f, piece_l = 0.f;
             if (lane < kFlight && mine < pieces) {
                 piece_l = p.rec_l[record(mine)];
@@ -1258,7 +1258,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
     __syncthreads();
     if (!live || part != 0)
         return;
-    for (int i = 1; i < 4; ++i) {
+    for (int i = 1; i < kParts; ++i) {
         const float4 v = sums[threadIdx.x + 32 * i];
         acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
         l += sum_l[warp + i];
@@ -1426,9 +1426,14 @@ cudaError_t launch_tree_attn(const TreeAttnArgs &a, cudaStream_t stream)
     }
     if (err != cudaSuccess)
         return err;
-    const dim3 grid(static_cast<unsigned>((a.M * p.g + kMergeThreads / 128 - 1) / (kMergeThreads / 128)),
-                    static_cast<unsigned>(a.Hkv), static_cast<unsigned>(a.B));
-    return launch_pdl(tree_merge_kernel, grid, dim3(kMergeThreads), 0, stream, p);
+    // Four warps a row where a (sequence, head) is cut into many pieces, one where
+    // there are many heads and few pieces each: t = 8192, 64 drafted tokens (20
+    // pieces) 25.1 us with four, 30.1 with one; B = 8, 64 drafted tokens, g = 8 (2
+    // or 3 pieces) 334 us with four, 279 with one.
+    const int parts = y.ctas >= 4ll * a.B * a.Hkv ? 4 : 1, per_block = kMergeThreads / 32 / parts;
+    const dim3 grid(static_cast<unsigned>((a.M * p.g + per_block - 1) / per_block), static_cast<unsigned>(a.Hkv),
+                    static_cast<unsigned>(a.B));
+    return launch_pdl(parts == 4 ? tree_merge_kernel<4> : tree_merge_kernel<1>, grid, dim3(kMergeThreads), 0, stream, p);
 }
 
 cudaError_t read_flags_tree_attn(unsigned *flags, bool clear)
