@@ -50,8 +50,8 @@
 //   B = 1, T = 131072, 16 drafted, g = 4, capped: 114 us, 4.7 TB/s (the cap's
 //     polynomial, and the run's start and end);
 //   B = 8, T = 16384, 64 drafted, g = 8: 279 us, 986 TFLOP/s and half as much again
-//     for lo, under the power limit (4000 clocks for two steps whose products take
-//     3072);
+//     for lo, under the power limit (4000 clocks for two steps, whose 48 products
+//     take 64 each);
 //   B = 1, T = 8192, g = 2: 16 drafted 20.9 us, 64 drafted 25.1 us (the lengths, the
 //     table and the first tile are three trips to memory before the first product;
 //     joining the pieces is a second kernel);
@@ -1396,10 +1396,11 @@ cudaError_t launch_tree_attn(const TreeAttnArgs &a, cudaStream_t stream)
     // factor does the same and keeps -inf * c, the score of a hidden key, -inf.
     p.c = std::fmin(std::fmax(std::fabs(a.scale) * kLog2e, FLT_MIN), FLT_MAX);
     if (a.softcap > 0.f) {
-        p.cap_u = std::fmin(std::fabs(a.scale) / a.softcap, FLT_MAX);
-        p.cap_out = a.softcap * kLog2e;
+        const float cap = std::fmin(a.softcap, 1e30f); // no cap to any score, and its products stay finite
+        p.cap_u = std::fmin(std::fabs(a.scale) / cap, FLT_MAX);
+        p.cap_out = cap * kLog2e;
         for (int k = 0; k < kTanhTerms; ++k)
-            p.tanh_c[k] = static_cast<float>(kTanh[k] * a.softcap * 1.4426950408889634);
+            p.tanh_c[k] = static_cast<float>(kTanh[k] * cap * 1.4426950408889634);
     }
     p.out_f32 = a.out_f32;
     p.out_bf16 = a.out_bf16;

@@ -196,8 +196,9 @@ def test_nonfinite_rows_reach_only_the_tokens_that_see_them(T):
             assert not np.isfinite(of[0, i][:, [5, 77]]).any()
 
 
-@pytest.mark.parametrize("softcap", [0.5, 5.0, 30.0, 1e4])
+@pytest.mark.parametrize("softcap", [1e-3, 0.5, 5.0, 30.0, 1e4, 3e38])
 def test_capped_scores(softcap):
+    """Scores far past the cap, around it and far below it."""
     c = Case(1600, [300, 77], 9, softcap=softcap)
     c.kv.k_cache[...] = scaled(c.kv.k_cache, 6.0)
     c.check()
@@ -730,6 +731,15 @@ def test_commit_long_paths_cross_chunks():
 def test_commit_ragged_drafts(P):
     paths = [[0], [], [1, 3], [0, 5]]
     check_commit(commit_case(3020 + P, 2, [300, 50, 20, 9], [1, 0, 4, 7], 7, paths, P=P))
+
+
+@pytest.mark.parametrize("Hkv", [1, 5, 8])
+def test_commit_of_many_sequences_and_layers(Hkv):
+    """More (sequence, layer) pairs than SMs: a block moves all heads of its pair."""
+    gen = inputs.generator(3025 + Hkv, 12)
+    paths = [sorted(int(x) for x in gen.choice(30, int(gen.integers(0, 31)), replace=False)) for _ in range(9)]
+    ctx = [30 + int(gen.integers(0, 100)) for _ in paths]
+    check_commit(commit_case(3025 + Hkv, 24, ctx, [30] * 9, 30, paths, Hkv=Hkv))
 
 
 def test_commit_many_layers_and_a_shared_table():
