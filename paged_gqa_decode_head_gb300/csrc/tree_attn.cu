@@ -756,9 +756,10 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
                 const bool tail = key0 + kTileKeys > prefix;
                 const bool fix = tail || valid != 0xFFu;
                 // Capped and biased scores, 16 keys at a time. Biased ones are formed
-                // in place, in a loop small enough for the instruction cache (109
-                // us for token decoding of 33 ragged sequences, 119 us unrolled in
-                // registers). What the common form does not cover (drafted tokens'
+                // in place, in a loop small enough for the instruction cache (118
+                // us for token decoding of 33 ragged sequences, 129 us unrolled in
+                // registers); capped ones in registers (t = 131072 113 us, in place
+                // 116 us). What the common form does not cover (drafted tokens'
                 // own positions, scores past their cap) is left as it is and done
                 // after it.
                 uint32_t left = 0; // a bit per 16 keys
