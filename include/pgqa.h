@@ -555,8 +555,9 @@ int qk_norm_rope_append_axes(const pgqa_bf16 *q, const pgqa_bf16 *k, const pgqa_
  *   workspace    device scratch of ws_bytes >= decode_attn_tree_workspace_size
  *                (of the current device); no initial value needed. Calls whose
  *                work may overlap on the GPU must not share one.
- * Limits: max_pages * page_size <= 2^30, B * M * Hq < 2^31, and fewer than 2^31
- * tiles of 128 keys over all sequences and KV heads (PGQA_ERR_UNSUPPORTED).
+ * Limits: max_pages * page_size <= 2^30, B * M * Hq < 2^31, Hkv < 2^16, num_pages
+ * * Hkv * page_size < 2^31, and fewer than 2^31 tiles of 128 keys over all
+ * sequences and KV heads (PGQA_ERR_UNSUPPORTED).
  * Every input is read after the previous kernel in the stream completes. A
  * sequence with n_b outside [0, M], T_b < n_b or T_b > max_pages * page_size
  * produces zeros in all its M rows (PGQA_DEVERR_BAD_CONTEXT); keys of a page

@@ -1030,7 +1030,8 @@ int kv_cache_commit_path(pgqa_bf16 *const *k_caches, pgqa_bf16 *const *v_caches,
         if (!aligned16(k_caches[l]) || !aligned16(v_caches[l]) || !aligned4(block_tables[l]))
             return fail(PGQA_ERR_MISALIGNED, "%s: layer %d: caches need 16-byte, the table 4-byte alignment", fn, l);
         for (int e = 0; e < l; ++e)
-            if (block_tables[e] == block_tables[l] && (k_caches[e] == k_caches[l] || v_caches[e] == v_caches[l]))
+            if (block_tables[e] == block_tables[l] && (k_caches[e] == k_caches[l] || v_caches[e] == v_caches[l] ||
+                                                       k_caches[e] == v_caches[l] || v_caches[e] == k_caches[l]))
                 return fail(PGQA_ERR_INVALID_ARG, "%s: layers %d and %d share a cache and its table", fn, e, l);
     }
     const auto overlap = [&](const int32_t *p, long long n) {

@@ -104,6 +104,12 @@ def test_commit_refuses(lib, kw, status):
     assert lib.pgqa_last_error()
 
 
+@pytest.mark.parametrize("ks,vs", [((BASE, BASE + 512), (BASE + 256, BASE)), ((BASE, BASE + 256), (BASE + 256, BASE + 512))])
+def test_commit_refuses_a_cache_that_is_k_of_one_layer_and_v_of_another(lib, ks, vs):
+    assert commit(lib, ks=ks, vs=vs, ts=(BASE, BASE)) == -1
+    assert lib.pgqa_last_error()
+
+
 def test_commit_of_no_sequences_is_a_no_op(lib):
     assert commit(lib, B=0, ctx=None, path=None, plen=None, out=None) == 0
 
