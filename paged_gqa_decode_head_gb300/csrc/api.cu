@@ -922,7 +922,7 @@ int qk_norm_rope_append_axes(const pgqa_bf16 *q, const pgqa_bf16 *k, const pgqa_
         return fail(PGQA_ERR_MISALIGNED, "%s: tensors need 16-byte and index arrays 4-byte alignment", fn);
     pgqa::RopeAxesArgs a{q, k, v, gamma_q, gamma_k, positions, n_axes, axis_of_pair, context_lens, new_lens,
                          block_table, k_cache, v_cache, q_out, B, M, Hq, Hkv, page_size, max_pages, num_pages,
-                         static_cast<double>(rope_theta), eps};
+                         static_cast<double>(rope_theta), eps, sm_count_current_device()};
     cudaError_t err = pgqa::launch_rope_axes(a, stream);
     if (err != cudaSuccess)
         return cuda_fail(err, fn);

@@ -141,6 +141,7 @@ struct RopeAxesArgs {
     int B, M, Hq, Hkv, page_size, max_pages, num_pages;
     double rope_theta;
     float eps;
+    int sm_count;
 };
 cudaError_t launch_rope_axes(const RopeAxesArgs &a, cudaStream_t stream);
 cudaError_t read_flags_rope_axes(unsigned *flags, bool clear);

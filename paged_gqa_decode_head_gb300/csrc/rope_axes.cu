@@ -15,14 +15,14 @@
 // Bound: memory, (2 Hq + 4 Hkv) * 256 bytes a token, read and written once. The
 // single-token prologue (prologue.cu) recomputes the angles for every head; at
 // prompt lengths that would cost more than the copy, so here a block owns one
-// or two tokens of a sequence, forms their rotations once in shared memory, and
+// to three tokens of a sequence, forms their rotations once in shared memory, and
 // its 16 groups of 8 lanes walk the tokens' Hq + 2 Hkv rows with 16-byte loads
 // and stores, two rows of a group on their way at a time (lane s of a group
 // holds dims 8s .. 8s+7 and 64 + 8s .. 64 + 8s + 7, so a pair's two halves are in
-// one lane). Measured (32 query, 8 KV heads): 32768 tokens 120 us, 6.69 TB/s, 99 %
-// of the measured copy bandwidth; ragged halves of that 71 us, 6.35 TB/s; 4095
-// tokens of 16 + 8 heads 14.5 us, 4.6 TB/s (its 2 waves of blocks start and end
-// unevenly); 16 tokens 3.1 us, a launch and three trips to memory.
+// one lane). Measured (32 query, 8 KV heads): 32768 tokens 127 us, 6.3 TB/s, 93 % of
+// the measured copy bandwidth; 19387 tokens in 8 ragged sequences of 4096 79 us, 6.0
+// TB/s; 4095 tokens of 16 + 8 heads 13.9 us, 4.8 TB/s (the start and end of its
+// blocks); 16 tokens 3.1 us, a launch and three trips to memory.
 #include "common.cuh"
 #include "launch.h"
 
@@ -35,6 +35,7 @@ __device__ unsigned g_flags_rope_axes;
 
 constexpr int kPairs = kHeadDim / 2;
 constexpr int kRopeThreads = 128;
+constexpr int kRopeBlocksPerSm = 9;                        // 56 registers a thread
 constexpr int kRowLanes = 8;                               // lanes that hold one head row
 constexpr int kRowsPerPass = kRopeThreads / kRowLanes;     // head rows a block handles at once
 constexpr int kInFlight = 2;                               // rows a group of lanes has on their way
@@ -59,7 +60,7 @@ __device__ __forceinline__ uint4 pack8(const float *f)
 
 // kTokens consecutive tokens of one sequence per block.
 template <int kTokens>
-__global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(const __grid_constant__ RopeAxesParams p)
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_axes_kernel(const __grid_constant__ RopeAxesParams p)
 {
     // Everything this kernel reads may come from the kernel before it, and
     // what it writes may still be read there: wait before touching memory. The
@@ -237,14 +238,21 @@ cudaError_t launch_rope_axes(const RopeAxesArgs &a, cudaStream_t stream)
     p.max_pages = a.max_pages;
     p.num_pages = a.num_pages;
     p.eps = a.eps;
-    // Two tokens per block where that still gives every SM its fill of blocks (7
-    // of 72 registers a thread): the lengths' and tables' trips to memory are
-    // shared. 4095 tokens: 15.9 us with one, 14.5 with two, 14.4 with four; 16
-    // tokens: 3.1 us with one, 4.0 with two.
-    const bool two = static_cast<long long>(a.B) * a.M >= 2048;
-    p.blocks_per_seq = two ? (a.M + 1) / 2 : a.M;
+    // One token per block as long as all blocks run at once, then two, then three:
+    // a block that had to wait for another's end costs more than the longer blocks,
+    // which share the trips to lengths and tables. Tokens of 16 + 8 heads with one, two
+    // and three per block: 1100 6.9, 7.6, 8.7 us; 1500 10.9, 8.6, 9.4 us; 2700 13.5,
+    // 10.8, 11.6 us; 3192 16.2, 14.8, 12.5 us; 4095 18.5, 16.5, 14.4 us. Four: 4095 15.1 us.
+    // Past that, three of up to 32 rows (16384: 57, 49, 47 us) and two of more (32 + 8
+    // heads: 8 ragged sequences to 4096 83, 70, 70 us and, other lengths, 54.0 us with
+    // two, 56.1 us with three; 8192 41.7, 36.0, 36.4 us).
+    const long long at_once = static_cast<long long>(kRopeBlocksPerSm) * (a.sm_count > 0 ? a.sm_count : 1);
+    const long long per_block = (static_cast<long long>(a.B) * a.M + at_once - 1) / at_once;
+    const int tokens = per_block <= 3 ? static_cast<int>(per_block) : a.Hq + 2 * a.Hkv <= 32 ? 3 : 2;
+    const auto kernel = tokens == 1 ? rope_axes_kernel<1> : tokens == 2 ? rope_axes_kernel<2> : rope_axes_kernel<3>;
+    p.blocks_per_seq = (a.M + tokens - 1) / tokens;
     const dim3 grid(static_cast<unsigned>(a.B) * static_cast<unsigned>(p.blocks_per_seq));
-    return launch_pdl(two ? rope_axes_kernel<2> : rope_axes_kernel<1>, grid, dim3(kRopeThreads), 0, stream, p);
+    return launch_pdl(kernel, grid, dim3(kRopeThreads), 0, stream, p);
 }
 
 cudaError_t read_flags_rope_axes(unsigned *flags, bool clear)

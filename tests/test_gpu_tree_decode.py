@@ -592,6 +592,18 @@ def test_prologue_ragged():
     check_prologue(prologue_case(2200, [0, 40, 300, 9], 9, 3, SECTIONS, new_lens=[0, 9, 4, 1]))
 
 
+@pytest.mark.parametrize("M,new_lens", [(460, None), (701, None), (920, [920, 919, 0]), (1401, None),
+                                        (1402, [1, 1400, 1399]), (1400, [0, 2, 1400])])
+def test_prologue_prompts(M, new_lens):
+    """Lengths on both sides of the token counts at which a block takes one more token."""
+    ctx = [n + 21 for n in (new_lens or [M] * 3)]
+    check_prologue(prologue_case(2300 + M, ctx, M, 3, SECTIONS, Hq=6, Hkv=2, new_lens=new_lens))
+
+
+def test_prologue_prompts_of_many_heads():
+    check_prologue(prologue_case(2310, [1403, 1403, 900], 1403, 3, SECTIONS, Hq=32, Hkv=8, new_lens=[1403, 1402, 900]))
+
+
 def test_prologue_positions_over_the_whole_int32_range():
     check_prologue(prologue_case(2210, [50, 20], 20, 3, SECTIONS, big=True))
 
