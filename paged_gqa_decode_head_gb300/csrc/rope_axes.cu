@@ -64,12 +64,11 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_axes_kern
 {
     // Everything this kernel reads may come from the kernel before it, and
     // what it writes may still be read there: wait before touching memory. The
-    // next kernel may read cache rows below T - 1 before it waits for this one
-    // (the decode kernels do): it may start early only where a single token's
-    // row, T - 1, is written here.
+    // next kernel may read cache rows before it waits for this one (the decode
+    // kernels do, up to a length of their own and through a table of their own):
+    // no early launch of it, not behind a single token's row either, and every
+    // write is performed before its thread ends.
     grid_dependency_wait();
-    if (p.M == 1)
-        allow_dependent_launch();
     const int tid = threadIdx.x;
     const int b = blockIdx.x / p.blocks_per_seq, i0 = (blockIdx.x - b * p.blocks_per_seq) * kTokens;
     const int n = p.new_lens ? p.new_lens[b] : p.M;
@@ -194,8 +193,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_axes_kern
             step(at);
         }
     }
-    if (p.M > 1)
-        __threadfence(); // performed before the thread ends, and so before the next kernel starts
+    __threadfence(); // performed before the thread ends, and so before the next kernel starts
 }
 
 } // namespace

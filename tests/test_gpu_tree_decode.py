@@ -922,3 +922,50 @@ def test_decode_may_follow_a_commit_or_a_prologue_directly():
         for _ in range(25):
             assert torch.equal(run(which, False), want), which
     assert pg.device_error_flags() == 0
+
+
+@pytest.mark.parametrize("follower", ["step", "attention"])
+def test_a_longer_decode_may_follow_a_single_token_prologue_directly(follower):
+    """A prologue of one token writes slot T - 1. The fused step of T + 1 tokens, and the attention of T + 1 where T
+    ends a chunk of 16 positions, request that row before they wait for the kernel before them: their results are
+    those of a synchronised run. The row holds NaN before each call."""
+    dev, Hq, Hkv, P = "cuda", 16, 8, 16
+    gen = inputs.generator(4200, 340)
+    base = [48, 16, 1024, 64, 4000, 640] if follower == "attention" else [48, 17, 1000, 64, 4001, 640]
+    B = len(base)
+    kv = inputs.paged_kv(4200, [x + 1 for x in base], Hkv=Hkv, page_size=P, fill_unused="normal")
+    for b, t in enumerate(base):
+        for cache in (kv.k_cache, kv.v_cache):
+            cache[kv.block_table[b, (t - 1) // P], :, (t - 1) % P] = inputs.BF16_NAN
+    new = lambda h: to_device_bf16(inputs.normal_bf16(gen, (B, 1, h, 128)), dev)  # noqa: E731
+    q, k, v, q2, k2, v2 = (new(h) for h in (Hq, Hkv, Hkv) * 2)
+    gq, gk = (to_device_bf16(inputs.uniform_bf16(gen, (128,), 0.5, 1.5), dev) for _ in range(2))
+    bt = to_device_i32(kv.block_table, dev)
+    cl, longer = to_device_i32(np.array(base), dev), to_device_i32(np.array(base) + 1, dev)
+    pos = (cl - 1).view(B, 1, 1)
+    n = pg.decode_attn_workspace_size(B, Hq, Hkv, 128, P, kv.max_pages, 0)
+    ws = torch.zeros(max(16, n), dtype=torch.uint8, device=dev)
+    kc, vc = to_device_bf16(kv.k_cache, dev), to_device_bf16(kv.v_cache, dev)
+    start_k, start_v = kc.clone(), vc.clone()
+    q_out = torch.empty_like(q)
+    out = torch.empty((B, Hq, 128), dtype=torch.float32, device=dev)
+
+    def run(sync):
+        kc.copy_(start_k), vc.copy_(start_v), out.fill_(SENTINEL)
+        torch.cuda.synchronize()
+        pg.qk_norm_rope_append_axes(q, k, v, gq, gk, pos, cl, bt, kc, vc, q_out, [0] * 64, THETA)
+        if sync:
+            torch.cuda.synchronize()
+        if follower == "step":
+            pg.decode_step_paged(q2[:, 0], k2[:, 0], v2[:, 0], gq, gk, longer, bt, kc, vc, SCALE, THETA, out_f32=out,
+                                 workspace=ws)
+        else:
+            pg.decode_attn_paged(q2[:, 0], kc, vc, bt, longer, SCALE, out_f32=out, workspace=ws)
+        torch.cuda.synchronize()
+        return out.cpu()
+
+    want = run(True)
+    assert torch.isfinite(want).all()
+    for _ in range(25):
+        assert torch.equal(run(False), want)
+    assert pg.device_error_flags() == 0
