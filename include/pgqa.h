@@ -538,9 +538,12 @@ int qk_norm_rope_append_axes(const pgqa_bf16 *q, const pgqa_bf16 *k, const pgqa_
  *   x_j = x_j + slopes[h] * (pos_j - pos_i)       if slopes
  *   out_ih = sum_j softmax(x)_j V_j over the keys it sees; 0 if there is none
  * with pos_j = j for prefix keys and the drafted tokens' given positions. M =
- * 1 with bit 0 set is single-token decoding with those score options. A key
- * that a query does not see does not reach it, whatever its K and V rows hold
- * (infinities and NaN too), and slots past T_b are not read as numbers.
+ * 1 with bit 0 set is single-token decoding with those score options. Of the
+ * bias, slopes[h] * pos_i is the same for all keys of a row and cancels in the
+ * softmax: it is formed relative to a key that weighs most in it, so
+ * positions far from the slots cost no accuracy. A key that a query does not
+ * see does not reach it, whatever its K and V rows hold (infinities and NaN
+ * too), and slots past T_b are not read as numbers.
  *   q            [B][M][Hq][D] bf16 (the prologue's q_out), 1 <= M <= 64
  *   tree_mask    [B][M] uint64, 8-byte aligned: bit j of entry (b, i) lets
  *                drafted token i see drafted token j (its ancestors and itself

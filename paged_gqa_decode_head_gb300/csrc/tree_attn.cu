@@ -64,6 +64,7 @@
 
 #include <atomic>
 #include <cfloat>
+#include <climits>
 #include <cmath>
 
 namespace pgqa {
@@ -607,7 +608,7 @@ __device__ __forceinline__ float prepare_scores(const TreeParams &p, float *x, f
 // 16 scores of any size from key `key` on, any of them drafted tokens, whose
 // positions are their own (pos_lo and pos_hi: this lane's, lane and lane + 32).
 template <int kScore>
-__device__ __forceinline__ void prepare_any_scores(const TreeParams &p, float *x, float slope, int key, int prefix, int pos,
+__device__ __forceinline__ void prepare_any_scores(const TreeParams &p, float *x, float slope, int key, int prefix, int anchor,
                                                    int pos_lo, int pos_hi)
 {
 #pragma unroll
@@ -629,7 +630,7 @@ __device__ __forceinline__ void prepare_any_scores(const TreeParams &p, float *x
         if constexpr ((kScore & 2) != 0) {
             const int d = key + j - prefix;
             const int drafted = __shfl_sync(0xFFFFFFFFu, d < 32 ? pos_lo : pos_hi, d & 31);
-            y = fmaf(slope, distance(d < 0 ? key + j : drafted, pos), y);
+            y = fmaf(slope, distance(d < 0 ? key + j : drafted, anchor), y);
         }
         x[j] = y;
     }
@@ -706,17 +707,15 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
     struct Row {
         uint64_t mask;
         float slope;
-        int pos, pos_lo, pos_hi; // its position; this lane's drafted tokens' (lane, lane + 32)
+        int pos_lo, pos_hi; // this lane's drafted tokens' positions (lane, lane + 32)
         bool live;
     };
     const auto fetch_row = [&](const Segments &of) {
-        Row r{0, 0.f, 0, 0, 0, real && token < of.n};
+        Row r{0, 0.f, 0, 0, real && token < of.n};
         if (r.live) {
             r.mask = p.tree_mask[static_cast<size_t>(of.b) * p.M + token];
-            if constexpr ((kScore & 2) != 0) {
+            if constexpr ((kScore & 2) != 0)
                 r.slope = p.slopes[of.h * p.g + row % p.g] * kLog2e;
-                r.pos = p.positions[static_cast<size_t>(of.b) * p.M + token];
-            }
         }
         if constexpr ((kScore & 2) != 0) {
             const int32_t *at = p.positions + static_cast<size_t>(of.b) * p.M;
@@ -736,7 +735,31 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
         const bool live = next_row.live;
         const uint64_t mask = seg.n < 64 ? next_row.mask & ((1ull << seg.n) - 1ull) : next_row.mask;
         const float slope = next_row.slope;
-        const int pos = next_row.pos, pos_lo = next_row.pos_lo, pos_hi = next_row.pos_hi;
+        const int pos_lo = next_row.pos_lo, pos_hi = next_row.pos_hi;
+        // A row's own position is a constant of its scores, slope * pos_i, and cancels in
+        // the softmax. The bias is taken relative to `anchor` instead, at or within 64
+        // positions of the visible key that it favours most, so that the scores that count
+        // keep their bits however far pos_i lies from them. It depends on the row alone,
+        // so the pieces of a (sequence, head) agree. Drafted tokens around the prefix's end
+        // leave the prefix's first or last key; others are looked through.
+        int anchor = 0;
+        if constexpr ((kScore & 2) != 0) {
+            const bool falls = slope < 0.f; // along the keys
+            const auto near = [&](int j, int pos) {
+                return j >= seg.n || static_cast<uint32_t>(pos) - static_cast<uint32_t>(prefix) + 64u < 128u;
+            };
+            anchor = falls ? 0 : prefix;
+            if (!__all_sync(0xFFFFFFFFu, near(lane, pos_lo) && near(lane + 32, pos_hi))) {
+                if (prefix == 0)
+                    anchor = falls ? INT_MAX : INT_MIN;
+#pragma unroll 1
+                for (int j = 0; j < seg.n; ++j) {
+                    const int pos = __shfl_sync(0xFFFFFFFFu, j < 32 ? pos_lo : pos_hi, j & 31);
+                    if (mask >> j & 1u)
+                        anchor = falls ? min(anchor, pos) : max(anchor, pos);
+                }
+            }
+        }
         const int seg_steps = (seg.seg_tile1 - seg.seg_tile0) * (pair ? 2 : 1);
         float m = -INFINITY; // the reference, in units of 1 / c
         float l = 0.f;
@@ -773,7 +796,7 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
                             tmem_wait_ld16(y[k]);
                             tmem_ld16(y[k ^ 1], tmem_s + 16 * ((i + k + 1) & 7));
                             const int key = key0 + 16 * (i + k);
-                            const float over = prepare_scores<kScore, 16>(p, y[k], slope, distance(key, pos));
+                            const float over = prepare_scores<kScore, 16>(p, y[k], slope, distance(key, anchor));
                             const bool rest = __any_sync(0xFFFFFFFFu, live && over > 1.f) || (key + 16 > prefix && key < seg.T);
                             if (rest)
                                 left |= 1u << (i + k);
@@ -803,7 +826,7 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
                             float y[16];
                             tmem_ld16(y, tmem_s + 16 * i);
                             tmem_wait_ld16(y);
-                            prepare_any_scores<kScore>(p, y, slope, key0 + 16 * i, prefix, pos, pos_lo, pos_hi);
+                            prepare_any_scores<kScore>(p, y, slope, key0 + 16 * i, prefix, anchor, pos_lo, pos_hi);
                             tmem_st16(tmem_s + 16 * i, y);
                         }
                     }

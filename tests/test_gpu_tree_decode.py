@@ -969,3 +969,42 @@ def test_a_longer_decode_may_follow_a_single_token_prologue_directly(follower):
     for _ in range(25):
         assert torch.equal(run(False), want)
     assert pg.device_error_flags() == 0
+
+
+@pytest.mark.parametrize("far", [-2 ** 31, -70000, 10 ** 6, 2 ** 31 - 1])
+def test_a_row_own_position_cancels(far):
+    """Rows that see only the prefix: slope (pos_j - pos_i) is the same for every pos_i up to a constant of the row,
+    which the softmax does not see, so the result and its bound are those of pos_i = prefix, wherever pos_i lies."""
+    c = Case(1870, [300, 77], 5, Hq=8, Hkv=4, masks=[[0] * 5] * 2, slopes=[0.5, 1.0, 2.0 ** -8, 0.07, 3.0, 0.3, 0.01, 0.0])
+    c.positions[:] = far
+    of, ob = c.run()
+    c.positions[:] = np.array([295, 72], np.int32)[:, None]
+    out, bound = c.reference()
+    check_outputs(of, ob, out, bound, c.n)
+
+
+@pytest.mark.parametrize("T", [300, 12000])
+def test_slopes_that_favour_the_first_keys(T):
+    """Negative slopes: the first keys weigh most, however far behind them the row is. The result and its bound are
+    those of pos_i = 0 (a constant of the row again)."""
+    c = Case(1880 + T, [T], 3, Hq=4, Hkv=2, masks=[[0] * 3], slopes=[-0.5, -1.0, -7.0, -0.02])
+    of, ob = c.run()
+    c.positions[:] = 0
+    out, bound = c.reference()
+    check_outputs(of, ob, out, bound, c.n)
+
+
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+def test_drafted_tokens_far_from_the_prefix(softcap):
+    """Drafted tokens whose positions lie 10^9 past the prefix (or before it, for the heads with a negative slope): with
+    slopes of at least 0.5 the prefix weighs nothing at 5000 positions already, so the result and its bound are those
+    of drafted tokens that are 5000 away."""
+    slopes = [0.5, 1.0, 0.7, 2.0]
+    for sign in (1, -1):
+        c = Case(1890, [300, 40], 24, Hq=4, Hkv=2, slopes=[sign * x for x in slopes], softcap=softcap, roots=2)
+        near = c.positions.copy()
+        c.positions = (near + sign * 10 ** 9).astype(np.int32)
+        of, ob = c.run()
+        c.positions = near + sign * 5000
+        out, bound = c.reference()
+        check_outputs(of, ob, out, bound, c.n)
