@@ -550,6 +550,18 @@ def _raw_stream(stream, device):
     return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
+def _axis_bytes(axis_of_pair) -> bytes:
+    """64 axis numbers as bytes, from a sequence, an array or a tensor of integers."""
+    if not isinstance(axis_of_pair, (list, tuple, bytes, bytearray)):
+        if isinstance(axis_of_pair, (int, str)):
+            raise TypeError("axis_of_pair must be a sequence of 64 axis numbers")
+        axis_of_pair = list(axis_of_pair)  # number by number: bytes() would take an array's memory
+    axes = bytes(axis_of_pair)
+    if len(axes) != 64:
+        raise ValueError(f"axis_of_pair must hold 64 axis numbers, got {len(axes)}")
+    return axes
+
+
 def qk_norm_rope_append_axes(q, k, v, gamma_q, gamma_k, positions, context_lens, block_table, k_cache, v_cache, q_out,
                              axis_of_pair, rope_theta: float, eps: float = 1e-6, new_lens=None, stream=None) -> None:
     """Prologue with given rotary positions on 1 to 4 axes: q [B, M, Hq, D], k/v [B, M, Hkv, D], positions
@@ -560,11 +572,7 @@ def qk_norm_rope_append_axes(q, k, v, gamma_q, gamma_k, positions, context_lens,
     B, M, Hq, D = q.shape
     num_pages, Hkv, P, _ = k_cache.shape
     max_pages, n_axes = block_table.shape[-1], positions.shape[-1]
-    if isinstance(axis_of_pair, int):
-        raise TypeError("axis_of_pair must be a sequence of 64 axis numbers")
-    axes = bytes(axis_of_pair)
-    if len(axes) != 64:
-        raise ValueError(f"axis_of_pair must hold 64 axis numbers, got {len(axes)}")
+    axes = _axis_bytes(axis_of_pair)
     new, cache = (B, M, Hkv, D), (num_pages, Hkv, P, D)
     st = lib.qk_norm_rope_append_axes(
         _arg(q, bf, q.shape, "q", here), _arg(k, bf, new, "k", here), _arg(v, bf, new, "v", here),

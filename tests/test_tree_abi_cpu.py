@@ -5,6 +5,7 @@ import math
 
 import numpy as np
 import pytest
+import torch
 
 import paged_gqa_decode_head_gb300 as pg
 import tree_reference as ref
@@ -151,3 +152,21 @@ def test_reference_rotation_keeps_relative_positions():
     a = at(x[0], [5, 9, 30]) @ at(x[1], [3, 2, 7])
     b = at(x[0], [105, 59, 1030]) @ at(x[1], [103, 52, 1007])
     assert abs(a - b) < 1e-9
+
+
+@pytest.mark.parametrize("make", [list, tuple, bytes, bytearray, np.array, lambda x: np.array(x, np.int32),
+                                  lambda x: np.array(x, np.uint8), torch.tensor,
+                                  lambda x: torch.tensor(x, dtype=torch.int32), iter])
+def test_axes_of_any_sequence(make):
+    """Axis numbers are taken one by one, whatever holds them."""
+    axes = [0] * 16 + [1] * 24 + [2] * 24
+    assert binding._axis_bytes(make(axes)) == bytes(axes)
+
+
+@pytest.mark.parametrize("axes", [[0] * 63, [0] * 65, 64, "0" * 64, np.zeros(16, np.int32), np.zeros(8, np.int64),
+                                  torch.zeros(16, dtype=torch.int32), [-1] * 64, [256] * 64, [0.0] * 64,
+                                  np.zeros((64, 1), np.int32), None])
+def test_axes_that_are_no_64_numbers_are_refused(axes):
+    """Among them arrays of 64 bytes of memory that hold fewer numbers."""
+    with pytest.raises((TypeError, ValueError)):
+        binding._axis_bytes(axes)
