@@ -1452,10 +1452,16 @@ cudaError_t launch_tree_attn(const TreeAttnArgs &a, cudaStream_t stream)
     if (err != cudaSuccess)
         return err;
     // Four warps a row where a (sequence, head) is cut into many pieces, one where
-    // there are many heads and few pieces each: t = 8192, 64 drafted tokens (20
-    // pieces) 25.1 us with four, 30.1 with one; B = 8, 64 drafted tokens, g = 8 (2
-    // or 3 pieces) 334 us with four, 279 with one.
-    const int parts = y.ctas >= 4ll * a.B * a.Hkv ? 4 : 1, per_block = kMergeThreads / 32 / parts;
+    // there are few pieces each or many rows (four times the blocks). With four and
+    // one, g = 2 unless said, pieces being CTAs per head: 19 pieces, 128 to 2048 rows in all
+    // (M = 8 to 32, g = 8 at last): 21.1 and 25.2, 16.9 and 23.5, 25.5 and 31.1 us; 9.5
+    // pieces, 1024, 2048 and 4096 rows: 22.0 and 24.5, 21.7 and 22.3, 37.7 and 32.2; 6.3
+    // pieces, 768 and 1536: 20.3 and 20.7, 27.1 and 25.9; 4.75 pieces, 1024 and 2048: 26.4
+    // and 27.2, 30.7 and 28.6; 3.2 pieces, 144, 384 and 1536: 30.4 and 30.3, 24.8 and 24.5,
+    // 26.8 and 25.0; 1.2 pieces, 32768 (g = 8): 153 and 102.
+    const long long heads = static_cast<long long>(a.B) * a.Hkv, rows_in_all = static_cast<long long>(a.B) * a.M * a.Hq;
+    const int parts = y.ctas >= 4 * heads && rows_in_all * heads <= 220ll * y.ctas ? 4 : 1;
+    const int per_block = kMergeThreads / 32 / parts;
     const dim3 grid(static_cast<unsigned>((a.M * p.g + per_block - 1) / per_block), static_cast<unsigned>(a.Hkv),
                     static_cast<unsigned>(a.B));
     return launch_pdl(parts == 4 ? tree_merge_kernel<4> : tree_merge_kernel<1>, grid, dim3(kMergeThreads), 0, stream, p);
