@@ -741,7 +741,9 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
         // positions of the visible key that it favours most, so that the scores that count
         // keep their bits however far pos_i lies from them. It depends on the row alone,
         // so the pieces of a (sequence, head) agree. Drafted tokens around the prefix's end
-        // leave the prefix's first or last key; others are looked through.
+        // and slopes of at most 2 in base 2 (a bias of at most 256 there: half a unit in the
+        // last place is 2^-17, as much as a weight's pair loses) leave the prefix's first key
+        // or its end; otherwise the drafted tokens are looked through.
         int anchor = 0;
         if constexpr ((kScore & 2) != 0) {
             const bool falls = slope < 0.f; // along the keys
@@ -749,7 +751,7 @@ __device__ bool soften(const TreeParams &p, TreeSmem &s, int rg, bool pair, int 
                 return j >= seg.n || static_cast<uint32_t>(pos) - static_cast<uint32_t>(prefix) + 64u < 128u;
             };
             anchor = falls ? 0 : prefix;
-            if (!__all_sync(0xFFFFFFFFu, near(lane, pos_lo) && near(lane + 32, pos_hi))) {
+            if (!__all_sync(0xFFFFFFFFu, near(lane, pos_lo) && near(lane + 32, pos_hi) && fabsf(slope) <= 2.f)) {
                 if (prefix == 0)
                     anchor = falls ? INT_MAX : INT_MIN;
 #pragma unroll 1

@@ -1008,3 +1008,14 @@ def test_drafted_tokens_far_from_the_prefix(softcap):
         c.positions = near + sign * 5000
         out, bound = c.reference()
         check_outputs(of, ob, out, bound, c.n)
+
+
+@pytest.mark.parametrize("T", [8, 60])
+def test_steep_slopes_keep_scores_of_equal_positions_apart(T):
+    """Drafted tokens that all lie 40 past the prefix, seen by all rows: among them the scores decide, however steep the
+    slope. A row's own position is one of them, so the bound counts the bias from there."""
+    c = Case(1900 + T, [T], 8, Hq=4, Hkv=2, masks=[[255] * 8], slopes=[1e4, -1e4, 1e30, -1e30])
+    c.positions[:] = T - 8 + 40
+    if T > 8:
+        c.slopes = np.abs(c.slopes)  # (a negative slope favours the prefix)
+    c.check()
