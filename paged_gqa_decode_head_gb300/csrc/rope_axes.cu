@@ -19,10 +19,10 @@
 // its 16 groups of 8 lanes walk the tokens' Hq + 2 Hkv rows with 16-byte loads
 // and stores, two rows of a group on their way at a time (lane s of a group
 // holds dims 8s .. 8s+7 and 64 + 8s .. 64 + 8s + 7, so a pair's two halves are in
-// one lane). Measured (32 query, 8 KV heads): 32768 tokens 127 us, 6.3 TB/s, 93 % of
-// the measured copy bandwidth; 19387 tokens in 8 ragged sequences of 4096 79 us, 6.0
-// TB/s; 4095 tokens of 16 + 8 heads 13.9 us, 4.8 TB/s (the start and end of its
-// blocks); 16 tokens 3.1 us, a launch and three trips to memory.
+// one lane). Measured (32 query, 8 KV heads): 32768 tokens 128 us, 6.3 TB/s, 93 % of
+// the measured copy bandwidth; 19658 tokens in 8 ragged sequences of up to 4096 80 us,
+// 6.0 TB/s; 4095 tokens of 16 + 8 heads 13.9 us, 4.8 TB/s (the start and end of its
+// blocks); 1 or 16 tokens 3.4 us, a launch and three trips to memory.
 #include "common.cuh"
 #include "launch.h"
 
@@ -239,11 +239,11 @@ cudaError_t launch_rope_axes(const RopeAxesArgs &a, cudaStream_t stream)
     // One token per block as long as all blocks run at once, then two, then three:
     // a block that had to wait for another's end costs more than the longer blocks,
     // which share the trips to lengths and tables. Tokens of 16 + 8 heads with one, two
-    // and three per block: 1100 6.9, 7.6, 8.7 us; 1500 10.9, 8.6, 9.4 us; 2700 13.5,
-    // 10.8, 11.6 us; 3192 16.2, 14.8, 12.5 us; 4095 18.5, 16.5, 14.4 us. Four: 4095 15.1 us.
-    // Past that, three of up to 32 rows (16384: 57, 49, 47 us) and two of more (32 + 8
-    // heads: 8 ragged sequences to 4096 83, 70, 70 us and, other lengths, 54.0 us with
-    // two, 56.1 us with three; 8192 41.7, 36.0, 36.4 us).
+    // and three per block: 16 3.4, 4.4, 5.4 us; 1100 6.6, 7.1, 8.1 us; 1500 9.9, 7.9, 8.7
+    // us; 2700 12.9, 10.2, 10.9 us; 3192 15.6, 14.4, 11.8 us; 4095 18.1, 16.0, 13.9 us (four:
+    // 15). Past that, three of up to 32 rows (16384: 57.1, 48.7, 47.0 us) and two of more
+    // (32 + 8 heads: 8192 41.8, 36.0, 36.4 us; 19658 in 8 ragged sequences 96.8, 80.2, 81.3
+    // us; 32768 144.6, 127.8, 128.0 us).
     const long long at_once = static_cast<long long>(kRopeBlocksPerSm) * (a.sm_count > 0 ? a.sm_count : 1);
     const long long per_block = (static_cast<long long>(a.B) * a.M + at_once - 1) / at_once;
     const int tokens = per_block <= 3 ? static_cast<int>(per_block) : a.Hq + 2 * a.Hkv <= 32 ? 3 : 2;

@@ -4,10 +4,11 @@
 // Mathematics. For the R = M * g query rows (drafted token, head) that share a
 // KV head: x = scale Q K^T, capped and biased; softmax over the keys that the
 // row sees (the prefix, and the drafted tokens of its mask); O = P V. Computed
-// over tiles of 128 keys with a running reference m and sum l per row (online
-// softmax in base 2): p = 2^(y - m), l += p, O += p V; when a row's scores rise
-// more than 8 above m, m moves up and l and O are scaled (2^8 is far inside
-// fp32's range, so most tiles need no rescale).
+// over tiles of 128 keys with a running reference m and sum l per row (the online
+// normaliser of Milakov and Gimelshein, 2018, in base 2): p = 2^(y - m), l += p, O
+// += p V. m need not be the maximum: only when a row's scores rise more than 8 above
+// it does it move up, and l and O are scaled (2^8 is far inside fp32's range, so
+// most tiles need no rescale).
 //
 // Bound. The cache is read once: 512 bytes per (key, KV head) against 4 * 128 * R
 // flops. Up to R of about 200 the memory bounds it, above that the tensor cores.
@@ -46,17 +47,20 @@
 // is half as much tensor work again; S, O, m and l are fp32.
 //
 // Measured (GB300; bf16 outputs; HBM at the measured copy bandwidth of 6.78 TB/s):
-//   B = 64, ragged to 32768, 16 drafted, g = 2: 597 us, 6.6 TB/s of K and V (97 %);
-//   B = 1, T = 131072, 16 drafted, g = 4, capped: 114 us, 4.7 TB/s (the cap's
-//     polynomial, and the run's start and end);
+//   B = 64, ragged to 32768, 16 drafted, g = 2 (3.9 GB): 614 us, 6.4 TB/s of K and V (95 %);
+//   B = 1, T = 131072, 16 drafted, g = 4, capped: 113 to 120 us, 4.5 to 4.7 TB/s (the
+//     cap's polynomial, and the run's start and end);
 //   B = 8, T = 16384, 64 drafted, g = 8: 279 us, 986 TFLOP/s and half as much again
 //     for lo, under the power limit (4000 clocks for two steps, whose 48 products
 //     take 64 each);
-//   B = 1, T = 8192, g = 2: 16 drafted 20.9 us, 64 drafted 25.1 us (the lengths, the
+//   B = 1, T = 8192, g = 2: 16 drafted 20.8 us, 64 drafted 24.8 us (the lengths, the
 //     table and the first tile are three trips to memory before the first product;
 //     joining the pieces is a second kernel);
-//   B = 33, ragged to 4001, one token, g = 3, capped and biased: 118 us, 2.3 TB/s (one
-//     warp of each stream holds all rows, both on the same SM partition).
+//   B = 33, ragged to 4001, one token, g = 3, capped and biased: 119 to 129 us, 2.1 to
+//     2.3 TB/s (one warp of each stream holds all rows, both on the same SM partition).
+// Chains of M * g <= 8 rows without cap and bias are faster in decode_attn_paged_multi
+// (T = 8192, g = 2, 1 and 4 tokens: 8.7 and 10.0 us, here 19.6 and 20.3; B = 64, ragged to
+// 32768, 4 tokens: 634 and 721 us).
 #include "common.cuh"
 #include "launch.h"
 #include "tcgen05.cuh"
