@@ -39,8 +39,8 @@ struct CommitParams {
 __global__ void __launch_bounds__(kCommitThreads) commit_path_kernel(const __grid_constant__ CommitParams p)
 {
     // The next kernel may read tables, lengths and cache rows before it waits for
-    // this one (the decode kernels do): no early launch of it here, and every
-    // write is performed before its thread ends.
+    // this one (the decode kernels do, rows by bulk copies): no early launch of it
+    // here, and every write is performed before its thread ends, rows for such reads too.
     grid_dependency_wait();
     __shared__ long long from[kMaxDrafted], to[kMaxDrafted]; // cache rows of KV head 0, -1: page outside the pool
     const int tid = threadIdx.x;
@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(kCommitThreads) commit_path_kernel(const __gri
         __syncthreads();
     }
     __threadfence();
+    fence_proxy_async_global();
 }
 
 } // namespace

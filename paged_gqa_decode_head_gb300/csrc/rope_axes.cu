@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_axes_kern
     // next kernel may read cache rows before it waits for this one (the decode
     // kernels do, up to a length of their own and through a table of their own):
     // no early launch of it, not behind a single token's row either, and every
-    // write is performed before its thread ends.
+    // write is performed before its thread ends, also for reads by bulk copies.
     grid_dependency_wait();
     const int tid = threadIdx.x;
     const int b = blockIdx.x / p.blocks_per_seq, i0 = (blockIdx.x - b * p.blocks_per_seq) * kTokens;
@@ -194,6 +194,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_axes_kern
         }
     }
     __threadfence(); // performed before the thread ends, and so before the next kernel starts
+    fence_proxy_async_global();
 }
 
 } // namespace
