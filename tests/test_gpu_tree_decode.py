@@ -1019,3 +1019,7 @@ def test_steep_slopes_keep_scores_of_equal_positions_apart(T):
     if T > 8:
         c.slopes = np.abs(c.slopes)  # (a negative slope favours the prefix)
     c.check()
+
+
+def test_prologue_of_single_tokens_that_may_be_absent():
+    check_prologue(prologue_case(2260, [0, 1, 40, 33], 1, 3, INTERLEAVED, new_lens=[0, 1, 0, 1], big=True))
