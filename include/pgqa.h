@@ -13,8 +13,10 @@
  *     tiles are streamed in from pinned host memory, and a zero-copy variant
  *     that reads a history held in pinned host memory directly;
  *   - drafted-tree decoding: a prologue whose rotary positions are given on
- *     several axes, attention of a tree of drafted tokens over the cache, and
- *     the move of the accepted path's rows behind the prefix.
+ *     several axes, attention of a tree of drafted tokens over the cache, the
+ *     verification of the drafted tokens against the target's logits, and the
+ *     move of the accepted path's rows behind the prefix, over bf16 and INT8
+ *     caches.
  *
  * Sources (page title, section):
  *   "From Qwen3 math to CUDA kernels: a 0.6B inference runtime"
@@ -497,7 +499,8 @@ int decode_attn_paged_static(const pgqa_bf16 *q, const pgqa_bf16 *k_cache,
  * occupies slot T_b - n_b + i until the step is committed. A step is
  * qk_norm_rope_append_axes, decode_attn_paged_tree (per layer), then
  * kv_cache_commit_path once for all layers.
- * The caches are bf16: an INT8 cache has no drafted-tree step. For a chain (or
+ * These calls take bf16 caches; the *_int8 calls below are the same step over an
+ * INT8 cache, and verify_drafted_tree finds the accepted path. For a chain (or
  * a single token) with M * (Hq / Hkv) <= 8 and neither cap nor slopes,
  * decode_attn_paged_multi (decode_attn_paged), or the fused step, gives the
  * same attention sooner: in half the time for one sequence of 8192.
@@ -615,6 +618,126 @@ int kv_cache_commit_path(pgqa_bf16 *const *k_caches, pgqa_bf16 *const *v_caches,
                          const int32_t *draft_lens, const int32_t *path, const int32_t *path_lens,
                          int32_t *context_lens_out, int B, int M, int A, int Hkv, int D, int page_size,
                          int max_pages, int num_pages, cudaStream_t stream);
+
+/*
+ * Drafted-tree decoding over an INT8 cache (layout and quantization as for
+ * qk_norm_rope_append_int8): the three calls above with codes and scales in the
+ * caches' place. All rules and limits of the bf16 forms hold.
+ *
+ * qk_norm_rope_append_axes_int8 -- K is quantized after its rotation and bf16
+ *   rounding, V as given; for the same rows the bytes are those of
+ *   qk_norm_rope_append_int8's quantization. A row with no finite maximum (an
+ *   infinity in it) has that as its scale.
+ * decode_attn_paged_tree_int8 -- K_j = code * k_scale_j, V_j = code * v_scale_j;
+ *   the codes enter the products exactly, as fp16, the scales multiply scores and
+ *   weights in fp32. The query must lie in the fp16 range (|q| < 65504). A key that a
+ *   query does not see does not reach it, whatever its scales hold. Weights enter
+ *   the product with V as an fp16 hi + lo pair. Workspace: device scratch of
+ *   ws_bytes >= decode_attn_tree_int8_workspace_size (of the current device); no
+ *   initial value needed. Calls whose work may overlap on the GPU must not share one.
+ * kv_cache_commit_path_int8 -- codes and scales move together, bit for bit.
+ *   k_caches8, v_caches8, k_scales, v_scales, block_tables: HOST arrays of n_layers
+ *   device pointers, read during the call; two layers may not share a table and
+ *   any cache or scale array.
+ */
+int qk_norm_rope_append_axes_int8(const pgqa_bf16 *q, const pgqa_bf16 *k, const pgqa_bf16 *v,
+                                  const pgqa_bf16 *gamma_q, const pgqa_bf16 *gamma_k, const int32_t *positions,
+                                  int n_axes, const uint8_t *axis_of_pair, const int32_t *context_lens,
+                                  const int32_t *new_lens, const int32_t *block_table, int8_t *k_cache8,
+                                  int8_t *v_cache8, float *k_scale, float *v_scale, pgqa_bf16 *q_out, int B,
+                                  int M, int Hq, int Hkv, int D, int page_size, int max_pages, int num_pages,
+                                  float rope_theta, float eps, cudaStream_t stream);
+size_t decode_attn_tree_int8_workspace_size(int B, int M, int Hq, int Hkv, int D, int page_size, int max_pages);
+int decode_attn_paged_tree_int8(const pgqa_bf16 *q, const int8_t *k_cache8, const int8_t *v_cache8,
+                                const float *k_scale, const float *v_scale, const int32_t *block_table,
+                                const int32_t *context_lens, const uint64_t *tree_mask, const int32_t *positions,
+                                const int32_t *draft_lens, const float *slopes, int B, int M, int Hq, int Hkv, int D,
+                                int page_size, int max_pages, int num_pages, float scale, float softcap,
+                                float *out_f32, pgqa_bf16 *out_bf16, void *workspace, size_t ws_bytes,
+                                cudaStream_t stream);
+int kv_cache_commit_path_int8(int8_t *const *k_caches8, int8_t *const *v_caches8, float *const *k_scales,
+                              float *const *v_scales, const int32_t *const *block_tables, int n_layers,
+                              const int32_t *context_lens, const int32_t *draft_lens, const int32_t *path,
+                              const int32_t *path_lens, int32_t *context_lens_out, int B, int M, int A, int Hkv,
+                              int D, int page_size, int max_pages, int num_pages, cudaStream_t stream);
+
+/*
+ * kv_cache_read_int8 -- rows of the INT8 cache read back as bf16(code * scale), for
+ * attention of a prompt's later chunks, for moving a sequence, or for inspection.
+ *   first        [B] int32, nullable (NULL: 0): the first slot read of each sequence
+ *   k_out, v_out [B][N][Hkv][D] bf16: row i holds slot first[b] + i, for the slots
+ *                below T_b; the other rows are left as they were. No overlap with
+ *                the inputs.
+ * N >= 0. A sequence with T_b outside [0, max_pages * page_size] or first[b] < 0 is
+ * skipped (PGQA_DEVERR_BAD_CONTEXT), rows of a page outside the pool are skipped
+ * (PGQA_DEVERR_BAD_PAGE). Every input is read after the previous kernel in the
+ * stream completes.
+ */
+int kv_cache_read_int8(const int8_t *k_cache8, const int8_t *v_cache8, const float *k_scale, const float *v_scale,
+                       const int32_t *block_table, const int32_t *context_lens, const int32_t *first,
+                       pgqa_bf16 *k_out, pgqa_bf16 *v_out, int B, int N, int Hkv, int D, int page_size,
+                       int max_pages, int num_pages, cudaStream_t stream);
+
+/*
+ * verify_drafted_tree -- which of the drafted tokens the target model accepts, and
+ * the token behind the accepted path, from given random numbers (no counterpart on
+ * the pages). Its path and path_lens are what kv_cache_commit_path takes.
+ *
+ * Token 0 is the root: the token that the last step ended with, which is part of
+ * the path without a test. At the path's last node, with p = softmax(target row /
+ * temperature), the node's children (drafted tokens i < n_b whose parent it is) are
+ * tested in order until one is accepted, which then is the path's next node:
+ *   without draft_logits the children are taken as given; child i, token t, is
+ *     accepted if accept_u[b][i] < p(t); a rejection takes t out of p and renormalises;
+ *   with draft_logits they were drawn one after the other, without replacement,
+ *     from q = softmax(draft row / temperature); child i is accepted if accept_u[b][i]
+ *     < p(t) / q(t); a rejection leaves p <- max(p - q, 0) and takes t out of p and q,
+ *     both renormalised. (A child counts as given once rounding leaves nothing of q.)
+ * Where no child is left, or the path has A entries, the last token is drawn from
+ * what is left of p: argmax_i p_i / noise[b][i] (an exponential race: with noise ~
+ * Exp(1) and accept_u ~ U[0, 1) the new tokens are distributed as if they had been
+ * sampled from the target one by one). Ties go to the lowest index. If rounding
+ * leaves nothing of p, the node's full p takes its place.
+ * temperature 0 is greedy: a child is accepted if its token is the row's first
+ * maximum, which is the last token otherwise; accept_u and noise are not used.
+ *
+ *   target_logits [B][M] rows of V logits, draft_logits the same or NULL: bf16, or
+ *                float if logits_f32; 16-byte aligned. target_stride, draft_stride:
+ *                elements from one row to the next, >= V (row (b, i) is number b * M +
+ *                i). -inf masks a token; NaN counts as -inf, +inf as the largest number.
+ *   tokens       [B][M] int32, the drafted tokens. One outside [0, V) is never accepted
+ *                and tests nothing (PGQA_DEVERR_BAD_PATH); tokens[b][0] is not read as one.
+ *   parents      [B][M] int32: the parent's index, below the token's own (others are
+ *                never reached); parents[b][0] is ignored
+ *   draft_lens   [B] int32, nullable: n_b in [0, M] (NULL: M)
+ *   temperatures [B] float >= 0
+ *   accept_u     [B][M] float in [0, 1)
+ *   noise        [B][V] float > 0, 16-byte aligned
+ *   path         [B][A] int32, 1 <= A <= M: the accepted tokens' indices, path[b][0] =
+ *                0, strictly increasing; -1 behind them
+ *   path_lens    [B] int32: entries of the path, which is also the number of new
+ *                tokens of the step (0 if n_b = 0)
+ *   new_tokens   [B][A] int32: entry i is the token that follows path[b][i], the last
+ *                one the drawn token (-1 where a row's logits are all masked); -1
+ *                behind them
+ *   logprobs     [B][A] float, nullable: log p of new_tokens in the node's full p
+ *                (temperature 1 where greedy); 0 where there is no token
+ *   workspace    device scratch of ws_bytes >= verify_drafted_tree_workspace_size (of
+ *                the current device; may be NULL when that is 0); no initial value
+ *                needed. Calls whose work may overlap on the GPU must not share one.
+ * The outputs must not overlap the inputs. V <= PGQA_MAX_VOCABULARY. A sequence with
+ * n_b outside [0, M] or a temperature that is negative or NaN gets an empty path
+ * (PGQA_DEVERR_BAD_CONTEXT). Every input is read after the previous kernel in the
+ * stream completes. Arithmetic in fp32; reproducible bit for bit for given
+ * arguments on a given device.
+ */
+#define PGQA_MAX_VOCABULARY (1 << 24)
+size_t verify_drafted_tree_workspace_size(int B, int M, int V);
+int verify_drafted_tree(const void *target_logits, const void *draft_logits, int logits_f32, long long target_stride,
+                        long long draft_stride, const int32_t *tokens, const int32_t *parents,
+                        const int32_t *draft_lens, const float *temperatures, const float *accept_u,
+                        const float *noise, int B, int M, int A, int V, int32_t *path, int32_t *path_lens,
+                        int32_t *new_tokens, float *logprobs, void *workspace, size_t ws_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -7,6 +7,7 @@ raises if the library is missing (there is no CPU fallback).
 """
 from .binding import (  # noqa: F401
     CacheLayers,
+    CacheLayersInt8,
     PgqaError,
     attn_host_direct,
     attn_host_direct_partition_count,
@@ -23,6 +24,8 @@ from .binding import (  # noqa: F401
     decode_attn_paged_multi,
     decode_attn_paged_static,
     decode_attn_paged_tree,
+    decode_attn_paged_tree_int8,
+    decode_attn_tree_int8_workspace_size,
     decode_attn_tree_workspace_size,
     decode_step_paged,
     decode_step_paged_int8,
@@ -31,10 +34,15 @@ from .binding import (  # noqa: F401
     decode_attn_workspace_size,
     device_error_flags,
     kv_cache_commit_path,
+    kv_cache_commit_path_int8,
+    kv_cache_read_int8,
     library_path,
     load_library,
     qk_norm_rope_append,
     qk_norm_rope_append_axes,
+    qk_norm_rope_append_axes_int8,
     qk_norm_rope_append_int8,
     qk_norm_rope_append_multi,
+    verify_drafted_tree,
+    verify_drafted_tree_workspace_size,
 )

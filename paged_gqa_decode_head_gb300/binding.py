@@ -51,6 +51,13 @@ EXPORTED = (
     "decode_attn_tree_workspace_size",
     "decode_attn_paged_tree",
     "kv_cache_commit_path",
+    "qk_norm_rope_append_axes_int8",
+    "decode_attn_tree_int8_workspace_size",
+    "decode_attn_paged_tree_int8",
+    "kv_cache_commit_path_int8",
+    "kv_cache_read_int8",
+    "verify_drafted_tree_workspace_size",
+    "verify_drafted_tree",
 )
 
 STATUS_NAMES = {
@@ -149,6 +156,21 @@ def load_library(path: str | None = None):
         lib.decode_attn_tree_workspace_size.restype = S
         lib.decode_attn_paged_tree.argtypes = [P] * 9 + [I] * 8 + [F, F, P, P, P, S, P]
         lib.decode_attn_paged_tree.restype = I
+        lib.qk_norm_rope_append_axes_int8.argtypes = [P] * 6 + [I, P] + [P] * 8 + [I] * 8 + [F, F, P]
+        lib.qk_norm_rope_append_axes_int8.restype = I
+        lib.decode_attn_tree_int8_workspace_size.argtypes = [I] * 7
+        lib.decode_attn_tree_int8_workspace_size.restype = S
+        lib.decode_attn_paged_tree_int8.argtypes = [P] * 11 + [I] * 8 + [F, F, P, P, P, S, P]
+        lib.decode_attn_paged_tree_int8.restype = I
+        lib.kv_cache_commit_path_int8.argtypes = [P] * 5 + [I] + [P] * 5 + [I] * 8 + [P]
+        lib.kv_cache_commit_path_int8.restype = I
+        lib.kv_cache_read_int8.argtypes = [P] * 9 + [I] * 7 + [P]
+        lib.kv_cache_read_int8.restype = I
+        lib.verify_drafted_tree_workspace_size.argtypes = [I] * 3
+        lib.verify_drafted_tree_workspace_size.restype = S
+        lib.verify_drafted_tree.argtypes = [P, P, I, ctypes.c_longlong, ctypes.c_longlong] + [P] * 6 + [I] * 4 + [
+            P, P, P, P, P, S, P]
+        lib.verify_drafted_tree.restype = I
         lib.kv_cache_commit_path.argtypes = [P, P, P, I] + [P] * 5 + [I] * 8 + [P]
         lib.kv_cache_commit_path.restype = I
         _lib = lib
@@ -656,3 +678,180 @@ def kv_cache_commit_path(layers: CacheLayers, context_lens, path, path_lens, con
         A, layers.Hkv, layers.D, layers.page_size, layers.max_pages, layers.num_pages, _raw_stream(stream, here))
     if st:
         _check("kv_cache_commit_path", st)
+
+
+# ---------------------------------------------------------------- drafted-tree decoding over an INT8 cache
+def qk_norm_rope_append_axes_int8(q, k, v, gamma_q, gamma_k, positions, context_lens, block_table, k_cache8, v_cache8,
+                                  k_scale, v_scale, q_out, axis_of_pair, rope_theta: float, eps: float = 1e-6,
+                                  new_lens=None, stream=None) -> None:
+    """qk_norm_rope_append_axes writing INT8 codes [num_pages, Hkv, P, D] and their rows' scales, float32
+    [num_pages, Hkv, P]."""
+    lib = load_library()
+    bf, i32, f32, i8, here = torch.bfloat16, torch.int32, torch.float32, torch.int8, torch.cuda.current_device()
+    B, M, Hq, D = q.shape
+    num_pages, Hkv, P, _ = k_cache8.shape
+    max_pages, n_axes = block_table.shape[-1], positions.shape[-1]
+    axes = _axis_bytes(axis_of_pair)
+    new, cache, rows = (B, M, Hkv, D), (num_pages, Hkv, P, D), (num_pages, Hkv, P)
+    st = lib.qk_norm_rope_append_axes_int8(
+        _arg(q, bf, q.shape, "q", here), _arg(k, bf, new, "k", here), _arg(v, bf, new, "v", here),
+        _arg(gamma_q, bf, (D,), "gamma_q", here), _arg(gamma_k, bf, (D,), "gamma_k", here),
+        _arg(positions, i32, (B, M, n_axes), "positions", here), n_axes, axes,
+        _arg(context_lens, i32, (B,), "context_lens", here), _opt(new_lens, i32, (B,), "new_lens", here),
+        _arg(block_table, i32, (B, max_pages), "block_table", here), _arg(k_cache8, i8, cache, "k_cache8", here),
+        _arg(v_cache8, i8, cache, "v_cache8", here), _arg(k_scale, f32, rows, "k_scale", here),
+        _arg(v_scale, f32, rows, "v_scale", here), _arg(q_out, bf, q.shape, "q_out", here), B, M, Hq, Hkv, D, P,
+        max_pages, num_pages, float(rope_theta), float(eps), _raw_stream(stream, here))
+    if st:
+        _check("qk_norm_rope_append_axes_int8", st)
+
+
+def decode_attn_tree_int8_workspace_size(B: int, M: int, Hq: int, Hkv: int, D: int, page_size: int,
+                                         max_pages: int) -> int:
+    return int(load_library().decode_attn_tree_int8_workspace_size(B, M, Hq, Hkv, D, page_size, max_pages))
+
+
+def decode_attn_paged_tree_int8(q, k_cache8, v_cache8, k_scale, v_scale, block_table, context_lens, tree_mask,
+                                scale: float, positions=None, draft_lens=None, slopes=None, softcap: float = 0.0,
+                                out_f32=None, out_bf16=None, workspace=None, stream=None) -> None:
+    """decode_attn_paged_tree over an INT8 cache: codes [num_pages, Hkv, P, D], scales float32 [num_pages, Hkv, P];
+    workspace of decode_attn_tree_int8_workspace_size bytes."""
+    lib = load_library()
+    bf, i32, f32, i8, here = torch.bfloat16, torch.int32, torch.float32, torch.int8, torch.cuda.current_device()
+    B, M, Hq, D = q.shape
+    num_pages, Hkv, P, _ = k_cache8.shape
+    cache, rows = (num_pages, Hkv, P, D), (num_pages, Hkv, P)
+    max_pages = block_table.shape[-1]
+    ws_bytes = workspace.numel() if workspace is not None else 0
+    st = lib.decode_attn_paged_tree_int8(
+        _arg(q, bf, q.shape, "q", here), _arg(k_cache8, i8, cache, "k_cache8", here),
+        _arg(v_cache8, i8, cache, "v_cache8", here), _arg(k_scale, f32, rows, "k_scale", here),
+        _arg(v_scale, f32, rows, "v_scale", here), _arg(block_table, i32, (B, max_pages), "block_table", here),
+        _arg(context_lens, i32, (B,), "context_lens", here), _arg(tree_mask, torch.int64, (B, M), "tree_mask", here),
+        _opt(positions, i32, (B, M), "positions", here), _opt(draft_lens, i32, (B,), "draft_lens", here),
+        _opt(slopes, f32, (Hq,), "slopes", here), B, M, Hq, Hkv, D, P, max_pages, num_pages, float(scale), float(softcap),
+        _opt(out_f32, f32, q.shape, "out_f32", here), _opt(out_bf16, bf, q.shape, "out_bf16", here),
+        _opt(workspace, torch.uint8, (ws_bytes,), "workspace", here), ws_bytes, _raw_stream(stream, here))
+    if st:
+        _check("decode_attn_paged_tree_int8", st)
+
+
+class CacheLayersInt8:
+    """The paged INT8 caches (codes and scales) and block tables of a model's layers, as kv_cache_commit_path_int8
+    takes them. Checked once here; the object keeps the tensors alive. All layers have the same shapes."""
+
+    def __init__(self, k_caches8, v_caches8, k_scales, v_scales, block_tables):
+        n = len(k_caches8)
+        if n < 1 or any(len(x) != n for x in (v_caches8, k_scales, v_scales, block_tables)):
+            raise ValueError("CacheLayersInt8 needs the same number (at least 1) of K and V codes, K and V scales and "
+                             "block tables")
+        self.num_pages, self.Hkv, self.page_size, self.D = cache = k_caches8[0].shape
+        self.B, self.max_pages = table = block_tables[0].shape
+        self.device = k_caches8[0].device
+        array, here = ctypes.c_void_p * n, self.device.index
+
+        def pointers(tensors, dtype, shape, name):
+            return array(*[_arg(t, dtype, shape, f"{name}[{i}]", here) for i, t in enumerate(tensors)])
+
+        self.k_ptrs = pointers(k_caches8, torch.int8, cache, "k_caches8")
+        self.v_ptrs = pointers(v_caches8, torch.int8, cache, "v_caches8")
+        self.k_scale_ptrs = pointers(k_scales, torch.float32, cache[:3], "k_scales")
+        self.v_scale_ptrs = pointers(v_scales, torch.float32, cache[:3], "v_scales")
+        self.table_ptrs = pointers(block_tables, torch.int32, table, "block_tables")
+        self.tensors = tuple(list(x) for x in (k_caches8, v_caches8, k_scales, v_scales, block_tables))
+
+    def __len__(self) -> int:
+        return len(self.k_ptrs)
+
+
+def kv_cache_commit_path_int8(layers: CacheLayersInt8, context_lens, path, path_lens, context_lens_out, M: int,
+                              draft_lens=None, stream=None) -> None:
+    """kv_cache_commit_path over INT8 caches: codes and scales move together."""
+    lib = load_library()
+    i32, here = torch.int32, torch.cuda.current_device()
+    B, A = path.shape
+    if B != layers.B:
+        raise ValueError(f"path has {B} sequences, the layers' block tables {layers.B}")
+    if layers.device.index != here:
+        raise ValueError(f"the layers are on {layers.device}, the current device is cuda:{here}")
+    st = lib.kv_cache_commit_path_int8(
+        layers.k_ptrs, layers.v_ptrs, layers.k_scale_ptrs, layers.v_scale_ptrs, layers.table_ptrs, len(layers),
+        _arg(context_lens, i32, (B,), "context_lens", here), _opt(draft_lens, i32, (B,), "draft_lens", here),
+        _arg(path, i32, (B, A), "path", here), _arg(path_lens, i32, (B,), "path_lens", here),
+        _arg(context_lens_out, i32, (B,), "context_lens_out", here), B, M, A, layers.Hkv, layers.D, layers.page_size,
+        layers.max_pages, layers.num_pages, _raw_stream(stream, here))
+    if st:
+        _check("kv_cache_commit_path_int8", st)
+
+
+def kv_cache_read_int8(k_cache8, v_cache8, k_scale, v_scale, block_table, context_lens, k_out, v_out, first=None,
+                       stream=None) -> None:
+    """Rows of an INT8 cache read back as bf16: row i of k_out and v_out, [B, N, Hkv, D], is slot first[b] + i
+    (first: int32 [B], default 0) where that lies below context_lens[b]; other rows are left as they were."""
+    lib = load_library()
+    bf, i32, f32, i8, here = torch.bfloat16, torch.int32, torch.float32, torch.int8, torch.cuda.current_device()
+    num_pages, Hkv, P, D = k_cache8.shape
+    B, N = k_out.shape[:2]
+    cache, rows, out, max_pages = (num_pages, Hkv, P, D), (num_pages, Hkv, P), (B, N, Hkv, D), block_table.shape[-1]
+    st = lib.kv_cache_read_int8(
+        _arg(k_cache8, i8, cache, "k_cache8", here), _arg(v_cache8, i8, cache, "v_cache8", here),
+        _arg(k_scale, f32, rows, "k_scale", here), _arg(v_scale, f32, rows, "v_scale", here),
+        _arg(block_table, i32, (B, max_pages), "block_table", here), _arg(context_lens, i32, (B,), "context_lens", here),
+        _opt(first, i32, (B,), "first", here), _arg(k_out, bf, out, "k_out", here), _arg(v_out, bf, out, "v_out", here), B,
+        N, Hkv, D, P, max_pages, num_pages, _raw_stream(stream, here))
+    if st:
+        _check("kv_cache_read_int8", st)
+
+
+# ---------------------------------------------------------------- verification of drafted trees
+def verify_drafted_tree_workspace_size(B: int, M: int, V: int) -> int:
+    return int(load_library().verify_drafted_tree_workspace_size(B, M, V))
+
+
+def _logit_rows(t, dtype, shape, name, device):
+    """Address and row stride of logits [B, M, V] whose rows lie at one distance from each other (contiguous, or a
+    slice [..., :V] of a padded vocabulary)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device):
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
+            raise TypeError(f"{name} must be a {dtype} tensor")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
+    if t.is_contiguous():
+        return t.data_ptr(), shape[2]
+    B, M, V = shape
+    row = t.stride(1) if M > 1 else t.stride(0)
+    if (V > 1 and t.stride(2) != 1) or row < V or (B > 1 and t.stride(0) != M * row):
+        raise ValueError(f"{name} must have unit stride over the vocabulary and rows at one distance, got strides "
+                         f"{list(t.stride())}")
+    return t.data_ptr(), row
+
+
+def verify_drafted_tree(target_logits, tokens, parents, temperatures, accept_u, noise, path, path_lens, new_tokens,
+                        logprobs=None, draft_logits=None, draft_lens=None, workspace=None, stream=None) -> None:
+    """Accept or reject drafted tokens against the target's logits [B, M, V] (bf16 or float32), from given random
+    numbers: accept_u [B, M] in [0, 1) and noise [B, V] ~ Exp(1). Token 0 is the root; parents int32 [B, M]. Writes
+    path [B, A], path_lens [B], new_tokens [B, A] and logprobs [B, A]; path and path_lens are what
+    kv_cache_commit_path takes. draft_logits [B, M, V]: the distributions that the children were drawn from, without
+    replacement; without them the children count as given. temperatures [B]: 0 is greedy."""
+    lib = load_library()
+    i32, f32, here = torch.int32, torch.float32, torch.cuda.current_device()
+    B, M, V = target_logits.shape
+    A, dtype = path.shape[-1], target_logits.dtype
+    if dtype is not torch.bfloat16 and dtype is not f32:
+        raise TypeError(f"target_logits must be bfloat16 or float32, got {dtype}")
+    target, target_stride = _logit_rows(target_logits, dtype, (B, M, V), "target_logits", here)
+    draft, draft_stride = None, V
+    if draft_logits is not None:
+        draft, draft_stride = _logit_rows(draft_logits, dtype, (B, M, V), "draft_logits", here)
+    ws_bytes = workspace.numel() if workspace is not None else 0
+    st = lib.verify_drafted_tree(
+        target, draft, dtype is f32, target_stride, draft_stride, _arg(tokens, i32, (B, M), "tokens", here),
+        _arg(parents, i32, (B, M), "parents", here), _opt(draft_lens, i32, (B,), "draft_lens", here),
+        _arg(temperatures, f32, (B,), "temperatures", here), _arg(accept_u, f32, (B, M), "accept_u", here),
+        _arg(noise, f32, (B, V), "noise", here), B, M, A, V, _arg(path, i32, (B, A), "path", here),
+        _arg(path_lens, i32, (B,), "path_lens", here), _arg(new_tokens, i32, (B, A), "new_tokens", here),
+        _opt(logprobs, f32, (B, A), "logprobs", here), _opt(workspace, torch.uint8, (ws_bytes,), "workspace", here),
+        ws_bytes, _raw_stream(stream, here))
+    if st:
+        _check("verify_drafted_tree", st)

@@ -115,7 +115,7 @@ int pgqa_device_error(unsigned *flags_out, int clear)
     cudaError_t err = cudaDeviceSynchronize();
     if (err != cudaSuccess)
         return cuda_fail(err, "pgqa_device_error");
-    unsigned a = 0, b = 0, c = 0, d = 0, e = 0, f = 0;
+    unsigned a = 0, b = 0, c = 0, d = 0, e = 0, f = 0, g = 0, h = 0, i = 0;
     if ((err = pgqa::read_flags_prologue(&a, clear != 0)) != cudaSuccess)
         return cuda_fail(err, "pgqa_device_error");
     if ((err = pgqa::read_flags_decode(&b, clear != 0)) != cudaSuccess)
@@ -128,7 +128,13 @@ int pgqa_device_error(unsigned *flags_out, int clear)
         return cuda_fail(err, "pgqa_device_error");
     if ((err = pgqa::read_flags_commit_path(&f, clear != 0)) != cudaSuccess)
         return cuda_fail(err, "pgqa_device_error");
-    *flags_out = a | b | c | d | e | f;
+    if ((err = pgqa::read_flags_read_int8(&g, clear != 0)) != cudaSuccess)
+        return cuda_fail(err, "pgqa_device_error");
+    if ((err = pgqa::read_flags_tree_attn_int8(&h, clear != 0)) != cudaSuccess)
+        return cuda_fail(err, "pgqa_device_error");
+    if ((err = pgqa::read_flags_verify_tree(&i, clear != 0)) != cudaSuccess)
+        return cuda_fail(err, "pgqa_device_error");
+    *flags_out = a | b | c | d | e | f | g | h | i;
     return ok();
 }
 
@@ -884,15 +890,20 @@ int decode_step_paged_int8(const pgqa_bf16 *q, const pgqa_bf16 *k, const pgqa_bf
 
 // ---------------------------------------------------------------- drafted-tree decoding
 
-int qk_norm_rope_append_axes(const pgqa_bf16 *q, const pgqa_bf16 *k, const pgqa_bf16 *v,
-                             const pgqa_bf16 *gamma_q, const pgqa_bf16 *gamma_k, const int32_t *positions,
-                             int n_axes, const uint8_t *axis_of_pair, const int32_t *context_lens,
-                             const int32_t *new_lens, const int32_t *block_table, pgqa_bf16 *k_cache,
-                             pgqa_bf16 *v_cache, pgqa_bf16 *q_out, int B, int M, int Hq, int Hkv, int D,
-                             int page_size, int max_pages, int num_pages, float rope_theta, float eps,
-                             cudaStream_t stream)
+// The prologue's caches: bf16, or INT8 codes and scales (k8 set).
+struct AppendCaches {
+    pgqa_bf16 *k, *v;
+    int8_t *k8, *v8;
+    float *k_scale, *v_scale;
+};
+
+static int axes_impl(const char *fn, const pgqa_bf16 *q, const pgqa_bf16 *k, const pgqa_bf16 *v,
+                     const pgqa_bf16 *gamma_q, const pgqa_bf16 *gamma_k, const int32_t *positions, int n_axes,
+                     const uint8_t *axis_of_pair, const int32_t *context_lens, const int32_t *new_lens,
+                     const int32_t *block_table, bool int8, const AppendCaches &c, pgqa_bf16 *q_out, int B, int M,
+                     int Hq, int Hkv, int D, int page_size, int max_pages, int num_pages, float rope_theta, float eps,
+                     cudaStream_t stream)
 {
-    const char *fn = "qk_norm_rope_append_axes";
     if (int st = check_heads(fn, B, Hq, Hkv, D))
         return st;
     if (int st = check_pages(fn, page_size, max_pages, num_pages))
@@ -913,39 +924,82 @@ int qk_norm_rope_append_axes(const pgqa_bf16 *q, const pgqa_bf16 *k, const pgqa_
                         axis_of_pair[r], n_axes);
     if (B == 0)
         return ok();
-    if (!q || !k || !v || !gamma_q || !gamma_k || !positions || !context_lens || !block_table || !k_cache ||
-        !v_cache || !q_out)
+    if (!q || !k || !v || !gamma_q || !gamma_k || !positions || !context_lens || !block_table || !q_out ||
+        (int8 ? !c.k8 || !c.v8 || !c.k_scale || !c.v_scale : !c.k || !c.v))
         return fail(PGQA_ERR_INVALID_ARG, "%s: a required pointer is NULL", fn);
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(gamma_q) || !aligned16(gamma_k) ||
-        !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(q_out) || !aligned4(positions) ||
-        !aligned4(context_lens) || !aligned4(block_table) || !aligned4(new_lens))
+        !aligned16(c.k) || !aligned16(c.v) || !aligned16(c.k8) || !aligned16(c.v8) || !aligned16(c.k_scale) ||
+        !aligned16(c.v_scale) || !aligned16(q_out) || !aligned4(positions) || !aligned4(context_lens) || !aligned4(block_table) || !aligned4(new_lens))
         return fail(PGQA_ERR_MISALIGNED, "%s: tensors need 16-byte and index arrays 4-byte alignment", fn);
     pgqa::RopeAxesArgs a{q, k, v, gamma_q, gamma_k, positions, n_axes, axis_of_pair, context_lens, new_lens,
-                         block_table, k_cache, v_cache, q_out, B, M, Hq, Hkv, page_size, max_pages, num_pages,
-                         static_cast<double>(rope_theta), eps, sm_count_current_device()};
+                         block_table, c.k, c.v, q_out, B, M, Hq, Hkv, page_size, max_pages, num_pages,
+                         static_cast<double>(rope_theta), eps, sm_count_current_device(), c.k8, c.v8, c.k_scale,
+                         c.v_scale};
     cudaError_t err = pgqa::launch_rope_axes(a, stream);
     if (err != cudaSuccess)
         return cuda_fail(err, fn);
     return ok();
 }
 
-size_t decode_attn_tree_workspace_size(int B, int M, int Hq, int Hkv, int D, int page_size, int max_pages)
+int qk_norm_rope_append_axes(const pgqa_bf16 *q, const pgqa_bf16 *k, const pgqa_bf16 *v,
+                             const pgqa_bf16 *gamma_q, const pgqa_bf16 *gamma_k, const int32_t *positions,
+                             int n_axes, const uint8_t *axis_of_pair, const int32_t *context_lens,
+                             const int32_t *new_lens, const int32_t *block_table, pgqa_bf16 *k_cache,
+                             pgqa_bf16 *v_cache, pgqa_bf16 *q_out, int B, int M, int Hq, int Hkv, int D,
+                             int page_size, int max_pages, int num_pages, float rope_theta, float eps,
+                             cudaStream_t stream)
 {
-    (void)D;
-    if (B < 0 || M < 1 || M > 64 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Hq / Hkv > pgqa::kMaxGroupHost ||
-        page_size <= 0 || max_pages < 0)
-        return 0;
-    return pgqa::tree_attn_workspace_bytes(B, M, Hq, Hkv, page_size, max_pages, sm_count_current_device());
+    return axes_impl("qk_norm_rope_append_axes", q, k, v, gamma_q, gamma_k, positions, n_axes, axis_of_pair,
+                     context_lens, new_lens, block_table, false, {k_cache, v_cache, nullptr, nullptr, nullptr, nullptr},
+                     q_out, B, M, Hq, Hkv, D, page_size, max_pages, num_pages, rope_theta, eps, stream);
 }
 
-int decode_attn_paged_tree(const pgqa_bf16 *q, const pgqa_bf16 *k_cache, const pgqa_bf16 *v_cache,
-                           const int32_t *block_table, const int32_t *context_lens, const uint64_t *tree_mask,
-                           const int32_t *positions, const int32_t *draft_lens, const float *slopes, int B,
-                           int M, int Hq, int Hkv, int D, int page_size, int max_pages, int num_pages,
-                           float scale, float softcap, float *out_f32, pgqa_bf16 *out_bf16, void *workspace,
-                           size_t ws_bytes, cudaStream_t stream)
+int qk_norm_rope_append_axes_int8(const pgqa_bf16 *q, const pgqa_bf16 *k, const pgqa_bf16 *v,
+                                  const pgqa_bf16 *gamma_q, const pgqa_bf16 *gamma_k, const int32_t *positions,
+                                  int n_axes, const uint8_t *axis_of_pair, const int32_t *context_lens,
+                                  const int32_t *new_lens, const int32_t *block_table, int8_t *k_cache8,
+                                  int8_t *v_cache8, float *k_scale, float *v_scale, pgqa_bf16 *q_out, int B, int M, int Hq, int Hkv, int D,
+                                  int page_size, int max_pages, int num_pages, float rope_theta, float eps,
+                                  cudaStream_t stream)
 {
-    const char *fn = "decode_attn_paged_tree";
+    return axes_impl("qk_norm_rope_append_axes_int8", q, k, v, gamma_q, gamma_k, positions, n_axes, axis_of_pair,
+                     context_lens, new_lens, block_table, true, {nullptr, nullptr, k_cache8, v_cache8, k_scale, v_scale},
+                     q_out, B, M, Hq, Hkv, D, page_size, max_pages, num_pages, rope_theta, eps, stream);
+}
+
+int kv_cache_read_int8(const int8_t *k_cache8, const int8_t *v_cache8, const float *k_scale, const float *v_scale,
+                       const int32_t *block_table, const int32_t *context_lens, const int32_t *first,
+                       pgqa_bf16 *k_out, pgqa_bf16 *v_out, int B, int N, int Hkv, int D, int page_size, int max_pages,
+                       int num_pages, cudaStream_t stream)
+{
+    const char *fn = "kv_cache_read_int8";
+    if (int st = check_heads(fn, B, Hkv, Hkv, D))
+        return st;
+    if (int st = check_pages(fn, page_size, max_pages, num_pages))
+        return st;
+    if (N < 0)
+        return fail(PGQA_ERR_INVALID_ARG, "%s: N = %d rows per sequence, need >= 0", fn, N);
+    if (Hkv > 65535)
+        return fail(PGQA_ERR_UNSUPPORTED, "%s: Hkv = %d exceeds 65535", fn, Hkv);
+    if (B == 0 || N == 0)
+        return ok();
+    if (!k_cache8 || !v_cache8 || !k_scale || !v_scale || !block_table || !context_lens || !k_out || !v_out)
+        return fail(PGQA_ERR_INVALID_ARG, "%s: a required pointer is NULL", fn);
+    if (!aligned16(k_cache8) || !aligned16(v_cache8) || !aligned16(k_scale) || !aligned16(v_scale) ||
+        !aligned16(k_out) || !aligned16(v_out) || !aligned4(block_table) || !aligned4(context_lens) || !aligned4(first))
+        return fail(PGQA_ERR_MISALIGNED, "%s: tensors need 16-byte and index arrays 4-byte alignment", fn);
+    pgqa::ReadInt8Args a{k_cache8, v_cache8, k_scale, v_scale, block_table, context_lens, first, k_out, v_out, B, N, Hkv,
+                         page_size, max_pages, num_pages, sm_count_current_device()};
+    cudaError_t err = pgqa::launch_read_int8(a, stream);
+    if (err != cudaSuccess)
+        return cuda_fail(err, fn);
+    return ok();
+}
+
+// What decode_attn_paged_tree and its INT8 form ask of sizes and scores.
+static int check_tree(const char *fn, int B, int M, int Hq, int Hkv, int D, int page_size, int max_pages, int num_pages,
+                      float scale, float softcap)
+{
     if (int st = check_heads(fn, B, Hq, Hkv, D))
         return st;
     if (int st = check_pages(fn, page_size, max_pages, num_pages))
@@ -966,6 +1020,28 @@ int decode_attn_paged_tree(const pgqa_bf16 *q, const pgqa_bf16 *k_cache, const p
         return fail(PGQA_ERR_UNSUPPORTED, "%s: max_pages * page_size exceeds 2^30 positions", fn);
     if ((static_cast<long long>(max_pages) * page_size / 128 + 1) * Hkv > 0x7FFFFFFFLL / (B > 0 ? B : 1))
         return fail(PGQA_ERR_UNSUPPORTED, "%s: B * Hkv * max_pages * page_size exceeds 2^31 tiles of 128 keys", fn);
+    return 0;
+}
+
+size_t decode_attn_tree_workspace_size(int B, int M, int Hq, int Hkv, int D, int page_size, int max_pages)
+{
+    (void)D;
+    if (B < 0 || M < 1 || M > 64 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Hq / Hkv > pgqa::kMaxGroupHost ||
+        page_size <= 0 || max_pages < 0)
+        return 0;
+    return pgqa::tree_attn_workspace_bytes(B, M, Hq, Hkv, page_size, max_pages, sm_count_current_device());
+}
+
+int decode_attn_paged_tree(const pgqa_bf16 *q, const pgqa_bf16 *k_cache, const pgqa_bf16 *v_cache,
+                           const int32_t *block_table, const int32_t *context_lens, const uint64_t *tree_mask,
+                           const int32_t *positions, const int32_t *draft_lens, const float *slopes, int B,
+                           int M, int Hq, int Hkv, int D, int page_size, int max_pages, int num_pages,
+                           float scale, float softcap, float *out_f32, pgqa_bf16 *out_bf16, void *workspace,
+                           size_t ws_bytes, cudaStream_t stream)
+{
+    const char *fn = "decode_attn_paged_tree";
+    if (int st = check_tree(fn, B, M, Hq, Hkv, D, page_size, max_pages, num_pages, scale, softcap))
+        return st;
     if (B == 0)
         return ok();
     if (!q || !k_cache || !v_cache || !block_table || !context_lens || !tree_mask)
@@ -995,13 +1071,67 @@ int decode_attn_paged_tree(const pgqa_bf16 *q, const pgqa_bf16 *k_cache, const p
     return ok();
 }
 
-int kv_cache_commit_path(pgqa_bf16 *const *k_caches, pgqa_bf16 *const *v_caches,
-                         const int32_t *const *block_tables, int n_layers, const int32_t *context_lens,
-                         const int32_t *draft_lens, const int32_t *path, const int32_t *path_lens,
-                         int32_t *context_lens_out, int B, int M, int A, int Hkv, int D, int page_size,
-                         int max_pages, int num_pages, cudaStream_t stream)
+size_t decode_attn_tree_int8_workspace_size(int B, int M, int Hq, int Hkv, int D, int page_size, int max_pages)
 {
-    const char *fn = "kv_cache_commit_path";
+    (void)D;
+    if (B < 0 || M < 1 || M > 64 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Hq / Hkv > pgqa::kMaxGroupHost ||
+        page_size <= 0 || max_pages < 0)
+        return 0;
+    return pgqa::tree_attn_int8_workspace_bytes(B, M, Hq, Hkv, page_size, max_pages, sm_count_current_device());
+}
+
+int decode_attn_paged_tree_int8(const pgqa_bf16 *q, const int8_t *k_cache8, const int8_t *v_cache8,
+                                const float *k_scale, const float *v_scale, const int32_t *block_table,
+                                const int32_t *context_lens, const uint64_t *tree_mask, const int32_t *positions,
+                                const int32_t *draft_lens, const float *slopes, int B, int M, int Hq, int Hkv, int D,
+                                int page_size, int max_pages, int num_pages, float scale, float softcap,
+                                float *out_f32, pgqa_bf16 *out_bf16, void *workspace, size_t ws_bytes,
+                                cudaStream_t stream)
+{
+    const char *fn = "decode_attn_paged_tree_int8";
+    if (int st = check_tree(fn, B, M, Hq, Hkv, D, page_size, max_pages, num_pages, scale, softcap))
+        return st;
+    if (B == 0)
+        return ok();
+    if (!q || !k_cache8 || !v_cache8 || !k_scale || !v_scale || !block_table || !context_lens || !tree_mask)
+        return fail(PGQA_ERR_INVALID_ARG, "%s: a required pointer is NULL", fn);
+    if (num_pages == 0)
+        return fail(PGQA_ERR_INVALID_ARG, "%s: the page pool is empty", fn);
+    if (slopes && !positions)
+        return fail(PGQA_ERR_INVALID_ARG, "%s: slopes need positions", fn);
+    if (!out_f32 && !out_bf16)
+        return fail(PGQA_ERR_INVALID_ARG, "%s: out_f32 and out_bf16 are both NULL", fn);
+    if (!aligned16(q) || !aligned16(k_cache8) || !aligned16(v_cache8) || !aligned16(k_scale) || !aligned16(v_scale) ||
+        !aligned16(out_f32) || !aligned16(out_bf16) || !aligned16(workspace))
+        return fail(PGQA_ERR_MISALIGNED, "%s: tensors need 16-byte alignment", fn);
+    if ((reinterpret_cast<uintptr_t>(tree_mask) & 7u) || !aligned4(block_table) || !aligned4(context_lens) ||
+        !aligned4(positions) || !aligned4(draft_lens) || !aligned4(slopes))
+        return fail(PGQA_ERR_MISALIGNED, "%s: tree_mask needs 8-byte, the other index arrays 4-byte alignment", fn);
+    pgqa::TreeAttnInt8Args a{q, k_cache8, v_cache8, k_scale, v_scale, block_table, context_lens, tree_mask, positions,
+                             draft_lens, slopes, B, M, Hq, Hkv, page_size, max_pages, num_pages, scale, softcap, out_f32,
+                             out_bf16, workspace, sm_count_current_device()};
+    const size_t need = pgqa::tree_attn_int8_workspace_bytes(B, M, Hq, Hkv, page_size, max_pages, a.sm_count);
+    if (need > 0 && (!workspace || ws_bytes < need))
+        return fail(PGQA_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, got %zu", fn, need,
+                    workspace ? ws_bytes : static_cast<size_t>(0));
+    cudaError_t err = pgqa::launch_tree_attn_int8(a, stream);
+    if (err != cudaSuccess)
+        return cuda_fail(err, fn);
+    return ok();
+}
+
+// The layers' caches: bf16 rows, or INT8 codes with scales.
+struct CommitCaches {
+    bool int8;
+    void *const *k, *const *v;
+    float *const *k_scale, *const *v_scale;
+};
+
+static int commit_impl(const char *fn, const CommitCaches &c, const int32_t *const *block_tables, int n_layers,
+                       const int32_t *context_lens, const int32_t *draft_lens, const int32_t *path,
+                       const int32_t *path_lens, int32_t *context_lens_out, int B, int M, int A, int Hkv, int D,
+                       int page_size, int max_pages, int num_pages, cudaStream_t stream)
+{
     if (int st = check_heads(fn, B, Hkv, Hkv, D))
         return st;
     if (Hkv > 65535)
@@ -1015,7 +1145,7 @@ int kv_cache_commit_path(pgqa_bf16 *const *k_caches, pgqa_bf16 *const *v_caches,
     if (n_layers < 1 || n_layers > PGQA_MAX_COMMIT_LAYERS)
         return fail(PGQA_ERR_UNSUPPORTED, "%s: n_layers = %d outside [1, %d]", fn, n_layers,
                     PGQA_MAX_COMMIT_LAYERS);
-    if (!k_caches || !v_caches || !block_tables)
+    if (!c.k || !c.v || !block_tables || (c.int8 && (!c.k_scale || !c.v_scale)))
         return fail(PGQA_ERR_INVALID_ARG, "%s: a required pointer is NULL", fn);
     if (B == 0)
         return ok();
@@ -1025,13 +1155,16 @@ int kv_cache_commit_path(pgqa_bf16 *const *k_caches, pgqa_bf16 *const *v_caches,
         !aligned4(context_lens_out))
         return fail(PGQA_ERR_MISALIGNED, "%s: index arrays need 4-byte alignment", fn);
     for (int l = 0; l < n_layers; ++l) {
-        if (!k_caches[l] || !v_caches[l] || !block_tables[l])
+        if (!c.k[l] || !c.v[l] || !block_tables[l] || (c.int8 && (!c.k_scale[l] || !c.v_scale[l])))
             return fail(PGQA_ERR_INVALID_ARG, "%s: a pointer of layer %d is NULL", fn, l);
-        if (!aligned16(k_caches[l]) || !aligned16(v_caches[l]) || !aligned4(block_tables[l]))
+        if (!aligned16(c.k[l]) || !aligned16(c.v[l]) || !aligned4(block_tables[l]) ||
+            (c.int8 && (!aligned16(c.k_scale[l]) || !aligned16(c.v_scale[l]))))
             return fail(PGQA_ERR_MISALIGNED, "%s: layer %d: caches need 16-byte, the table 4-byte alignment", fn, l);
         for (int e = 0; e < l; ++e)
-            if (block_tables[e] == block_tables[l] && (k_caches[e] == k_caches[l] || v_caches[e] == v_caches[l] ||
-                                                       k_caches[e] == v_caches[l] || v_caches[e] == k_caches[l]))
+            if (block_tables[e] == block_tables[l] &&
+                (c.k[e] == c.k[l] || c.v[e] == c.v[l] || c.k[e] == c.v[l] || c.v[e] == c.k[l] ||
+                 (c.int8 && (c.k_scale[e] == c.k_scale[l] || c.v_scale[e] == c.v_scale[l] ||
+                             c.k_scale[e] == c.v_scale[l] || c.v_scale[e] == c.k_scale[l]))))
                 return fail(PGQA_ERR_INVALID_ARG, "%s: layers %d and %d share a cache and its table", fn, e, l);
     }
     const auto overlap = [&](const int32_t *p, long long n) {
@@ -1041,10 +1174,113 @@ int kv_cache_commit_path(pgqa_bf16 *const *k_caches, pgqa_bf16 *const *v_caches,
     if (overlap(context_lens, B) || overlap(draft_lens, B) || overlap(path_lens, B) ||
         overlap(path, static_cast<long long>(B) * A))
         return fail(PGQA_ERR_INVALID_ARG, "%s: context_lens_out overlaps another index array", fn);
-    pgqa::CommitPathArgs a{k_caches, v_caches, block_tables, n_layers, context_lens, draft_lens, path, path_lens,
-                           context_lens_out, B, M, A, Hkv, page_size, max_pages, num_pages,
-                           sm_count_current_device()};
+    pgqa::CommitPathArgs a{};
+    if (c.int8) {
+        a.k_caches8 = reinterpret_cast<int8_t *const *>(c.k);
+        a.v_caches8 = reinterpret_cast<int8_t *const *>(c.v);
+        a.k_scales = c.k_scale;
+        a.v_scales = c.v_scale;
+    } else {
+        a.k_caches = reinterpret_cast<pgqa_bf16 *const *>(c.k);
+        a.v_caches = reinterpret_cast<pgqa_bf16 *const *>(c.v);
+    }
+    a.block_tables = block_tables;
+    a.n_layers = n_layers;
+    a.context_lens = context_lens;
+    a.draft_lens = draft_lens;
+    a.path = path;
+    a.path_lens = path_lens;
+    a.context_lens_out = context_lens_out;
+    a.B = B;
+    a.M = M;
+    a.A = A;
+    a.Hkv = Hkv;
+    a.page_size = page_size;
+    a.max_pages = max_pages;
+    a.num_pages = num_pages;
+    a.sm_count = sm_count_current_device();
     cudaError_t err = pgqa::launch_commit_path(a, stream);
+    if (err != cudaSuccess)
+        return cuda_fail(err, fn);
+    return ok();
+}
+
+int kv_cache_commit_path(pgqa_bf16 *const *k_caches, pgqa_bf16 *const *v_caches,
+                         const int32_t *const *block_tables, int n_layers, const int32_t *context_lens,
+                         const int32_t *draft_lens, const int32_t *path, const int32_t *path_lens,
+                         int32_t *context_lens_out, int B, int M, int A, int Hkv, int D, int page_size,
+                         int max_pages, int num_pages, cudaStream_t stream)
+{
+    return commit_impl("kv_cache_commit_path",
+                       {false, reinterpret_cast<void *const *>(k_caches), reinterpret_cast<void *const *>(v_caches),
+                        nullptr, nullptr},
+                       block_tables, n_layers, context_lens,
+                       draft_lens, path, path_lens, context_lens_out, B, M, A, Hkv, D, page_size, max_pages, num_pages,
+                       stream);
+}
+
+int kv_cache_commit_path_int8(int8_t *const *k_caches8, int8_t *const *v_caches8, float *const *k_scales,
+                              float *const *v_scales, const int32_t *const *block_tables, int n_layers,
+                              const int32_t *context_lens, const int32_t *draft_lens, const int32_t *path,
+                              const int32_t *path_lens, int32_t *context_lens_out, int B, int M, int A, int Hkv, int D,
+                              int page_size, int max_pages, int num_pages, cudaStream_t stream)
+{
+    return commit_impl("kv_cache_commit_path_int8",
+                       {true, reinterpret_cast<void *const *>(k_caches8), reinterpret_cast<void *const *>(v_caches8),
+                        k_scales, v_scales},
+                       block_tables, n_layers, context_lens,
+                       draft_lens, path, path_lens, context_lens_out, B, M, A, Hkv, D, page_size, max_pages, num_pages,
+                       stream);
+}
+
+size_t verify_drafted_tree_workspace_size(int B, int M, int V)
+{
+    if (B < 0 || M < 1 || M > 64 || V < 1)
+        return 0;
+    return pgqa::verify_tree_workspace_bytes(B, M, V, sm_count_current_device());
+}
+
+int verify_drafted_tree(const void *target_logits, const void *draft_logits, int logits_f32, long long target_stride,
+                        long long draft_stride, const int32_t *tokens, const int32_t *parents,
+                        const int32_t *draft_lens, const float *temperatures, const float *accept_u,
+                        const float *noise, int B, int M, int A, int V, int32_t *path, int32_t *path_lens,
+                        int32_t *new_tokens, float *logprobs, void *workspace, size_t ws_bytes, cudaStream_t stream)
+{
+    const char *fn = "verify_drafted_tree";
+    if (B < 0)
+        return fail(PGQA_ERR_INVALID_ARG, "%s: need B >= 0 (got %d)", fn, B);
+    if (B > 65535)
+        return fail(PGQA_ERR_UNSUPPORTED, "%s: B = %d exceeds 65535", fn, B);
+    if (M < 1 || M > 64)
+        return fail(PGQA_ERR_INVALID_ARG, "%s: M = %d drafted tokens per sequence outside [1, 64]", fn, M);
+    if (A < 1 || A > M)
+        return fail(PGQA_ERR_INVALID_ARG, "%s: paths of A = %d entries, need 1 <= A <= M = %d", fn, A, M);
+    if (V < 1)
+        return fail(PGQA_ERR_INVALID_ARG, "%s: V = %d logits a row, need >= 1", fn, V);
+    if (V > PGQA_MAX_VOCABULARY)
+        return fail(PGQA_ERR_UNSUPPORTED, "%s: V = %d exceeds %d", fn, V, PGQA_MAX_VOCABULARY);
+    if (target_stride < V || (draft_logits && draft_stride < V))
+        return fail(PGQA_ERR_INVALID_ARG, "%s: a row stride is below V = %d", fn, V);
+    if (target_stride > (1LL << 32) || draft_stride > (1LL << 32))
+        return fail(PGQA_ERR_UNSUPPORTED, "%s: a row stride exceeds 2^32 elements", fn);
+    if (B == 0)
+        return ok();
+    if (!target_logits || !tokens || !parents || !temperatures || !accept_u || !noise || !path || !path_lens ||
+        !new_tokens)
+        return fail(PGQA_ERR_INVALID_ARG, "%s: a required pointer is NULL", fn);
+    if (!aligned16(target_logits) || !aligned16(draft_logits) || !aligned16(noise) || !aligned16(workspace))
+        return fail(PGQA_ERR_MISALIGNED, "%s: logits, noise and workspace need 16-byte alignment", fn);
+    if (!aligned4(tokens) || !aligned4(parents) || !aligned4(draft_lens) || !aligned4(temperatures) ||
+        !aligned4(accept_u) || !aligned4(path) || !aligned4(path_lens) || !aligned4(new_tokens) || !aligned4(logprobs))
+        return fail(PGQA_ERR_MISALIGNED, "%s: the small arrays need 4-byte alignment", fn);
+    pgqa::VerifyTreeArgs a{target_logits, draft_logits, logits_f32 != 0, target_stride, draft_stride, tokens, parents,
+                           draft_lens, temperatures, accept_u, noise, B, M, A, V, path, path_lens, new_tokens, logprobs,
+                           workspace, sm_count_current_device()};
+    const size_t need = pgqa::verify_tree_workspace_bytes(B, M, V, a.sm_count);
+    if (need > 0 && (!workspace || ws_bytes < need))
+        return fail(PGQA_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, got %zu", fn, need,
+                    workspace ? ws_bytes : static_cast<size_t>(0));
+    cudaError_t err = pgqa::launch_verify_tree(a, stream);
     if (err != cudaSuccess)
         return cuda_fail(err, fn);
     return ok();

@@ -1,5 +1,6 @@
-// commit_path.cu -- kv_cache_commit_path: the accepted path of a drafted tree
-// moves behind the prefix, in every layer and KV head, in one launch.
+// commit_path.cu -- kv_cache_commit_path and kv_cache_commit_path_int8: the accepted
+// path of a drafted tree moves behind the prefix, in every layer and KV head, in
+// one launch (rows of bf16, or of INT8 codes with their scales).
 //
 // Slot base + path[i] goes to slot base + i. The path is strictly increasing,
 // so path[i] >= i: a destination i is a source only of entries before i. Rows
@@ -23,21 +24,31 @@ namespace {
 __device__ unsigned g_flags_commit_path;
 
 constexpr int kCommitThreads = 256;
-constexpr int kLanesPerRow = kRowBytes / 16;               // 16
-constexpr int kRowsAtOnce = kCommitThreads / kLanesPerRow; // 16 rows per unit
-constexpr int kUnits = 4;                                  // units in registers at a time
+constexpr int kUnits = 4; // units (of rows side by side) in registers at a time
 constexpr int kMaxDrafted = 64;
 
-struct CommitParams {
+template <bool kInt8> struct CommitParams;
+template <> struct CommitParams<false> {
     uint16_t *k_caches[PGQA_MAX_COMMIT_LAYERS], *v_caches[PGQA_MAX_COMMIT_LAYERS];
     const int32_t *block_tables[PGQA_MAX_COMMIT_LAYERS];
     const int32_t *context_lens, *draft_lens, *path, *path_lens;
     int32_t *context_lens_out;
     int M, A, Hkv, heads, log2_page, max_pages, num_pages; // heads: per block
 };
+template <> struct CommitParams<true> {
+    int8_t *k_caches[PGQA_MAX_COMMIT_LAYERS], *v_caches[PGQA_MAX_COMMIT_LAYERS];
+    float *k_scales[PGQA_MAX_COMMIT_LAYERS], *v_scales[PGQA_MAX_COMMIT_LAYERS];
+    const int32_t *block_tables[PGQA_MAX_COMMIT_LAYERS];
+    const int32_t *context_lens, *draft_lens, *path, *path_lens;
+    int32_t *context_lens_out;
+    int M, A, Hkv, heads, log2_page, max_pages, num_pages;
+};
 
-__global__ void __launch_bounds__(kCommitThreads) commit_path_kernel(const __grid_constant__ CommitParams p)
+template <bool kInt8>
+__global__ void __launch_bounds__(kCommitThreads) commit_path_kernel(const __grid_constant__ CommitParams<kInt8> p)
 {
+    constexpr int kLanesPerRow = (kInt8 ? kHeadDim : kRowBytes) / 16; // 16-byte pieces
+    constexpr int kRowsAtOnce = kCommitThreads / kLanesPerRow;
     // The next kernel may read tables, lengths and cache rows before it waits for
     // this one (the decode kernels do, rows by bulk copies): no early launch of it
     // here, and every write is performed before its thread ends, rows for such reads too.
@@ -96,7 +107,9 @@ __global__ void __launch_bounds__(kCommitThreads) commit_path_kernel(const __gri
     const int per_entry = 2 * heads, items = moved * per_entry; // item: entry, then head, then K or V
     for (int first = 0; first < items; first += kRowsAtOnce * kUnits) {
         uint4 row[kUnits];
-        uint16_t *dst[kUnits];
+        uint4 *dst[kUnits];
+        [[maybe_unused]] float scale[kUnits];
+        [[maybe_unused]] float *scale_dst[kUnits];
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
             const int item = first + u * kRowsAtOnce + group;
@@ -104,18 +117,28 @@ __global__ void __launch_bounds__(kCommitThreads) commit_path_kernel(const __gri
             if (item < items) {
                 const int i = item / per_entry, e = a - moved + i, rest = item - i * per_entry;
                 if (from[e] >= 0 && to[e] >= 0) {
-                    uint16_t *cache = rest & 1 ? p.v_caches[layer] : p.k_caches[layer];
+                    auto *cache = rest & 1 ? p.v_caches[layer] : p.k_caches[layer];
                     const long long head = static_cast<long long>(h0 + (rest >> 1)) << p.log2_page;
                     row[u] = reinterpret_cast<const uint4 *>(cache + (from[e] + head) * kHeadDim)[lane];
-                    dst[u] = cache + (to[e] + head) * kHeadDim;
+                    dst[u] = reinterpret_cast<uint4 *>(cache + (to[e] + head) * kHeadDim) + lane;
+                    if constexpr (kInt8) {
+                        float *scales = rest & 1 ? p.v_scales[layer] : p.k_scales[layer];
+                        scale_dst[u] = scales + to[e] + head;
+                        scale[u] = lane == 0 ? scales[from[e] + head] : 0.f;
+                    }
                 }
             }
         }
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < kUnits; ++u)
-            if (dst[u])
-                reinterpret_cast<uint4 *>(dst[u])[lane] = row[u];
+            if (dst[u]) {
+                *dst[u] = row[u];
+                if constexpr (kInt8) {
+                    if (lane == 0)
+                        *scale_dst[u] = scale[u];
+                }
+            }
         __syncthreads();
     }
     __threadfence();
@@ -124,14 +147,13 @@ __global__ void __launch_bounds__(kCommitThreads) commit_path_kernel(const __gri
 
 } // namespace
 
-cudaError_t launch_commit_path(const CommitPathArgs &a, cudaStream_t stream)
+namespace {
+
+template <bool kInt8>
+cudaError_t launch_commit(const CommitPathArgs &a, CommitParams<kInt8> &p, cudaStream_t stream)
 {
-    CommitParams p{};
-    for (int l = 0; l < a.n_layers; ++l) {
-        p.k_caches[l] = a.k_caches[l];
-        p.v_caches[l] = a.v_caches[l];
+    for (int l = 0; l < a.n_layers; ++l)
         p.block_tables[l] = a.block_tables[l];
-    }
     p.context_lens = a.context_lens;
     p.draft_lens = a.draft_lens;
     p.path = a.path;
@@ -146,10 +168,32 @@ cudaError_t launch_commit_path(const CommitPathArgs &a, cudaStream_t stream)
     // One block per (sequence, layer), or per head while these do not give each
     // SM a block.
     p.heads = static_cast<long long>(a.B) * a.n_layers >= a.sm_count ? a.Hkv : 1;
-    return launch_pdl(commit_path_kernel,
+    return launch_pdl(commit_path_kernel<kInt8>,
                       dim3(static_cast<unsigned>((a.Hkv + p.heads - 1) / p.heads), static_cast<unsigned>(a.B),
                            static_cast<unsigned>(a.n_layers)),
                       dim3(kCommitThreads), 0, stream, p);
+}
+
+} // namespace
+
+cudaError_t launch_commit_path(const CommitPathArgs &a, cudaStream_t stream)
+{
+    if (a.k_caches8) {
+        CommitParams<true> p{};
+        for (int l = 0; l < a.n_layers; ++l) {
+            p.k_caches[l] = a.k_caches8[l];
+            p.v_caches[l] = a.v_caches8[l];
+            p.k_scales[l] = a.k_scales[l];
+            p.v_scales[l] = a.v_scales[l];
+        }
+        return launch_commit(a, p, stream);
+    }
+    CommitParams<false> p{};
+    for (int l = 0; l < a.n_layers; ++l) {
+        p.k_caches[l] = a.k_caches[l];
+        p.v_caches[l] = a.v_caches[l];
+    }
+    return launch_commit(a, p, stream);
 }
 
 cudaError_t read_flags_commit_path(unsigned *flags, bool clear)

@@ -142,6 +142,9 @@ struct RopeAxesArgs {
     double rope_theta;
     float eps;
     int sm_count;
+    // INT8 cache instead of k_cache / v_cache when k_cache8 is set
+    int8_t *k_cache8, *v_cache8;
+    float *k_scale, *v_scale;
 };
 cudaError_t launch_rope_axes(const RopeAxesArgs &a, cudaStream_t stream);
 cudaError_t read_flags_rope_axes(unsigned *flags, bool clear);
@@ -171,9 +174,61 @@ struct CommitPathArgs {
     int32_t *context_lens_out;
     int B, M, A, Hkv, page_size, max_pages, num_pages;
     int sm_count;
+    // INT8 caches instead of k_caches / v_caches when k_caches8 is set
+    int8_t *const *k_caches8, *const *v_caches8;
+    float *const *k_scales, *const *v_scales;
 };
 cudaError_t launch_commit_path(const CommitPathArgs &a, cudaStream_t stream);
 cudaError_t read_flags_commit_path(unsigned *flags, bool clear);
+
+// Rows of an INT8 cache read back as bf16 (read_int8.cu).
+struct ReadInt8Args {
+    const int8_t *k_cache8, *v_cache8;
+    const float *k_scale, *v_scale;
+    const int32_t *block_table, *context_lens, *first; // first: nullable
+    pgqa_bf16 *k_out, *v_out;
+    int B, N, Hkv, page_size, max_pages, num_pages;
+    int sm_count;
+};
+cudaError_t launch_read_int8(const ReadInt8Args &a, cudaStream_t stream);
+cudaError_t read_flags_read_int8(unsigned *flags, bool clear);
+
+// Attention of a drafted tree over an INT8 cache (tree_attn_int8.cu).
+struct TreeAttnInt8Args {
+    const pgqa_bf16 *q;
+    const int8_t *k_cache8, *v_cache8;
+    const float *k_scale, *v_scale;
+    const int32_t *block_table, *context_lens;
+    const uint64_t *tree_mask;
+    const int32_t *positions, *draft_lens; // nullable
+    const float *slopes;                   // nullable
+    int B, M, Hq, Hkv, page_size, max_pages, num_pages;
+    float scale, softcap;
+    float *out_f32;      // nullable
+    pgqa_bf16 *out_bf16; // nullable
+    void *ws;
+    int sm_count;
+};
+size_t tree_attn_int8_workspace_bytes(int B, int M, int Hq, int Hkv, int page_size, int max_pages, int sm_count);
+cudaError_t launch_tree_attn_int8(const TreeAttnInt8Args &a, cudaStream_t stream);
+cudaError_t read_flags_tree_attn_int8(unsigned *flags, bool clear);
+
+// Verification of drafted trees (verify_tree.cu).
+struct VerifyTreeArgs {
+    const void *target, *draft; // bf16 or fp32 logits; draft: nullable
+    bool f32;
+    long long target_stride, draft_stride; // elements between two rows
+    const int32_t *tokens, *parents, *draft_lens; // draft_lens: nullable
+    const float *temperatures, *accept, *noise;
+    int B, M, A, V;
+    int32_t *path, *path_lens, *new_tokens;
+    float *logprobs; // nullable
+    void *ws;
+    int sm_count;
+};
+size_t verify_tree_workspace_bytes(int B, int M, int V, int sm_count);
+cudaError_t launch_verify_tree(const VerifyTreeArgs &a, cudaStream_t stream);
+cudaError_t read_flags_verify_tree(unsigned *flags, bool clear);
 
 // Launch `kernel` on `stream` with programmatic stream serialisation: it may
 // start while the previous kernel in the stream is still running, and must

@@ -1,6 +1,7 @@
-// rope_axes.cu -- qk_norm_rope_append_axes: per-head Q/K RMSNorm, rotary
-// positions with several axes, and the paged K/V append of M tokens per
-// sequence (drafted trees, image and video patches, prompts).
+// rope_axes.cu -- qk_norm_rope_append_axes and qk_norm_rope_append_axes_int8:
+// per-head Q/K RMSNorm, rotary positions with several axes, and the paged K/V
+// append of M tokens per sequence (drafted trees, image and video patches,
+// prompts), as bf16 rows or as INT8 codes with a scale per row.
 //
 // For token i with positions p_0 .. p_(A-1) and pair r (dims r and r + 64):
 //   xhat = x * gamma / sqrt(mean(x^2) + eps)
@@ -46,6 +47,8 @@ struct RopeAxesParams {
     const uint16_t *q, *k, *v, *gamma_q, *gamma_k;
     const int32_t *positions, *context_lens, *new_lens, *block_table;
     uint16_t *k_cache, *v_cache, *q_out;
+    int8_t *k_cache8, *v_cache8; // the INT8 form's caches
+    float *k_scale, *v_scale;
     int M, Hq, Hkv, n_axes, log2_page, max_pages, num_pages;
     int blocks_per_seq;
     float eps;
@@ -58,8 +61,36 @@ __device__ __forceinline__ uint4 pack8(const float *f)
                       pack_bf16x2(f[6], f[7]));
 }
 
+// Quantizes the row that this lane's group of eight holds (lo, hi: dims 8s .. and
+// 64 + 8s ..) as quantize_int8.cuh defines it, in the same operations and so to the
+// same bytes: s = amax / 127, code = round_half_even(x / s), both divisions
+// correctly rounded. Called by the whole warp.
+__device__ __forceinline__ float quantize_row(const float *lo, const float *hi, uint2 &codes_lo, uint2 &codes_hi)
+{
+    float amax = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        amax = fmaxf(amax, fmaxf(fabsf(lo[j]), fabsf(hi[j])));
+#pragma unroll
+    for (int off = kRowLanes / 2; off > 0; off >>= 1)
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
+    const float s = __fdiv_rn(amax, 127.0f);
+    const auto pack4 = [&](const float *x) {
+        uint32_t w = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int code = amax > 0.f ? max(-127, min(127, __float2int_rn(__fdiv_rn(x[j], s)))) : 0;
+            w |= static_cast<uint32_t>(code & 0xFF) << (8 * j);
+        }
+        return w;
+    };
+    codes_lo = make_uint2(pack4(lo), pack4(lo + 4));
+    codes_hi = make_uint2(pack4(hi), pack4(hi + 4));
+    return s;
+}
+
 // kTokens consecutive tokens of one sequence per block.
-template <int kTokens>
+template <int kTokens, bool kInt8>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_axes_kernel(const __grid_constant__ RopeAxesParams p)
 {
     // Everything this kernel reads may come from the kernel before it, and
@@ -180,15 +211,39 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_axes_kern
                     out_lo = pack8(a);
                     out_hi = pack8(c);
                 }
+                if constexpr (kInt8) { // K goes in as its bf16 rounding, what the bf16 cache would hold
+                    if (!is_q) {
+                        unpack8(out_lo, a);
+                        unpack8(out_hi, c);
+                    }
+                }
                 uint16_t *dst;
                 if (is_q)
                     dst = p.q_out + ((tok0 + t) * p.Hq + at.row) * kHeadDim;
+                else if (kInt8)
+                    dst = nullptr;
                 else if (!is_v)
                     dst = p.k_cache + (cell + (at.row - p.Hq) * P) * kHeadDim;
                 else
                     dst = p.v_cache + (cell + (at.row - p.Hq - p.Hkv) * P) * kHeadDim;
-                *reinterpret_cast<uint4 *>(dst + 8 * lane8) = out_lo;
-                *reinterpret_cast<uint4 *>(dst + kPairs + 8 * lane8) = out_hi;
+                if (!kInt8 || is_q) {
+                    *reinterpret_cast<uint4 *>(dst + 8 * lane8) = out_lo;
+                    *reinterpret_cast<uint4 *>(dst + kPairs + 8 * lane8) = out_hi;
+                }
+            }
+            if constexpr (kInt8) {
+                if (__any_sync(0xFFFFFFFFu, here && !is_q)) {
+                    uint2 codes_lo, codes_hi;
+                    const float s = quantize_row(a, c, codes_lo, codes_hi);
+                    if (here && !is_q && cell >= 0) {
+                        const long long row = cell + (at.row - p.Hq - (is_v ? p.Hkv : 0)) * static_cast<long long>(P);
+                        int8_t *dst = (is_v ? p.v_cache8 : p.k_cache8) + row * kHeadDim;
+                        *reinterpret_cast<uint2 *>(dst + 8 * lane8) = codes_lo;
+                        *reinterpret_cast<uint2 *>(dst + kPairs + 8 * lane8) = codes_hi;
+                        if (lane8 == 0)
+                            (is_v ? p.v_scale : p.k_scale)[row] = s;
+                    }
+                }
             }
             step(at);
         }
@@ -228,6 +283,10 @@ cudaError_t launch_rope_axes(const RopeAxesArgs &a, cudaStream_t stream)
     p.block_table = a.block_table;
     p.k_cache = a.k_cache;
     p.v_cache = a.v_cache;
+    p.k_cache8 = a.k_cache8;
+    p.v_cache8 = a.v_cache8;
+    p.k_scale = a.k_scale;
+    p.v_scale = a.v_scale;
     p.q_out = a.q_out;
     p.M = a.M;
     p.Hq = a.Hq;
@@ -248,7 +307,9 @@ cudaError_t launch_rope_axes(const RopeAxesArgs &a, cudaStream_t stream)
     const long long at_once = static_cast<long long>(kRopeBlocksPerSm) * (a.sm_count > 0 ? a.sm_count : 1);
     const long long per_block = (static_cast<long long>(a.B) * a.M + at_once - 1) / at_once;
     const int tokens = per_block <= 3 ? static_cast<int>(per_block) : a.Hq + 2 * a.Hkv <= 32 ? 3 : 2;
-    const auto kernel = tokens == 1 ? rope_axes_kernel<1> : tokens == 2 ? rope_axes_kernel<2> : rope_axes_kernel<3>;
+    const auto bf16 = tokens == 1 ? rope_axes_kernel<1, false> : tokens == 2 ? rope_axes_kernel<2, false> : rope_axes_kernel<3, false>;
+    const auto int8 = tokens == 1 ? rope_axes_kernel<1, true> : tokens == 2 ? rope_axes_kernel<2, true> : rope_axes_kernel<3, true>;
+    const auto kernel = a.k_cache8 ? int8 : bf16;
     p.blocks_per_seq = (a.M + tokens - 1) / tokens;
     const dim3 grid(static_cast<unsigned>(a.B) * static_cast<unsigned>(p.blocks_per_seq));
     return launch_pdl(kernel, grid, dim3(kRopeThreads), 0, stream, p);
