@@ -1,11 +1,48 @@
 // tree_attn_int8.cu -- decode_attn_paged_tree_int8: attention of a tree of
-// drafted tokens over the paged INT8 cache.
+// drafted tokens over the paged INT8 cache, with an optional tanh cap and
+// distance bias.
 //
-// First form: one warp per query row, keys 32 at a time, scores and the running
-// softmax in fp64 where the bias needs it.
+// Mathematics. As decode_attn_paged_tree (tree_attn.cu): x = scale Q K^T, capped
+// and biased, softmax over the keys that a row sees, O = P V, in tiles of 128 keys
+// with a running reference m and sum l per row. A key's K row is ks * code, its V
+// row vs * code: the codes enter the products exactly, as fp16, and the scales
+// multiply what stands for that key, the scores (ks) and the weights (vs).
+//
+// Layout. The keys are the M = 128 rows of both products and the query rows (drafted
+// token, head) their N columns: S^T = K Q^T, O^T = V^T P^T. So
+//   - a softmax thread owns a key: its two scales are two registers, and the work
+//     grows with the rows that there are (8, 16, 32 or 64 columns), not with a tile of 128;
+//   - K^T's operand comes from tensor memory, lane = key, written there by the thread
+//     that converted the key's codes; V's and P's lie in shared memory, dims and rows
+//     contiguous;
+//   - the maximum over the keys is not needed in a tile: a thread only asks whether one
+//     of its scores rises more than 8 (base 2) above the row's reference. If one does in
+//     any of the 128 threads, the references move and l and O are rescaled.
+// Sums l stay in the threads, one per row, until a segment's end.
+//
+// Rounding. P vs enters its product as an fp16 pair hi + lo (22 bits), two columns of
+// one product; vs is scaled by a power of two F so that the largest of a stream's run
+// lies in [8, 64) and the pair neither overflows nor meets fp16's small end. S, O, m and
+// l are fp32; for fp32 outputs O moves out of the tensor core every kSpan tiles, as in
+// tree_attn.cu.
+//
+// Bound. The cache is read once: 264 bytes per (key, KV head), 33 KB a tile of K and V.
+//
+// CTA: one per SM. Two streams of four warps take alternate tiles of the
+// CTA's run, each with tensor memory and shared memory of its own; a stream's step is
+//   K's codes -> fp16 in tensor memory; S issued; V's codes -> fp16 in shared memory
+//   meanwhile; S -> P -> shared memory; O issued, and on to the next tile's K.
+// Warp 8 requests codes (TMA, one lane per page of a tile) and scales (bulk copies),
+// warp 9 prepares the next segment's queries, masks and slopes.
 #include "common.cuh"
 #include "launch.h"
+#include "tcgen05.cuh"
+#include "tensor_map.h"
+#include "tree_runs.cuh"
 
+#include <atomic>
+#include <cfloat>
+#include <climits>
 #include <cmath>
 
 namespace pgqa {
@@ -13,108 +50,1017 @@ namespace {
 
 __device__ unsigned g_flags_tree_int8;
 
-struct Params8 {
-    TreeAttnInt8Args a;
-    int log2_page, g;
+constexpr int kCodeBytes = kTileKeys * kHeadDim; // 16 KB of K or V codes
+constexpr int kInt8Threads = 384; // three warpgroups (the last two warps idle)
+constexpr int kCodeWarp = 8, kQueryWarp = 9;
+constexpr float kRise = 8.f;  // rise of a row's scores (base 2) that moves its reference
+constexpr int kSpan = 16;     // a stream's tiles between two moves of O out of the tensor core (fp32 outputs)
+constexpr int kMaxRows = 64;  // query rows of a CTA
+
+// TMEM columns of stream s, + 256 s: S^T (64), K (64, two fp16 each), O^T (128).
+constexpr uint32_t kColS = 0, kColK = 64, kColO = 128, kStreamColumns = 256;
+
+struct TreeInt8Params {
+    static constexpr int kTilesPerRecord = 1, kRowsPerTile = kMaxRows;
+    static __device__ void raise(unsigned flag) { atomicOr(&g_flags_tree_int8, flag); }
+    const uint16_t *q;
+    const float *k_scale, *v_scale;
+    const int32_t *block_table, *context_lens;
+    const uint64_t *tree_mask;
+    const int32_t *positions, *draft_lens;
+    const float *slopes;
+    int B, M, Hq, Hkv, log2_page, max_pages, num_pages;
+    int g;             // query heads per KV head
+    int tile_tokens;   // drafted tokens per CTA (g * tile_tokens <= 64 rows)
+    int row_groups;    // CTAs that share a run of tiles
+    int rec_rows;      // rows of a partial record
+    int ctas;          // grid size / row_groups
+    float c;               // plain scores: y = c ks S, c = scale log2 e
+    float cap_u, cap_out;  // capped: y = cap_out tanh(cap_u ks S)
+    float tanh_c[7];       // cap_out times the polynomial's coefficients
+    float *out_f32;
+    uint16_t *out_bf16;
+    int32_t *unit_base;    // [B + 1] first tile number of each sequence, total
+    float *rec_m, *rec_l;  // [2 * grid][rec_rows]
+    float *rec_acc;        // [2 * grid][rec_rows][128]
+    float *sums;           // [2 * grid][rows][128]: O of earlier spans; null: bf16 outputs only
 };
 
-__global__ void __launch_bounds__(128) tree_rows_kernel(const __grid_constant__ Params8 p)
+// Rows: the columns that the softmax works on.
+template <int kRows> struct Shape {
+    static constexpr int kScoreColumns = kRows < 16 ? 16 : kRows; // of S^T = K Q^T
+    static constexpr int kOutColumns = kRows == 64 ? 128 : 64;    // of O^T: hi, then lo
+    static constexpr int kLo = kOutColumns / 2;                   // lo's first column
+    static constexpr int kRing = kRows == 64 ? 2 : 3;             // slots of a stream's ring
+    static constexpr int kQueries = kRows == 64 ? 1 : 2;          // segments whose queries are kept
+};
+
+template <int kRows> struct __align__(1024) TreeInt8Smem {
+    using Sh = Shape<kRows>;
+    unsigned char codes[2][Sh::kRing][kCodeBytes]; // per stream, K and V in turn
+    unsigned char v16[2][kTileKeys * kRowBytes];
+    unsigned char p16[2][kTileKeys * Sh::kOutColumns * 2];
+    unsigned char q16[Sh::kQueries][Sh::kScoreColumns * kRowBytes];
+    float scales[2][Sh::kRing][kTileKeys];
+    // what a segment's rows bring, for two segments in turn
+    uint64_t sees[2][64]; // drafted token j: the rows that see it
+    float slope_up[2][kMaxRows], slope_down[2][kMaxRows]; // slopes (base 2), split by sign
+    int anchor[2][kMaxRows];
+    int by_sign[2]; // every row's anchor is the prefix's end, or its first key for a falling slope
+    // a stream's rows
+    float neg_m[2][kMaxRows]; // minus the reference
+    float f_l[2][kMaxRows], f_o[2][kMaxRows], g_sums[2][kMaxRows];
+    float warp_part[2][4][kMaxRows], warp_vs[2][4];
+    float m_end[2][kMaxRows], l_end[2][kMaxRows], inv_f[2];
+    float weight[2][2][kMaxRows]; // by the stream that writes; of stream 0's and 1's O
+    uint64_t code_full[2][Sh::kRing], code_empty[2][Sh::kRing];
+    uint64_t q_full[Sh::kQueries], q_empty[Sh::kQueries];
+    uint64_t rows_full[2], rows_empty[2];
+    uint64_t s_full[2], o_done[2];
+    uint32_t valid[2][Sh::kRing]; // pages inside the pool, a bit per 16 keys of a tile
+    uint32_t tmem_base;
+    int start_b, start_h, start_tile, start_T, start_n, units; // this CTA's run
+    int scan[kInt8Threads / 32];
+    float zero;
+};
+template <int kRows> constexpr int kInt8Smem = sizeof(TreeInt8Smem<kRows>);
+static_assert(kInt8Smem<32> <= 232448 && kInt8Smem<64> <= 232448, "one CTA's shared memory");
+
+__device__ __forceinline__ void stream_sync(int stream)
 {
-    grid_dependency_wait();
-    allow_dependent_launch();
-    const TreeAttnInt8Args &a = p.a;
-    __shared__ float qs[4][kHeadDim];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long r = blockIdx.x * 4ll + warp;
-    if (r >= static_cast<long long>(a.B) * a.M * a.Hq)
-        return;
-    const int hq = static_cast<int>(r % a.Hq), i = static_cast<int>(r / a.Hq % a.M), b = static_cast<int>(r / a.Hq / a.M);
-    const int h = hq / p.g;
-    const int T = a.context_lens[b], n = a.draft_lens ? a.draft_lens[b] : a.M;
-    const bool good = n >= 0 && n <= a.M && T >= n && T <= (a.max_pages << p.log2_page);
-    if (!good && lane == 0)
-        atomicOr(&g_flags_tree_int8, PGQA_DEVERR_BAD_CONTEXT);
-    if (good && i >= n)
-        return;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    double m = -INFINITY, l = 0.0;
-    if (good) {
-        for (int d = lane; d < kHeadDim; d += 32)
-            qs[warp][d] = __uint_as_float(static_cast<uint32_t>(a.q[r * kHeadDim + d]) << 16);
+    asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + stream) : "memory");
+}
+__device__ __forceinline__ bool stream_any(int stream, bool x)
+{
+    uint32_t y;
+    asm volatile("{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %2, 0;\n\tbarrier.cta.red.or.pred b, %1, 128, a;\n\t"
+                 "selp.u32 %0, 1, 0, b;\n\t}"
+                 : "=r"(y)
+                 : "r"(1 + stream), "r"(x ? 1u : 0u)
+                 : "memory");
+    return y != 0;
+}
+__device__ __forceinline__ void both_streams_sync() { asm volatile("barrier.cta.sync 3, 256;" ::: "memory"); }
+
+__device__ __forceinline__ float warp_max(float x)
+{
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// As tmem_ld16, 8 columns.
+__device__ __forceinline__ void tmem_ld8(float *r, uint32_t addr)
+{
+    uint32_t *u = reinterpret_cast<uint32_t *>(r);
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait_ld8(float *r)
+{
+    uint32_t *u = reinterpret_cast<uint32_t *>(r);
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(u[0]), "+r"(u[1]), "+r"(u[2]), "+r"(u[3]), "+r"(u[4]), "+r"(u[5]), "+r"(u[6]), "+r"(u[7])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const float *r)
+{
+    const uint32_t *u = reinterpret_cast<const uint32_t *>(r);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(u[0]),
+                 "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
+}
+
+// Instruction descriptor of kind::f16 with fp16 A and B, fp32 D, M = 128 (tcgen05.cuh);
+// A "MN-major" (its M dimension contiguous) in bit 15.
+__host__ __device__ constexpr uint32_t tc_idesc_f16(uint32_t n, bool mn_major)
+{
+    return (1u << 4) | ((mn_major ? 3u : 0u) << 15) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// The fp16 pair (22 bits) of two floats.
+__device__ __forceinline__ void split_f16(f32x2 w, uint32_t &hi, uint32_t &lo)
+{
+    float a, b, ra, rb;
+    w.get(a, b);
+    hi = pack_f16x2(a, b);
+    fma2(f32x2(f16_lo(hi), f16_hi(hi)), f32x2(-1.f, -1.f), w).get(ra, rb);
+    lo = pack_f16x2(ra, rb);
+}
+
+// Sums over a warp's lanes of N values: lane i / (32 / N) gets that of value i (N <= 32).
+template <int N> __device__ __forceinline__ float sum_lanes(float *x)
+{
+    const int lane = threadIdx.x & 31;
+    int off = 16;
+#pragma unroll
+    for (int n = N / 2; n >= 1; n /= 2, off /= 2) {
+        const bool upper = lane & off;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float keep = upper ? x[i + n] : x[i], give = upper ? x[i] : x[i + n];
+            x[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, off);
+        }
+    }
+    for (; off >= 1; off /= 2)
+        x[0] += __shfl_xor_sync(0xFFFFFFFFu, x[0], off);
+    return x[0];
+}
+
+// ---------------------------------------------------------------- codes and scales
+template <int kRows>
+__device__ bool fetch_codes(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, const CUtensorMap *mk, const CUtensorMap *mv)
+{
+    constexpr int kRing = Shape<kRows>::kRing;
+    const int lane = threadIdx.x & 31;
+    const int P = 1 << p.log2_page;
+    const int box_keys = min(P, kTileKeys);
+    const int boxes = kTileKeys / box_keys; // pages of a tile
+    const int outside = static_cast<int>(static_cast<long long>(p.num_pages) * p.Hkv << p.log2_page);
+    // one row group reads the cache once; of several, running side by side, the
+    // first leaves it in L2 for the others
+    const uint64_t policy = p.row_groups == 1 ? l2_evict_first_policy() : l2_evict_normal_policy();
+    bool ok = true;
+    int puts[2] = {0, 0}; // loads requested by stream
+    Segments seg(s);
+    int unit = 0;
+    while (seg.next(p)) {
+        const int32_t *table = p.block_table + static_cast<size_t>(seg.b) * p.max_pages;
+        const auto entry = [&](int tile) {
+            const int key = tile * kTileKeys + lane * box_keys;
+            return lane < boxes && key < seg.T ? table[key >> p.log2_page] : 0;
+        };
+        int phys_next = entry(seg.seg_tile0);
+        for (int tile = seg.seg_tile0; tile < seg.seg_tile1; ++tile, ++unit) {
+            const int phys = phys_next;
+            if (tile + 1 < seg.seg_tile1)
+                phys_next = entry(tile + 1);
+            const int key = tile * kTileKeys + lane * box_keys;
+            const bool needed = lane < boxes && key < seg.T;
+            const bool in_pool = phys >= 0 && phys < p.num_pages;
+            const bool here = needed && in_pool;
+            if (needed && !in_pool)
+                atomicOr(&g_flags_tree_int8, PGQA_DEVERR_BAD_PAGE);
+            const int row = here ? ((phys * p.Hkv + seg.h) << p.log2_page) + (key & (P - 1)) : outside;
+            const uint32_t valid = __ballot_sync(0xFFFFFFFFu, !needed || in_pool);
+            const int bytes = kCodeBytes + 4 * box_keys * __popc(__ballot_sync(0xFFFFFFFFu, here));
+            uint32_t by16 = 0; // a bit per 16 keys
+            for (int i = 0; i < 8; ++i)
+                by16 |= ((valid >> (i * 16 / box_keys)) & 1u) << i;
+            const int stream = unit & 1;
+#pragma unroll
+            for (int is_v = 0; is_v < 2; ++is_v) {
+                const int put = (unit >> 1) * 2 + is_v, slot = put % kRing;
+                ok = ok && warp_wait(&s.code_empty[stream][slot], ((put / kRing) & 1) ^ 1);
+                if (!ok)
+                    break;
+                uint64_t *full = &s.code_full[stream][slot];
+                if (lane == 0) {
+                    s.valid[stream][slot] = by16;
+                    mbar_arrive_expect_tx(full, bytes);
+                }
+                __syncwarp();
+                if (lane < boxes) {
+                    // a box outside the tensor arrives as zeros
+                    tma_load_2d(s.codes[stream][slot] + lane * box_keys * kHeadDim, is_v ? mv : mk, 0, row, full, policy);
+                    if (here)
+                        bulk_copy_g2s(s.scales[stream][slot] + lane * box_keys, (is_v ? p.v_scale : p.k_scale) + row,
+                                      4 * box_keys, full, policy);
+                }
+                puts[stream] = put + 1;
+            }
+            if (!ok)
+                break;
+        }
+        if (!ok)
+            break;
+    }
+    // nothing may still be on its way into shared memory when the CTA ends
+    for (int stream = 0; stream < 2; ++stream)
+        for (int put = max(0, puts[stream] - kRing); put < puts[stream]; ++put) // a slot's last load each
+            ok = warp_wait(&s.code_full[stream][put % kRing], (put / kRing) & 1) && ok;
+    return ok;
+}
+
+// ---------------------------------------------------------------- queries and masks
+template <int kScore, int kRows>
+__device__ bool fetch_rows(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, int rg)
+{
+    using Sh = Shape<kRows>;
+    const int lane = threadIdx.x & 31;
+    const int rows = p.tile_tokens * p.g;
+    bool ok = true;
+    Segments seg(s);
+    for (int index = 0; ok && seg.next(p); ++index) {
+        const int buf = index & 1, qbuf = index % Sh::kQueries;
+        const int n = seg.n, prefix = seg.T - n;
+        ok = warp_wait(&s.rows_empty[buf], ((index >> 1) & 1) ^ 1);
+        if (!ok)
+            break;
+        const int token0 = rg * p.tile_tokens;
+        const auto live = [&](int row) { return row < rows && token0 + row / p.g < n; };
+        // masks by row become rows by drafted token
+        const uint64_t *masks = p.tree_mask + static_cast<size_t>(seg.b) * p.M + token0;
+        const uint64_t m0 = live(lane) ? masks[lane / p.g] : 0, m1 = live(lane + 32) ? masks[(lane + 32) / p.g] : 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) {
+            const uint32_t lo = __ballot_sync(0xFFFFFFFFu, (m0 >> j) & 1u);
+            const uint32_t hi = kRows > 32 ? __ballot_sync(0xFFFFFFFFu, (m1 >> j) & 1u) : 0u;
+            if (lane == (j & 31))
+                s.sees[buf][j] = static_cast<uint64_t>(hi) << 32 | lo;
+        }
+        if constexpr ((kScore & 2) != 0) {
+            // A row's own position is a constant of its scores and cancels in the softmax: the
+            // bias is taken relative to a key that it favours, as in tree_attn.cu.
+            const int32_t *at = p.positions + static_cast<size_t>(seg.b) * p.M;
+            const int pos_lo = lane < n ? at[lane] : 0, pos_hi = lane + 32 < n ? at[lane + 32] : 0;
+            const auto near = [&](int j, int pos) {
+                return j >= n || static_cast<uint32_t>(pos) - static_cast<uint32_t>(prefix) + 64u < 128u;
+            };
+            bool by_sign = near(lane, pos_lo) && near(lane + 32, pos_hi);
+            float slope[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int row = lane + 32 * i;
+                slope[i] = live(row) ? p.slopes[seg.h * p.g + row % p.g] * kLog2e : 0.f;
+                by_sign = by_sign && fabsf(slope[i]) <= 2.f;
+            }
+            by_sign = __all_sync(0xFFFFFFFFu, by_sign);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const bool falls = slope[i] < 0.f;
+                int anchor = falls ? 0 : prefix;
+                if (!by_sign) {
+                    if (prefix == 0)
+                        anchor = falls ? INT_MAX : INT_MIN;
+                    const uint64_t mask = i ? m1 : m0;
+#pragma unroll 1
+                    for (int j = 0; j < n; ++j) {
+                        const int pos = __shfl_sync(0xFFFFFFFFu, j < 32 ? pos_lo : pos_hi, j & 31);
+                        if (mask >> j & 1u)
+                            anchor = falls ? min(anchor, pos) : max(anchor, pos);
+                    }
+                }
+                s.slope_up[buf][lane + 32 * i] = fmaxf(slope[i], 0.f);
+                s.slope_down[buf][lane + 32 * i] = fminf(slope[i], 0.f);
+                s.anchor[buf][lane + 32 * i] = anchor;
+            }
+            if (lane == 0)
+                s.by_sign[buf] = by_sign;
+        }
         __syncwarp();
-        const uint64_t mask = a.tree_mask[static_cast<size_t>(b) * a.M + i];
-        const int prefix = T - n;
-        for (int k0 = 0; k0 < T; k0 += 32) {
-            const int key = k0 + lane;
-            double y = -INFINITY;
-            size_t row = 0;
-            bool seen = key < T && (key < prefix || (mask >> (key - prefix) & 1u));
-            if (key < T) {
-                const int phys = a.block_table[static_cast<size_t>(b) * a.max_pages + (key >> p.log2_page)];
-                if (phys < 0 || phys >= a.num_pages) {
-                    seen = false;
-                    atomicOr(&g_flags_tree_int8, PGQA_DEVERR_BAD_PAGE);
-                } else {
-                    row = ((static_cast<size_t>(phys) * a.Hkv + h) << p.log2_page) + (key & ((1 << p.log2_page) - 1));
-                }
+        if (lane == 0)
+            mbar_arrive(&s.rows_full[buf]);
+        ok = warp_wait(&s.q_empty[qbuf], ((index / Sh::kQueries) & 1) ^ 1);
+        if (!ok)
+            break;
+        // Q as the K-major operand: two halves of 64 dims, swizzled 8-row atoms; rows that
+        // do not exist are zeros
+        const int part = lane & 15, half = part >> 3;
+        constexpr int kFlight = Sh::kScoreColumns / 2 < 8 ? Sh::kScoreColumns / 2 : 8;
+#pragma unroll 1
+        for (int r0 = 0; r0 < Sh::kScoreColumns; r0 += 2 * kFlight) {
+            uint4 x[kFlight];
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) {
+                const int row = r0 + 2 * i + (lane >> 4);
+                x[i] = make_uint4(0, 0, 0, 0);
+                if (live(row))
+                    x[i] = reinterpret_cast<const uint4 *>(
+                        p.q + ((static_cast<size_t>(seg.b) * p.M + token0 + row / p.g) * p.Hq + seg.h * p.g + row % p.g) *
+                                  kHeadDim)[part];
             }
-            if (seen) {
-                float dot = 0.f;
-                for (int d = 0; d < kHeadDim; ++d)
-                    dot = fmaf(static_cast<float>(a.k_cache8[row * kHeadDim + d]), qs[warp][d], dot);
-                y = static_cast<double>(dot) * a.k_scale[row] * a.scale;
-                if (a.softcap > 0.f)
-                    y = a.softcap * tanh(y / a.softcap);
-                if (a.slopes) {
-                    const int32_t *pos = a.positions + static_cast<size_t>(b) * a.M;
-                    const long long at = key < prefix ? key : pos[key - prefix];
-                    y += static_cast<double>(a.slopes[hq]) * static_cast<double>(at - pos[i]);
-                }
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) {
+                const int row = r0 + 2 * i + (lane >> 4);
+                const auto convert = [](uint32_t pair) { return pack_f16x2(bf16_lo(pair), bf16_hi(pair)); };
+                *reinterpret_cast<uint4 *>(s.q16[qbuf] + half * (Sh::kScoreColumns * 128) + row * 128 +
+                                           (((part & 7) ^ (row & 7)) << 4)) =
+                    make_uint4(convert(x[i].x), convert(x[i].y), convert(x[i].z), convert(x[i].w));
             }
-            double top = fmax(m, y);
-            for (int off = 16; off > 0; off >>= 1)
-                top = fmax(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
-            if (top == -INFINITY)
-                continue;
-            const double f = m == -INFINITY ? 0.0 : exp(m - top);
-            const double w = seen ? exp(y - top) : 0.0;
-            m = top;
-            l *= f;
-            for (int e = 0; e < 4; ++e)
-                acc[e] *= static_cast<float>(f);
-            double sum = w;
-            for (int off = 16; off > 0; off >>= 1)
-                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
-            l += sum;
-            const float wv = seen ? static_cast<float>(w * a.v_scale[row]) : 0.f;
-            for (int j = 0; j < 32; ++j) {
-                const float pj = __shfl_sync(0xFFFFFFFFu, wv, j);
-                const size_t rj = __shfl_sync(0xFFFFFFFFu, row, j);
-                if (__shfl_sync(0xFFFFFFFFu, seen, j))
-                    for (int e = 0; e < 4; ++e)
-                        acc[e] = fmaf(pj, static_cast<float>(a.v_cache8[rj * kHeadDim + lane + 32 * e]), acc[e]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&s.q_full[qbuf]);
+    }
+    return ok;
+}
+
+// ---------------------------------------------------------------- a stream
+// 16 codes of a row -> 16 fp16, as two times 16 bytes.
+__device__ __forceinline__ void widen_codes(const uint4 &codes, uint32_t *out)
+{
+    const uint32_t words[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t biased = words[i] ^ 0x80808080u;
+        out[2 * i] = biased8x2_to_f16x2(biased, 0x100u);
+        out[2 * i + 1] = biased8x2_to_f16x2(biased, 0x302u);
+    }
+}
+
+// The scores of this thread's key, in base 2, without the reference: kScore bit 0: capped,
+// bit 1: biased; plain ones are left as S (the caller has the factor).
+template <int kScore, int kRows>
+__device__ __forceinline__ void load_scores(const TreeInt8Params &p, const TreeInt8Smem<kRows> &s, float *x, uint32_t tmem_s,
+                                            float factor, int buf, int prefix, int pos)
+{
+    constexpr int kStep = kRows < 16 ? 8 : 16;
+#pragma unroll
+    for (int j = 0; j < kRows; j += kStep) {
+        if constexpr (kStep == 16)
+            tmem_ld16(x + j, tmem_s + j);
+        else
+            tmem_ld8(x + j, tmem_s + j);
+    }
+#pragma unroll
+    for (int j = 0; j < kRows; j += kStep) {
+        if constexpr (kStep == 16)
+            tmem_wait_ld16(x + j);
+        else
+            tmem_wait_ld8(x + j);
+    }
+    if constexpr ((kScore & 1) != 0) {
+#pragma unroll
+        for (int j0 = 0; j0 < kRows; j0 += kStep) {
+            float over = 0.f;
+#pragma unroll
+            for (int j = j0; j < j0 + kStep; j += 2) {
+                const f32x2 u = mul2(f32x2(x[j], x[j + 1]), f32x2(factor, factor)), t = mul2(u, u);
+                float t0, t1;
+                t.get(t0, t1);
+                over = max3(over, t0, t1);
+                f32x2 y(p.tanh_c[kTanhTerms - 1], p.tanh_c[kTanhTerms - 1]);
+#pragma unroll
+                for (int k = kTanhTerms - 2; k >= 0; --k)
+                    y = fma2(y, t, f32x2(p.tanh_c[k], p.tanh_c[k]));
+                mul2(u, y).get(x[j], x[j + 1]);
+            }
+            // scores past their cap are formed again, from S
+            if (__any_sync(0xFFFFFFFFu, over > 1.f)) {
+#pragma unroll 1
+                for (int j8 = 0; j8 < kStep; j8 += 8) {
+                    float again[8];
+                    tmem_ld8(again, tmem_s + j0 + j8);
+                    tmem_wait_ld8(again);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float u = again[j] * factor, size = fabsf(u);
+                        const float rest = rcp(1.f + ex2(size * (2.f * kLog2e)));
+                        const float y = copysignf(fmaf(-2.f * p.cap_out, rest, p.cap_out), u);
+                        if (size > 1.f) {
+#pragma unroll
+                            for (int i = 0; i < kStep / 8; ++i) // j8 is a variable, x an array in registers
+                                if (j8 == 8 * i)
+                                    x[j0 + 8 * i + j] = y;
+                        }
+                    }
+                }
             }
         }
     }
-    const float inv = l == 0.0 ? 0.f : static_cast<float>(1.0 / l);
-    for (int e = 0; e < 4; ++e) {
-        const float o = acc[e] * inv;
-        if (a.out_f32)
-            a.out_f32[r * kHeadDim + lane + 32 * e] = o;
-        if (a.out_bf16)
-            a.out_bf16[r * kHeadDim + lane + 32 * e] = f32_to_bf16_bits(o);
+    if constexpr ((kScore & 2) != 0) {
+        if constexpr ((kScore & 1) == 0) {
+#pragma unroll
+            for (int j = 0; j < kRows; ++j)
+                x[j] *= factor;
+        }
+        if (s.by_sign[buf]) {
+            const float up = distance(pos, prefix), down = distance(pos, 0);
+#pragma unroll
+            for (int j = 0; j < kRows; j += 2) {
+                const f32x2 a(s.slope_up[buf][j], s.slope_up[buf][j + 1]), d(s.slope_down[buf][j], s.slope_down[buf][j + 1]);
+                fma2(a, f32x2(up, up), fma2(d, f32x2(down, down), f32x2(x[j], x[j + 1]))).get(x[j], x[j + 1]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kRows; ++j)
+                x[j] = fmaf(s.slope_up[buf][j] + s.slope_down[buf][j], distance(pos, s.anchor[buf][j]), x[j]);
+        }
+    }
+}
+
+template <int kScore, int kRows> __device__ bool attend(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, int rg, int stream)
+{
+    using Sh = Shape<kRows>;
+    constexpr int kRing = Sh::kRing;
+    const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+    const int key_row = warp * 32 + lane; // of a tile; of O^T: the dim
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t tmem = warp_uniform(s.tmem_base + stream * kStreamColumns);
+    const uint32_t idesc_s = tc_idesc_f16(Sh::kScoreColumns, false);
+    const uint32_t idesc_o = tc_idesc_f16(Sh::kOutColumns, true);
+    const bool leader = warp == 0 && elect_one();
+    unsigned char *v16 = s.v16[stream], *p16 = s.p16[stream];
+    // A wait that ran out ends no loop: all of a stream's warps meet at its barriers, and
+    // do so to the end, without further waits.
+    bool ok = true;
+    const auto wait = [&](uint64_t *bar, uint32_t parity) { ok = ok && warp_wait(bar, parity); };
+    float *sums = p.sums ? p.sums + static_cast<size_t>(2 * blockIdx.x + stream) * kRows * kHeadDim + key_row : nullptr;
+
+    Segments seg(s);
+    int unit0 = 0; // the segment's first tile in the run
+    int step = 0;  // this stream's tiles so far
+    for (int index = 0; seg.next(p); ++index) {
+        const int buf = index & 1, qbuf = index % Sh::kQueries;
+        const int tiles = seg.seg_tile1 - seg.seg_tile0;
+        const int prefix = seg.T - seg.n;
+        wait(&s.rows_full[buf], (index >> 1) & 1);
+        wait(&s.q_full[qbuf], (index / Sh::kQueries) & 1);
+        if (key_row < kRows) {
+            s.neg_m[stream][key_row] = INFINITY; // nothing seen yet
+            s.g_sums[stream][key_row] = 1.f;
+        }
+        float l[kRows];
+#pragma unroll
+        for (int j = 0; j < kRows; ++j)
+            l[j] = 0.f;
+        float f = 1.f, vs_limit = 0.f; // F, and the V scale that needs a smaller one
+        bool summed = false;           // `sums` holds earlier spans
+        bool large = false;            // a reference beyond 65536
+        const int first = (unit0 ^ stream) & 1;
+        for (int i = first; i < tiles; i += 2, ++step) {
+            const int key0 = (seg.seg_tile0 + i) * kTileKeys, key = key0 + key_row;
+            // ---- K: codes -> fp16 in tensor memory
+            int put = 2 * step, slot = put % kRing;
+            wait(&s.code_full[stream][slot], (put / kRing) & 1);
+            const uint32_t valid = s.valid[stream][slot];
+            float ks = s.scales[stream][slot][key_row];
+            const unsigned char *codes = s.codes[stream][slot] + key_row * kHeadDim;
+#pragma unroll
+            for (int c = 0; c < 8; c += 2) {
+                uint32_t w[16];
+                widen_codes(*reinterpret_cast<const uint4 *>(codes + ((c ^ (key_row & 7)) << 4)), w);
+                widen_codes(*reinterpret_cast<const uint4 *>(codes + (((c + 1) ^ (key_row & 7)) << 4)), w + 8);
+                tmem_st16(tmem + lanes + kColK + 8 * c, reinterpret_cast<const float *>(w));
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&s.code_empty[stream][slot]);
+            stream_sync(stream);
+            if (leader) { // S^T = K Q^T
+                tc_fence_after();
+                const uint32_t qa = tc_desc_low(smem_addr(s.q16[qbuf]), 16);
+#pragma unroll
+                for (int k = 0; k < kHeadDim / 16; ++k) // 64 dims a half, 32 bytes a step
+                    tc_mma_ts(tmem + kColS, tmem + kColK + 8 * k,
+                              qa + (k >> 2) * (Sh::kScoreColumns * 128 / 16) + (k & 3) * 2, tc_desc_high(1024), idesc_s, k > 0);
+                tc_commit(&s.s_full[stream]);
+                if (i + 2 >= tiles)
+                    tc_commit(&s.q_empty[qbuf]);
+            }
+            __syncwarp();
+            // ---- V: codes -> fp16 in shared memory, once the last tile's product is through with it
+            ++put, slot = put % kRing;
+            wait(&s.code_full[stream][slot], (put / kRing) & 1);
+            float vs = s.scales[stream][slot][key_row];
+            codes = s.codes[stream][slot] + key_row * kHeadDim;
+            if (step > 0)
+                wait(&s.o_done[stream], (step - 1) & 1);
+            tc_fence_after();
+            unsigned char *v_row = v16 + (key_row >> 3) * 2048 + (key_row & 7) * 128;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                uint32_t w[8];
+                widen_codes(*reinterpret_cast<const uint4 *>(codes + ((c ^ (key_row & 7)) << 4)), w);
+                unsigned char *half = v_row + (c >> 2) * 1024;
+                *reinterpret_cast<uint4 *>(half + (((2 * c & 7) ^ (key_row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4 *>(half + (((2 * c + 1 & 7) ^ (key_row & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&s.code_empty[stream][slot]);
+            // ---- the rows that see this key
+            uint32_t sees_lo = 0xFFFFFFFFu, sees_hi = 0xFFFFFFFFu;
+            const bool fix = key0 + kTileKeys > prefix || valid != 0xFFu;
+            if (fix) {
+                const uint64_t sees = !(valid >> (key_row >> 4) & 1u) || key >= seg.T ? 0
+                                      : key < prefix                                  ? ~0ull
+                                                                                      : s.sees[buf][key - prefix];
+                sees_lo = static_cast<uint32_t>(sees), sees_hi = static_cast<uint32_t>(sees >> 32);
+                if (!sees)
+                    ks = vs = 0.f; // may hold anything
+            }
+            const auto hide = [&](float *x, float what) {
+#pragma unroll
+                for (int j = 0; j < kRows; ++j)
+                    x[j] = ((j < 32 ? sees_lo : sees_hi) >> (j & 31)) & 1u ? x[j] : what;
+            };
+            int pos = key;
+            if constexpr ((kScore & 2) != 0) {
+                if (key >= prefix && key < seg.T)
+                    pos = p.positions[static_cast<size_t>(seg.b) * p.M + key - prefix];
+            }
+            const float factor = ks * (kScore & 1 ? p.cap_u : p.c);
+            const float mul = kScore ? 1.f : factor;
+            wait(&s.s_full[stream], step & 1);
+            tc_fence_after();
+            // every span O moves out of the tensor core, to be added up to nearest
+            const bool span = sums && i > first + 1 && ((i - first) >> 1) % kSpan == 0;
+            if (span) {
+#pragma unroll 1
+                for (int j = 0; j < kRows; j += 8) {
+                    float hi[8], lo[8];
+                    tmem_ld8(hi, tmem + lanes + kColO + j);
+                    tmem_ld8(lo, tmem + lanes + kColO + Sh::kLo + j);
+                    tmem_wait_ld8(hi), tmem_wait_ld8(lo);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        float v = hi[k] + lo[k];
+                        if (summed)
+                            v = fmaf(sums[(j + k) * kHeadDim], s.g_sums[stream][j + k], v);
+                        sums[(j + k) * kHeadDim] = v;
+                    }
+                }
+                summed = true;
+                stream_sync(stream);
+                if (key_row < kRows)
+                    s.g_sums[stream][key_row] = 1.f;
+                stream_sync(stream);
+            }
+            const bool keep = i > first + 1 && !span; // O holds earlier tiles
+            // ---- scores relative to the references, which move if they have to
+            float x[kRows];
+#pragma unroll 1
+            for (int turn = 0;; ++turn) {
+                load_scores<kScore, kRows>(p, s, x, tmem + lanes + kColS, factor, buf, prefix, pos);
+                if (turn == 1) {
+                    // this tile's maxima by row, and of the V scales
+#pragma unroll
+                    for (int j = 0; j < kRows; ++j) {
+                        const float top = warp_max(((j < 32 ? sees_lo : sees_hi) >> (j & 31)) & 1u ? __fmul_rn(x[j], mul) : -INFINITY);
+                        if (lane == (j & 31))
+                            s.warp_part[stream][warp][j] = top;
+                    }
+                    const float size = fabsf(vs);
+                    const float top_vs = warp_max(size <= FLT_MAX ? size : 0.f);
+                    if (lane == 0)
+                        s.warp_vs[stream][warp] = top_vs;
+                    stream_sync(stream);
+                    float fv = 1.f;
+                    {
+                        const float *v = s.warp_vs[stream];
+                        const float all = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+                        if (all > vs_limit) {
+                            // F all in [8, 16)
+                            const int e = min(126, max(-126, 130 - static_cast<int>(__float_as_uint(all) >> 23)));
+                            const int was = static_cast<int>(__float_as_uint(f) >> 23) - 127;
+                            fv = ex2(static_cast<float>(e - was));
+                            f = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+                            vs_limit = 64.f / f;
+                        }
+                    }
+                    bool far = false;
+                    if (key_row < kRows) {
+                        const float (*w)[kMaxRows] = s.warp_part[stream];
+                        const float top = fmaxf(fmaxf(w[0][key_row], w[1][key_row]), fmaxf(w[2][key_row], w[3][key_row]));
+                        const float m = -s.neg_m[stream][key_row];
+                        const bool move = m == -INFINITY ? top > -INFINITY : top - m > kRise;
+                        const float fm = !move ? 1.f : m == -INFINITY ? 0.f : ex2(m - top);
+                        if (move)
+                            s.neg_m[stream][key_row] = -top;
+                        far = fabsf(move ? top : m) > 65536.f && (move || m > -INFINITY);
+                        s.f_l[stream][key_row] = fm;
+                        s.f_o[stream][key_row] = fm * fv;
+                        s.g_sums[stream][key_row] *= fm * fv;
+                    }
+                    large = stream_any(stream, far);
+#pragma unroll
+                    for (int j = 0; j < kRows; ++j)
+                        l[j] *= s.f_l[stream][j];
+                    if (keep) {
+#pragma unroll 1
+                        for (int j = 0; j < Sh::kOutColumns; j += 8) {
+                            float o[8];
+                            if ((j & (Sh::kLo - 1)) >= kRows)
+                                continue;
+                            tmem_ld8(o, tmem + lanes + kColO + j);
+                            tmem_wait_ld8(o);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                o[k] *= s.f_o[stream][(j & (Sh::kLo - 1)) + k];
+                            tmem_st8(tmem + lanes + kColO + j, o);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                float top = -INFINITY;
+                // For references so large that their rounding matters the scores are rounded as
+                // they were, before the difference (a packed product and sum would be fused).
+                if (kScore == 0 && large) {
+#pragma unroll
+                    for (int j = 0; j < kRows; ++j)
+                        x[j] = __fadd_rn(__fmul_rn(x[j], mul), s.neg_m[stream][j]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kRows; j += 2)
+                        fma2(f32x2(x[j], x[j + 1]), f32x2(mul, mul), f32x2(s.neg_m[stream][j], s.neg_m[stream][j + 1]))
+                            .get(x[j], x[j + 1]);
+                }
+                if (fix)
+                    hide(x, -INFINITY);
+                if (turn == 1)
+                    break;
+#pragma unroll
+                for (int j = 0; j < kRows; j += 2)
+                    top = max3(top, x[j], x[j + 1]);
+                if (!stream_any(stream, top > kRise || (fabsf(vs) > vs_limit && fabsf(vs) <= FLT_MAX)))
+                    break;
+            }
+            // ---- weights: their sum, and with the V scale as a pair into shared memory
+            const float vf = vs * f;
+            unsigned char *p_row = p16 + (kRows == 64 ? (key_row >> 3) * 2048 : (key_row >> 3) * 1024) + (key_row & 7) * 128;
+#pragma unroll
+            for (int j = 0; j < kRows; j += 8) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int k = 0; k < 8; k += 2) {
+                    const f32x2 w(ex2(x[j + k]), ex2(x[j + k + 1]));
+                    add2(f32x2(l[j + k], l[j + k + 1]), w).get(l[j + k], l[j + k + 1]);
+                    f32x2 wv = mul2(w, f32x2(vf, vf));
+                    if (fix) { // a scale that is no number stays with those who see it
+                        float a, b;
+                        wv.get(a, b);
+                        const uint32_t bits = (j < 32 ? sees_lo : sees_hi) >> (j & 31);
+                        a = bits >> k & 1u ? a : 0.f, b = bits >> (k + 1) & 1u ? b : 0.f;
+                        wv = f32x2(a, b);
+                    }
+                    split_f16(wv, hi[k / 2], lo[k / 2]);
+                }
+                *reinterpret_cast<uint4 *>(p_row + (((j >> 3) ^ (key_row & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                unsigned char *lo_at = kRows == 64 ? p_row + 1024 + (((j >> 3) ^ (key_row & 7)) << 4)
+                                                   : p_row + ((((j + Sh::kLo) >> 3) ^ (key_row & 7)) << 4);
+                *reinterpret_cast<uint4 *>(lo_at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            stream_sync(stream);
+            if (leader) { // O^T += V^T P^T
+                tc_fence_after();
+                const uint32_t va = tc_desc_low(smem_addr(v16), 1024), pa = tc_desc_low(smem_addr(p16), 1024);
+                constexpr int kStepP = kRows == 64 ? 4096 : 2048; // 16 keys
+#pragma unroll
+                for (int k = 0; k < kTileKeys / 16; ++k)
+                    tc_mma_ss(tmem + kColO, va + k * (4096 / 16), tc_desc_high(2048), pa + k * (kStepP / 16),
+                              tc_desc_high(kStepP / 2), idesc_o, k > 0 || keep);
+                tc_commit(&s.o_done[stream]);
+            }
+            __syncwarp();
+        }
+        if (first >= tiles && leader) // no tile of this segment is this stream's
+            mbar_arrive(&s.q_empty[qbuf]);
+        unit0 += tiles;
+
+        // ---- the end of the segment: both streams' states joined, O written
+#pragma unroll
+        for (int j0 = 0; j0 < kRows; j0 += 32) {
+            constexpr int kAtOnce = kRows < 32 ? kRows : 32;
+            const float sum = sum_lanes<kAtOnce>(l + j0);
+            if (lane % (32 / kAtOnce) == 0)
+                s.warp_part[stream][warp][j0 + lane / (32 / kAtOnce)] = sum;
+        }
+        if (first < tiles)
+            wait(&s.o_done[stream], (step - 1) & 1);
+        tc_fence_after();
+        if (summed) {
+#pragma unroll 1
+            for (int j = 0; j < kRows; j += 8) {
+                float hi[8];
+                tmem_ld8(hi, tmem + lanes + kColO + j);
+                tmem_wait_ld8(hi);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    hi[k] = fmaf(sums[(j + k) * kHeadDim], s.g_sums[stream][j + k], hi[k]);
+                tmem_st8(tmem + lanes + kColO + j, hi);
+            }
+            tmem_wait_st();
+        }
+        tc_fence_before();
+        stream_sync(stream);
+        if (key_row < kRows) {
+            const float (*w)[kMaxRows] = s.warp_part[stream];
+            s.l_end[stream][key_row] = (w[0][key_row] + w[1][key_row]) + (w[2][key_row] + w[3][key_row]);
+            s.m_end[stream][key_row] = -s.neg_m[stream][key_row];
+            if (key_row == 0)
+                s.inv_f[stream] = 1.f / f;
+        }
+        both_streams_sync();
+        tc_fence_after();
+        const bool whole = seg.seg_tile0 == 0 && seg.seg_tile1 == seg.tiles;
+        const int token0 = rg * p.tile_tokens;
+        const int live_rows = min(p.tile_tokens, seg.n - token0) * p.g; // may be negative
+        const size_t rec = static_cast<size_t>(2 * blockIdx.x + (seg.seg_tile0 > 0 ? 0 : 1)) * p.rec_rows;
+        if (key_row < kRows) {
+            const float m0 = s.m_end[0][key_row], m1 = s.m_end[1][key_row];
+            const float l0 = s.l_end[0][key_row], l1 = s.l_end[1][key_row];
+            const float top = fmaxf(l0 == 0.f ? -INFINITY : m0, l1 == 0.f ? -INFINITY : m1);
+            float w0 = l0 == 0.f ? 0.f : ex2(m0 - top), w1 = l1 == 0.f ? 0.f : ex2(m1 - top);
+            const float sum = (l0 == 0.f ? 0.f : l0 * w0) + (l1 == 0.f ? 0.f : l1 * w1);
+            const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+            s.weight[stream][0][key_row] = w0 * inv * s.inv_f[0];
+            s.weight[stream][1][key_row] = w1 * inv * s.inv_f[1];
+            if (!whole && stream == 0 && key_row < live_rows) {
+                p.rec_m[rec + key_row] = top;
+                p.rec_l[rec + key_row] = sum;
+            }
+        }
+        stream_sync(stream);
+        // eight rows at a time, the streams in turn; a thread has a dim
+#pragma unroll 1
+        for (int j = 8 * stream; j < min(kRows, live_rows); j += 16) {
+            const uint32_t o = s.tmem_base + lanes + kColO + j;
+            float h0[8], g0[8], h1[8], g1[8];
+            tmem_ld8(h0, o), tmem_ld8(g0, o + Sh::kLo);
+            tmem_ld8(h1, o + kStreamColumns), tmem_ld8(g1, o + kStreamColumns + Sh::kLo);
+            tmem_wait_ld8(h0), tmem_wait_ld8(g0), tmem_wait_ld8(h1), tmem_wait_ld8(g1);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int row = j + k;
+                if (row >= live_rows)
+                    break;
+                const float w0 = s.weight[stream][0][row], w1 = s.weight[stream][1][row];
+                // a stream without a visible key may hold anything
+                float v = w0 == 0.f ? 0.f : (h0[k] + g0[k]) * w0;
+                v = w1 == 0.f ? v : fmaf(h1[k] + g1[k], w1, v);
+                if (!whole) {
+                    p.rec_acc[(rec + row) * kHeadDim + key_row] = v;
+                } else {
+                    const size_t at = ((static_cast<size_t>(seg.b) * p.M + token0 + row / p.g) * p.Hq + seg.h * p.g +
+                                       row % p.g) * kHeadDim + key_row;
+                    if (p.out_f32)
+                        p.out_f32[at] = v;
+                    if (p.out_bf16)
+                        p.out_bf16[at] = f32_to_bf16_bits(v);
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&s.rows_empty[buf]);
+        // neither stream's O or state may be overwritten before both have it
+        tc_fence_before();
+        both_streams_sync();
+        tc_fence_after();
+    }
+    return ok;
+}
+
+template <int kScore, int kRows>
+__global__ void __launch_bounds__(kInt8Threads, 1)
+    tree_int8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                     const __grid_constant__ TreeInt8Params p)
+{
+    using Sh = Shape<kRows>;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    TreeInt8Smem<kRows> &s = *reinterpret_cast<TreeInt8Smem<kRows> *>(smem_raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rg = blockIdx.x % p.row_groups, cta = blockIdx.x / p.row_groups;
+    if (tid == 0) {
+        prefetch_tensormap(&mk), prefetch_tensormap(&mv);
+        for (int w = 0; w < 2; ++w) {
+            for (int i = 0; i < Sh::kRing; ++i)
+                mbar_init(&s.code_full[w][i], 1), mbar_init(&s.code_empty[w][i], 4);
+            mbar_init(&s.rows_full[w], 1), mbar_init(&s.rows_empty[w], 8);
+            mbar_init(&s.s_full[w], 1), mbar_init(&s.o_done[w], 1);
+        }
+        for (int i = 0; i < Sh::kQueries; ++i)
+            mbar_init(&s.q_full[i], 1), mbar_init(&s.q_empty[i], 2);
+        fence_mbar_init();
+    }
+    if (warp == kCodeWarp)
+        tmem_alloc_all(&s.tmem_base);
+    // columns of P that no row fills stay zero
+    for (int i = tid; i < static_cast<int>(sizeof(s.p16) / 16); i += kInt8Threads)
+        reinterpret_cast<uint4 *>(&s.p16[0][0])[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+
+    // Everything read from here on may come from the kernel before this one, and
+    // the next kernel may start once that one is done.
+    grid_dependency_wait();
+    allow_dependent_launch();
+    plan_run<kInt8Threads>(p, s, cta);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+
+    // Registers move from the third warpgroup to the streams: 256 * 208 + 128 * 88 =
+    // 384 * 168 as launched.
+    bool ok = true;
+    if (warp >= kCodeWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == kCodeWarp && s.units > 0)
+            ok = fetch_codes(p, s, &mk, &mv);
+        else if (warp == kQueryWarp && s.units > 0)
+            ok = fetch_rows<kScore>(p, s, rg);
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        if (s.units > 0)
+            ok = attend<kScore>(p, s, rg, warp >> 2);
+    }
+    if (!ok && lane == 0)
+        atomicOr(&g_flags_tree_int8, PGQA_DEVERR_WAIT_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kCodeWarp)
+        tmem_free_all(s.tmem_base);
+}
+
+// How a call's rows and CTAs are laid out; from sizes alone, so that the
+// workspace query and the launch agree.
+struct Layout {
+    int rows, tile_tokens, row_groups, rec_rows, ctas;
+    size_t base_bytes, stat_bytes, acc_bytes, sum_bytes;
+};
+
+size_t align256(size_t x) { return (x + 255) & ~size_t{255}; }
+
+Layout layout(int B, int M, int Hq, int Hkv, int page_size, int max_pages, int sm_count)
+{
+    Layout y{};
+    const int g = Hq / Hkv;
+    const int most = kMaxRows / g; // tokens of a CTA
+    y.row_groups = (M + most - 1) / most;
+    y.tile_tokens = (M + y.row_groups - 1) / y.row_groups;
+    y.row_groups = (M + y.tile_tokens - 1) / y.tile_tokens;
+    y.rec_rows = y.tile_tokens * g;
+    y.rows = y.rec_rows <= 8 ? 8 : y.rec_rows <= 16 ? 16 : y.rec_rows <= 32 ? 32 : 64;
+    const long long tiles = (static_cast<long long>(max_pages) * page_size + kTileKeys - 1) / kTileKeys;
+    const long long units = tiles * B * Hkv;
+    const int ctas = sm_count / y.row_groups;
+    y.ctas = static_cast<int>(units < ctas ? units : ctas);
+    if (y.ctas < 1)
+        y.ctas = 1;
+    const size_t records = static_cast<size_t>(2) * y.ctas * y.row_groups;
+    y.base_bytes = align256((static_cast<size_t>(B) + 1) * sizeof(int32_t));
+    y.stat_bytes = align256(records * y.rec_rows * sizeof(float));
+    y.acc_bytes = align256(records * y.rec_rows * kHeadDim * sizeof(float));
+    // a stream passes a span only where a (sequence, head) has that many tiles
+    y.sum_bytes = tiles > kSpan ? records * y.rows * kHeadDim * sizeof(float) : 0;
+    return y;
+}
+
+CUresult encode_codes(EncodeTiledFn fn, CUtensorMap *map, const void *base, long long rows, int page_size)
+{
+    const cuuint64_t dims[2] = {kHeadDim, static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {kHeadDim};
+    const cuuint32_t box[2] = {kHeadDim, static_cast<cuuint32_t>(page_size < kTileKeys ? page_size : kTileKeys)};
+    const cuuint32_t elem[2] = {1u, 1u};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, elem,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+constexpr int kMaxDevices = 64;
+
+template <int kScore, int kRows>
+cudaError_t launch_rows(const CUtensorMap &mk, const CUtensorMap &mv, const TreeInt8Params &p, cudaStream_t stream)
+{
+    static std::atomic<bool> configured[kMaxDevices];
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess)
+        return err;
+    const auto kernel = tree_int8_kernel<kScore, kRows>;
+    if (dev >= kMaxDevices || !configured[dev].load(std::memory_order_acquire)) {
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kInt8Smem<kRows>);
+        if (err != cudaSuccess)
+            return err;
+        if (dev < kMaxDevices)
+            configured[dev].store(true, std::memory_order_release);
+    }
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(p.ctas * p.row_groups)), dim3(kInt8Threads), kInt8Smem<kRows>,
+                      stream, mk, mv, p);
+}
+
+template <int kScore>
+cudaError_t launch_score(int rows, const CUtensorMap &mk, const CUtensorMap &mv, const TreeInt8Params &p, cudaStream_t stream)
+{
+    switch (rows) {
+    case 8: return launch_rows<kScore, 8>(mk, mv, p, stream);
+    case 16: return launch_rows<kScore, 16>(mk, mv, p, stream);
+    case 32: return launch_rows<kScore, 32>(mk, mv, p, stream);
+    default: return launch_rows<kScore, 64>(mk, mv, p, stream);
     }
 }
 
 } // namespace
 
-size_t tree_attn_int8_workspace_bytes(int, int, int, int, int, int, int) { return 0; }
+size_t tree_attn_int8_workspace_bytes(int B, int M, int Hq, int Hkv, int page_size, int max_pages, int sm_count)
+{
+    if (B == 0)
+        return 0;
+    const Layout y = layout(B, M, Hq, Hkv, page_size, max_pages, sm_count);
+    return y.base_bytes + 2 * y.stat_bytes + y.acc_bytes + y.sum_bytes;
+}
 
 cudaError_t launch_tree_attn_int8(const TreeAttnInt8Args &a, cudaStream_t stream)
 {
-    const Params8 p{a, __builtin_ctz(static_cast<unsigned>(a.page_size)), a.Hq / a.Hkv};
-    const long long rows = static_cast<long long>(a.B) * a.M * a.Hq;
-    return launch_pdl(tree_rows_kernel, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, stream, p);
+    const EncodeTiledFn fn = tensor_map_encoder();
+    if (!fn)
+        return cudaErrorNotSupported;
+    const Layout y = layout(a.B, a.M, a.Hq, a.Hkv, a.page_size, a.max_pages, a.sm_count);
+    TreeInt8Params p{};
+    p.q = a.q;
+    p.k_scale = a.k_scale;
+    p.v_scale = a.v_scale;
+    p.block_table = a.block_table;
+    p.context_lens = a.context_lens;
+    p.tree_mask = a.tree_mask;
+    p.positions = a.positions;
+    p.draft_lens = a.draft_lens;
+    p.slopes = a.slopes;
+    p.B = a.B;
+    p.M = a.M;
+    p.Hq = a.Hq;
+    p.Hkv = a.Hkv;
+    p.log2_page = __builtin_ctz(static_cast<unsigned>(a.page_size));
+    p.max_pages = a.max_pages;
+    p.num_pages = a.num_pages;
+    p.g = a.Hq / a.Hkv;
+    p.tile_tokens = y.tile_tokens;
+    p.row_groups = y.row_groups;
+    p.rec_rows = y.rec_rows;
+    p.ctas = y.ctas;
+    p.c = std::fmin(std::fmax(a.scale * kLog2e, -FLT_MAX), FLT_MAX);
+    if (a.softcap > 0.f) {
+        const float cap = std::fmin(a.softcap, 1e30f); // no cap to any score, and its products stay finite
+        p.cap_u = std::fmin(std::fmax(a.scale / cap, -FLT_MAX), FLT_MAX);
+        p.cap_out = cap * kLog2e;
+        for (int k = 0; k < kTanhTerms; ++k)
+            p.tanh_c[k] = static_cast<float>(kTanh[k] * cap * 1.4426950408889634);
+    } else {
+        p.cap_u = p.c;
+    }
+    p.out_f32 = a.out_f32;
+    p.out_bf16 = a.out_bf16;
+    unsigned char *ws = static_cast<unsigned char *>(a.ws);
+    p.unit_base = reinterpret_cast<int32_t *>(ws);
+    p.rec_m = reinterpret_cast<float *>(ws + y.base_bytes);
+    p.rec_l = reinterpret_cast<float *>(ws + y.base_bytes + y.stat_bytes);
+    p.rec_acc = reinterpret_cast<float *>(ws + y.base_bytes + 2 * y.stat_bytes);
+    if (a.out_f32 && y.sum_bytes)
+        p.sums = reinterpret_cast<float *>(ws + y.base_bytes + 2 * y.stat_bytes + y.acc_bytes);
+    CUtensorMap mk, mv;
+    const long long rows = static_cast<long long>(a.num_pages) * a.Hkv * a.page_size;
+    if (encode_codes(fn, &mk, a.k_cache8, rows, a.page_size) != CUDA_SUCCESS ||
+        encode_codes(fn, &mv, a.v_cache8, rows, a.page_size) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    cudaError_t err;
+    switch ((a.softcap > 0.f ? 1 : 0) | (a.slopes ? 2 : 0)) {
+    case 0: err = launch_score<0>(y.rows, mk, mv, p, stream); break;
+    case 1: err = launch_score<1>(y.rows, mk, mv, p, stream); break;
+    case 2: err = launch_score<2>(y.rows, mk, mv, p, stream); break;
+    default: err = launch_score<3>(y.rows, mk, mv, p, stream); break;
+    }
+    if (err != cudaSuccess)
+        return err;
+    return launch_tree_merge(p, y.ctas, stream);
 }
 
 cudaError_t read_flags_tree_attn_int8(unsigned *flags, bool clear)
