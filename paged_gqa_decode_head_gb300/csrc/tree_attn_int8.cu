@@ -28,12 +28,15 @@
 //
 // Bound. The cache is read once: 264 bytes per (key, KV head), 33 KB a tile of K and V.
 //
-// CTA: one per SM. Two streams of four warps take alternate tiles of the
-// CTA's run, each with tensor memory and shared memory of its own; a stream's step is
-//   K's codes -> fp16 in tensor memory; S issued; V's codes -> fp16 in shared memory
-//   meanwhile; S -> P -> shared memory; O issued, and on to the next tile's K.
-// Warp 8 requests codes (TMA, one lane per page of a tile) and scales (bulk copies),
-// warp 9 prepares the next segment's queries, masks and slopes.
+// CTA: one per SM, four warpgroups around tensor memory and a ring of six (four) code
+// tiles, K and V in turn. Two streams take alternate tiles of the CTA's run:
+//   warps 0-3, 4-7    one softmax warpgroup per stream: S -> P -> shared memory;
+//   warps 8-11        widen codes to fp16, K's into tensor memory, V's into shared memory,
+//                     for both streams;
+//   warp 12           requests codes (TMA, one lane per page of a tile) and scales (bulk copies);
+//   warp 13           prepares the next segment's queries, masks and slopes;
+//   warps 14, 15      issue one stream's products each: the next S as soon as the
+//                     softmax has read the last one, then the last tile's O += P V.
 #include "common.cuh"
 #include "launch.h"
 #include "tcgen05.cuh"
@@ -51,8 +54,11 @@ namespace {
 __device__ unsigned g_flags_tree_int8;
 
 constexpr int kCodeBytes = kTileKeys * kHeadDim; // 16 KB of K or V codes
-constexpr int kInt8Threads = 384; // three warpgroups (the last two warps idle)
-constexpr int kCodeWarp = 8, kQueryWarp = 9;
+constexpr int kInt8Threads = 512;
+constexpr int kWidenWarp = 8, kCodeWarp = 12, kQueryWarp = 13, kMmaWarp = 14; // and kMmaWarp + 1
+// Tiles whose scales are kept. A tile is requested once K of the one three before it is
+// widened (a ring of six), and that waits for the product with V of the one six before.
+constexpr int kScaleRing = 8;
 constexpr float kRise = 8.f;  // rise of a row's scores (base 2) that moves its reference
 constexpr int kSpan = 16;     // a stream's tiles between two moves of O out of the tensor core (fp32 outputs)
 constexpr int kMaxRows = 64;  // query rows of a CTA
@@ -91,17 +97,17 @@ template <int kRows> struct Shape {
     static constexpr int kScoreColumns = kRows < 16 ? 16 : kRows; // of S^T = K Q^T
     static constexpr int kOutColumns = kRows == 64 ? 128 : 64;    // of O^T: hi, then lo
     static constexpr int kLo = kOutColumns / 2;                   // lo's first column
-    static constexpr int kRing = kRows == 64 ? 2 : 3;             // slots of a stream's ring
+    static constexpr int kRing = kRows == 64 ? 4 : 6;             // slots of codes
     static constexpr int kQueries = kRows == 64 ? 1 : 2;          // segments whose queries are kept
 };
 
 template <int kRows> struct __align__(1024) TreeInt8Smem {
     using Sh = Shape<kRows>;
-    unsigned char codes[2][Sh::kRing][kCodeBytes]; // per stream, K and V in turn
+    unsigned char codes[Sh::kRing][kCodeBytes]; // K and V of a tile in turn
     unsigned char v16[2][kTileKeys * kRowBytes];
     unsigned char p16[2][kTileKeys * Sh::kOutColumns * 2];
     unsigned char q16[Sh::kQueries][Sh::kScoreColumns * kRowBytes];
-    float scales[2][Sh::kRing][kTileKeys];
+    float scales[kScaleRing][2][kTileKeys]; // of K, of V
     // what a segment's rows bring, for two segments in turn
     uint64_t sees[2][64]; // drafted token j: the rows that see it
     float slope_up[2][kMaxRows], slope_down[2][kMaxRows]; // slopes (base 2), split by sign
@@ -113,11 +119,13 @@ template <int kRows> struct __align__(1024) TreeInt8Smem {
     float warp_part[2][4][kMaxRows], warp_vs[2][4];
     float m_end[2][kMaxRows], l_end[2][kMaxRows], inv_f[2];
     float weight[2][2][kMaxRows]; // by the stream that writes; of stream 0's and 1's O
-    uint64_t code_full[2][Sh::kRing], code_empty[2][Sh::kRing];
+    uint32_t warp_over[2][4];
+    uint64_t code_full[Sh::kRing], code_empty[Sh::kRing];
     uint64_t q_full[Sh::kQueries], q_empty[Sh::kQueries];
     uint64_t rows_full[2], rows_empty[2];
-    uint64_t s_full[2], o_done[2];
-    uint32_t valid[2][Sh::kRing]; // pages inside the pool, a bit per 16 keys of a tile
+    uint64_t k_ready[2], v_ready[2]; // a tile's codes are widened
+    uint64_t s_full[2], s_read[2], p_ready[2], o_done[2], drain[2];
+    uint32_t valid[kScaleRing]; // pages inside the pool, a bit per 16 keys of a tile
     uint32_t tmem_base;
     int start_b, start_h, start_tile, start_T, start_n, units; // this CTA's run
     int scan[kInt8Threads / 32];
@@ -147,6 +155,18 @@ __device__ __forceinline__ float warp_max(float x)
     float r;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
     return r;
+}
+
+// Whether the phase with the given parity has completed; does not wait.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done)
+                 : "r"(smem_addr(bar)), "r"(parity)
+                 : "memory");
+    return done != 0;
 }
 
 // As tmem_ld16, 8 columns.
@@ -223,7 +243,7 @@ __device__ bool fetch_codes(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, con
     // first leaves it in L2 for the others
     const uint64_t policy = p.row_groups == 1 ? l2_evict_first_policy() : l2_evict_normal_policy();
     bool ok = true;
-    int puts[2] = {0, 0}; // loads requested by stream
+    int put = 0; // loads requested
     Segments seg(s);
     int unit = 0;
     while (seg.next(p)) {
@@ -245,31 +265,32 @@ __device__ bool fetch_codes(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, con
                 atomicOr(&g_flags_tree_int8, PGQA_DEVERR_BAD_PAGE);
             const int row = here ? ((phys * p.Hkv + seg.h) << p.log2_page) + (key & (P - 1)) : outside;
             const uint32_t valid = __ballot_sync(0xFFFFFFFFu, !needed || in_pool);
-            const int bytes = kCodeBytes + 4 * box_keys * __popc(__ballot_sync(0xFFFFFFFFu, here));
+            const int bytes = kCodeBytes + 8 * box_keys * __popc(__ballot_sync(0xFFFFFFFFu, here));
             uint32_t by16 = 0; // a bit per 16 keys
             for (int i = 0; i < 8; ++i)
                 by16 |= ((valid >> (i * 16 / box_keys)) & 1u) << i;
-            const int stream = unit & 1;
 #pragma unroll
-            for (int is_v = 0; is_v < 2; ++is_v) {
-                const int put = (unit >> 1) * 2 + is_v, slot = put % kRing;
-                ok = ok && warp_wait(&s.code_empty[stream][slot], ((put / kRing) & 1) ^ 1);
+            for (int is_v = 0; is_v < 2; ++is_v, ++put) {
+                const int slot = put % kRing;
+                ok = ok && warp_wait(&s.code_empty[slot], ((put / kRing) & 1) ^ 1);
                 if (!ok)
                     break;
-                uint64_t *full = &s.code_full[stream][slot];
+                uint64_t *full = &s.code_full[slot];
                 if (lane == 0) {
-                    s.valid[stream][slot] = by16;
-                    mbar_arrive_expect_tx(full, bytes);
+                    if (!is_v)
+                        s.valid[unit % kScaleRing] = by16;
+                    mbar_arrive_expect_tx(full, is_v ? kCodeBytes : bytes);
                 }
                 __syncwarp();
                 if (lane < boxes) {
                     // a box outside the tensor arrives as zeros
-                    tma_load_2d(s.codes[stream][slot] + lane * box_keys * kHeadDim, is_v ? mv : mk, 0, row, full, policy);
-                    if (here)
-                        bulk_copy_g2s(s.scales[stream][slot] + lane * box_keys, (is_v ? p.v_scale : p.k_scale) + row,
-                                      4 * box_keys, full, policy);
+                    tma_load_2d(s.codes[slot] + lane * box_keys * kHeadDim, is_v ? mv : mk, 0, row, full, policy);
+                    if (!is_v && here) { // both scales come with K
+                        float (*scales)[kTileKeys] = s.scales[unit % kScaleRing];
+                        bulk_copy_g2s(scales[0] + lane * box_keys, p.k_scale + row, 4 * box_keys, full, policy);
+                        bulk_copy_g2s(scales[1] + lane * box_keys, p.v_scale + row, 4 * box_keys, full, policy);
+                    }
                 }
-                puts[stream] = put + 1;
             }
             if (!ok)
                 break;
@@ -278,9 +299,8 @@ __device__ bool fetch_codes(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, con
             break;
     }
     // nothing may still be on its way into shared memory when the CTA ends
-    for (int stream = 0; stream < 2; ++stream)
-        for (int put = max(0, puts[stream] - kRing); put < puts[stream]; ++put) // a slot's last load each
-            ok = warp_wait(&s.code_full[stream][put % kRing], (put / kRing) & 1) && ok;
+    for (int last = max(0, put - kRing); last < put; ++last) // a slot's last load each
+        ok = warp_wait(&s.code_full[last % kRing], (last / kRing) & 1) && ok;
     return ok;
 }
 
@@ -402,118 +422,237 @@ __device__ __forceinline__ void widen_codes(const uint4 &codes, uint32_t *out)
     }
 }
 
-// The scores of this thread's key, in base 2, without the reference: kScore bit 0: capped,
-// bit 1: biased; plain ones are left as S (the caller has the factor).
-template <int kScore, int kRows>
-__device__ __forceinline__ void load_scores(const TreeInt8Params &p, const TreeInt8Smem<kRows> &s, float *x, uint32_t tmem_s,
-                                            float factor, int buf, int prefix, int pos)
+// Both streams' codes, widened tile by tile: a thread has a key.
+template <int kRows> __device__ bool widen(const TreeInt8Params &p, TreeInt8Smem<kRows> &s)
 {
-    constexpr int kStep = kRows < 16 ? 8 : 16;
+    constexpr int kRing = Shape<kRows>::kRing;
+    const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+    const int key_row = warp * 32 + lane;
+    bool ok = true;
+    for (int unit = 0; unit < s.units; ++unit) {
+        const int stream = unit & 1, step = unit >> 1;
+        const uint32_t tmem_k = s.tmem_base + (static_cast<uint32_t>(warp * 32) << 16) + stream * kStreamColumns + kColK;
+        int put = 2 * unit, slot = put % kRing;
+        ok = ok && warp_wait(&s.code_full[slot], (put / kRing) & 1);
+        // the last K of the stream is read
+        if (step > 0)
+            ok = ok && warp_wait(&s.s_full[stream], (step - 1) & 1);
+        tc_fence_after();
+        uint4 row[8]; // all of the row's codes are on their way at once
+        const auto load_row = [&] {
+            const unsigned char *codes = s.codes[slot] + key_row * kHeadDim;
 #pragma unroll
-    for (int j = 0; j < kRows; j += kStep) {
-        if constexpr (kStep == 16)
-            tmem_ld16(x + j, tmem_s + j);
-        else
-            tmem_ld8(x + j, tmem_s + j);
+            for (int c = 0; c < 8; ++c)
+                row[c] = *reinterpret_cast<const uint4 *>(codes + ((c ^ (key_row & 7)) << 4));
+        };
+        load_row();
+#pragma unroll
+        for (int c = 0; c < 8; c += 2) {
+            uint32_t w[16];
+            widen_codes(row[c], w);
+            widen_codes(row[c + 1], w + 8);
+            tmem_st16(tmem_k + 8 * c, reinterpret_cast<const float *>(w));
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(&s.code_empty[slot]);
+            mbar_arrive(&s.k_ready[stream]);
+        }
+        ++put, slot = put % kRing;
+        ok = ok && warp_wait(&s.code_full[slot], (put / kRing) & 1);
+        // the last tile's product with V is through with the buffer
+        if (step > 0)
+            ok = ok && warp_wait(&s.o_done[stream], (step - 1) & 1);
+        load_row();
+        unsigned char *v_row = s.v16[stream] + (key_row >> 3) * 2048 + (key_row & 7) * 128;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            uint32_t w[8];
+            widen_codes(row[c], w);
+            unsigned char *half = v_row + (c >> 2) * 1024;
+            *reinterpret_cast<uint4 *>(half + (((2 * c & 7) ^ (key_row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4 *>(half + (((2 * c + 1 & 7) ^ (key_row & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(&s.code_empty[slot]);
+            mbar_arrive(&s.v_ready[stream]);
+        }
     }
+    return ok;
+}
+
+// ---------------------------------------------------------------- matrix products
+template <int kRows> __device__ bool multiply(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, int stream)
+{
+    using Sh = Shape<kRows>;
+    const bool leader = elect_one(); // issues every product and commit
+    const uint32_t tmem = warp_uniform(s.tmem_base + stream * kStreamColumns);
+    const uint32_t idesc_s = tc_idesc_f16(Sh::kScoreColumns, false);
+    const uint32_t idesc_o = tc_idesc_f16(Sh::kOutColumns, true);
+    const uint32_t va = warp_uniform(tc_desc_low(smem_addr(s.v16[stream]), 1024));
+    const uint32_t pa = warp_uniform(tc_desc_low(smem_addr(s.p16[stream]), 1024));
+    constexpr int kStepP = kRows == 64 ? 4096 : 2048; // 16 keys of P
+    bool ok = true;
+    const auto wait = [&](uint64_t *bar, uint32_t parity) { ok = ok && warp_wait(bar, parity); };
+    const auto passed = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity)); };
+    const auto add_values = [&](int step, bool keep) { // O^T (+)= V^T P^T
+        wait(&s.v_ready[stream], step & 1);
+        wait(&s.p_ready[stream], step & 1);
+        tc_fence_after();
+        if (ok && leader) {
 #pragma unroll
-    for (int j = 0; j < kRows; j += kStep) {
-        if constexpr (kStep == 16)
-            tmem_wait_ld16(x + j);
-        else
-            tmem_wait_ld8(x + j);
-    }
-    if constexpr ((kScore & 1) != 0) {
-#pragma unroll
-        for (int j0 = 0; j0 < kRows; j0 += kStep) {
-            float over = 0.f;
-#pragma unroll
-            for (int j = j0; j < j0 + kStep; j += 2) {
-                const f32x2 u = mul2(f32x2(x[j], x[j + 1]), f32x2(factor, factor)), t = mul2(u, u);
-                float t0, t1;
-                t.get(t0, t1);
-                over = max3(over, t0, t1);
-                f32x2 y(p.tanh_c[kTanhTerms - 1], p.tanh_c[kTanhTerms - 1]);
-#pragma unroll
-                for (int k = kTanhTerms - 2; k >= 0; --k)
-                    y = fma2(y, t, f32x2(p.tanh_c[k], p.tanh_c[k]));
-                mul2(u, y).get(x[j], x[j + 1]);
-            }
-            // scores past their cap are formed again, from S
-            if (__any_sync(0xFFFFFFFFu, over > 1.f)) {
-#pragma unroll 1
-                for (int j8 = 0; j8 < kStep; j8 += 8) {
-                    float again[8];
-                    tmem_ld8(again, tmem_s + j0 + j8);
-                    tmem_wait_ld8(again);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float u = again[j] * factor, size = fabsf(u);
-                        const float rest = rcp(1.f + ex2(size * (2.f * kLog2e)));
-                        const float y = copysignf(fmaf(-2.f * p.cap_out, rest, p.cap_out), u);
-                        if (size > 1.f) {
-#pragma unroll
-                            for (int i = 0; i < kStep / 8; ++i) // j8 is a variable, x an array in registers
-                                if (j8 == 8 * i)
-                                    x[j0 + 8 * i + j] = y;
-                        }
-                    }
+            for (int k = 0; k < kTileKeys / 16; ++k)
+                tc_mma_ss(tmem + kColO, va + k * (4096 / 16), tc_desc_high(2048), pa + k * (kStepP / 16),
+                          tc_desc_high(kStepP / 2), idesc_o, k > 0 || keep);
+            tc_commit(&s.o_done[stream]);
+        }
+        __syncwarp();
+    };
+    Segments seg(s);
+    int unit0 = 0, step = 0;
+    bool keep = false;    // the last tile's product adds to O
+    bool pending = false; // the last tile's product is not issued yet
+    for (int index = 0; ok && seg.next(p); ++index) {
+        const int qbuf = index % Sh::kQueries, tiles = seg.seg_tile1 - seg.seg_tile0;
+        const int first = (unit0 ^ stream) & 1;
+        // Without a tile in this segment nothing here waits for the last one's: its end must
+        // come before the rows of the segment after this.
+        if (first >= tiles && pending) {
+            add_values(step - 1, keep);
+            pending = false;
+        }
+        wait(&s.q_full[qbuf], (index / Sh::kQueries) & 1);
+        const uint32_t qa = warp_uniform(tc_desc_low(smem_addr(s.q16[qbuf]), 16));
+        if (first >= tiles && leader)
+            mbar_arrive(&s.q_empty[qbuf]);
+        for (int i = first; ok && i < tiles; i += 2, ++step) {
+            // the last tile's product with V goes first if it can before the scores can
+            const auto scores_ready = [&] {
+                return passed(&s.k_ready[stream], step & 1) && (step == 0 || passed(&s.s_read[stream], (step - 1) & 1));
+            };
+            const long long start = clock64();
+            while (ok && !scores_ready()) {
+                if (pending && passed(&s.p_ready[stream], (step - 1) & 1) && passed(&s.v_ready[stream], (step - 1) & 1)) {
+                    add_values(step - 1, keep);
+                    pending = false;
                 }
+                ok = ok && __all_sync(0xFFFFFFFFu, clock64() - start < kWaitLimitClocks);
+            }
+            tc_fence_after();
+            if (ok && leader) { // S^T = K Q^T
+#pragma unroll
+                for (int k = 0; k < kHeadDim / 16; ++k) // 64 dims a half, 32 bytes a step
+                    tc_mma_ts(tmem + kColS, tmem + kColK + 8 * k,
+                              qa + (k >> 2) * (Sh::kScoreColumns * 128 / 16) + (k & 3) * 2, tc_desc_high(1024), idesc_s, k > 0);
+                tc_commit(&s.s_full[stream]);
+                mbar_arrive(&s.s_full[stream]); // orders scales and page mask before their readers
+                if (i + 2 >= tiles)
+                    tc_commit(&s.q_empty[qbuf]);
+            }
+            __syncwarp();
+            if (pending)
+                add_values(step - 1, keep);
+            keep = i > first + 1 && !(p.sums && ((i - first) >> 1) % kSpan == 0);
+            pending = true;
+        }
+        unit0 += tiles;
+    }
+    if (ok && pending)
+        add_values(step - 1, keep);
+    // no product may still be running when the CTA ends
+    if (leader)
+        tc_commit(&s.drain[stream]);
+    return warp_wait(&s.drain[stream], 0) && ok;
+}
+
+// ---------------------------------------------------------------- softmax
+// Eight scores of this thread's key, from S to base 2 without the reference; kScore bit 0:
+// capped, bit 1: biased; plain ones are left as S (the caller has the factor). j: the first
+// one's row.
+template <int kScore, int kRows>
+__device__ __forceinline__ void form_scores(const TreeInt8Params &p, const TreeInt8Smem<kRows> &s, float *x, int j, float factor,
+                                            int buf, float up, float down, int pos)
+{
+    if constexpr ((kScore & 1) != 0) {
+        float u[8], over = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; k += 2) {
+            const f32x2 v = mul2(f32x2(x[k], x[k + 1]), f32x2(factor, factor)), t = mul2(v, v);
+            float t0, t1;
+            t.get(t0, t1);
+            over = max3(over, t0, t1);
+            f32x2 y(p.tanh_c[kTanhTerms - 1], p.tanh_c[kTanhTerms - 1]);
+#pragma unroll
+            for (int i = kTanhTerms - 2; i >= 0; --i)
+                y = fma2(y, t, f32x2(p.tanh_c[i], p.tanh_c[i]));
+            v.get(u[k], u[k + 1]);
+            mul2(v, y).get(x[k], x[k + 1]);
+        }
+        if (__any_sync(0xFFFFFFFFu, over > 1.f)) { // scores past their cap
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float size = fabsf(u[k]), rest = rcp(1.f + ex2(size * (2.f * kLog2e)));
+                const float y = copysignf(fmaf(-2.f * p.cap_out, rest, p.cap_out), u[k]);
+                x[k] = size > 1.f ? y : x[k];
             }
         }
     }
     if constexpr ((kScore & 2) != 0) {
         if constexpr ((kScore & 1) == 0) {
 #pragma unroll
-            for (int j = 0; j < kRows; ++j)
-                x[j] *= factor;
+            for (int k = 0; k < 8; ++k)
+                x[k] *= factor;
         }
+        const float *slope_up = s.slope_up[buf] + j, *slope_down = s.slope_down[buf] + j;
         if (s.by_sign[buf]) {
-            const float up = distance(pos, prefix), down = distance(pos, 0);
 #pragma unroll
-            for (int j = 0; j < kRows; j += 2) {
-                const f32x2 a(s.slope_up[buf][j], s.slope_up[buf][j + 1]), d(s.slope_down[buf][j], s.slope_down[buf][j + 1]);
-                fma2(a, f32x2(up, up), fma2(d, f32x2(down, down), f32x2(x[j], x[j + 1]))).get(x[j], x[j + 1]);
-            }
+            for (int k = 0; k < 8; k += 2)
+                fma2(f32x2(slope_up[k], slope_up[k + 1]), f32x2(up, up),
+                     fma2(f32x2(slope_down[k], slope_down[k + 1]), f32x2(down, down), f32x2(x[k], x[k + 1])))
+                    .get(x[k], x[k + 1]);
         } else {
 #pragma unroll
-            for (int j = 0; j < kRows; ++j)
-                x[j] = fmaf(s.slope_up[buf][j] + s.slope_down[buf][j], distance(pos, s.anchor[buf][j]), x[j]);
+            for (int k = 0; k < 8; ++k)
+                x[k] = fmaf(slope_up[k] + slope_down[k], distance(pos, s.anchor[buf][j + k]), x[k]);
         }
     }
 }
 
-template <int kScore, int kRows> __device__ bool attend(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, int rg, int stream)
+template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, int rg, int stream)
 {
     using Sh = Shape<kRows>;
-    constexpr int kRing = Sh::kRing;
+    constexpr int kGroups = kRows / 8; // rows are taken eight at a time
     const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
     const int key_row = warp * 32 + lane; // of a tile; of O^T: the dim
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t tmem = warp_uniform(s.tmem_base + stream * kStreamColumns);
-    const uint32_t idesc_s = tc_idesc_f16(Sh::kScoreColumns, false);
-    const uint32_t idesc_o = tc_idesc_f16(Sh::kOutColumns, true);
-    const bool leader = warp == 0 && elect_one();
-    unsigned char *v16 = s.v16[stream], *p16 = s.p16[stream];
+    const uint32_t tmem_s = s.tmem_base + lanes + stream * kStreamColumns + kColS;
+    const uint32_t tmem_o = s.tmem_base + lanes + stream * kStreamColumns + kColO;
     // A wait that ran out ends no loop: all of a stream's warps meet at its barriers, and
     // do so to the end, without further waits.
     bool ok = true;
     const auto wait = [&](uint64_t *bar, uint32_t parity) { ok = ok && warp_wait(bar, parity); };
     float *sums = p.sums ? p.sums + static_cast<size_t>(2 * blockIdx.x + stream) * kRows * kHeadDim + key_row : nullptr;
+    // what the threads of one stream share by row
+    float *neg_m = s.neg_m[stream], *f_l = s.f_l[stream], *f_o = s.f_o[stream], *g_sums = s.g_sums[stream];
+    float (*warp_part)[kMaxRows] = s.warp_part[stream];
 
     Segments seg(s);
     int unit0 = 0; // the segment's first tile in the run
     int step = 0;  // this stream's tiles so far
     for (int index = 0; seg.next(p); ++index) {
-        const int buf = index & 1, qbuf = index % Sh::kQueries;
+        const int buf = index & 1;
         const int tiles = seg.seg_tile1 - seg.seg_tile0;
         const int prefix = seg.T - seg.n;
         wait(&s.rows_full[buf], (index >> 1) & 1);
-        wait(&s.q_full[qbuf], (index / Sh::kQueries) & 1);
         if (key_row < kRows) {
-            s.neg_m[stream][key_row] = INFINITY; // nothing seen yet
-            s.g_sums[stream][key_row] = 1.f;
+            neg_m[key_row] = INFINITY; // nothing seen yet
+            g_sums[key_row] = 1.f;
         }
+        stream_sync(stream);
         float l[kRows];
 #pragma unroll
         for (int j = 0; j < kRows; ++j)
@@ -524,57 +663,11 @@ template <int kScore, int kRows> __device__ bool attend(const TreeInt8Params &p,
         const int first = (unit0 ^ stream) & 1;
         for (int i = first; i < tiles; i += 2, ++step) {
             const int key0 = (seg.seg_tile0 + i) * kTileKeys, key = key0 + key_row;
-            // ---- K: codes -> fp16 in tensor memory
-            int put = 2 * step, slot = put % kRing;
-            wait(&s.code_full[stream][slot], (put / kRing) & 1);
-            const uint32_t valid = s.valid[stream][slot];
-            float ks = s.scales[stream][slot][key_row];
-            const unsigned char *codes = s.codes[stream][slot] + key_row * kHeadDim;
-#pragma unroll
-            for (int c = 0; c < 8; c += 2) {
-                uint32_t w[16];
-                widen_codes(*reinterpret_cast<const uint4 *>(codes + ((c ^ (key_row & 7)) << 4)), w);
-                widen_codes(*reinterpret_cast<const uint4 *>(codes + (((c + 1) ^ (key_row & 7)) << 4)), w + 8);
-                tmem_st16(tmem + lanes + kColK + 8 * c, reinterpret_cast<const float *>(w));
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&s.code_empty[stream][slot]);
-            stream_sync(stream);
-            if (leader) { // S^T = K Q^T
-                tc_fence_after();
-                const uint32_t qa = tc_desc_low(smem_addr(s.q16[qbuf]), 16);
-#pragma unroll
-                for (int k = 0; k < kHeadDim / 16; ++k) // 64 dims a half, 32 bytes a step
-                    tc_mma_ts(tmem + kColS, tmem + kColK + 8 * k,
-                              qa + (k >> 2) * (Sh::kScoreColumns * 128 / 16) + (k & 3) * 2, tc_desc_high(1024), idesc_s, k > 0);
-                tc_commit(&s.s_full[stream]);
-                if (i + 2 >= tiles)
-                    tc_commit(&s.q_empty[qbuf]);
-            }
-            __syncwarp();
-            // ---- V: codes -> fp16 in shared memory, once the last tile's product is through with it
-            ++put, slot = put % kRing;
-            wait(&s.code_full[stream][slot], (put / kRing) & 1);
-            float vs = s.scales[stream][slot][key_row];
-            codes = s.codes[stream][slot] + key_row * kHeadDim;
-            if (step > 0)
-                wait(&s.o_done[stream], (step - 1) & 1);
+            const int place = (unit0 + i) % kScaleRing;
+            wait(&s.s_full[stream], step & 1);
             tc_fence_after();
-            unsigned char *v_row = v16 + (key_row >> 3) * 2048 + (key_row & 7) * 128;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                uint32_t w[8];
-                widen_codes(*reinterpret_cast<const uint4 *>(codes + ((c ^ (key_row & 7)) << 4)), w);
-                unsigned char *half = v_row + (c >> 2) * 1024;
-                *reinterpret_cast<uint4 *>(half + (((2 * c & 7) ^ (key_row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-                *reinterpret_cast<uint4 *>(half + (((2 * c + 1 & 7) ^ (key_row & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
-            }
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&s.code_empty[stream][slot]);
+            const uint32_t valid = s.valid[place];
+            float ks = s.scales[place][0][key_row], vs = s.scales[place][1][key_row];
             // ---- the rows that see this key
             uint32_t sees_lo = 0xFFFFFFFFu, sees_hi = 0xFFFFFFFFu;
             const bool fix = key0 + kTileKeys > prefix || valid != 0xFFu;
@@ -586,135 +679,196 @@ template <int kScore, int kRows> __device__ bool attend(const TreeInt8Params &p,
                 if (!sees)
                     ks = vs = 0.f; // may hold anything
             }
-            const auto hide = [&](float *x, float what) {
+            const auto seen = [&](int j) { return (j < 32 ? sees_lo : sees_hi) >> (j & 31); };
+            // Capped and biased scores are formed in place, in a loop small enough for the
+            // instruction cache.
+            if constexpr (kScore != 0) {
+                int pos = key;
+                float up = 0.f, down = 0.f;
+                if constexpr ((kScore & 2) != 0) {
+                    if (key >= prefix && key < seg.T)
+                        pos = p.positions[static_cast<size_t>(seg.b) * p.M + key - prefix];
+                    up = distance(pos, prefix), down = distance(pos, 0);
+                }
+                const float factor = ks * (kScore & 1 ? p.cap_u : p.c);
+                float y[2][8];
+                tmem_ld8(y[0], tmem_s);
+                const auto group = [&](int j, float *now, float *next) {
+                    tmem_wait_ld8(now);
+                    if (j + 8 < kRows)
+                        tmem_ld8(next, tmem_s + j + 8);
+                    form_scores<kScore, kRows>(p, s, now, j, factor, buf, up, down, pos);
+                    tmem_st8(tmem_s + j, now);
+                };
+#pragma unroll 1
+                for (int j = 0; j < kRows; j += 16) {
+                    group(j, y[0], y[1]);
+                    if (j + 8 < kRows)
+                        group(j + 8, y[1], y[0]);
+                }
+                tmem_wait_st();
+            }
+            const float mul = kScore ? 1.f : ks * p.c;
+            const float vs_size = fabsf(vs) <= FLT_MAX ? fabsf(vs) : 0.f;
+            bool there = step == 0; // the last tile's product with V is done
+            const bool span = sums && i > first + 1 && ((i - first) >> 1) % kSpan == 0;
+            float x[kRows];
+            // Once more after the references moved (which settles it; the limit is for no case known).
+#pragma unroll 1
+            for (int turn = 0;; ++turn) {
+                if constexpr (kRows == 8) {
+                    tmem_ld8(x, tmem_s);
+                    tmem_wait_ld8(x);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kRows; j += 16)
+                        tmem_ld16(x + j, tmem_s + j);
+#pragma unroll
+                    for (int j = 0; j < kRows; j += 16)
+                        tmem_wait_ld16(x + j);
+                }
+                // For references so large that their rounding matters the scores are rounded
+                // as they were, before the difference (a packed product and sum would be fused).
+                if (kScore == 0 && large) {
+#pragma unroll
+                    for (int j = 0; j < kRows; ++j)
+                        x[j] = __fadd_rn(__fmul_rn(x[j], mul), neg_m[j]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kRows; j += 2)
+                        fma2(f32x2(x[j], x[j + 1]), f32x2(mul, mul), f32x2(neg_m[j], neg_m[j + 1])).get(x[j], x[j + 1]);
+                }
+                if (fix) {
+#pragma unroll
+                    for (int j = 0; j < kRows; ++j)
+                        x[j] = seen(j) & 1u ? x[j] : -INFINITY;
+                }
+                float tops[kGroups];
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    const float *y = x + 8 * g;
+                    tops[g] = fmaxf(max3(max3(y[0], y[1], y[2]), y[3], y[4]), max3(y[5], y[6], y[7]));
+                }
+                float top = tops[0];
+#pragma unroll
+                for (int g = 1; g < kGroups; ++g)
+                    top = fmaxf(top, tops[g]);
+                if (!stream_any(stream, top > kRise || vs_size > vs_limit) || turn == 4)
+                    break;
+                // ---- references move in the groups that need it; F may too
+                if (!there)
+                    wait(&s.o_done[stream], (step - 1) & 1);
+                there = true;
+                tc_fence_after();
+                uint32_t over = 0;
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g)
+                    over |= tops[g] > kRise ? 1u << g : 0u;
+                over = __reduce_or_sync(0xFFFFFFFFu, over);
+                const float warp_vs = warp_max(vs_size);
+                if (lane == 0)
+                    s.warp_over[stream][warp] = over, s.warp_vs[stream][warp] = warp_vs;
+                stream_sync(stream);
+                const uint32_t *o4 = s.warp_over[stream];
+                over = o4[0] | o4[1] | o4[2] | o4[3];
+#pragma unroll 1
+                for (uint32_t rest = over; rest; rest &= rest - 1) {
+                    const int j = 8 * (__ffs(rest) - 1);
+                    float y[8];
+                    tmem_ld8(y, tmem_s + j);
+                    tmem_wait_ld8(y);
+                    const uint32_t bits = seen(j);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float most = warp_max(bits >> k & 1u ? __fmul_rn(y[k], mul) : -INFINITY);
+                        if (lane == k)
+                            warp_part[warp][j + k] = most;
+                    }
+                }
+                float fv = 1.f;
+                const float *v4 = s.warp_vs[stream];
+                const float all = fmaxf(fmaxf(v4[0], v4[1]), fmaxf(v4[2], v4[3]));
+                if (all > vs_limit) { // F all in [8, 16)
+                    const int e = min(126, max(-126, 130 - static_cast<int>(__float_as_uint(all) >> 23)));
+                    const int was = static_cast<int>(__float_as_uint(f) >> 23) - 127;
+                    fv = ex2(static_cast<float>(e - was));
+                    f = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+                    vs_limit = 64.f / f;
+                }
+                stream_sync(stream);
+                bool far = false;
+                if (key_row < kRows) {
+                    float fm = 1.f, m = -neg_m[key_row];
+                    if (over >> (key_row >> 3) & 1u) {
+                        const float most = fmaxf(fmaxf(warp_part[0][key_row], warp_part[1][key_row]),
+                                                 fmaxf(warp_part[2][key_row], warp_part[3][key_row]));
+                        if (m == -INFINITY ? most > -INFINITY : most - m > kRise) {
+                            fm = m == -INFINITY ? 0.f : ex2(m - most);
+                            m = most;
+                            neg_m[key_row] = -most;
+                        }
+                    }
+                    far = fabsf(m) > 65536.f && m > -INFINITY;
+                    f_l[key_row] = fm;
+                    f_o[key_row] = fm * fv;
+                    g_sums[key_row] *= fm * fv;
+                }
+                large = stream_any(stream, far);
 #pragma unroll
                 for (int j = 0; j < kRows; ++j)
-                    x[j] = ((j < 32 ? sees_lo : sees_hi) >> (j & 31)) & 1u ? x[j] : what;
-            };
-            int pos = key;
-            if constexpr ((kScore & 2) != 0) {
-                if (key >= prefix && key < seg.T)
-                    pos = p.positions[static_cast<size_t>(seg.b) * p.M + key - prefix];
+                    l[j] *= f_l[j];
+                if (i > first + 1) {
+#pragma unroll 1
+                    for (uint32_t rest = fv == 1.f ? over : (1u << kGroups) - 1u; rest; rest &= rest - 1) {
+                        const int j = 8 * (__ffs(rest) - 1);
+                        float hi[8], lo[8];
+                        tmem_ld8(hi, tmem_o + j);
+                        tmem_ld8(lo, tmem_o + Sh::kLo + j);
+                        tmem_wait_ld8(hi), tmem_wait_ld8(lo);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            hi[k] *= f_o[j + k], lo[k] *= f_o[j + k];
+                        tmem_st8(tmem_o + j, hi);
+                        tmem_st8(tmem_o + Sh::kLo + j, lo);
+                    }
+                    tmem_wait_st();
+                }
             }
-            const float factor = ks * (kScore & 1 ? p.cap_u : p.c);
-            const float mul = kScore ? 1.f : factor;
-            wait(&s.s_full[stream], step & 1);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&s.s_read[stream]);
+            if (!there)
+                wait(&s.o_done[stream], (step - 1) & 1);
             tc_fence_after();
             // every span O moves out of the tensor core, to be added up to nearest
-            const bool span = sums && i > first + 1 && ((i - first) >> 1) % kSpan == 0;
             if (span) {
 #pragma unroll 1
                 for (int j = 0; j < kRows; j += 8) {
                     float hi[8], lo[8];
-                    tmem_ld8(hi, tmem + lanes + kColO + j);
-                    tmem_ld8(lo, tmem + lanes + kColO + Sh::kLo + j);
+                    tmem_ld8(hi, tmem_o + j);
+                    tmem_ld8(lo, tmem_o + Sh::kLo + j);
                     tmem_wait_ld8(hi), tmem_wait_ld8(lo);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         float v = hi[k] + lo[k];
                         if (summed)
-                            v = fmaf(sums[(j + k) * kHeadDim], s.g_sums[stream][j + k], v);
+                            v = fmaf(sums[(j + k) * kHeadDim], g_sums[j + k], v);
                         sums[(j + k) * kHeadDim] = v;
                     }
                 }
                 summed = true;
                 stream_sync(stream);
                 if (key_row < kRows)
-                    s.g_sums[stream][key_row] = 1.f;
+                    g_sums[key_row] = 1.f;
                 stream_sync(stream);
             }
-            const bool keep = i > first + 1 && !span; // O holds earlier tiles
-            // ---- scores relative to the references, which move if they have to
-            float x[kRows];
-#pragma unroll 1
-            for (int turn = 0;; ++turn) {
-                load_scores<kScore, kRows>(p, s, x, tmem + lanes + kColS, factor, buf, prefix, pos);
-                if (turn == 1) {
-                    // this tile's maxima by row, and of the V scales
-#pragma unroll
-                    for (int j = 0; j < kRows; ++j) {
-                        const float top = warp_max(((j < 32 ? sees_lo : sees_hi) >> (j & 31)) & 1u ? __fmul_rn(x[j], mul) : -INFINITY);
-                        if (lane == (j & 31))
-                            s.warp_part[stream][warp][j] = top;
-                    }
-                    const float size = fabsf(vs);
-                    const float top_vs = warp_max(size <= FLT_MAX ? size : 0.f);
-                    if (lane == 0)
-                        s.warp_vs[stream][warp] = top_vs;
-                    stream_sync(stream);
-                    float fv = 1.f;
-                    {
-                        const float *v = s.warp_vs[stream];
-                        const float all = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-                        if (all > vs_limit) {
-                            // F all in [8, 16)
-                            const int e = min(126, max(-126, 130 - static_cast<int>(__float_as_uint(all) >> 23)));
-                            const int was = static_cast<int>(__float_as_uint(f) >> 23) - 127;
-                            fv = ex2(static_cast<float>(e - was));
-                            f = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-                            vs_limit = 64.f / f;
-                        }
-                    }
-                    bool far = false;
-                    if (key_row < kRows) {
-                        const float (*w)[kMaxRows] = s.warp_part[stream];
-                        const float top = fmaxf(fmaxf(w[0][key_row], w[1][key_row]), fmaxf(w[2][key_row], w[3][key_row]));
-                        const float m = -s.neg_m[stream][key_row];
-                        const bool move = m == -INFINITY ? top > -INFINITY : top - m > kRise;
-                        const float fm = !move ? 1.f : m == -INFINITY ? 0.f : ex2(m - top);
-                        if (move)
-                            s.neg_m[stream][key_row] = -top;
-                        far = fabsf(move ? top : m) > 65536.f && (move || m > -INFINITY);
-                        s.f_l[stream][key_row] = fm;
-                        s.f_o[stream][key_row] = fm * fv;
-                        s.g_sums[stream][key_row] *= fm * fv;
-                    }
-                    large = stream_any(stream, far);
-#pragma unroll
-                    for (int j = 0; j < kRows; ++j)
-                        l[j] *= s.f_l[stream][j];
-                    if (keep) {
-#pragma unroll 1
-                        for (int j = 0; j < Sh::kOutColumns; j += 8) {
-                            float o[8];
-                            if ((j & (Sh::kLo - 1)) >= kRows)
-                                continue;
-                            tmem_ld8(o, tmem + lanes + kColO + j);
-                            tmem_wait_ld8(o);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                o[k] *= s.f_o[stream][(j & (Sh::kLo - 1)) + k];
-                            tmem_st8(tmem + lanes + kColO + j, o);
-                        }
-                        tmem_wait_st();
-                    }
-                }
-                float top = -INFINITY;
-                // For references so large that their rounding matters the scores are rounded as
-                // they were, before the difference (a packed product and sum would be fused).
-                if (kScore == 0 && large) {
-#pragma unroll
-                    for (int j = 0; j < kRows; ++j)
-                        x[j] = __fadd_rn(__fmul_rn(x[j], mul), s.neg_m[stream][j]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < kRows; j += 2)
-                        fma2(f32x2(x[j], x[j + 1]), f32x2(mul, mul), f32x2(s.neg_m[stream][j], s.neg_m[stream][j + 1]))
-                            .get(x[j], x[j + 1]);
-                }
-                if (fix)
-                    hide(x, -INFINITY);
-                if (turn == 1)
-                    break;
-#pragma unroll
-                for (int j = 0; j < kRows; j += 2)
-                    top = max3(top, x[j], x[j + 1]);
-                if (!stream_any(stream, top > kRise || (fabsf(vs) > vs_limit && fabsf(vs) <= FLT_MAX)))
-                    break;
-            }
             // ---- weights: their sum, and with the V scale as a pair into shared memory
-            const float vf = vs * f;
-            unsigned char *p_row = p16 + (kRows == 64 ? (key_row >> 3) * 2048 : (key_row >> 3) * 1024) + (key_row & 7) * 128;
+            const bool number = fabsf(vs) <= FLT_MAX;
+            const float vf = number ? vs * f : 0.f;
+            unsigned char *p_row = s.p16[stream] + (kRows == 64 ? (key_row >> 3) * 2048 : (key_row >> 3) * 1024) + (key_row & 7) * 128;
+            // lo's place: the other half of the key's row, or its second panel
+            const int lo_by = kRows == 64 ? 1024 : 0, lo_part = kRows == 64 ? 0 : Sh::kLo / 8;
 #pragma unroll
             for (int j = 0; j < kRows; j += 8) {
                 uint32_t hi[4], lo[4];
@@ -722,38 +876,26 @@ template <int kScore, int kRows> __device__ bool attend(const TreeInt8Params &p,
                 for (int k = 0; k < 8; k += 2) {
                     const f32x2 w(ex2(x[j + k]), ex2(x[j + k + 1]));
                     add2(f32x2(l[j + k], l[j + k + 1]), w).get(l[j + k], l[j + k + 1]);
-                    f32x2 wv = mul2(w, f32x2(vf, vf));
-                    if (fix) { // a scale that is no number stays with those who see it
-                        float a, b;
-                        wv.get(a, b);
-                        const uint32_t bits = (j < 32 ? sees_lo : sees_hi) >> (j & 31);
-                        a = bits >> k & 1u ? a : 0.f, b = bits >> (k + 1) & 1u ? b : 0.f;
-                        wv = f32x2(a, b);
-                    }
-                    split_f16(wv, hi[k / 2], lo[k / 2]);
+                    split_f16(mul2(w, f32x2(vf, vf)), hi[k / 2], lo[k / 2]);
                 }
                 *reinterpret_cast<uint4 *>(p_row + (((j >> 3) ^ (key_row & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                unsigned char *lo_at = kRows == 64 ? p_row + 1024 + (((j >> 3) ^ (key_row & 7)) << 4)
-                                                   : p_row + ((((j + Sh::kLo) >> 3) ^ (key_row & 7)) << 4);
-                *reinterpret_cast<uint4 *>(lo_at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                *reinterpret_cast<uint4 *>(p_row + lo_by + ((((j >> 3) + lo_part) ^ (key_row & 7)) << 4)) =
+                    make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+            // a V scale that is no number goes as it is to those who see it
+            if (!number) {
+#pragma unroll 1
+                for (int j = 0; j < kRows; ++j)
+                    if (seen(j) & 1u)
+                        *reinterpret_cast<uint16_t *>(p_row + (((j >> 3) ^ (key_row & 7)) << 4) + 2 * (j & 7)) =
+                            vs != vs ? 0x7FFFu : vs > 0.f ? 0x7C00u : 0xFC00u;
             }
             fence_proxy_async_smem();
             tc_fence_before();
-            stream_sync(stream);
-            if (leader) { // O^T += V^T P^T
-                tc_fence_after();
-                const uint32_t va = tc_desc_low(smem_addr(v16), 1024), pa = tc_desc_low(smem_addr(p16), 1024);
-                constexpr int kStepP = kRows == 64 ? 4096 : 2048; // 16 keys
-#pragma unroll
-                for (int k = 0; k < kTileKeys / 16; ++k)
-                    tc_mma_ss(tmem + kColO, va + k * (4096 / 16), tc_desc_high(2048), pa + k * (kStepP / 16),
-                              tc_desc_high(kStepP / 2), idesc_o, k > 0 || keep);
-                tc_commit(&s.o_done[stream]);
-            }
             __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&s.p_ready[stream]);
         }
-        if (first >= tiles && leader) // no tile of this segment is this stream's
-            mbar_arrive(&s.q_empty[qbuf]);
         unit0 += tiles;
 
         // ---- the end of the segment: both streams' states joined, O written
@@ -762,7 +904,7 @@ template <int kScore, int kRows> __device__ bool attend(const TreeInt8Params &p,
             constexpr int kAtOnce = kRows < 32 ? kRows : 32;
             const float sum = sum_lanes<kAtOnce>(l + j0);
             if (lane % (32 / kAtOnce) == 0)
-                s.warp_part[stream][warp][j0 + lane / (32 / kAtOnce)] = sum;
+                warp_part[warp][j0 + lane / (32 / kAtOnce)] = sum;
         }
         if (first < tiles)
             wait(&s.o_done[stream], (step - 1) & 1);
@@ -771,21 +913,21 @@ template <int kScore, int kRows> __device__ bool attend(const TreeInt8Params &p,
 #pragma unroll 1
             for (int j = 0; j < kRows; j += 8) {
                 float hi[8];
-                tmem_ld8(hi, tmem + lanes + kColO + j);
+                tmem_ld8(hi, tmem_o + j);
                 tmem_wait_ld8(hi);
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    hi[k] = fmaf(sums[(j + k) * kHeadDim], s.g_sums[stream][j + k], hi[k]);
-                tmem_st8(tmem + lanes + kColO + j, hi);
+                    hi[k] = fmaf(sums[(j + k) * kHeadDim], g_sums[j + k], hi[k]);
+                tmem_st8(tmem_o + j, hi);
             }
             tmem_wait_st();
         }
         tc_fence_before();
         stream_sync(stream);
         if (key_row < kRows) {
-            const float (*w)[kMaxRows] = s.warp_part[stream];
-            s.l_end[stream][key_row] = (w[0][key_row] + w[1][key_row]) + (w[2][key_row] + w[3][key_row]);
-            s.m_end[stream][key_row] = -s.neg_m[stream][key_row];
+            s.l_end[stream][key_row] = (warp_part[0][key_row] + warp_part[1][key_row]) +
+                                       (warp_part[2][key_row] + warp_part[3][key_row]);
+            s.m_end[stream][key_row] = -neg_m[key_row];
             if (key_row == 0)
                 s.inv_f[stream] = 1.f / f;
         }
@@ -862,11 +1004,14 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
     const int rg = blockIdx.x % p.row_groups, cta = blockIdx.x / p.row_groups;
     if (tid == 0) {
         prefetch_tensormap(&mk), prefetch_tensormap(&mv);
+        for (int i = 0; i < Sh::kRing; ++i)
+            mbar_init(&s.code_full[i], 1), mbar_init(&s.code_empty[i], 4);
         for (int w = 0; w < 2; ++w) {
-            for (int i = 0; i < Sh::kRing; ++i)
-                mbar_init(&s.code_full[w][i], 1), mbar_init(&s.code_empty[w][i], 4);
             mbar_init(&s.rows_full[w], 1), mbar_init(&s.rows_empty[w], 8);
-            mbar_init(&s.s_full[w], 1), mbar_init(&s.o_done[w], 1);
+            mbar_init(&s.k_ready[w], 4), mbar_init(&s.v_ready[w], 4); // a warp each
+            mbar_init(&s.s_read[w], 4), mbar_init(&s.p_ready[w], 4);
+            mbar_init(&s.s_full[w], 2); // the products' completion, and the issuing thread
+            mbar_init(&s.o_done[w], 1), mbar_init(&s.drain[w], 1);
         }
         for (int i = 0; i < Sh::kQueries; ++i)
             mbar_init(&s.q_full[i], 1), mbar_init(&s.q_empty[i], 2);
@@ -888,19 +1033,24 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
     __syncthreads();
     tc_fence_after();
 
-    // Registers move from the third warpgroup to the streams: 256 * 208 + 128 * 88 =
-    // 384 * 168 as launched.
+    // Registers move to the softmax: 256 * 176 + 256 * 80 = 512 * 128 as launched.
     bool ok = true;
-    if (warp >= kCodeWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-        if (warp == kCodeWarp && s.units > 0)
-            ok = fetch_codes(p, s, &mk, &mv);
-        else if (warp == kQueryWarp && s.units > 0)
-            ok = fetch_rows<kScore>(p, s, rg);
+    if (warp >= kWidenWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (s.units > 0) {
+            if (warp < kCodeWarp)
+                ok = widen(p, s);
+            else if (warp == kCodeWarp)
+                ok = fetch_codes(p, s, &mk, &mv);
+            else if (warp == kQueryWarp)
+                ok = fetch_rows<kScore>(p, s, rg);
+            else
+                ok = multiply(p, s, warp - kMmaWarp);
+        }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         if (s.units > 0)
-            ok = attend<kScore>(p, s, rg, warp >> 2);
+            ok = soften<kScore>(p, s, rg, warp >> 2);
     }
     if (!ok && lane == 0)
         atomicOr(&g_flags_tree_int8, PGQA_DEVERR_WAIT_TIMEOUT);
