@@ -33,7 +33,7 @@
 //   warps 0-3, 4-7    one softmax warpgroup per stream: S -> P -> shared memory;
 //   warps 8-11        widen codes to fp16, K's into tensor memory, V's into shared memory,
 //                     for both streams;
-//   warp 12           requests codes (TMA, one lane per page of a tile) and scales (bulk copies);
+//   warp 12           requests codes (TMA, one lane per page of a tile) and scales;
 //   warp 13           prepares the next segment's queries, masks and slopes;
 //   warps 14, 15      issue one stream's products each: the next S as soon as the
 //                     softmax has read the last one, then the last tile's O += P V.
@@ -132,6 +132,7 @@ template <int kRows> struct __align__(1024) TreeInt8Smem {
     float zero;
 };
 template <int kRows> constexpr int kInt8Smem = sizeof(TreeInt8Smem<kRows>);
+static_assert(Shape<32>::kRing % 2 == 0 && Shape<64>::kRing % 2 == 0, "K's and V's slots");
 static_assert(kInt8Smem<32> <= 232448 && kInt8Smem<64> <= 232448, "one CTA's shared memory");
 
 __device__ __forceinline__ void stream_sync(int stream)
@@ -167,6 +168,16 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity)
                  : "r"(smem_addr(bar)), "r"(parity)
                  : "memory");
     return done != 0;
+}
+
+// An asynchronous copy of 16 bytes, and this thread's arrival at a barrier once its copies are done.
+__device__ __forceinline__ void cp_async16(void *dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
 // As tmem_ld16, 8 columns.
@@ -265,7 +276,10 @@ __device__ bool fetch_codes(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, con
                 atomicOr(&g_flags_tree_int8, PGQA_DEVERR_BAD_PAGE);
             const int row = here ? ((phys * p.Hkv + seg.h) << p.log2_page) + (key & (P - 1)) : outside;
             const uint32_t valid = __ballot_sync(0xFFFFFFFFu, !needed || in_pool);
-            const int bytes = kCodeBytes + 8 * box_keys * __popc(__ballot_sync(0xFFFFFFFFu, here));
+            // this lane's four keys of the scales
+            const int box = lane * 4 / box_keys;
+            const int scale_row = __shfl_sync(0xFFFFFFFFu, row, box) + (lane * 4 & (box_keys - 1));
+            const bool scales_here = __shfl_sync(0xFFFFFFFFu, here, box);
             uint32_t by16 = 0; // a bit per 16 keys
             for (int i = 0; i < 8; ++i)
                 by16 |= ((valid >> (i * 16 / box_keys)) & 1u) << i;
@@ -279,17 +293,18 @@ __device__ bool fetch_codes(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, con
                 if (lane == 0) {
                     if (!is_v)
                         s.valid[unit % kScaleRing] = by16;
-                    mbar_arrive_expect_tx(full, is_v ? kCodeBytes : bytes);
+                    mbar_arrive_expect_tx(full, kCodeBytes);
                 }
                 __syncwarp();
-                if (lane < boxes) {
-                    // a box outside the tensor arrives as zeros
+                if (lane < boxes) // a box outside the tensor arrives as zeros
                     tma_load_2d(s.codes[slot] + lane * box_keys * kHeadDim, is_v ? mv : mk, 0, row, full, policy);
-                    if (!is_v && here) { // both scales come with K
-                        float (*scales)[kTileKeys] = s.scales[unit % kScaleRing];
-                        bulk_copy_g2s(scales[0] + lane * box_keys, p.k_scale + row, 4 * box_keys, full, policy);
-                        bulk_copy_g2s(scales[1] + lane * box_keys, p.v_scale + row, 4 * box_keys, full, policy);
+                if (!is_v) { // both scales come with K, 16 bytes a lane
+                    float (*scales)[kTileKeys] = s.scales[unit % kScaleRing];
+                    if (scales_here) {
+                        cp_async16(scales[0] + lane * 4, p.k_scale + scale_row);
+                        cp_async16(scales[1] + lane * 4, p.v_scale + scale_row);
                     }
+                    cp_async_arrive(full);
                 }
             }
             if (!ok)
@@ -1004,8 +1019,8 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
     const int rg = blockIdx.x % p.row_groups, cta = blockIdx.x / p.row_groups;
     if (tid == 0) {
         prefetch_tensormap(&mk), prefetch_tensormap(&mv);
-        for (int i = 0; i < Sh::kRing; ++i)
-            mbar_init(&s.code_full[i], 1), mbar_init(&s.code_empty[i], 4);
+        for (int i = 0; i < Sh::kRing; ++i) // K's slots are even: the codes, and 32 lanes' scales
+            mbar_init(&s.code_full[i], i & 1 ? 1 : 33), mbar_init(&s.code_empty[i], 4);
         for (int w = 0; w < 2; ++w) {
             mbar_init(&s.rows_full[w], 1), mbar_init(&s.rows_empty[w], 8);
             mbar_init(&s.k_ready[w], 4), mbar_init(&s.v_ready[w], 4); // a warp each
