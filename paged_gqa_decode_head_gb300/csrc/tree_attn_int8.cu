@@ -56,8 +56,9 @@ __device__ unsigned g_flags_tree_int8;
 constexpr int kCodeBytes = kTileKeys * kHeadDim; // 16 KB of K or V codes
 constexpr int kInt8Threads = 512;
 constexpr int kWidenWarp = 8, kCodeWarp = 12, kQueryWarp = 13, kMmaWarp = 14; // and kMmaWarp + 1
-// Tiles whose scales are kept. A tile is requested once K of the one three before it is
-// widened (a ring of six), and that waits for the product with V of the one six before.
+// Tiles whose scales are kept. Tile u is requested once K of tile u - 3 is widened (a ring of
+// three). V of u - 5 was widened before that, and V of u - 6; they waited for the products with
+// V of u - 7 and of u - 8, whose softmax is then done.
 constexpr int kScaleRing = 8;
 constexpr float kRise = 8.f;  // rise of a row's scores (base 2) that moves its reference
 constexpr int kSpan = 16;     // a stream's tiles between two moves of O out of the tensor core (fp32 outputs)
@@ -97,13 +98,13 @@ template <int kRows> struct Shape {
     static constexpr int kScoreColumns = kRows < 16 ? 16 : kRows; // of S^T = K Q^T
     static constexpr int kOutColumns = kRows == 64 ? 128 : 64;    // of O^T: hi, then lo
     static constexpr int kLo = kOutColumns / 2;                   // lo's first column
-    static constexpr int kRing = kRows == 64 ? 4 : 6;             // slots of codes
+    static constexpr int kRing = kRows == 64 ? 2 : 3;             // slots of K's codes, and of V's
     static constexpr int kQueries = kRows == 64 ? 1 : 2;          // segments whose queries are kept
 };
 
 template <int kRows> struct __align__(1024) TreeInt8Smem {
     using Sh = Shape<kRows>;
-    unsigned char codes[Sh::kRing][kCodeBytes]; // K and V of a tile in turn
+    unsigned char codes[2][Sh::kRing][kCodeBytes]; // K's, V's
     unsigned char v16[2][kTileKeys * kRowBytes];
     unsigned char p16[2][kTileKeys * Sh::kOutColumns * 2];
     unsigned char q16[Sh::kQueries][Sh::kScoreColumns * kRowBytes];
@@ -120,7 +121,7 @@ template <int kRows> struct __align__(1024) TreeInt8Smem {
     float m_end[2][kMaxRows], l_end[2][kMaxRows], inv_f[2];
     float weight[2][2][kMaxRows]; // by the stream that writes; of stream 0's and 1's O
     uint32_t warp_over[2][4];
-    uint64_t code_full[Sh::kRing], code_empty[Sh::kRing];
+    uint64_t code_full[2][Sh::kRing], code_empty[2][Sh::kRing];
     uint64_t q_full[Sh::kQueries], q_empty[Sh::kQueries];
     uint64_t rows_full[2], rows_empty[2];
     uint64_t k_ready[2], v_ready[2]; // a tile's codes are widened
@@ -132,7 +133,6 @@ template <int kRows> struct __align__(1024) TreeInt8Smem {
     float zero;
 };
 template <int kRows> constexpr int kInt8Smem = sizeof(TreeInt8Smem<kRows>);
-static_assert(Shape<32>::kRing % 2 == 0 && Shape<64>::kRing % 2 == 0, "K's and V's slots");
 static_assert(kInt8Smem<32> <= 232448 && kInt8Smem<64> <= 232448, "one CTA's shared memory");
 
 __device__ __forceinline__ void stream_sync(int stream)
@@ -254,17 +254,29 @@ __device__ bool fetch_codes(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, con
     // first leaves it in L2 for the others
     const uint64_t policy = p.row_groups == 1 ? l2_evict_first_policy() : l2_evict_normal_policy();
     bool ok = true;
-    int put = 0; // loads requested
+    int unit = 0; // K's requested; V's are one behind, as they are widened
+    int v_row = 0;
+    const auto request = [&](int is_v, int u, int row) { // one tile's codes
+        const int slot = u % kRing;
+        ok = ok && warp_wait(&s.code_empty[is_v][slot], ((u / kRing) & 1) ^ 1);
+        if (!ok)
+            return;
+        uint64_t *full = &s.code_full[is_v][slot];
+        if (lane == 0)
+            mbar_arrive_expect_tx(full, kCodeBytes);
+        __syncwarp();
+        if (lane < boxes) // a box outside the tensor arrives as zeros
+            tma_load_2d(s.codes[is_v][slot] + lane * box_keys * kHeadDim, is_v ? mv : mk, 0, row, full, policy);
+    };
     Segments seg(s);
-    int unit = 0;
-    while (seg.next(p)) {
+    while (ok && seg.next(p)) {
         const int32_t *table = p.block_table + static_cast<size_t>(seg.b) * p.max_pages;
         const auto entry = [&](int tile) {
             const int key = tile * kTileKeys + lane * box_keys;
             return lane < boxes && key < seg.T ? table[key >> p.log2_page] : 0;
         };
         int phys_next = entry(seg.seg_tile0);
-        for (int tile = seg.seg_tile0; tile < seg.seg_tile1; ++tile, ++unit) {
+        for (int tile = seg.seg_tile0; ok && tile < seg.seg_tile1; ++tile) {
             const int phys = phys_next;
             if (tile + 1 < seg.seg_tile1)
                 phys_next = entry(tile + 1);
@@ -283,39 +295,33 @@ __device__ bool fetch_codes(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, con
             uint32_t by16 = 0; // a bit per 16 keys
             for (int i = 0; i < 8; ++i)
                 by16 |= ((valid >> (i * 16 / box_keys)) & 1u) << i;
-#pragma unroll
-            for (int is_v = 0; is_v < 2; ++is_v, ++put) {
-                const int slot = put % kRing;
-                ok = ok && warp_wait(&s.code_empty[slot], ((put / kRing) & 1) ^ 1);
-                if (!ok)
-                    break;
-                uint64_t *full = &s.code_full[slot];
-                if (lane == 0) {
-                    if (!is_v)
-                        s.valid[unit % kScaleRing] = by16;
-                    mbar_arrive_expect_tx(full, kCodeBytes);
-                }
-                __syncwarp();
-                if (lane < boxes) // a box outside the tensor arrives as zeros
-                    tma_load_2d(s.codes[slot] + lane * box_keys * kHeadDim, is_v ? mv : mk, 0, row, full, policy);
-                if (!is_v) { // both scales come with K, 16 bytes a lane
-                    float (*scales)[kTileKeys] = s.scales[unit % kScaleRing];
-                    if (scales_here) {
-                        cp_async16(scales[0] + lane * 4, p.k_scale + scale_row);
-                        cp_async16(scales[1] + lane * 4, p.v_scale + scale_row);
-                    }
-                    cp_async_arrive(full);
-                }
-            }
+            request(0, unit, row);
             if (!ok)
                 break;
+            // both scales come with K, 16 bytes a lane
+            float (*scales)[kTileKeys] = s.scales[unit % kScaleRing];
+            if (lane == 0)
+                s.valid[unit % kScaleRing] = by16;
+            if (scales_here) {
+                cp_async16(scales[0] + lane * 4, p.k_scale + scale_row);
+                cp_async16(scales[1] + lane * 4, p.v_scale + scale_row);
+            }
+            cp_async_arrive(&s.code_full[0][unit % kRing]);
+            if (unit > 0)
+                request(1, unit - 1, v_row);
+            v_row = row;
+            ++unit;
         }
-        if (!ok)
-            break;
     }
-    // nothing may still be on its way into shared memory when the CTA ends
-    for (int last = max(0, put - kRing); last < put; ++last) // a slot's last load each
-        ok = warp_wait(&s.code_full[last % kRing], (last / kRing) & 1) && ok;
+    if (unit > 0)
+        request(1, unit - 1, v_row);
+    // Nothing may still be on its way into shared memory when the CTA ends: a slot's last
+    // load each. (After a wait that ran out the last K's may have no V.)
+    const int last_v = ok ? unit : unit - 1;
+    for (int u = max(0, unit - kRing); u < unit; ++u)
+        ok = warp_wait(&s.code_full[0][u % kRing], (u / kRing) & 1) && ok;
+    for (int u = max(0, last_v - kRing); u < last_v; ++u)
+        ok = warp_wait(&s.code_full[1][u % kRing], (u / kRing) & 1) && ok;
     return ok;
 }
 
@@ -437,64 +443,68 @@ __device__ __forceinline__ void widen_codes(const uint4 &codes, uint32_t *out)
     }
 }
 
-// Both streams' codes, widened tile by tile: a thread has a key.
+// Both streams' codes, widened tile by tile: a thread has a key. V follows one tile behind
+// K, whose product and softmax come before V is wanted.
 template <int kRows> __device__ bool widen(const TreeInt8Params &p, TreeInt8Smem<kRows> &s)
 {
     constexpr int kRing = Shape<kRows>::kRing;
     const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
     const int key_row = warp * 32 + lane;
     bool ok = true;
-    for (int unit = 0; unit < s.units; ++unit) {
-        const int stream = unit & 1, step = unit >> 1;
-        const uint32_t tmem_k = s.tmem_base + (static_cast<uint32_t>(warp * 32) << 16) + stream * kStreamColumns + kColK;
-        int put = 2 * unit, slot = put % kRing;
-        ok = ok && warp_wait(&s.code_full[slot], (put / kRing) & 1);
-        // the last K of the stream is read
-        if (step > 0)
-            ok = ok && warp_wait(&s.s_full[stream], (step - 1) & 1);
-        tc_fence_after();
-        uint4 row[8]; // all of the row's codes are on their way at once
-        const auto load_row = [&] {
-            const unsigned char *codes = s.codes[slot] + key_row * kHeadDim;
+    uint4 row[8]; // all of the row's codes are on their way at once
+    const auto load_row = [&](const unsigned char *codes) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                row[c] = *reinterpret_cast<const uint4 *>(codes + ((c ^ (key_row & 7)) << 4));
-        };
-        load_row();
+        for (int c = 0; c < 8; ++c)
+            row[c] = *reinterpret_cast<const uint4 *>(codes + key_row * kHeadDim + ((c ^ (key_row & 7)) << 4));
+    };
+    for (int unit = 0; unit <= s.units; ++unit) {
+        if (unit < s.units) {
+            const int stream = unit & 1, step = unit >> 1, slot = unit % kRing;
+            const uint32_t tmem_k = s.tmem_base + (static_cast<uint32_t>(warp * 32) << 16) + stream * kStreamColumns + kColK;
+            ok = ok && warp_wait(&s.code_full[0][slot], (unit / kRing) & 1);
+            // the last K of the stream is read
+            if (step > 0)
+                ok = ok && warp_wait(&s.s_full[stream], (step - 1) & 1);
+            tc_fence_after();
+            load_row(s.codes[0][slot]);
 #pragma unroll
-        for (int c = 0; c < 8; c += 2) {
-            uint32_t w[16];
-            widen_codes(row[c], w);
-            widen_codes(row[c + 1], w + 8);
-            tmem_st16(tmem_k + 8 * c, reinterpret_cast<const float *>(w));
+            for (int c = 0; c < 8; c += 2) {
+                uint32_t w[16];
+                widen_codes(row[c], w);
+                widen_codes(row[c + 1], w + 8);
+                tmem_st16(tmem_k + 8 * c, reinterpret_cast<const float *>(w));
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&s.code_empty[0][slot]);
+                mbar_arrive(&s.k_ready[stream]);
+            }
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-            mbar_arrive(&s.code_empty[slot]);
-            mbar_arrive(&s.k_ready[stream]);
-        }
-        ++put, slot = put % kRing;
-        ok = ok && warp_wait(&s.code_full[slot], (put / kRing) & 1);
-        // the last tile's product with V is through with the buffer
-        if (step > 0)
-            ok = ok && warp_wait(&s.o_done[stream], (step - 1) & 1);
-        load_row();
-        unsigned char *v_row = s.v16[stream] + (key_row >> 3) * 2048 + (key_row & 7) * 128;
+        if (unit > 0) {
+            const int last = unit - 1, stream = last & 1, step = last >> 1, slot = last % kRing;
+            ok = ok && warp_wait(&s.code_full[1][slot], (last / kRing) & 1);
+            // the last tile's product with V is through with the buffer
+            if (step > 0)
+                ok = ok && warp_wait(&s.o_done[stream], (step - 1) & 1);
+            load_row(s.codes[1][slot]);
+            unsigned char *v_row = s.v16[stream] + (key_row >> 3) * 2048 + (key_row & 7) * 128;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            uint32_t w[8];
-            widen_codes(row[c], w);
-            unsigned char *half = v_row + (c >> 2) * 1024;
-            *reinterpret_cast<uint4 *>(half + (((2 * c & 7) ^ (key_row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4 *>(half + (((2 * c + 1 & 7) ^ (key_row & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            mbar_arrive(&s.code_empty[slot]);
-            mbar_arrive(&s.v_ready[stream]);
+            for (int c = 0; c < 8; ++c) {
+                uint32_t w[8];
+                widen_codes(row[c], w);
+                unsigned char *half = v_row + (c >> 2) * 1024;
+                *reinterpret_cast<uint4 *>(half + (((2 * c & 7) ^ (key_row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4 *>(half + (((2 * c + 1 & 7) ^ (key_row & 7)) << 4)) =
+                    make_uint4(w[4], w[5], w[6], w[7]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&s.code_empty[1][slot]);
+                mbar_arrive(&s.v_ready[stream]);
+            }
         }
     }
     return ok;
@@ -514,19 +524,6 @@ template <int kRows> __device__ bool multiply(const TreeInt8Params &p, TreeInt8S
     bool ok = true;
     const auto wait = [&](uint64_t *bar, uint32_t parity) { ok = ok && warp_wait(bar, parity); };
     const auto passed = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity)); };
-    const auto add_values = [&](int step, bool keep) { // O^T (+)= V^T P^T
-        wait(&s.v_ready[stream], step & 1);
-        wait(&s.p_ready[stream], step & 1);
-        tc_fence_after();
-        if (ok && leader) {
-#pragma unroll
-            for (int k = 0; k < kTileKeys / 16; ++k)
-                tc_mma_ss(tmem + kColO, va + k * (4096 / 16), tc_desc_high(2048), pa + k * (kStepP / 16),
-                          tc_desc_high(kStepP / 2), idesc_o, k > 0 || keep);
-            tc_commit(&s.o_done[stream]);
-        }
-        __syncwarp();
-    };
     Segments seg(s);
     int unit0 = 0, step = 0;
     bool keep = false;    // the last tile's product adds to O
@@ -534,50 +531,56 @@ template <int kRows> __device__ bool multiply(const TreeInt8Params &p, TreeInt8S
     for (int index = 0; ok && seg.next(p); ++index) {
         const int qbuf = index % Sh::kQueries, tiles = seg.seg_tile1 - seg.seg_tile0;
         const int first = (unit0 ^ stream) & 1;
-        // Without a tile in this segment nothing here waits for the last one's: its end must
-        // come before the rows of the segment after this.
-        if (first >= tiles && pending) {
-            add_values(step - 1, keep);
-            pending = false;
-        }
         wait(&s.q_full[qbuf], (index / Sh::kQueries) & 1);
         const uint32_t qa = warp_uniform(tc_desc_low(smem_addr(s.q16[qbuf]), 16));
         if (first >= tiles && leader)
             mbar_arrive(&s.q_empty[qbuf]);
-        for (int i = first; ok && i < tiles; i += 2, ++step) {
-            // the last tile's product with V goes first if it can before the scores can
-            const auto scores_ready = [&] {
-                return passed(&s.k_ready[stream], step & 1) && (step == 0 || passed(&s.s_read[stream], (step - 1) & 1));
-            };
+        // The last tile's product with V is left to the turn of the next one's scores. Where the
+        // segment has no tile for this stream it is made at once: its end must come before the
+        // rows of the segment after this. So is that of the run's last tile.
+        const int end = first >= tiles || seg.left <= 0 ? tiles + 2 : tiles;
+        for (int i = first; ok && i < end; i += 2) {
+            bool scores = i < tiles; // to be issued
             const long long start = clock64();
-            while (ok && !scores_ready()) {
+            while (ok && (scores || pending)) {
+                if (scores && passed(&s.k_ready[stream], step & 1) && (step == 0 || passed(&s.s_read[stream], (step - 1) & 1))) {
+                    tc_fence_after();
+                    if (leader) { // S^T = K Q^T
+#pragma unroll
+                        for (int k = 0; k < kHeadDim / 16; ++k) // 64 dims a half, 32 bytes a step
+                            tc_mma_ts(tmem + kColS, tmem + kColK + 8 * k,
+                                      qa + (k >> 2) * (Sh::kScoreColumns * 128 / 16) + (k & 3) * 2, tc_desc_high(1024),
+                                      idesc_s, k > 0);
+                        tc_commit(&s.s_full[stream]);
+                        mbar_arrive(&s.s_full[stream]); // orders scales and page mask before their readers
+                        if (i + 2 >= tiles)
+                            tc_commit(&s.q_empty[qbuf]);
+                    }
+                    __syncwarp();
+                    scores = false;
+                }
                 if (pending && passed(&s.p_ready[stream], (step - 1) & 1) && passed(&s.v_ready[stream], (step - 1) & 1)) {
-                    add_values(step - 1, keep);
+                    tc_fence_after();
+                    if (leader) { // O^T (+)= V^T P^T
+#pragma unroll
+                        for (int k = 0; k < kTileKeys / 16; ++k)
+                            tc_mma_ss(tmem + kColO, va + k * (4096 / 16), tc_desc_high(2048), pa + k * (kStepP / 16),
+                                      tc_desc_high(kStepP / 2), idesc_o, k > 0 || keep);
+                        tc_commit(&s.o_done[stream]);
+                    }
+                    __syncwarp();
                     pending = false;
                 }
-                ok = ok && __all_sync(0xFFFFFFFFu, clock64() - start < kWaitLimitClocks);
+                ok = __all_sync(0xFFFFFFFFu, clock64() - start < kWaitLimitClocks);
             }
-            tc_fence_after();
-            if (ok && leader) { // S^T = K Q^T
-#pragma unroll
-                for (int k = 0; k < kHeadDim / 16; ++k) // 64 dims a half, 32 bytes a step
-                    tc_mma_ts(tmem + kColS, tmem + kColK + 8 * k,
-                              qa + (k >> 2) * (Sh::kScoreColumns * 128 / 16) + (k & 3) * 2, tc_desc_high(1024), idesc_s, k > 0);
-                tc_commit(&s.s_full[stream]);
-                mbar_arrive(&s.s_full[stream]); // orders scales and page mask before their readers
-                if (i + 2 >= tiles)
-                    tc_commit(&s.q_empty[qbuf]);
+            if (i < tiles) {
+                keep = i > first + 1 && !(p.sums && ((i - first) >> 1) % kSpan == 0);
+                pending = true;
+                ++step;
             }
-            __syncwarp();
-            if (pending)
-                add_values(step - 1, keep);
-            keep = i > first + 1 && !(p.sums && ((i - first) >> 1) % kSpan == 0);
-            pending = true;
         }
         unit0 += tiles;
     }
-    if (ok && pending)
-        add_values(step - 1, keep);
     // no product may still be running when the CTA ends
     if (leader)
         tc_commit(&s.drain[stream]);
@@ -1019,8 +1022,11 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
     const int rg = blockIdx.x % p.row_groups, cta = blockIdx.x / p.row_groups;
     if (tid == 0) {
         prefetch_tensormap(&mk), prefetch_tensormap(&mv);
-        for (int i = 0; i < Sh::kRing; ++i) // K's slots are even: the codes, and 32 lanes' scales
-            mbar_init(&s.code_full[i], i & 1 ? 1 : 33), mbar_init(&s.code_empty[i], 4);
+        for (int i = 0; i < Sh::kRing; ++i) {
+            mbar_init(&s.code_full[0][i], 33); // the codes, and 32 lanes' scales
+            mbar_init(&s.code_full[1][i], 1);
+            mbar_init(&s.code_empty[0][i], 4), mbar_init(&s.code_empty[1][i], 4);
+        }
         for (int w = 0; w < 2; ++w) {
             mbar_init(&s.rows_full[w], 1), mbar_init(&s.rows_empty[w], 8);
             mbar_init(&s.k_ready[w], 4), mbar_init(&s.v_ready[w], 4); // a warp each
