@@ -17,7 +17,9 @@
 //     contiguous;
 //   - the maximum over the keys is not needed in a tile: a thread only asks whether one
 //     of its scores rises more than 8 (base 2) above the row's reference. If one does in
-//     any of the 128 threads, the references move and l and O are rescaled.
+//     any of the 128 threads, the references move and l and O are rescaled. The tiles of a
+//     run are taken from its end, so that under a distance bias, whose usual sign favours
+//     the nearest keys, the first ones bring the maximum.
 // Sums l stay in the threads, one per row, until a segment's end.
 //
 // Rounding. P vs enters its product as an fp16 pair hi + lo (22 bits), two columns of
@@ -275,11 +277,11 @@ __device__ bool fetch_codes(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, con
             const int key = tile * kTileKeys + lane * box_keys;
             return lane < boxes && key < seg.T ? table[key >> p.log2_page] : 0;
         };
-        int phys_next = entry(seg.seg_tile0);
-        for (int tile = seg.seg_tile0; ok && tile < seg.seg_tile1; ++tile) {
+        int phys_next = entry(seg.seg_tile1 - 1);
+        for (int tile = seg.seg_tile1 - 1; ok && tile >= seg.seg_tile0; --tile) {
             const int phys = phys_next;
-            if (tile + 1 < seg.seg_tile1)
-                phys_next = entry(tile + 1);
+            if (tile > seg.seg_tile0)
+                phys_next = entry(tile - 1);
             const int key = tile * kTileKeys + lane * box_keys;
             const bool needed = lane < boxes && key < seg.T;
             const bool in_pool = phys >= 0 && phys < p.num_pages;
@@ -680,7 +682,7 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
         bool large = false;            // a reference beyond 65536
         const int first = (unit0 ^ stream) & 1;
         for (int i = first; i < tiles; i += 2, ++step) {
-            const int key0 = (seg.seg_tile0 + i) * kTileKeys, key = key0 + key_row;
+            const int key0 = (seg.seg_tile1 - 1 - i) * kTileKeys, key = key0 + key_row;
             const int place = (unit0 + i) % kScaleRing;
             wait(&s.s_full[stream], step & 1);
             tc_fence_after();
