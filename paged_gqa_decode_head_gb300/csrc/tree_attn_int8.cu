@@ -35,7 +35,7 @@
 //   warps 0-3, 4-7    one softmax warpgroup per stream: S -> P -> shared memory;
 //   warps 8-11        widen codes to fp16, K's into tensor memory, V's into shared memory,
 //                     for both streams;
-//   warp 12           requests codes (TMA, one lane per page of a tile) and scales;
+//   warp 12           requests codes (TMA, a box per page of a tile) and scales;
 //   warp 13           prepares the next segment's queries, masks and slopes;
 //   warps 14, 15      issue one stream's products each: the next S as soon as the
 //                     softmax has read the last one, then the last tile's O += P V.
@@ -256,6 +256,7 @@ __device__ bool fetch_codes(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, con
     // first leaves it in L2 for the others
     const uint64_t policy = p.row_groups == 1 ? l2_evict_first_policy() : l2_evict_normal_policy();
     bool ok = true;
+    const bool leader = elect_one();
     int unit = 0; // K's requested; V's are one behind, as they are widened
     int v_row = 0;
     const auto request = [&](int is_v, int u, int row) { // one tile's codes
@@ -264,11 +265,20 @@ __device__ bool fetch_codes(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, con
         if (!ok)
             return;
         uint64_t *full = &s.code_full[is_v][slot];
-        if (lane == 0)
+        int rows[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            rows[i] = __shfl_sync(0xFFFFFFFFu, row, i);
+        // One thread issues all boxes: a lane each would take its turn with all of a request's
+        // latency, 66 clocks (of some 1400 in which the memory brings a tile).
+        if (leader) {
             mbar_arrive_expect_tx(full, kCodeBytes);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < boxes) // a box outside the tensor arrives as zeros
+                    tma_load_2d(s.codes[is_v][slot] + i * box_keys * kHeadDim, is_v ? mv : mk, 0, rows[i], full, policy);
+        }
         __syncwarp();
-        if (lane < boxes) // a box outside the tensor arrives as zeros
-            tma_load_2d(s.codes[is_v][slot] + lane * box_keys * kHeadDim, is_v ? mv : mk, 0, row, full, policy);
     };
     Segments seg(s);
     while (ok && seg.next(p)) {
