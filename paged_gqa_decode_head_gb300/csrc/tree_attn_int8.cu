@@ -35,7 +35,7 @@
 //   warps 0-3, 4-7    one softmax warpgroup per stream: S -> P -> shared memory;
 //   warps 8-11        widen codes to fp16, K's into tensor memory, V's into shared memory,
 //                     for both streams;
-//   warp 12           requests codes (TMA, a box per page of a tile) and scales;
+//   warp 12           requests codes (TMA, a box per page of a tile);
 //   warp 13           prepares the next segment's queries, masks and slopes;
 //   warps 14, 15      issue one stream's products each: the next S as soon as the
 //                     softmax has read the last one, then the last tile's O += P V.
@@ -58,10 +58,6 @@ __device__ unsigned g_flags_tree_int8;
 constexpr int kCodeBytes = kTileKeys * kHeadDim; // 16 KB of K or V codes
 constexpr int kInt8Threads = 512;
 constexpr int kWidenWarp = 8, kCodeWarp = 12, kQueryWarp = 13, kMmaWarp = 14; // and kMmaWarp + 1
-// Tiles whose scales are kept. Tile u is requested once K of tile u - 3 is widened (a ring of
-// three). V of u - 5 was widened before that, and V of u - 6; they waited for the products with
-// V of u - 7 and of u - 8, whose softmax is then done.
-constexpr int kScaleRing = 8;
 constexpr float kRise = 8.f;  // rise of a row's scores (base 2) that moves its reference
 constexpr int kSpan = 16;     // a stream's tiles between two moves of O out of the tensor core (fp32 outputs)
 constexpr int kMaxRows = 64;  // query rows of a CTA
@@ -110,7 +106,6 @@ template <int kRows> struct __align__(1024) TreeInt8Smem {
     unsigned char v16[2][kTileKeys * kRowBytes];
     unsigned char p16[2][kTileKeys * Sh::kOutColumns * 2];
     unsigned char q16[Sh::kQueries][Sh::kScoreColumns * kRowBytes];
-    float scales[kScaleRing][2][kTileKeys]; // of K, of V
     // what a segment's rows bring, for two segments in turn
     uint64_t sees[2][64]; // drafted token j: the rows that see it
     float slope_up[2][kMaxRows], slope_down[2][kMaxRows]; // slopes (base 2), split by sign
@@ -128,7 +123,6 @@ template <int kRows> struct __align__(1024) TreeInt8Smem {
     uint64_t rows_full[2], rows_empty[2];
     uint64_t k_ready[2], v_ready[2]; // a tile's codes are widened
     uint64_t s_full[2], s_read[2], p_ready[2], o_done[2], drain[2];
-    uint32_t valid[kScaleRing]; // pages inside the pool, a bit per 16 keys of a tile
     uint32_t tmem_base;
     int start_b, start_h, start_tile, start_T, start_n, units; // this CTA's run
     int scan[kInt8Threads / 32];
@@ -170,16 +164,6 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity)
                  : "r"(smem_addr(bar)), "r"(parity)
                  : "memory");
     return done != 0;
-}
-
-// An asynchronous copy of 16 bytes, and this thread's arrival at a barrier once its copies are done.
-__device__ __forceinline__ void cp_async16(void *dst, const void *src)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
-{
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
 // As tmem_ld16, 8 columns.
@@ -242,7 +226,7 @@ template <int N> __device__ __forceinline__ float sum_lanes(float *x)
     return x[0];
 }
 
-// ---------------------------------------------------------------- codes and scales
+// ---------------------------------------------------------------- codes
 template <int kRows>
 __device__ bool fetch_codes(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, const CUtensorMap *mk, const CUtensorMap *mv)
 {
@@ -299,26 +283,9 @@ __device__ bool fetch_codes(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, con
             if (needed && !in_pool)
                 atomicOr(&g_flags_tree_int8, PGQA_DEVERR_BAD_PAGE);
             const int row = here ? ((phys * p.Hkv + seg.h) << p.log2_page) + (key & (P - 1)) : outside;
-            const uint32_t valid = __ballot_sync(0xFFFFFFFFu, !needed || in_pool);
-            // this lane's four keys of the scales
-            const int box = lane * 4 / box_keys;
-            const int scale_row = __shfl_sync(0xFFFFFFFFu, row, box) + (lane * 4 & (box_keys - 1));
-            const bool scales_here = __shfl_sync(0xFFFFFFFFu, here, box);
-            uint32_t by16 = 0; // a bit per 16 keys
-            for (int i = 0; i < 8; ++i)
-                by16 |= ((valid >> (i * 16 / box_keys)) & 1u) << i;
             request(0, unit, row);
             if (!ok)
                 break;
-            // both scales come with K, 16 bytes a lane
-            float (*scales)[kTileKeys] = s.scales[unit % kScaleRing];
-            if (lane == 0)
-                s.valid[unit % kScaleRing] = by16;
-            if (scales_here) {
-                cp_async16(scales[0] + lane * 4, p.k_scale + scale_row);
-                cp_async16(scales[1] + lane * 4, p.v_scale + scale_row);
-            }
-            cp_async_arrive(&s.code_full[0][unit % kRing]);
             if (unit > 0)
                 request(1, unit - 1, v_row);
             v_row = row;
@@ -463,13 +430,15 @@ template <int kRows> __device__ bool widen(const TreeInt8Params &p, TreeInt8Smem
     const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
     const int key_row = warp * 32 + lane;
     bool ok = true;
-    uint4 row[8]; // all of the row's codes are on their way at once
-    const auto load_row = [&](const unsigned char *codes) {
+    // A row's chunks of 16 codes, four at a time: the loops are small enough to stay in the
+    // scheduler's own instruction cache.
+    const auto load4 = [&](const unsigned char *codes, int c0, uint4 *row) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-            row[c] = *reinterpret_cast<const uint4 *>(codes + key_row * kHeadDim + ((c ^ (key_row & 7)) << 4));
+        for (int c = 0; c < 4; ++c)
+            row[c] = *reinterpret_cast<const uint4 *>(codes + key_row * kHeadDim + (((c0 + c) ^ (key_row & 7)) << 4));
     };
     for (int unit = 0; unit <= s.units; ++unit) {
+        uint4 row[4];
         if (unit < s.units) {
             const int stream = unit & 1, step = unit >> 1, slot = unit % kRing;
             const uint32_t tmem_k = s.tmem_base + (static_cast<uint32_t>(warp * 32) << 16) + stream * kStreamColumns + kColK;
@@ -478,13 +447,16 @@ template <int kRows> __device__ bool widen(const TreeInt8Params &p, TreeInt8Smem
             if (step > 0)
                 ok = ok && warp_wait(&s.s_full[stream], (step - 1) & 1);
             tc_fence_after();
-            load_row(s.codes[0][slot]);
+#pragma unroll 1
+            for (int c = 0; c < 8; c += 4) {
+                load4(s.codes[0][slot], c, row);
 #pragma unroll
-            for (int c = 0; c < 8; c += 2) {
-                uint32_t w[16];
-                widen_codes(row[c], w);
-                widen_codes(row[c + 1], w + 8);
-                tmem_st16(tmem_k + 8 * c, reinterpret_cast<const float *>(w));
+                for (int i = 0; i < 4; i += 2) {
+                    uint32_t w[16];
+                    widen_codes(row[i], w);
+                    widen_codes(row[i + 1], w + 8);
+                    tmem_st16(tmem_k + 8 * (c + i), reinterpret_cast<const float *>(w));
+                }
             }
             tmem_wait_st();
             tc_fence_before();
@@ -500,16 +472,19 @@ template <int kRows> __device__ bool widen(const TreeInt8Params &p, TreeInt8Smem
             // the last tile's product with V is through with the buffer
             if (step > 0)
                 ok = ok && warp_wait(&s.o_done[stream], (step - 1) & 1);
-            load_row(s.codes[1][slot]);
             unsigned char *v_row = s.v16[stream] + (key_row >> 3) * 2048 + (key_row & 7) * 128;
+#pragma unroll 1
+            for (int c = 0; c < 8; c += 4) { // half a row of fp16
+                load4(s.codes[1][slot], c, row);
+                unsigned char *half = v_row + c * 256;
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                uint32_t w[8];
-                widen_codes(row[c], w);
-                unsigned char *half = v_row + (c >> 2) * 1024;
-                *reinterpret_cast<uint4 *>(half + (((2 * c & 7) ^ (key_row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-                *reinterpret_cast<uint4 *>(half + (((2 * c + 1 & 7) ^ (key_row & 7)) << 4)) =
-                    make_uint4(w[4], w[5], w[6], w[7]);
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t w[8];
+                    widen_codes(row[i], w);
+                    *reinterpret_cast<uint4 *>(half + ((2 * i ^ (key_row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4 *>(half + ((2 * i + 1 ^ (key_row & 7)) << 4)) =
+                        make_uint4(w[4], w[5], w[6], w[7]);
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -564,7 +539,6 @@ template <int kRows> __device__ bool multiply(const TreeInt8Params &p, TreeInt8S
                                       qa + (k >> 2) * (Sh::kScoreColumns * 128 / 16) + (k & 3) * 2, tc_desc_high(1024),
                                       idesc_s, k > 0);
                         tc_commit(&s.s_full[stream]);
-                        mbar_arrive(&s.s_full[stream]); // orders scales and page mask before their readers
                         if (i + 2 >= tiles)
                             tc_commit(&s.q_empty[qbuf]);
                     }
@@ -691,20 +665,37 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
         bool summed = false;           // `sums` holds earlier spans
         bool large = false;            // a reference beyond 65536
         const int first = (unit0 ^ stream) & 1;
+        // This thread's key's scales come a tile ahead of their use, its page two.
+        const int32_t *table = p.block_table + static_cast<size_t>(seg.b) * p.max_pages;
+        const auto page_of = [&](int i) {
+            const int at = (seg.seg_tile1 - 1 - i) * kTileKeys + key_row;
+            return i < tiles && at < seg.T ? table[at >> p.log2_page] : -1;
+        };
+        float next_ks = 0.f, next_vs = 0.f;
+        bool next_valid = false;
+        int next_page = page_of(first);
+        const auto load_scales = [&](int i) { // of tile i, whose page next_page is
+            next_valid = static_cast<unsigned>(next_page) < static_cast<unsigned>(p.num_pages);
+            const size_t row = (static_cast<size_t>(next_page) * p.Hkv + seg.h << p.log2_page) +
+                               ((seg.seg_tile1 - 1 - i) * kTileKeys + key_row & ((1 << p.log2_page) - 1));
+            next_ks = next_vs = 0.f;
+            if (next_valid)
+                next_ks = p.k_scale[row], next_vs = p.v_scale[row];
+            next_page = page_of(i + 2);
+        };
+        load_scales(first);
         for (int i = first; i < tiles; i += 2, ++step) {
             const int key0 = (seg.seg_tile1 - 1 - i) * kTileKeys, key = key0 + key_row;
-            const int place = (unit0 + i) % kScaleRing;
+            float ks = next_ks, vs = next_vs;
+            const bool valid = next_valid;
+            load_scales(i + 2);
             wait(&s.s_full[stream], step & 1);
             tc_fence_after();
-            const uint32_t valid = s.valid[place];
-            float ks = s.scales[place][0][key_row], vs = s.scales[place][1][key_row];
             // ---- the rows that see this key
             uint32_t sees_lo = 0xFFFFFFFFu, sees_hi = 0xFFFFFFFFu;
-            const bool fix = key0 + kTileKeys > prefix || valid != 0xFFu;
+            const bool fix = __any_sync(0xFFFFFFFFu, key >= prefix || !valid);
             if (fix) {
-                const uint64_t sees = !(valid >> (key_row >> 4) & 1u) || key >= seg.T ? 0
-                                      : key < prefix                                  ? ~0ull
-                                                                                      : s.sees[buf][key - prefix];
+                const uint64_t sees = !valid ? 0 : key < prefix ? ~0ull : s.sees[buf][key - prefix];
                 sees_lo = static_cast<uint32_t>(sees), sees_hi = static_cast<uint32_t>(sees >> 32);
                 if (!sees)
                     ks = vs = 0.f; // may hold anything
@@ -1035,16 +1026,14 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
     if (tid == 0) {
         prefetch_tensormap(&mk), prefetch_tensormap(&mv);
         for (int i = 0; i < Sh::kRing; ++i) {
-            mbar_init(&s.code_full[0][i], 33); // the codes, and 32 lanes' scales
-            mbar_init(&s.code_full[1][i], 1);
+            mbar_init(&s.code_full[0][i], 1), mbar_init(&s.code_full[1][i], 1);
             mbar_init(&s.code_empty[0][i], 4), mbar_init(&s.code_empty[1][i], 4);
         }
         for (int w = 0; w < 2; ++w) {
             mbar_init(&s.rows_full[w], 1), mbar_init(&s.rows_empty[w], 8);
             mbar_init(&s.k_ready[w], 4), mbar_init(&s.v_ready[w], 4); // a warp each
             mbar_init(&s.s_read[w], 4), mbar_init(&s.p_ready[w], 4);
-            mbar_init(&s.s_full[w], 2); // the products' completion, and the issuing thread
-            mbar_init(&s.o_done[w], 1), mbar_init(&s.drain[w], 1);
+            mbar_init(&s.s_full[w], 1), mbar_init(&s.o_done[w], 1), mbar_init(&s.drain[w], 1);
         }
         for (int i = 0; i < Sh::kQueries; ++i)
             mbar_init(&s.q_full[i], 1), mbar_init(&s.q_empty[i], 2);
