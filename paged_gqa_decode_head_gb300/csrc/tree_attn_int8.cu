@@ -30,15 +30,17 @@
 //
 // Bound. The cache is read once: 264 bytes per (key, KV head), 33 KB a tile of K and V.
 //
-// CTA: one per SM, four warpgroups around tensor memory and a ring of six (four) code
-// tiles, K and V in turn. Two streams take alternate tiles of the CTA's run:
+// CTA: one per SM, five warpgroups (four at 64 rows, whose softmax wants the registers)
+// around tensor memory and rings of three (two) tiles of K's and V's codes. Two streams take
+// alternate tiles of the CTA's run:
 //   warps 0-3, 4-7    one softmax warpgroup per stream: S -> P -> shared memory;
-//   warps 8-11        widen codes to fp16, K's into tensor memory, V's into shared memory,
-//                     for both streams;
-//   warp 12           requests codes (TMA, a box per page of a tile);
-//   warp 13           prepares the next segment's queries, masks and slopes;
-//   warps 14, 15      issue one stream's products each: the next S as soon as the
-//                     softmax has read the last one, then the last tile's O += P V.
+//   warps 8-11        widen K's codes to fp16 into tensor memory, for both streams;
+//   warps 12-15       widen V's into shared memory (at 64 rows warps 8-11 do);
+// and four warps alone:
+//   the first         requests codes (TMA, a box per page of a tile);
+//   the second        prepares the next segment's queries, masks and slopes;
+//   the other two     issue one stream's products each, S and O += P V, as their operands
+//                     come.
 #include "common.cuh"
 #include "launch.h"
 #include "tcgen05.cuh"
@@ -56,8 +58,6 @@ namespace {
 __device__ unsigned g_flags_tree_int8;
 
 constexpr int kCodeBytes = kTileKeys * kHeadDim; // 16 KB of K or V codes
-constexpr int kInt8Threads = 512;
-constexpr int kWidenWarp = 8, kCodeWarp = 12, kQueryWarp = 13, kMmaWarp = 14; // and kMmaWarp + 1
 constexpr float kRise = 8.f;  // rise of a row's scores (base 2) that moves its reference
 constexpr int kSpan = 16;     // a stream's tiles between two moves of O out of the tensor core (fp32 outputs)
 constexpr int kMaxRows = 64;  // query rows of a CTA
@@ -98,6 +98,13 @@ template <int kRows> struct Shape {
     static constexpr int kLo = kOutColumns / 2;                   // lo's first column
     static constexpr int kRing = kRows == 64 ? 2 : 3;             // slots of K's codes, and of V's
     static constexpr int kQueries = kRows == 64 ? 1 : 2;          // segments whose queries are kept
+    // Warps: softmax from 0, widening from 8 (K's and V's apart, or both), then four alone.
+    static constexpr bool kApart = kRows < 64;
+    static constexpr int kThreads = kApart ? 640 : 512;
+    static constexpr int kCodeWarp = kThreads / 32 - 4, kQueryWarp = kCodeWarp + 1, kMmaWarp = kCodeWarp + 2; // and + 3
+    // Registers move to the softmax, within those of the launch: 96 or 128 a thread.
+    static constexpr int kMost = kApart ? 128 : 176, kLeast = kApart ? 72 : 80;
+    static_assert(256 * kMost + (kThreads - 256) * kLeast <= kThreads * (kApart ? 96 : 128), "registers of the launch");
 };
 
 template <int kRows> struct __align__(1024) TreeInt8Smem {
@@ -125,7 +132,7 @@ template <int kRows> struct __align__(1024) TreeInt8Smem {
     uint64_t s_full[2], s_read[2], p_ready[2], o_done[2], drain[2];
     uint32_t tmem_base;
     int start_b, start_h, start_tile, start_T, start_n, units; // this CTA's run
-    int scan[kInt8Threads / 32];
+    int scan[Sh::kThreads / 32];
     float zero;
 };
 template <int kRows> constexpr int kInt8Smem = sizeof(TreeInt8Smem<kRows>);
@@ -422,9 +429,9 @@ __device__ __forceinline__ void widen_codes(const uint4 &codes, uint32_t *out)
     }
 }
 
-// Both streams' codes, widened tile by tile: a thread has a key. V follows one tile behind
-// K, whose product and softmax come before V is wanted.
-template <int kRows> __device__ bool widen(const TreeInt8Params &p, TreeInt8Smem<kRows> &s)
+// Both streams' codes, widened tile by tile: a thread has a key. Where one warpgroup has K and
+// V, V follows one tile behind, as K's product and softmax come before V is wanted.
+template <int kRows, bool kHasK, bool kHasV> __device__ bool widen(const TreeInt8Params &p, TreeInt8Smem<kRows> &s)
 {
     constexpr int kRing = Shape<kRows>::kRing;
     const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
@@ -437,9 +444,9 @@ template <int kRows> __device__ bool widen(const TreeInt8Params &p, TreeInt8Smem
         for (int c = 0; c < 4; ++c)
             row[c] = *reinterpret_cast<const uint4 *>(codes + key_row * kHeadDim + (((c0 + c) ^ (key_row & 7)) << 4));
     };
-    for (int unit = 0; unit <= s.units; ++unit) {
+    for (int unit = kHasK ? 0 : 1; unit < s.units + kHasV; ++unit) {
         uint4 row[4];
-        if (unit < s.units) {
+        if (kHasK && unit < s.units) {
             const int stream = unit & 1, step = unit >> 1, slot = unit % kRing;
             const uint32_t tmem_k = s.tmem_base + (static_cast<uint32_t>(warp * 32) << 16) + stream * kStreamColumns + kColK;
             ok = ok && warp_wait(&s.code_full[0][slot], (unit / kRing) & 1);
@@ -466,7 +473,7 @@ template <int kRows> __device__ bool widen(const TreeInt8Params &p, TreeInt8Smem
                 mbar_arrive(&s.k_ready[stream]);
             }
         }
-        if (unit > 0) {
+        if (kHasV && unit > 0) {
             const int last = unit - 1, stream = last & 1, step = last >> 1, slot = last % kRing;
             ok = ok && warp_wait(&s.code_full[1][slot], (last / kRing) & 1);
             // the last tile's product with V is through with the buffer
@@ -1014,7 +1021,7 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
 }
 
 template <int kScore, int kRows>
-__global__ void __launch_bounds__(kInt8Threads, 1)
+__global__ void __launch_bounds__(Shape<kRows>::kThreads, 1)
     tree_int8_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                      const __grid_constant__ TreeInt8Params p)
 {
@@ -1039,10 +1046,10 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
             mbar_init(&s.q_full[i], 1), mbar_init(&s.q_empty[i], 2);
         fence_mbar_init();
     }
-    if (warp == kCodeWarp)
+    if (warp == Sh::kCodeWarp)
         tmem_alloc_all(&s.tmem_base);
     // columns of P that no row fills stay zero
-    for (int i = tid; i < static_cast<int>(sizeof(s.p16) / 16); i += kInt8Threads)
+    for (int i = tid; i < static_cast<int>(sizeof(s.p16) / 16); i += Sh::kThreads)
         reinterpret_cast<uint4 *>(&s.p16[0][0])[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
 
@@ -1050,27 +1057,28 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
     // the next kernel may start once that one is done.
     grid_dependency_wait();
     allow_dependent_launch();
-    plan_run<kInt8Threads>(p, s, cta);
+    plan_run<Sh::kThreads>(p, s, cta);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
 
-    // Registers move to the softmax: 256 * 176 + 256 * 80 = 512 * 128 as launched.
     bool ok = true;
-    if (warp >= kWidenWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Sh::kLeast));
         if (s.units > 0) {
-            if (warp < kCodeWarp)
-                ok = widen(p, s);
-            else if (warp == kCodeWarp)
+            if (warp < 12)
+                ok = widen<kRows, true, !Sh::kApart>(p, s);
+            else if (Sh::kApart && warp < 16)
+                ok = widen<kRows, false, true>(p, s);
+            else if (warp == Sh::kCodeWarp)
                 ok = fetch_codes(p, s, &mk, &mv);
-            else if (warp == kQueryWarp)
+            else if (warp == Sh::kQueryWarp)
                 ok = fetch_rows<kScore>(p, s, rg);
             else
-                ok = multiply(p, s, warp - kMmaWarp);
+                ok = multiply(p, s, warp - Sh::kMmaWarp);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Sh::kMost));
         if (s.units > 0)
             ok = soften<kScore>(p, s, rg, warp >> 2);
     }
@@ -1079,7 +1087,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kCodeWarp)
+    if (warp == Sh::kCodeWarp)
         tmem_free_all(s.tmem_base);
 }
 
@@ -1146,7 +1154,7 @@ cudaError_t launch_rows(const CUtensorMap &mk, const CUtensorMap &mv, const Tree
         if (dev < kMaxDevices)
             configured[dev].store(true, std::memory_order_release);
     }
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(p.ctas * p.row_groups)), dim3(kInt8Threads), kInt8Smem<kRows>,
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(p.ctas * p.row_groups)), dim3(Shape<kRows>::kThreads), kInt8Smem<kRows>,
                       stream, mk, mv, p);
 }
 
