@@ -674,28 +674,26 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
         const int first = (unit0 ^ stream) & 1;
         // This thread's key's scales come a tile ahead of their use, its page two.
         const int32_t *table = p.block_table + static_cast<size_t>(seg.b) * p.max_pages;
-        const auto page_of = [&](int i) {
-            const int at = (seg.seg_tile1 - 1 - i) * kTileKeys + key_row;
-            return i < tiles && at < seg.T ? table[at >> p.log2_page] : -1;
-        };
+        const int first_key = seg.seg_tile0 * kTileKeys + key_row;
+        int next_key = (seg.seg_tile1 - 1 - first) * kTileKeys + key_row;
         float next_ks = 0.f, next_vs = 0.f;
         bool next_valid = false;
-        int next_page = page_of(first);
-        const auto load_scales = [&](int i) { // of tile i, whose page next_page is
+        int next_page = next_key >= first_key && next_key < seg.T ? table[next_key >> p.log2_page] : -1;
+        const auto load_scales = [&] { // of next_key, whose page next_page is
             next_valid = static_cast<unsigned>(next_page) < static_cast<unsigned>(p.num_pages);
-            const size_t row = (static_cast<size_t>(next_page) * p.Hkv + seg.h << p.log2_page) +
-                               ((seg.seg_tile1 - 1 - i) * kTileKeys + key_row & ((1 << p.log2_page) - 1));
+            const int row = ((next_page * p.Hkv + seg.h) << p.log2_page) + (next_key & ((1 << p.log2_page) - 1));
             next_ks = next_vs = 0.f;
             if (next_valid)
                 next_ks = p.k_scale[row], next_vs = p.v_scale[row];
-            next_page = page_of(i + 2);
+            next_key -= 2 * kTileKeys;
+            next_page = next_key >= first_key ? table[next_key >> p.log2_page] : -1;
         };
-        load_scales(first);
+        load_scales();
         for (int i = first; i < tiles; i += 2, ++step) {
             const int key0 = (seg.seg_tile1 - 1 - i) * kTileKeys, key = key0 + key_row;
             float ks = next_ks, vs = next_vs;
             const bool valid = next_valid;
-            load_scales(i + 2);
+            load_scales();
             wait(&s.s_full[stream], step & 1);
             tc_fence_after();
             // ---- the rows that see this key
