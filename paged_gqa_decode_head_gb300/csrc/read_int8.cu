@@ -20,7 +20,6 @@ __device__ unsigned g_flags_read_int8;
 constexpr int kReadThreads = 256;
 constexpr int kReadLanes = 8;                               // lanes of a row
 constexpr int kReadRows = kReadThreads / kReadLanes;        // rows of a block's pass
-constexpr int kInFlight = 4;                                // passes on their way at once
 
 struct ReadParams {
     const int8_t *k_cache8, *v_cache8;
@@ -51,52 +50,33 @@ __global__ void __launch_bounds__(kReadThreads) read_int8_kernel(const __grid_co
         return;
     const int lane8 = threadIdx.x % kReadLanes;
     const int rows = 2 * live * p.Hkv; // all of K, then all of V, each [slot][head]
-    // four rows of a thread on their way at once: a block's usual 128 rows in one trip to the
-    // table, one to the cache
-    for (int r0 = threadIdx.x / kReadLanes; r0 < rows; r0 += kInFlight * kReadRows) {
-        int phys[kInFlight];
-        size_t row[kInFlight], to[kInFlight];
-        uint4 codes[kInFlight];
-        float s[kInFlight];
+    for (int r = threadIdx.x / kReadLanes; r < rows; r += kReadRows) {
+        const bool is_v = r >= live * p.Hkv;
+        const int in = is_v ? r - live * p.Hkv : r;
+        const int i = in / p.Hkv, h = in - i * p.Hkv;
+        const int slot = first + i0 + i;
+        const int phys = p.block_table[static_cast<size_t>(b) * p.max_pages + (slot >> p.log2_page)];
+        if (phys < 0 || phys >= p.num_pages) {
+            atomicOr(&g_flags_read_int8, PGQA_DEVERR_BAD_PAGE);
+            continue;
+        }
+        const size_t row = ((static_cast<size_t>(phys) * p.Hkv + h) << p.log2_page) + (slot & ((1 << p.log2_page) - 1));
+        const uint4 codes = *reinterpret_cast<const uint4 *>((is_v ? p.v_cache8 : p.k_cache8) + row * kHeadDim + 16 * lane8);
+        const float s = (is_v ? p.v_scale : p.k_scale)[row];
+        const uint32_t words[4] = {codes.x, codes.y, codes.z, codes.w};
+        uint32_t out[8];
 #pragma unroll
-        for (int k = 0; k < kInFlight; ++k) {
-            const int r = r0 + k * kReadRows, in = r >= live * p.Hkv ? r - live * p.Hkv : r;
-            const int i = in / p.Hkv, h = in - i * p.Hkv, slot = first + i0 + i;
-            phys[k] = r < rows ? p.block_table[static_cast<size_t>(b) * p.max_pages + (slot >> p.log2_page)] : -1;
-            if (r < rows && (phys[k] < 0 || phys[k] >= p.num_pages)) {
-                atomicOr(&g_flags_read_int8, PGQA_DEVERR_BAD_PAGE);
-                phys[k] = -1;
+        for (int w = 0; w < 4; ++w)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const float lo = static_cast<float>(static_cast<int8_t>(words[w] >> (16 * half)));
+                const float hi = static_cast<float>(static_cast<int8_t>(words[w] >> (16 * half + 8)));
+                out[2 * w + half] = pack_bf16x2(lo * s, hi * s);
             }
-            row[k] = ((static_cast<size_t>(phys[k]) * p.Hkv + h) << p.log2_page) + (slot & ((1 << p.log2_page) - 1));
-            to[k] = (static_cast<size_t>(b) * p.N + i0 + i) * p.Hkv + h;
-        }
-#pragma unroll
-        for (int k = 0; k < kInFlight; ++k) {
-            const bool is_v = r0 + k * kReadRows >= live * p.Hkv;
-            if (phys[k] >= 0) {
-                codes[k] = *reinterpret_cast<const uint4 *>((is_v ? p.v_cache8 : p.k_cache8) + row[k] * kHeadDim + 16 * lane8);
-                s[k] = (is_v ? p.v_scale : p.k_scale)[row[k]];
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < kInFlight; ++k) {
-            if (phys[k] < 0)
-                continue;
-            const bool is_v = r0 + k * kReadRows >= live * p.Hkv;
-            const uint32_t words[4] = {codes[k].x, codes[k].y, codes[k].z, codes[k].w};
-            uint32_t out[8];
-#pragma unroll
-            for (int w = 0; w < 4; ++w)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const float lo = static_cast<float>(static_cast<int8_t>(words[w] >> (16 * half)));
-                    const float hi = static_cast<float>(static_cast<int8_t>(words[w] >> (16 * half + 8)));
-                    out[2 * w + half] = pack_bf16x2(lo * s[k], hi * s[k]);
-                }
-            uint4 *dst = reinterpret_cast<uint4 *>((is_v ? p.v_out : p.k_out) + to[k] * kHeadDim + 16 * lane8);
-            dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
-            dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
-        }
+        uint4 *dst = reinterpret_cast<uint4 *>((is_v ? p.v_out : p.k_out) +
+                                               ((static_cast<size_t>(b) * p.N + i0 + i) * p.Hkv + h) * kHeadDim + 16 * lane8);
+        dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+        dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
     }
 }
 
