@@ -8,7 +8,8 @@
 // Bound: memory, 132 bytes read and 256 written per (slot, KV head) of K and of
 // V. Eight lanes take a row (16 codes each, two 16-byte stores), a warp four
 // rows at a time; rows in the output's order, so that the writes, two thirds of the
-// traffic, are contiguous over the whole block.
+// traffic, are contiguous over the whole block. Measured: 19387 slots of 8 heads in 8 ragged
+// sequences 22.8 us, 5.3 TB/s (four rows of a thread in flight: 28.1 us, with half the warps).
 #include "common.cuh"
 #include "launch.h"
 

@@ -23,7 +23,8 @@
 // one lane). Measured (32 query, 8 KV heads): 32768 tokens 128 us, 6.3 TB/s, 93 % of
 // the measured copy bandwidth; 19658 tokens in 8 ragged sequences of up to 4096 80 us,
 // 6.0 TB/s; 4095 tokens of 16 + 8 heads 13.9 us, 4.8 TB/s (the start and end of its
-// blocks); 1 or 16 tokens 3.4 us, a launch and three trips to memory.
+// blocks); 1 or 16 tokens 3.4 us, a launch and three trips to memory. With INT8 caches 19387
+// tokens in 8 ragged sequences (32 + 8 heads) take 103 us, bound by instructions (issue 71 %).
 #include "common.cuh"
 #include "launch.h"
 

@@ -28,7 +28,17 @@
 // l are fp32; for fp32 outputs O moves out of the tensor core every kSpan tiles, as in
 // tree_attn.cu.
 //
-// Bound. The cache is read once: 264 bytes per (key, KV head), 33 KB a tile of K and V.
+// Bound. The cache is read once: 264 bytes per (key, KV head), 33 KB a tile of K and V, some
+// 1440 clocks of an SM's share of the memory. Measured: 64 sequences of 16384 keys and 8 heads
+// at 8 rows 377 us, 5.9 TB/s, 0.87 of the measured copy bandwidth (pages of 64; of 16, whose
+// 16 boxes a tile one thread issues in some 1300 clocks, 408 us); at 32 rows 489 us, 4.5 TB/s,
+// the two softmax warpgroups' work (2300 clocks a tile: one key's rows a thread in sequence,
+// and code that the instruction caches do not hold); 512 rows per KV head, 16384 keys, 8
+// sequences 596 us, 461 TFLOP/s, the same at 64 rows.
+//
+// Pairs. Where a (sequence, KV head) has more than 64 rows a CTA has two groups of them, one
+// for each stream, which both take every tile: its codes are widened once for 128 rows (512
+// rows: 707 us with a CTA per group of 64, 596 us in pairs).
 //
 // CTA: one per SM, five warpgroups (four at 64 rows, whose softmax wants the registers)
 // around tensor memory and rings of three (two) tiles of K's and V's codes. Two streams take
@@ -60,7 +70,7 @@ __device__ unsigned g_flags_tree_int8;
 constexpr int kCodeBytes = kTileKeys * kHeadDim; // 16 KB of K or V codes
 constexpr float kRise = 8.f;  // rise of a row's scores (base 2) that moves its reference
 constexpr int kSpan = 16;     // a stream's tiles between two moves of O out of the tensor core (fp32 outputs)
-constexpr int kMaxRows = 64;  // query rows of a CTA
+constexpr int kMaxRows = 64;  // query rows of a row group
 
 // TMEM columns of stream s, + 256 s: S^T (64), K (64, two fp16 each), O^T (128).
 constexpr uint32_t kColS = 0, kColK = 64, kColO = 128, kStreamColumns = 256;
@@ -76,30 +86,35 @@ struct TreeInt8Params {
     const float *slopes;
     int B, M, Hq, Hkv, log2_page, max_pages, num_pages;
     int g;             // query heads per KV head
-    int tile_tokens;   // drafted tokens per CTA (g * tile_tokens <= 64 rows)
-    int row_groups;    // CTAs that share a run of tiles
+    int tile_tokens;   // drafted tokens of a row group (g * tile_tokens <= 64 rows)
+    int row_groups;    // that share a run of tiles
     int rec_rows;      // rows of a partial record
-    int ctas;          // grid size / row_groups
+    int ctas;          // runs of tiles
     float c;               // plain scores: y = c ks S, c = scale log2 e
     float cap_u, cap_out;  // capped: y = cap_out tanh(cap_u ks S)
     float tanh_c[7];       // cap_out times the polynomial's coefficients
     float *out_f32;
     uint16_t *out_bf16;
     int32_t *unit_base;    // [B + 1] first tile number of each sequence, total
-    float *rec_m, *rec_l;  // [2 * grid][rec_rows]
-    float *rec_acc;        // [2 * grid][rec_rows][128]
+    float *rec_m, *rec_l;  // [2 * ctas * row_groups][rec_rows]
+    float *rec_acc;        // [2 * ctas * row_groups][rec_rows][128]
     float *sums;           // [2 * grid][rows][128]: O of earlier spans; null: bf16 outputs only
 };
 
-// Rows: the columns that the softmax works on.
+// kRows: query rows of a CTA. Up to 64 both streams have all of them and take the tiles in
+// turn. 128: a pair of row groups, 64 rows for each stream, which both take every tile.
 template <int kRows> struct Shape {
-    static constexpr int kScoreColumns = kRows < 16 ? 16 : kRows; // of S^T = K Q^T
-    static constexpr int kOutColumns = kRows == 64 ? 128 : 64;    // of O^T: hi, then lo
+    static constexpr bool kPair = kRows == 128;
+    static constexpr int kOwn = kPair ? 64 : kRows;               // rows of a stream: the softmax's columns
+    static constexpr int kSets = kPair ? 2 : 1, kTurns = kPair ? 1 : 2; // sets of rows; a stream's tiles are every kTurns-th
+    static constexpr int kScoreColumns = kOwn < 16 ? 16 : kOwn;   // of S^T = K Q^T
+    static constexpr int kOutColumns = kOwn == 64 ? 128 : 64;     // of O^T: hi, then lo
     static constexpr int kLo = kOutColumns / 2;                   // lo's first column
-    static constexpr int kRing = kRows == 64 ? 2 : 3;             // slots of K's codes, and of V's
-    static constexpr int kQueries = kRows == 64 ? 1 : 2;          // segments whose queries are kept
+    static constexpr int kRing = kOwn == 64 ? 2 : 3;              // slots of K's codes
+    static constexpr int kRingV = kPair ? 1 : kRing;              // and of V's
+    static constexpr int kQueries = kOwn == 64 ? 1 : 2;           // segments whose queries are kept
     // Warps: softmax from 0, widening from 8 (K's and V's apart, or both), then four alone.
-    static constexpr bool kApart = kRows < 64;
+    static constexpr bool kApart = kOwn < 64;
     static constexpr int kThreads = kApart ? 640 : 512;
     static constexpr int kCodeWarp = kThreads / 32 - 4, kQueryWarp = kCodeWarp + 1, kMmaWarp = kCodeWarp + 2; // and + 3
     // Registers move to the softmax, within those of the launch: 96 or 128 a thread.
@@ -109,26 +124,27 @@ template <int kRows> struct Shape {
 
 template <int kRows> struct __align__(1024) TreeInt8Smem {
     using Sh = Shape<kRows>;
-    unsigned char codes[2][Sh::kRing][kCodeBytes]; // K's, V's
+    unsigned char codes[Sh::kRing + Sh::kRingV][kCodeBytes]; // K's, V's
     unsigned char v16[2][kTileKeys * kRowBytes];
     unsigned char p16[2][kTileKeys * Sh::kOutColumns * 2];
-    unsigned char q16[Sh::kQueries][Sh::kScoreColumns * kRowBytes];
+    unsigned char q16[Sh::kQueries][Sh::kSets][Sh::kScoreColumns * kRowBytes];
     // what a segment's rows bring, for two segments in turn
-    uint64_t sees[2][64]; // drafted token j: the rows that see it
-    float slope_up[2][kMaxRows], slope_down[2][kMaxRows]; // slopes (base 2), split by sign
-    int anchor[2][kMaxRows];
-    int by_sign[2]; // every row's anchor is the prefix's end, or its first key for a falling slope
+    uint64_t sees[2][Sh::kSets][64]; // drafted token j: the rows that see it
+    float slope_up[2][Sh::kSets][Sh::kOwn], slope_down[2][Sh::kSets][Sh::kOwn]; // slopes (base 2), split by sign
+    int anchor[2][Sh::kSets][Sh::kOwn];
+    int by_sign[2][Sh::kSets]; // every row's anchor is the prefix's end, or its first key for a falling slope
     // a stream's rows
-    float neg_m[2][kMaxRows]; // minus the reference
-    float f_l[2][kMaxRows], f_o[2][kMaxRows], g_sums[2][kMaxRows];
-    float warp_part[2][4][kMaxRows], warp_vs[2][4];
-    float m_end[2][kMaxRows], l_end[2][kMaxRows], inv_f[2];
-    float weight[2][2][kMaxRows]; // by the stream that writes; of stream 0's and 1's O
+    float neg_m[2][Sh::kOwn]; // minus the reference
+    float f_l[2][Sh::kOwn], f_o[2][Sh::kOwn], g_sums[2][Sh::kOwn];
+    float warp_part[2][4][Sh::kOwn], warp_vs[2][4];
+    float m_end[2][Sh::kOwn], l_end[2][Sh::kOwn], inv_f[2];
+    float weight[2][2][Sh::kOwn]; // by the stream that writes; of stream 0's and 1's O
     uint32_t warp_over[2][4];
-    uint64_t code_full[2][Sh::kRing], code_empty[2][Sh::kRing];
+    uint64_t code_full[Sh::kRing + Sh::kRingV], code_empty[Sh::kRing + Sh::kRingV];
     uint64_t q_full[Sh::kQueries], q_empty[Sh::kQueries];
     uint64_t rows_full[2], rows_empty[2];
-    uint64_t k_ready[2], v_ready[2]; // a tile's codes are widened
+    uint64_t k_ready[2], v_ready[2]; // a tile's codes are widened, in two places in turn
+    uint64_t k_free[2], v_free[2];   // pairs: both streams' products have read them
     uint64_t s_full[2], s_read[2], p_ready[2], o_done[2], drain[2];
     uint32_t tmem_base;
     int start_b, start_h, start_tile, start_T, start_n, units; // this CTA's run
@@ -136,7 +152,7 @@ template <int kRows> struct __align__(1024) TreeInt8Smem {
     float zero;
 };
 template <int kRows> constexpr int kInt8Smem = sizeof(TreeInt8Smem<kRows>);
-static_assert(kInt8Smem<32> <= 232448 && kInt8Smem<64> <= 232448, "one CTA's shared memory");
+static_assert(kInt8Smem<32> <= 232448 && kInt8Smem<64> <= 232448 && kInt8Smem<128> <= 232448, "one CTA's shared memory");
 
 __device__ __forceinline__ void stream_sync(int stream)
 {
@@ -237,7 +253,7 @@ template <int N> __device__ __forceinline__ float sum_lanes(float *x)
 template <int kRows>
 __device__ bool fetch_codes(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, const CUtensorMap *mk, const CUtensorMap *mv)
 {
-    constexpr int kRing = Shape<kRows>::kRing;
+    using Sh = Shape<kRows>;
     const int lane = threadIdx.x & 31;
     const int P = 1 << p.log2_page;
     const int box_keys = min(P, kTileKeys);
@@ -245,17 +261,17 @@ __device__ bool fetch_codes(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, con
     const int outside = static_cast<int>(static_cast<long long>(p.num_pages) * p.Hkv << p.log2_page);
     // one row group reads the cache once; of several, running side by side, the
     // first leaves it in L2 for the others
-    const uint64_t policy = p.row_groups == 1 ? l2_evict_first_policy() : l2_evict_normal_policy();
+    const uint64_t policy = p.row_groups <= Sh::kSets ? l2_evict_first_policy() : l2_evict_normal_policy();
     bool ok = true;
     const bool leader = elect_one();
     int unit = 0; // K's requested; V's are one behind, as they are widened
     int v_row = 0;
     const auto request = [&](int is_v, int u, int row) { // one tile's codes
-        const int slot = u % kRing;
-        ok = ok && warp_wait(&s.code_empty[is_v][slot], ((u / kRing) & 1) ^ 1);
+        const int ring = is_v ? Sh::kRingV : Sh::kRing, slot = (is_v ? Sh::kRing : 0) + u % ring;
+        ok = ok && warp_wait(&s.code_empty[slot], ((u / ring) & 1) ^ 1);
         if (!ok)
             return;
-        uint64_t *full = &s.code_full[is_v][slot];
+        uint64_t *full = &s.code_full[slot];
         int rows[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -267,7 +283,7 @@ __device__ bool fetch_codes(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, con
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 if (i < boxes) // a box outside the tensor arrives as zeros
-                    tma_load_2d(s.codes[is_v][slot] + i * box_keys * kHeadDim, is_v ? mv : mk, 0, rows[i], full, policy);
+                    tma_load_2d(s.codes[slot] + i * box_keys * kHeadDim, is_v ? mv : mk, 0, rows[i], full, policy);
         }
         __syncwarp();
     };
@@ -304,10 +320,10 @@ __device__ bool fetch_codes(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, con
     // Nothing may still be on its way into shared memory when the CTA ends: a slot's last
     // load each. (After a wait that ran out the last K's may have no V.)
     const int last_v = ok ? unit : unit - 1;
-    for (int u = max(0, unit - kRing); u < unit; ++u)
-        ok = warp_wait(&s.code_full[0][u % kRing], (u / kRing) & 1) && ok;
-    for (int u = max(0, last_v - kRing); u < last_v; ++u)
-        ok = warp_wait(&s.code_full[1][u % kRing], (u / kRing) & 1) && ok;
+    for (int u = max(0, unit - Sh::kRing); u < unit; ++u)
+        ok = warp_wait(&s.code_full[u % Sh::kRing], (u / Sh::kRing) & 1) && ok;
+    for (int u = max(0, last_v - Sh::kRingV); u < last_v; ++u)
+        ok = warp_wait(&s.code_full[Sh::kRing + u % Sh::kRingV], (u / Sh::kRingV) & 1) && ok;
     return ok;
 }
 
@@ -326,56 +342,61 @@ __device__ bool fetch_rows(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, int 
         ok = warp_wait(&s.rows_empty[buf], ((index >> 1) & 1) ^ 1);
         if (!ok)
             break;
-        const int token0 = rg * p.tile_tokens;
-        const auto live = [&](int row) { return row < rows && token0 + row / p.g < n; };
-        // masks by row become rows by drafted token
-        const uint64_t *masks = p.tree_mask + static_cast<size_t>(seg.b) * p.M + token0;
-        const uint64_t m0 = live(lane) ? masks[lane / p.g] : 0, m1 = live(lane + 32) ? masks[(lane + 32) / p.g] : 0;
-#pragma unroll 4
-        for (int j = 0; j < n; ++j) {
-            const uint32_t lo = __ballot_sync(0xFFFFFFFFu, (m0 >> j) & 1u);
-            const uint32_t hi = kRows > 32 ? __ballot_sync(0xFFFFFFFFu, (m1 >> j) & 1u) : 0u;
-            if (lane == (j & 31))
-                s.sees[buf][j] = static_cast<uint64_t>(hi) << 32 | lo;
-        }
-        if constexpr ((kScore & 2) != 0) {
-            // A row's own position is a constant of its scores and cancels in the softmax: the
-            // bias is taken relative to a key that it favours, as in tree_attn.cu.
-            const int32_t *at = p.positions + static_cast<size_t>(seg.b) * p.M;
-            const int pos_lo = lane < n ? at[lane] : 0, pos_hi = lane + 32 < n ? at[lane + 32] : 0;
-            const auto near = [&](int j, int pos) {
-                return j >= n || static_cast<uint32_t>(pos) - static_cast<uint32_t>(prefix) + 64u < 128u;
-            };
-            bool by_sign = near(lane, pos_lo) && near(lane + 32, pos_hi);
-            float slope[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int row = lane + 32 * i;
-                slope[i] = live(row) ? p.slopes[seg.h * p.g + row % p.g] * kLog2e : 0.f;
-                by_sign = by_sign && fabsf(slope[i]) <= 2.f;
-            }
-            by_sign = __all_sync(0xFFFFFFFFu, by_sign);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const bool falls = slope[i] < 0.f;
-                int anchor = falls ? 0 : prefix;
-                if (!by_sign) {
-                    if (prefix == 0)
-                        anchor = falls ? INT_MAX : INT_MIN;
-                    const uint64_t mask = i ? m1 : m0;
 #pragma unroll 1
-                    for (int j = 0; j < n; ++j) {
-                        const int pos = __shfl_sync(0xFFFFFFFFu, j < 32 ? pos_lo : pos_hi, j & 31);
-                        if (mask >> j & 1u)
-                            anchor = falls ? min(anchor, pos) : max(anchor, pos);
+        for (int set = 0; set < Sh::kSets; ++set) {
+            const int token0 = (rg + set) * p.tile_tokens;
+            const auto live = [&](int row) { return row < rows && token0 + row / p.g < n; };
+            // masks by row become rows by drafted token
+            const uint64_t *masks = p.tree_mask + static_cast<size_t>(seg.b) * p.M + token0;
+            const uint64_t m0 = live(lane) ? masks[lane / p.g] : 0, m1 = live(lane + 32) ? masks[(lane + 32) / p.g] : 0;
+#pragma unroll 4
+            for (int j = 0; j < n; ++j) {
+                const uint32_t lo = __ballot_sync(0xFFFFFFFFu, (m0 >> j) & 1u);
+                const uint32_t hi = Sh::kOwn > 32 ? __ballot_sync(0xFFFFFFFFu, (m1 >> j) & 1u) : 0u;
+                if (lane == (j & 31))
+                    s.sees[buf][set][j] = static_cast<uint64_t>(hi) << 32 | lo;
+            }
+            if constexpr ((kScore & 2) != 0) {
+                // A row's own position is a constant of its scores and cancels in the softmax: the
+                // bias is taken relative to a key that it favours, as in tree_attn.cu.
+                const int32_t *at = p.positions + static_cast<size_t>(seg.b) * p.M;
+                const int pos_lo = lane < n ? at[lane] : 0, pos_hi = lane + 32 < n ? at[lane + 32] : 0;
+                const auto near = [&](int j, int pos) {
+                    return j >= n || static_cast<uint32_t>(pos) - static_cast<uint32_t>(prefix) + 64u < 128u;
+                };
+                bool by_sign = near(lane, pos_lo) && near(lane + 32, pos_hi);
+                float slope[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int row = lane + 32 * i;
+                    slope[i] = live(row) ? p.slopes[seg.h * p.g + row % p.g] * kLog2e : 0.f;
+                    by_sign = by_sign && fabsf(slope[i]) <= 2.f;
+                }
+                by_sign = __all_sync(0xFFFFFFFFu, by_sign);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const bool falls = slope[i] < 0.f;
+                    int anchor = falls ? 0 : prefix;
+                    if (!by_sign) {
+                        if (prefix == 0)
+                            anchor = falls ? INT_MAX : INT_MIN;
+                        const uint64_t mask = i ? m1 : m0;
+#pragma unroll 1
+                        for (int j = 0; j < n; ++j) {
+                            const int pos = __shfl_sync(0xFFFFFFFFu, j < 32 ? pos_lo : pos_hi, j & 31);
+                            if (mask >> j & 1u)
+                                anchor = falls ? min(anchor, pos) : max(anchor, pos);
+                        }
+                    }
+                    if (lane + 32 * i < Sh::kOwn) {
+                        s.slope_up[buf][set][lane + 32 * i] = fmaxf(slope[i], 0.f);
+                        s.slope_down[buf][set][lane + 32 * i] = fminf(slope[i], 0.f);
+                        s.anchor[buf][set][lane + 32 * i] = anchor;
                     }
                 }
-                s.slope_up[buf][lane + 32 * i] = fmaxf(slope[i], 0.f);
-                s.slope_down[buf][lane + 32 * i] = fminf(slope[i], 0.f);
-                s.anchor[buf][lane + 32 * i] = anchor;
+                if (lane == 0)
+                    s.by_sign[buf][set] = by_sign;
             }
-            if (lane == 0)
-                s.by_sign[buf] = by_sign;
         }
         __syncwarp();
         if (lane == 0)
@@ -388,7 +409,10 @@ __device__ bool fetch_rows(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, int 
         const int part = lane & 15, half = part >> 3;
         constexpr int kFlight = Sh::kScoreColumns / 2 < 8 ? Sh::kScoreColumns / 2 : 8;
 #pragma unroll 1
-        for (int r0 = 0; r0 < Sh::kScoreColumns; r0 += 2 * kFlight) {
+        for (int at = 0; at < Sh::kSets * Sh::kScoreColumns; at += 2 * kFlight) {
+            const int set = at / Sh::kScoreColumns, r0 = at % Sh::kScoreColumns;
+            const int token0 = (rg + set) * p.tile_tokens;
+            const auto live = [&](int row) { return row < rows && token0 + row / p.g < n; };
             uint4 x[kFlight];
 #pragma unroll
             for (int i = 0; i < kFlight; ++i) {
@@ -403,7 +427,7 @@ __device__ bool fetch_rows(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, int 
             for (int i = 0; i < kFlight; ++i) {
                 const int row = r0 + 2 * i + (lane >> 4);
                 const auto convert = [](uint32_t pair) { return pack_f16x2(bf16_lo(pair), bf16_hi(pair)); };
-                *reinterpret_cast<uint4 *>(s.q16[qbuf] + half * (Sh::kScoreColumns * 128) + row * 128 +
+                *reinterpret_cast<uint4 *>(s.q16[qbuf][set] + half * (Sh::kScoreColumns * 128) + row * 128 +
                                            (((part & 7) ^ (row & 7)) << 4)) =
                     make_uint4(convert(x[i].x), convert(x[i].y), convert(x[i].z), convert(x[i].w));
             }
@@ -433,7 +457,9 @@ __device__ __forceinline__ void widen_codes(const uint4 &codes, uint32_t *out)
 // V, V follows one tile behind, as K's product and softmax come before V is wanted.
 template <int kRows, bool kHasK, bool kHasV> __device__ bool widen(const TreeInt8Params &p, TreeInt8Smem<kRows> &s)
 {
-    constexpr int kRing = Shape<kRows>::kRing;
+    using Sh = Shape<kRows>;
+    constexpr int kRing = Sh::kRing, kRingV = Sh::kRingV;
+    uint64_t *k_free = Sh::kPair ? s.k_free : s.s_full, *v_free = Sh::kPair ? s.v_free : s.o_done;
     const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
     const int key_row = warp * 32 + lane;
     bool ok = true;
@@ -449,14 +475,14 @@ template <int kRows, bool kHasK, bool kHasV> __device__ bool widen(const TreeInt
         if (kHasK && unit < s.units) {
             const int stream = unit & 1, step = unit >> 1, slot = unit % kRing;
             const uint32_t tmem_k = s.tmem_base + (static_cast<uint32_t>(warp * 32) << 16) + stream * kStreamColumns + kColK;
-            ok = ok && warp_wait(&s.code_full[0][slot], (unit / kRing) & 1);
+            ok = ok && warp_wait(&s.code_full[slot], (unit / kRing) & 1);
             // the last K of the stream is read
             if (step > 0)
-                ok = ok && warp_wait(&s.s_full[stream], (step - 1) & 1);
+                ok = ok && warp_wait(&k_free[stream], (step - 1) & 1);
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < 8; c += 4) {
-                load4(s.codes[0][slot], c, row);
+                load4(s.codes[slot], c, row);
 #pragma unroll
                 for (int i = 0; i < 4; i += 2) {
                     uint32_t w[16];
@@ -469,20 +495,20 @@ template <int kRows, bool kHasK, bool kHasV> __device__ bool widen(const TreeInt
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&s.code_empty[0][slot]);
+                mbar_arrive(&s.code_empty[slot]);
                 mbar_arrive(&s.k_ready[stream]);
             }
         }
         if (kHasV && unit > 0) {
-            const int last = unit - 1, stream = last & 1, step = last >> 1, slot = last % kRing;
-            ok = ok && warp_wait(&s.code_full[1][slot], (last / kRing) & 1);
+            const int last = unit - 1, stream = last & 1, step = last >> 1, slot = kRing + last % kRingV;
+            ok = ok && warp_wait(&s.code_full[slot], (last / kRingV) & 1);
             // the last tile's product with V is through with the buffer
             if (step > 0)
-                ok = ok && warp_wait(&s.o_done[stream], (step - 1) & 1);
+                ok = ok && warp_wait(&v_free[stream], (step - 1) & 1);
             unsigned char *v_row = s.v16[stream] + (key_row >> 3) * 2048 + (key_row & 7) * 128;
 #pragma unroll 1
             for (int c = 0; c < 8; c += 4) { // half a row of fp16
-                load4(s.codes[1][slot], c, row);
+                load4(s.codes[slot], c, row);
                 unsigned char *half = v_row + c * 256;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -496,7 +522,7 @@ template <int kRows, bool kHasK, bool kHasV> __device__ bool widen(const TreeInt
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&s.code_empty[1][slot]);
+                mbar_arrive(&s.code_empty[slot]);
                 mbar_arrive(&s.v_ready[stream]);
             }
         }
@@ -512,9 +538,13 @@ template <int kRows> __device__ bool multiply(const TreeInt8Params &p, TreeInt8S
     const uint32_t tmem = warp_uniform(s.tmem_base + stream * kStreamColumns);
     const uint32_t idesc_s = tc_idesc_f16(Sh::kScoreColumns, false);
     const uint32_t idesc_o = tc_idesc_f16(Sh::kOutColumns, true);
-    const uint32_t va = warp_uniform(tc_desc_low(smem_addr(s.v16[stream]), 1024));
+    // where tile `step` of this stream is widened to, and how often that was filled before
+    const auto place = [&](int step) { return Sh::kPair ? step & 1 : stream; };
+    const auto filled = [&](int step) { return Sh::kPair ? step >> 1 : step; };
+    const uint32_t va0 = warp_uniform(tc_desc_low(smem_addr(s.v16[0]), 1024));
+    const uint32_t va1 = warp_uniform(tc_desc_low(smem_addr(s.v16[1]), 1024));
     const uint32_t pa = warp_uniform(tc_desc_low(smem_addr(s.p16[stream]), 1024));
-    constexpr int kStepP = kRows == 64 ? 4096 : 2048; // 16 keys of P
+    constexpr int kStepP = Sh::kOwn == 64 ? 4096 : 2048; // 16 keys of P
     bool ok = true;
     const auto wait = [&](uint64_t *bar, uint32_t parity) { ok = ok && warp_wait(bar, parity); };
     const auto passed = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity)); };
@@ -524,42 +554,49 @@ template <int kRows> __device__ bool multiply(const TreeInt8Params &p, TreeInt8S
     bool pending = false; // the last tile's product is not issued yet
     for (int index = 0; ok && seg.next(p); ++index) {
         const int qbuf = index % Sh::kQueries, tiles = seg.seg_tile1 - seg.seg_tile0;
-        const int first = (unit0 ^ stream) & 1;
+        const int first = Sh::kPair ? 0 : (unit0 ^ stream) & 1;
         wait(&s.q_full[qbuf], (index / Sh::kQueries) & 1);
-        const uint32_t qa = warp_uniform(tc_desc_low(smem_addr(s.q16[qbuf]), 16));
+        const uint32_t qa = warp_uniform(tc_desc_low(smem_addr(s.q16[qbuf][Sh::kPair ? stream : 0]), 16));
         if (first >= tiles && leader)
             mbar_arrive(&s.q_empty[qbuf]);
         // The last tile's product with V is left to the turn of the next one's scores. Where the
         // segment has no tile for this stream it is made at once: its end must come before the
         // rows of the segment after this. So is that of the run's last tile.
-        const int end = first >= tiles || seg.left <= 0 ? tiles + 2 : tiles;
-        for (int i = first; ok && i < end; i += 2) {
+        const int end = first >= tiles || seg.left <= 0 ? tiles + Sh::kTurns : tiles;
+        for (int i = first; ok && i < end; i += Sh::kTurns) {
             bool scores = i < tiles; // to be issued
             const long long start = clock64();
             while (ok && (scores || pending)) {
-                if (scores && passed(&s.k_ready[stream], step & 1) && (step == 0 || passed(&s.s_read[stream], (step - 1) & 1))) {
+                if (scores && passed(&s.k_ready[place(step)], filled(step) & 1) && (step == 0 || passed(&s.s_read[stream], (step - 1) & 1))) {
                     tc_fence_after();
+                    const uint32_t tmem_k = warp_uniform(s.tmem_base + place(step) * kStreamColumns + kColK);
                     if (leader) { // S^T = K Q^T
 #pragma unroll
                         for (int k = 0; k < kHeadDim / 16; ++k) // 64 dims a half, 32 bytes a step
-                            tc_mma_ts(tmem + kColS, tmem + kColK + 8 * k,
+                            tc_mma_ts(tmem + kColS, tmem_k + 8 * k,
                                       qa + (k >> 2) * (Sh::kScoreColumns * 128 / 16) + (k & 3) * 2, tc_desc_high(1024),
                                       idesc_s, k > 0);
                         tc_commit(&s.s_full[stream]);
-                        if (i + 2 >= tiles)
+                        if (Sh::kPair)
+                            tc_commit(&s.k_free[step & 1]);
+                        if (i + Sh::kTurns >= tiles)
                             tc_commit(&s.q_empty[qbuf]);
                     }
                     __syncwarp();
                     scores = false;
                 }
-                if (pending && passed(&s.p_ready[stream], (step - 1) & 1) && passed(&s.v_ready[stream], (step - 1) & 1)) {
+                if (pending && passed(&s.p_ready[stream], (step - 1) & 1) &&
+                    passed(&s.v_ready[place(step - 1)], filled(step - 1) & 1)) {
                     tc_fence_after();
+                    const uint32_t va = warp_uniform(place(step - 1) ? va1 : va0);
                     if (leader) { // O^T (+)= V^T P^T
 #pragma unroll
                         for (int k = 0; k < kTileKeys / 16; ++k)
                             tc_mma_ss(tmem + kColO, va + k * (4096 / 16), tc_desc_high(2048), pa + k * (kStepP / 16),
                                       tc_desc_high(kStepP / 2), idesc_o, k > 0 || keep);
                         tc_commit(&s.o_done[stream]);
+                        if (Sh::kPair)
+                            tc_commit(&s.v_free[(step - 1) & 1]);
                     }
                     __syncwarp();
                     pending = false;
@@ -567,7 +604,7 @@ template <int kRows> __device__ bool multiply(const TreeInt8Params &p, TreeInt8S
                 ok = __all_sync(0xFFFFFFFFu, clock64() - start < kWaitLimitClocks);
             }
             if (i < tiles) {
-                keep = i > first + 1 && !(p.sums && ((i - first) >> 1) % kSpan == 0);
+                keep = i > first && !(p.sums && (i - first) / Sh::kTurns % kSpan == 0);
                 pending = true;
                 ++step;
             }
@@ -586,7 +623,7 @@ template <int kRows> __device__ bool multiply(const TreeInt8Params &p, TreeInt8S
 // one's row.
 template <int kScore, int kRows>
 __device__ __forceinline__ void form_scores(const TreeInt8Params &p, const TreeInt8Smem<kRows> &s, float *x, int j, float factor,
-                                            int buf, float up, float down, int pos)
+                                            int buf, int set, float up, float down, int pos)
 {
     if constexpr ((kScore & 1) != 0) {
         float u[8], over = 0.f;
@@ -618,8 +655,8 @@ __device__ __forceinline__ void form_scores(const TreeInt8Params &p, const TreeI
             for (int k = 0; k < 8; ++k)
                 x[k] *= factor;
         }
-        const float *slope_up = s.slope_up[buf] + j, *slope_down = s.slope_down[buf] + j;
-        if (s.by_sign[buf]) {
+        const float *slope_up = s.slope_up[buf][set] + j, *slope_down = s.slope_down[buf][set] + j;
+        if (s.by_sign[buf][set]) {
 #pragma unroll
             for (int k = 0; k < 8; k += 2)
                 fma2(f32x2(slope_up[k], slope_up[k + 1]), f32x2(up, up),
@@ -628,7 +665,7 @@ __device__ __forceinline__ void form_scores(const TreeInt8Params &p, const TreeI
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                x[k] = fmaf(slope_up[k] + slope_down[k], distance(pos, s.anchor[buf][j + k]), x[k]);
+                x[k] = fmaf(slope_up[k] + slope_down[k], distance(pos, s.anchor[buf][set][j + k]), x[k]);
         }
     }
 }
@@ -636,9 +673,11 @@ __device__ __forceinline__ void form_scores(const TreeInt8Params &p, const TreeI
 template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, int rg, int stream)
 {
     using Sh = Shape<kRows>;
-    constexpr int kGroups = kRows / 8; // rows are taken eight at a time
+    constexpr int kOwn = Sh::kOwn, kTurns = Sh::kTurns;
+    constexpr int kGroups = kOwn / 8; // rows are taken eight at a time
     const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
     const int key_row = warp * 32 + lane; // of a tile; of O^T: the dim
+    const int set = Sh::kPair ? stream : 0; // of the segment's rows
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t tmem_s = s.tmem_base + lanes + stream * kStreamColumns + kColS;
     const uint32_t tmem_o = s.tmem_base + lanes + stream * kStreamColumns + kColO;
@@ -646,10 +685,10 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
     // do so to the end, without further waits.
     bool ok = true;
     const auto wait = [&](uint64_t *bar, uint32_t parity) { ok = ok && warp_wait(bar, parity); };
-    float *sums = p.sums ? p.sums + static_cast<size_t>(2 * blockIdx.x + stream) * kRows * kHeadDim + key_row : nullptr;
+    float *sums = p.sums ? p.sums + static_cast<size_t>(2 * blockIdx.x + stream) * kOwn * kHeadDim + key_row : nullptr;
     // what the threads of one stream share by row
     float *neg_m = s.neg_m[stream], *f_l = s.f_l[stream], *f_o = s.f_o[stream], *g_sums = s.g_sums[stream];
-    float (*warp_part)[kMaxRows] = s.warp_part[stream];
+    float (*warp_part)[kOwn] = s.warp_part[stream];
 
     Segments seg(s);
     int unit0 = 0; // the segment's first tile in the run
@@ -659,19 +698,19 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
         const int tiles = seg.seg_tile1 - seg.seg_tile0;
         const int prefix = seg.T - seg.n;
         wait(&s.rows_full[buf], (index >> 1) & 1);
-        if (key_row < kRows) {
+        if (key_row < kOwn) {
             neg_m[key_row] = INFINITY; // nothing seen yet
             g_sums[key_row] = 1.f;
         }
         stream_sync(stream);
-        float l[kRows];
+        float l[kOwn];
 #pragma unroll
-        for (int j = 0; j < kRows; ++j)
+        for (int j = 0; j < kOwn; ++j)
             l[j] = 0.f;
         float f = 1.f, vs_limit = 0.f; // F, and the V scale that needs a smaller one
         bool summed = false;           // `sums` holds earlier spans
         bool large = false;            // a reference beyond 65536
-        const int first = (unit0 ^ stream) & 1;
+        const int first = Sh::kPair ? 0 : (unit0 ^ stream) & 1;
         // This thread's key's scales come a tile ahead of their use, its page two.
         const int32_t *table = p.block_table + static_cast<size_t>(seg.b) * p.max_pages;
         const int first_key = seg.seg_tile0 * kTileKeys + key_row;
@@ -685,11 +724,11 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
             next_ks = next_vs = 0.f;
             if (next_valid)
                 next_ks = p.k_scale[row], next_vs = p.v_scale[row];
-            next_key -= 2 * kTileKeys;
+            next_key -= kTurns * kTileKeys;
             next_page = next_key >= first_key ? table[next_key >> p.log2_page] : -1;
         };
         load_scales();
-        for (int i = first; i < tiles; i += 2, ++step) {
+        for (int i = first; i < tiles; i += kTurns, ++step) {
             const int key0 = (seg.seg_tile1 - 1 - i) * kTileKeys, key = key0 + key_row;
             float ks = next_ks, vs = next_vs;
             const bool valid = next_valid;
@@ -700,7 +739,7 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
             uint32_t sees_lo = 0xFFFFFFFFu, sees_hi = 0xFFFFFFFFu;
             const bool fix = __any_sync(0xFFFFFFFFu, key >= prefix || !valid);
             if (fix) {
-                const uint64_t sees = !valid ? 0 : key < prefix ? ~0ull : s.sees[buf][key - prefix];
+                const uint64_t sees = !valid ? 0 : key < prefix ? ~0ull : s.sees[buf][set][key - prefix];
                 sees_lo = static_cast<uint32_t>(sees), sees_hi = static_cast<uint32_t>(sees >> 32);
                 if (!sees)
                     ks = vs = 0.f; // may hold anything
@@ -721,15 +760,15 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
                 tmem_ld8(y[0], tmem_s);
                 const auto group = [&](int j, float *now, float *next) {
                     tmem_wait_ld8(now);
-                    if (j + 8 < kRows)
+                    if (j + 8 < kOwn)
                         tmem_ld8(next, tmem_s + j + 8);
-                    form_scores<kScore, kRows>(p, s, now, j, factor, buf, up, down, pos);
+                    form_scores<kScore, kRows>(p, s, now, j, factor, buf, set, up, down, pos);
                     tmem_st8(tmem_s + j, now);
                 };
 #pragma unroll 1
-                for (int j = 0; j < kRows; j += 16) {
+                for (int j = 0; j < kOwn; j += 16) {
                     group(j, y[0], y[1]);
-                    if (j + 8 < kRows)
+                    if (j + 8 < kOwn)
                         group(j + 8, y[1], y[0]);
                 }
                 tmem_wait_st();
@@ -737,36 +776,36 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
             const float mul = kScore ? 1.f : ks * p.c;
             const float vs_size = fabsf(vs) <= FLT_MAX ? fabsf(vs) : 0.f;
             bool there = step == 0; // the last tile's product with V is done
-            const bool span = sums && i > first + 1 && ((i - first) >> 1) % kSpan == 0;
-            float x[kRows];
+            const bool span = sums && i > first && (i - first) / kTurns % kSpan == 0;
+            float x[kOwn];
             // Once more after the references moved (which settles it; the limit is for no case known).
 #pragma unroll 1
             for (int turn = 0;; ++turn) {
-                if constexpr (kRows == 8) {
+                if constexpr (kOwn == 8) {
                     tmem_ld8(x, tmem_s);
                     tmem_wait_ld8(x);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < kRows; j += 16)
+                    for (int j = 0; j < kOwn; j += 16)
                         tmem_ld16(x + j, tmem_s + j);
 #pragma unroll
-                    for (int j = 0; j < kRows; j += 16)
+                    for (int j = 0; j < kOwn; j += 16)
                         tmem_wait_ld16(x + j);
                 }
                 // For references so large that their rounding matters the scores are rounded
                 // as they were, before the difference (a packed product and sum would be fused).
                 if (kScore == 0 && large) {
 #pragma unroll
-                    for (int j = 0; j < kRows; ++j)
+                    for (int j = 0; j < kOwn; ++j)
                         x[j] = __fadd_rn(__fmul_rn(x[j], mul), neg_m[j]);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < kRows; j += 2)
+                    for (int j = 0; j < kOwn; j += 2)
                         fma2(f32x2(x[j], x[j + 1]), f32x2(mul, mul), f32x2(neg_m[j], neg_m[j + 1])).get(x[j], x[j + 1]);
                 }
                 if (fix) {
 #pragma unroll
-                    for (int j = 0; j < kRows; ++j)
+                    for (int j = 0; j < kOwn; ++j)
                         x[j] = seen(j) & 1u ? x[j] : -INFINITY;
                 }
                 float tops[kGroups];
@@ -823,7 +862,7 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
                 }
                 stream_sync(stream);
                 bool far = false;
-                if (key_row < kRows) {
+                if (key_row < kOwn) {
                     float fm = 1.f, m = -neg_m[key_row];
                     if (over >> (key_row >> 3) & 1u) {
                         const float most = fmaxf(fmaxf(warp_part[0][key_row], warp_part[1][key_row]),
@@ -841,9 +880,9 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
                 }
                 large = stream_any(stream, far);
 #pragma unroll
-                for (int j = 0; j < kRows; ++j)
+                for (int j = 0; j < kOwn; ++j)
                     l[j] *= f_l[j];
-                if (i > first + 1) {
+                if (i > first) {
 #pragma unroll 1
                     for (uint32_t rest = fv == 1.f ? over : (1u << kGroups) - 1u; rest; rest &= rest - 1) {
                         const int j = 8 * (__ffs(rest) - 1);
@@ -870,7 +909,7 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
             // every span O moves out of the tensor core, to be added up to nearest
             if (span) {
 #pragma unroll 1
-                for (int j = 0; j < kRows; j += 8) {
+                for (int j = 0; j < kOwn; j += 8) {
                     float hi[8], lo[8];
                     tmem_ld8(hi, tmem_o + j);
                     tmem_ld8(lo, tmem_o + Sh::kLo + j);
@@ -885,18 +924,18 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
                 }
                 summed = true;
                 stream_sync(stream);
-                if (key_row < kRows)
+                if (key_row < kOwn)
                     g_sums[key_row] = 1.f;
                 stream_sync(stream);
             }
             // ---- weights: their sum, and with the V scale as a pair into shared memory
             const bool number = fabsf(vs) <= FLT_MAX;
             const float vf = number ? vs * f : 0.f;
-            unsigned char *p_row = s.p16[stream] + (kRows == 64 ? (key_row >> 3) * 2048 : (key_row >> 3) * 1024) + (key_row & 7) * 128;
+            unsigned char *p_row = s.p16[stream] + (kOwn == 64 ? (key_row >> 3) * 2048 : (key_row >> 3) * 1024) + (key_row & 7) * 128;
             // lo's place: the other half of the key's row, or its second panel
-            const int lo_by = kRows == 64 ? 1024 : 0, lo_part = kRows == 64 ? 0 : Sh::kLo / 8;
+            const int lo_by = kOwn == 64 ? 1024 : 0, lo_part = kOwn == 64 ? 0 : Sh::kLo / 8;
 #pragma unroll
-            for (int j = 0; j < kRows; j += 8) {
+            for (int j = 0; j < kOwn; j += 8) {
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int k = 0; k < 8; k += 2) {
@@ -911,7 +950,7 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
             // a V scale that is no number goes as it is to those who see it
             if (!number) {
 #pragma unroll 1
-                for (int j = 0; j < kRows; ++j)
+                for (int j = 0; j < kOwn; ++j)
                     if (seen(j) & 1u)
                         *reinterpret_cast<uint16_t *>(p_row + (((j >> 3) ^ (key_row & 7)) << 4) + 2 * (j & 7)) =
                             vs != vs ? 0x7FFFu : vs > 0.f ? 0x7C00u : 0xFC00u;
@@ -926,8 +965,8 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
 
         // ---- the end of the segment: both streams' states joined, O written
 #pragma unroll
-        for (int j0 = 0; j0 < kRows; j0 += 32) {
-            constexpr int kAtOnce = kRows < 32 ? kRows : 32;
+        for (int j0 = 0; j0 < kOwn; j0 += 32) {
+            constexpr int kAtOnce = kOwn < 32 ? kOwn : 32;
             const float sum = sum_lanes<kAtOnce>(l + j0);
             if (lane % (32 / kAtOnce) == 0)
                 warp_part[warp][j0 + lane / (32 / kAtOnce)] = sum;
@@ -937,7 +976,7 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
         tc_fence_after();
         if (summed) {
 #pragma unroll 1
-            for (int j = 0; j < kRows; j += 8) {
+            for (int j = 0; j < kOwn; j += 8) {
                 float hi[8];
                 tmem_ld8(hi, tmem_o + j);
                 tmem_wait_ld8(hi);
@@ -950,7 +989,7 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
         }
         tc_fence_before();
         stream_sync(stream);
-        if (key_row < kRows) {
+        if (key_row < kOwn) {
             s.l_end[stream][key_row] = (warp_part[0][key_row] + warp_part[1][key_row]) +
                                        (warp_part[2][key_row] + warp_part[3][key_row]);
             s.m_end[stream][key_row] = -neg_m[key_row];
@@ -962,17 +1001,19 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
         const bool whole = seg.seg_tile0 == 0 && seg.seg_tile1 == seg.tiles;
         const int token0 = rg * p.tile_tokens;
         const int live_rows = min(p.tile_tokens, seg.n - token0) * p.g; // may be negative
-        const size_t rec = static_cast<size_t>(2 * blockIdx.x + (seg.seg_tile0 > 0 ? 0 : 1)) * p.rec_rows;
-        if (key_row < kRows) {
-            const float m0 = s.m_end[0][key_row], m1 = s.m_end[1][key_row];
-            const float l0 = s.l_end[0][key_row], l1 = s.l_end[1][key_row];
+        const int cta = blockIdx.x / ((p.row_groups + Sh::kSets - 1) / Sh::kSets);
+        const size_t rec = static_cast<size_t>(2 * (cta * p.row_groups + rg) + (seg.seg_tile0 > 0 ? 0 : 1)) * p.rec_rows;
+        if (key_row < kOwn) {
+            // of a pair each stream has rows of its own, and no other has a share in them
+            const float m0 = s.m_end[set][key_row], m1 = s.m_end[1][key_row];
+            const float l0 = s.l_end[set][key_row], l1 = Sh::kPair ? 0.f : s.l_end[1][key_row];
             const float top = fmaxf(l0 == 0.f ? -INFINITY : m0, l1 == 0.f ? -INFINITY : m1);
             float w0 = l0 == 0.f ? 0.f : ex2(m0 - top), w1 = l1 == 0.f ? 0.f : ex2(m1 - top);
             const float sum = (l0 == 0.f ? 0.f : l0 * w0) + (l1 == 0.f ? 0.f : l1 * w1);
             const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-            s.weight[stream][0][key_row] = w0 * inv * s.inv_f[0];
+            s.weight[stream][0][key_row] = w0 * inv * s.inv_f[set];
             s.weight[stream][1][key_row] = w1 * inv * s.inv_f[1];
-            if (!whole && stream == 0 && key_row < live_rows) {
+            if (!whole && stream == set && key_row < live_rows) {
                 p.rec_m[rec + key_row] = top;
                 p.rec_l[rec + key_row] = sum;
             }
@@ -980,12 +1021,15 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
         stream_sync(stream);
         // eight rows at a time, the streams in turn; a thread has a dim
 #pragma unroll 1
-        for (int j = 8 * stream; j < min(kRows, live_rows); j += 16) {
-            const uint32_t o = s.tmem_base + lanes + kColO + j;
+        for (int j = Sh::kPair ? 0 : 8 * stream; j < min(kOwn, live_rows); j += 8 * kTurns) {
+            const uint32_t o = s.tmem_base + lanes + set * kStreamColumns + kColO + j;
             float h0[8], g0[8], h1[8], g1[8];
             tmem_ld8(h0, o), tmem_ld8(g0, o + Sh::kLo);
-            tmem_ld8(h1, o + kStreamColumns), tmem_ld8(g1, o + kStreamColumns + Sh::kLo);
-            tmem_wait_ld8(h0), tmem_wait_ld8(g0), tmem_wait_ld8(h1), tmem_wait_ld8(g1);
+            if constexpr (!Sh::kPair) {
+                tmem_ld8(h1, o + kStreamColumns), tmem_ld8(g1, o + kStreamColumns + Sh::kLo);
+                tmem_wait_ld8(h1), tmem_wait_ld8(g1);
+            }
+            tmem_wait_ld8(h0), tmem_wait_ld8(g0);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const int row = j + k;
@@ -994,7 +1038,8 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
                 const float w0 = s.weight[stream][0][row], w1 = s.weight[stream][1][row];
                 // a stream without a visible key may hold anything
                 float v = w0 == 0.f ? 0.f : (h0[k] + g0[k]) * w0;
-                v = w1 == 0.f ? v : fmaf(h1[k] + g1[k], w1, v);
+                if constexpr (!Sh::kPair)
+                    v = w1 == 0.f ? v : fmaf(h1[k] + g1[k], w1, v);
                 if (!whole) {
                     p.rec_acc[(rec + row) * kHeadDim + key_row] = v;
                 } else {
@@ -1027,16 +1072,17 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1)
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     TreeInt8Smem<kRows> &s = *reinterpret_cast<TreeInt8Smem<kRows> *>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rg = blockIdx.x % p.row_groups, cta = blockIdx.x / p.row_groups;
+    // one CTA for a row group or a pair of them (the second of the last pair may not exist)
+    const int groups = (p.row_groups + Sh::kSets - 1) / Sh::kSets;
+    const int rg = blockIdx.x % groups * Sh::kSets, cta = blockIdx.x / groups;
     if (tid == 0) {
         prefetch_tensormap(&mk), prefetch_tensormap(&mv);
-        for (int i = 0; i < Sh::kRing; ++i) {
-            mbar_init(&s.code_full[0][i], 1), mbar_init(&s.code_full[1][i], 1);
-            mbar_init(&s.code_empty[0][i], 4), mbar_init(&s.code_empty[1][i], 4);
-        }
+        for (int i = 0; i < Sh::kRing + Sh::kRingV; ++i)
+            mbar_init(&s.code_full[i], 1), mbar_init(&s.code_empty[i], 4);
         for (int w = 0; w < 2; ++w) {
             mbar_init(&s.rows_full[w], 1), mbar_init(&s.rows_empty[w], 8);
             mbar_init(&s.k_ready[w], 4), mbar_init(&s.v_ready[w], 4); // a warp each
+            mbar_init(&s.k_free[w], 2), mbar_init(&s.v_free[w], 2);
             mbar_init(&s.s_read[w], 4), mbar_init(&s.p_ready[w], 4);
             mbar_init(&s.s_full[w], 1), mbar_init(&s.o_done[w], 1), mbar_init(&s.drain[w], 1);
         }
@@ -1078,7 +1124,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1)
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Sh::kMost));
         if (s.units > 0)
-            ok = soften<kScore>(p, s, rg, warp >> 2);
+            ok = soften<kScore>(p, s, Sh::kPair ? rg + (warp >> 2) : rg, warp >> 2);
     }
     if (!ok && lane == 0)
         atomicOr(&g_flags_tree_int8, PGQA_DEVERR_WAIT_TIMEOUT);
@@ -1092,7 +1138,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1)
 // How a call's rows and CTAs are laid out; from sizes alone, so that the
 // workspace query and the launch agree.
 struct Layout {
-    int rows, tile_tokens, row_groups, rec_rows, ctas;
+    int rows, tile_tokens, row_groups, cta_groups, rec_rows, ctas;
     size_t base_bytes, stat_bytes, acc_bytes, sum_bytes;
 };
 
@@ -1110,7 +1156,10 @@ Layout layout(int B, int M, int Hq, int Hkv, int page_size, int max_pages, int s
     y.rows = y.rec_rows <= 8 ? 8 : y.rec_rows <= 16 ? 16 : y.rec_rows <= 32 ? 32 : 64;
     const long long tiles = (static_cast<long long>(max_pages) * page_size + kTileKeys - 1) / kTileKeys;
     const long long units = tiles * B * Hkv;
-    const int ctas = sm_count / y.row_groups;
+    if (y.row_groups > 1)
+        y.rows = 128;
+    y.cta_groups = y.rows == 128 ? (y.row_groups + 1) / 2 : 1;
+    const int ctas = sm_count / y.cta_groups;
     y.ctas = static_cast<int>(units < ctas ? units : ctas);
     if (y.ctas < 1)
         y.ctas = 1;
@@ -1119,7 +1168,7 @@ Layout layout(int B, int M, int Hq, int Hkv, int page_size, int max_pages, int s
     y.stat_bytes = align256(records * y.rec_rows * sizeof(float));
     y.acc_bytes = align256(records * y.rec_rows * kHeadDim * sizeof(float));
     // a stream passes a span only where a (sequence, head) has that many tiles
-    y.sum_bytes = tiles > kSpan ? records * y.rows * kHeadDim * sizeof(float) : 0;
+    y.sum_bytes = tiles > kSpan ? records * (y.rows < kMaxRows ? y.rows : kMaxRows) * kHeadDim * sizeof(float) : 0;
     return y;
 }
 
@@ -1152,7 +1201,7 @@ cudaError_t launch_rows(const CUtensorMap &mk, const CUtensorMap &mv, const Tree
         if (dev < kMaxDevices)
             configured[dev].store(true, std::memory_order_release);
     }
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(p.ctas * p.row_groups)), dim3(Shape<kRows>::kThreads), kInt8Smem<kRows>,
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(p.ctas * ((p.row_groups + Shape<kRows>::kSets - 1) / Shape<kRows>::kSets))), dim3(Shape<kRows>::kThreads), kInt8Smem<kRows>,
                       stream, mk, mv, p);
 }
 
@@ -1163,7 +1212,8 @@ cudaError_t launch_score(int rows, const CUtensorMap &mk, const CUtensorMap &mv,
     case 8: return launch_rows<kScore, 8>(mk, mv, p, stream);
     case 16: return launch_rows<kScore, 16>(mk, mv, p, stream);
     case 32: return launch_rows<kScore, 32>(mk, mv, p, stream);
-    default: return launch_rows<kScore, 64>(mk, mv, p, stream);
+    case 64: return launch_rows<kScore, 64>(mk, mv, p, stream);
+    default: return launch_rows<kScore, 128>(mk, mv, p, stream);
     }
 }
 
