@@ -154,6 +154,28 @@ def test_long_runs_of_tiles(M, g):
     c.check()
 
 
+@pytest.mark.parametrize("M,g,P", [(33, 5, 16), (17, 8, 64), (50, 3, 256), (64, 8, 32)])
+def test_row_groups_in_pairs(M, g, P):
+    """More than 64 rows per KV head: two to eight groups of rows (three for the first three: the last pair lacks one),
+    an absent draft, each output alone."""
+    c = Case(2470 + M, [3000, 40, 900], M, Hq=2 * g, Hkv=2, P=P, draft_lens=[M, 0, M - 3])
+    of = c.check()
+    _, ob = c.results()
+    c.upload()
+    c.launch(f32=False)
+    assert np.array_equal(c.results()[1], ob) and (c.d["of"] == SENTINEL).all()
+    c.upload()
+    c.launch(bf16=False)
+    assert np.array_equal(c.results()[0], of) and (c.d["ob"] == SENTINEL).all()
+
+
+def test_row_groups_in_pairs_over_long_runs():
+    """Some 24 tiles a CTA: O leaves the tensor core on the way, a page lies outside the pool."""
+    c = Case(2480, [60000], 33, Hq=20, Hkv=4)
+    c.table[0, 1000] = -1
+    c.check(flags=binding.DEVERR_BAD_PAGE, skip=lambda b, j: j // 16 == 1000)
+
+
 def test_ragged_drafts_leave_other_rows_alone():
     Case(2500, [300, 1, 5, 16, 200, 129], 16, draft_lens=[0, 1, 5, 16, 9, 16]).check()
 

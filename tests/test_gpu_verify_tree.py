@@ -154,6 +154,31 @@ def test_stars_and_chains():
         assert (plen[:6] <= 2).all() and plen[6:].max() >= 2
 
 
+@pytest.mark.parametrize("V", [500, 6000, 70001])
+def test_what_rejections_leave(V):
+    """Given children of known probability, large ones and small ones first: each test against what is left of the row,
+    while much is left and when hardly anything is. The numbers lie 5 % from the thresholds."""
+    shares = [[0.4, 0.3, 0.2, 0.05, 0.02], [0.02, 0.05, 0.2, 0.3, 0.4], [0.9, 0.09, 0.005, 0.002, 0.001], [0.75, 0.2, 1e-3, 1e-4, 1e-5]]
+    c = Case(317, 24, 6, V, draft=False, dtype=torch.float32, temps=[1.0] * 24, sharp=0.5)
+    c.parents[:, 1:] = 0
+    gen = np.random.default_rng(318)
+    for b in range(24):
+        tokens = gen.permutation(V)[:5]
+        c.tokens[b, 1:] = tokens
+        x = c.target[b, 0].numpy().astype(np.float64)
+        others = np.setdiff1d(np.arange(V), tokens)
+        share = np.array(shares[b % 4])
+        x[others] += np.log(1 - share.sum()) - np.log(np.exp(x[others]).sum())
+        x[tokens] = np.log(share)
+        c.target[b, 0] = torch.from_numpy(x).float()
+        left = 1 - np.concatenate([[0], np.cumsum(share)[:-1]])
+        c.u[b, 1:] = np.minimum(share / left * 1.05, 0.999)
+        if b // 4 < 5:
+            c.u[b, 1 + b // 4] = share[b // 4] / left[b // 4] * 0.95
+    path, plen, _, _ = c.check(decided=1.0)
+    assert (path[:20, 1] == 1 + np.arange(20) // 4).all() and (plen[20:] == 1).all()
+
+
 @pytest.mark.parametrize("draft", [False, True])
 def test_a_chain_accepted_to_its_end(draft):
     """Numbers of 0 accept every token that the target allows at all: paths of 64."""
