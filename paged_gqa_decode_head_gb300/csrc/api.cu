@@ -929,7 +929,8 @@ static int axes_impl(const char *fn, const pgqa_bf16 *q, const pgqa_bf16 *k, con
         return fail(PGQA_ERR_INVALID_ARG, "%s: a required pointer is NULL", fn);
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(gamma_q) || !aligned16(gamma_k) ||
         !aligned16(c.k) || !aligned16(c.v) || !aligned16(c.k8) || !aligned16(c.v8) || !aligned16(c.k_scale) ||
-        !aligned16(c.v_scale) || !aligned16(q_out) || !aligned4(positions) || !aligned4(context_lens) || !aligned4(block_table) || !aligned4(new_lens))
+        !aligned16(c.v_scale) || !aligned16(q_out) || !aligned4(positions) || !aligned4(context_lens) ||
+        !aligned4(block_table) || !aligned4(new_lens))
         return fail(PGQA_ERR_MISALIGNED, "%s: tensors need 16-byte and index arrays 4-byte alignment", fn);
     pgqa::RopeAxesArgs a{q, k, v, gamma_q, gamma_k, positions, n_axes, axis_of_pair, context_lens, new_lens,
                          block_table, c.k, c.v, q_out, B, M, Hq, Hkv, page_size, max_pages, num_pages,
@@ -958,8 +959,8 @@ int qk_norm_rope_append_axes_int8(const pgqa_bf16 *q, const pgqa_bf16 *k, const 
                                   const pgqa_bf16 *gamma_q, const pgqa_bf16 *gamma_k, const int32_t *positions,
                                   int n_axes, const uint8_t *axis_of_pair, const int32_t *context_lens,
                                   const int32_t *new_lens, const int32_t *block_table, int8_t *k_cache8,
-                                  int8_t *v_cache8, float *k_scale, float *v_scale, pgqa_bf16 *q_out, int B, int M, int Hq, int Hkv, int D,
-                                  int page_size, int max_pages, int num_pages, float rope_theta, float eps,
+                                  int8_t *v_cache8, float *k_scale, float *v_scale, pgqa_bf16 *q_out, int B, int M,
+                                  int Hq, int Hkv, int D, int page_size, int max_pages, int num_pages, float rope_theta, float eps,
                                   cudaStream_t stream)
 {
     return axes_impl("qk_norm_rope_append_axes_int8", q, k, v, gamma_q, gamma_k, positions, n_axes, axis_of_pair,

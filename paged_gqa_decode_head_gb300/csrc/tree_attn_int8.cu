@@ -567,7 +567,8 @@ template <int kRows> __device__ bool multiply(const TreeInt8Params &p, TreeInt8S
             bool scores = i < tiles; // to be issued
             const long long start = clock64();
             while (ok && (scores || pending)) {
-                if (scores && passed(&s.k_ready[place(step)], filled(step) & 1) && (step == 0 || passed(&s.s_read[stream], (step - 1) & 1))) {
+                if (scores && passed(&s.k_ready[place(step)], filled(step) & 1) &&
+                    (step == 0 || passed(&s.s_read[stream], (step - 1) & 1))) {
                     tc_fence_after();
                     const uint32_t tmem_k = warp_uniform(s.tmem_base + place(step) * kStreamColumns + kColK);
                     if (leader) { // S^T = K Q^T
@@ -622,8 +623,8 @@ template <int kRows> __device__ bool multiply(const TreeInt8Params &p, TreeInt8S
 // capped, bit 1: biased; plain ones are left as S (the caller has the factor). j: the first
 // one's row.
 template <int kScore, int kRows>
-__device__ __forceinline__ void form_scores(const TreeInt8Params &p, const TreeInt8Smem<kRows> &s, float *x, int j, float factor,
-                                            int buf, int set, float up, float down, int pos)
+__device__ __forceinline__ void form_scores(const TreeInt8Params &p, const TreeInt8Smem<kRows> &s, float *x, int j,
+                                            float factor, int buf, int set, float up, float down, int pos)
 {
     if constexpr ((kScore & 1) != 0) {
         float u[8], over = 0.f;
@@ -931,7 +932,7 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
             // ---- weights: their sum, and with the V scale as a pair into shared memory
             const bool number = fabsf(vs) <= FLT_MAX;
             const float vf = number ? vs * f : 0.f;
-            unsigned char *p_row = s.p16[stream] + (kOwn == 64 ? (key_row >> 3) * 2048 : (key_row >> 3) * 1024) + (key_row & 7) * 128;
+            unsigned char *p_row = s.p16[stream] + (key_row >> 3) * (kOwn == 64 ? 2048 : 1024) + (key_row & 7) * 128;
             // lo's place: the other half of the key's row, or its second panel
             const int lo_by = kOwn == 64 ? 1024 : 0, lo_part = kOwn == 64 ? 0 : Sh::kLo / 8;
 #pragma unroll
@@ -1148,7 +1149,7 @@ Layout layout(int B, int M, int Hq, int Hkv, int page_size, int max_pages, int s
 {
     Layout y{};
     const int g = Hq / Hkv;
-    const int most = kMaxRows / g; // tokens of a CTA
+    const int most = kMaxRows / g; // tokens of a row group
     y.row_groups = (M + most - 1) / most;
     y.tile_tokens = (M + y.row_groups - 1) / y.row_groups;
     y.row_groups = (M + y.tile_tokens - 1) / y.tile_tokens;
@@ -1201,7 +1202,8 @@ cudaError_t launch_rows(const CUtensorMap &mk, const CUtensorMap &mv, const Tree
         if (dev < kMaxDevices)
             configured[dev].store(true, std::memory_order_release);
     }
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(p.ctas * ((p.row_groups + Shape<kRows>::kSets - 1) / Shape<kRows>::kSets))), dim3(Shape<kRows>::kThreads), kInt8Smem<kRows>,
+    const int groups = (p.row_groups + Shape<kRows>::kSets - 1) / Shape<kRows>::kSets; // that have CTAs of their own
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(p.ctas * groups)), dim3(Shape<kRows>::kThreads), kInt8Smem<kRows>,
                       stream, mk, mv, p);
 }
 
