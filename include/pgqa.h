@@ -630,8 +630,9 @@ int kv_cache_commit_path(pgqa_bf16 *const *k_caches, pgqa_bf16 *const *v_caches,
  *   infinity in it) has that as its scale.
  * decode_attn_paged_tree_int8 -- K_j = code * k_scale_j, V_j = code * v_scale_j;
  *   the codes enter the products exactly, as fp16, the scales multiply scores and
- *   weights in fp32. The query must lie in the fp16 range (|q| < 65504). A key that a
- *   query does not see does not reach it, whatever its scales hold. Weights enter
+ *   weights in fp32. A query row (of any size) enters as fp16 times a power of two: its
+ *   elements are exact down to 2^-13 of its largest, and off by 2^-21 of that below. A key
+ *   that a query does not see does not reach it, whatever its scales hold. Weights enter
  *   the product with V as an fp16 hi + lo pair. Workspace: device scratch of
  *   ws_bytes >= decode_attn_tree_int8_workspace_size (of the current device); no
  *   initial value needed. Calls whose work may overlap on the GPU must not share one.

@@ -22,6 +22,12 @@
 //     the nearest keys, the first ones bring the maximum.
 // Sums l stay in the threads, one per row, until a segment's end.
 //
+// Queries enter their product as fp16. bf16's range is far larger, so a row is divided by a
+// unit 2^(16 k) to a largest element in [2^-4, 2^12): its elements are exact down to 2^-13 of
+// the largest at least, and off by 2^-21 of the largest below. k is 0 for rows whose largest
+// lies there, as normalised queries' does; where all rows of a CTA have one k, the unit
+// multiplies the keys' scales, and only rows of very different sizes take a factor per score.
+//
 // Rounding. P vs enters its product as an fp16 pair hi + lo (22 bits), two columns of
 // one product; vs is scaled by a power of two F so that the largest of a stream's run
 // lies in [8, 64) and the pair neither overflows nor meets fp16's small end. S, O, m and
@@ -132,6 +138,8 @@ template <int kRows> struct __align__(1024) TreeInt8Smem {
     uint64_t sees[2][Sh::kSets][64]; // drafted token j: the rows that see it
     float slope_up[2][Sh::kSets][Sh::kOwn], slope_down[2][Sh::kSets][Sh::kOwn]; // slopes (base 2), split by sign
     int anchor[2][Sh::kSets][Sh::kOwn];
+    // what the rows' queries were divided by twice; 0: each row by its own
+    float q_root[2][Sh::kSets], q_roots[2][Sh::kSets][Sh::kOwn];
     int by_sign[2][Sh::kSets]; // every row's anchor is the prefix's end, or its first key for a falling slope
     // a stream's rows
     float neg_m[2][Sh::kOwn]; // minus the reference
@@ -328,6 +336,29 @@ __device__ bool fetch_codes(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, con
 }
 
 // ---------------------------------------------------------------- queries and masks
+// The square root of a row's unit 2^(16 k): the unit itself may lie past fp32's range.
+__device__ __forceinline__ float root_of_unit(int k) { return __uint_as_float(static_cast<uint32_t>(127 + 8 * k) << 23); }
+
+// The larger of two pairs' elements each, by size (their signs are of no use).
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Eight bf16 elements divided by root twice (exact but for what falls below bf16's smallest).
+__device__ __forceinline__ uint4 divided_twice(uint4 x, float root)
+{
+    const uint32_t inv = (254u << 7) - (__float_as_uint(root) >> 16), pair = inv << 16 | inv; // 1 / root
+    const auto times = [pair](uint32_t v) {
+        uint32_t r;
+        asm("{\n\t.reg .b32 t;\n\tmul.rn.bf16x2 t, %1, %2;\n\tmul.rn.bf16x2 %0, t, %2;\n\t}" : "=r"(r) : "r"(v), "r"(pair));
+        return r;
+    };
+    return make_uint4(times(x.x), times(x.y), times(x.z), times(x.w));
+}
+
 template <int kScore, int kRows>
 __device__ bool fetch_rows(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, int rg)
 {
@@ -398,6 +429,41 @@ __device__ bool fetch_rows(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, int 
                     s.by_sign[buf][set] = by_sign;
             }
         }
+        // Every row's unit, from its largest element. A row has a few lanes, whose loads are on
+        // their way together (and bring it near for its conversion).
+        constexpr int kLanes = Sh::kOwn < 32 ? 32 / Sh::kOwn : 1;
+#pragma unroll 1
+        for (int set = 0; set < Sh::kSets; ++set) {
+            const int token0 = (rg + set) * p.tile_tokens;
+            int least = INT_MAX, most = INT_MIN; // k of the set's rows
+#pragma unroll 1
+            for (int row = lane / kLanes; row < Sh::kOwn; row += 32) {
+                uint32_t pairs = 0; // the largest elements so far
+                if (row < rows && token0 + row / p.g < n) {
+                    const uint4 *from = reinterpret_cast<const uint4 *>(
+                        p.q + ((static_cast<size_t>(seg.b) * p.M + token0 + row / p.g) * p.Hq + seg.h * p.g + row % p.g) *
+                                  kHeadDim) + lane % kLanes;
+#pragma unroll 8
+                    for (int i = 0; i < 16 / kLanes; ++i) {
+                        const uint4 x = from[i * kLanes];
+                        pairs = larger(larger(larger(larger(pairs, x.x), x.y), x.z), x.w);
+                    }
+                }
+                uint32_t top = max(pairs & 0x7FFFu, pairs >> 16 & 0x7FFFu); // ordered as the sizes
+#pragma unroll
+                for (int off = kLanes / 2; off >= 1; off /= 2)
+                    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+                // 2^e <= the largest < 2^(e + 1), e = (top >> 7) - 127: k = floor((e + 4) / 16), -8 .. 8
+                const int k = top ? (static_cast<int>(top >> 7) - 123) >> 4 : 0;
+                if (top) // zeros fit any unit
+                    least = min(least, k), most = max(most, k);
+                s.q_roots[buf][set][row] = root_of_unit(k);
+            }
+            least = __reduce_min_sync(0xFFFFFFFFu, least);
+            most = __reduce_max_sync(0xFFFFFFFFu, most);
+            if (lane == 0)
+                s.q_root[buf][set] = most > least ? 0.f : root_of_unit(most < least ? 0 : least);
+        }
         __syncwarp();
         if (lane == 0)
             mbar_arrive(&s.rows_full[buf]);
@@ -422,6 +488,14 @@ __device__ bool fetch_rows(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, int 
                     x[i] = reinterpret_cast<const uint4 *>(
                         p.q + ((static_cast<size_t>(seg.b) * p.M + token0 + row / p.g) * p.Hq + seg.h * p.g + row % p.g) *
                                   kHeadDim)[part];
+            }
+            if (__builtin_expect(s.q_root[buf][set] != 1.f, 0)) {
+#pragma unroll
+                for (int i = 0; i < kFlight; ++i) {
+                    const int row = r0 + 2 * i + (lane >> 4);
+                    if (row < Sh::kOwn)
+                        x[i] = divided_twice(x[i], s.q_roots[buf][set][row]);
+                }
             }
 #pragma unroll
             for (int i = 0; i < kFlight; ++i) {
@@ -671,6 +745,23 @@ __device__ __forceinline__ void form_scores(const TreeInt8Params &p, const TreeI
     }
 }
 
+// A key's scores in place, each by its factor and its row's unit (a call, as it is rarely made and
+// its code would take registers and instruction cache from the loop around it).
+__device__ __noinline__ void apply_units(uint32_t tmem_s, float factor, const float *roots, int n)
+{
+#pragma unroll 1
+    for (int j = 0; j < n; j += 8) {
+        float y[8];
+        tmem_ld8(y, tmem_s + j);
+        tmem_wait_ld8(y);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            y[k] *= factor * roots[j + k] * roots[j + k];
+        tmem_st8(tmem_s + j, y);
+    }
+    tmem_wait_st();
+}
+
 template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, int rg, int stream)
 {
     using Sh = Shape<kRows>;
@@ -698,7 +789,6 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
         const int buf = index & 1;
         const int tiles = seg.seg_tile1 - seg.seg_tile0;
         const int prefix = seg.T - seg.n;
-        wait(&s.rows_full[buf], (index >> 1) & 1);
         if (key_row < kOwn) {
             neg_m[key_row] = INFINITY; // nothing seen yet
             g_sums[key_row] = 1.f;
@@ -729,9 +819,14 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
             next_page = next_key >= first_key ? table[next_key >> p.log2_page] : -1;
         };
         load_scales();
+        wait(&s.rows_full[buf], (index >> 1) & 1);
+        // scale log2 e, or scale / cap, in the unit of the rows' queries
+        const float root = s.q_root[buf][set];
+        const bool uneven = root == 0.f;
+        const float by = (kScore & 1 ? p.cap_u : p.c) * (uneven ? 1.f : root) * (uneven ? 1.f : root);
         for (int i = first; i < tiles; i += kTurns, ++step) {
             const int key0 = (seg.seg_tile1 - 1 - i) * kTileKeys, key = key0 + key_row;
-            float ks = next_ks, vs = next_vs;
+            float factor = next_ks * by, vs = next_vs; // a score is S times the factor
             const bool valid = next_valid;
             load_scales();
             wait(&s.s_full[stream], step & 1);
@@ -743,9 +838,13 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
                 const uint64_t sees = !valid ? 0 : key < prefix ? ~0ull : s.sees[buf][set][key - prefix];
                 sees_lo = static_cast<uint32_t>(sees), sees_hi = static_cast<uint32_t>(sees >> 32);
                 if (!sees)
-                    ks = vs = 0.f; // may hold anything
+                    factor = vs = 0.f; // may hold anything
             }
             const auto seen = [&](int j) { return (j < 32 ? sees_lo : sees_hi) >> (j & 31); };
+            if (__builtin_expect(uneven, 0)) {
+                apply_units(tmem_s, factor, s.q_roots[buf][set], kOwn);
+                factor = 1.f;
+            }
             // Capped and biased scores are formed in place, in a loop small enough for the
             // instruction cache.
             if constexpr (kScore != 0) {
@@ -756,7 +855,6 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
                         pos = p.positions[static_cast<size_t>(seg.b) * p.M + key - prefix];
                     up = distance(pos, prefix), down = distance(pos, 0);
                 }
-                const float factor = ks * (kScore & 1 ? p.cap_u : p.c);
                 float y[2][8];
                 tmem_ld8(y[0], tmem_s);
                 const auto group = [&](int j, float *now, float *next) {
@@ -774,7 +872,7 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
                 }
                 tmem_wait_st();
             }
-            const float mul = kScore ? 1.f : ks * p.c;
+            const float mul = kScore ? 1.f : factor;
             const float vs_size = fabsf(vs) <= FLT_MAX ? fabsf(vs) : 0.f;
             bool there = step == 0; // the last tile's product with V is done
             const bool span = sums && i > first && (i - first) / kTurns % kSpan == 0;
