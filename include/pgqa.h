@@ -633,7 +633,10 @@ int kv_cache_commit_path(pgqa_bf16 *const *k_caches, pgqa_bf16 *const *v_caches,
  *   weights in fp32. A query row (of any size) enters as fp16 times a power of two: its
  *   elements are exact down to 2^-13 of its largest, and off by 2^-21 of that below. A key
  *   that a query does not see does not reach it, whatever its scales hold. Weights enter
- *   the product with V as an fp16 hi + lo pair. Workspace: device scratch of
+ *   the product with V as an fp16 hi + lo pair, relative to the query's largest weight
+ *   times V scale: exact to 2^-22 of each, and to 2^-31 of the largest. (This holds as long
+ *   as the V scales of a sequence and KV head, those that are 0 or not a number apart, span
+ *   less than 2^120.) Workspace: device scratch of
  *   ws_bytes >= decode_attn_tree_int8_workspace_size (of the current device); no
  *   initial value needed. Calls whose work may overlap on the GPU must not share one.
  * kv_cache_commit_path_int8 -- codes and scales move together, bit for bit.

@@ -16,9 +16,9 @@
 //     that converted the key's codes; V's and P's lie in shared memory, dims and rows
 //     contiguous;
 //   - the maximum over the keys is not needed in a tile: a thread only asks whether one
-//     of its scores rises more than 8 (base 2) above the row's reference. If one does in
-//     any of the 128 threads, the references move and l and O are rescaled. The tiles of a
-//     run are taken from its end, so that under a distance bias, whose usual sign favours
+//     of its terms 2^x vs rises more than 8 (base 2) above the row's reference. If one does
+//     in any of the 128 threads, the references move and l and O are rescaled. The tiles of
+//     a run are taken from its end, so that under a distance bias, whose usual sign favours
 //     the nearest keys, the first ones bring the maximum.
 // Sums l stay in the threads, one per row, until a segment's end.
 //
@@ -29,8 +29,14 @@
 // multiplies the keys' scales, and only rows of very different sizes take a factor per score.
 //
 // Rounding. P vs enters its product as an fp16 pair hi + lo (22 bits), two columns of
-// one product; vs is scaled by a power of two F so that the largest of a stream's run
-// lies in [8, 64) and the pair neither overflows nor meets fp16's small end. S, O, m and
+// one product. A row's reference r belongs to what goes in there, not to its scores: the
+// largest term 2^(x - r) |vs| that the row has met lies in [2^6, 2^15), so that the pair does
+// not overflow, and what half its smallest step, 2^-25, takes from a term is at most 2^-31 of
+// the row's largest, whatever the V scales of keys that other rows see or that hardly weigh.
+// Sums l take the same 2^(x - r): up to 2^95 for keys whose V is next to nothing (a V scale
+// counts as 2^-80 at least), which fp32 holds for 2^30 keys. V scales are in units of F, a
+// power of two which brings the largest in the first tile, of the keys that all rows see, to
+// [8, 16), so that their own size does not matter; one above 2^60 makes F smaller. S, O, m and
 // l are fp32; for fp32 outputs O moves out of the tensor core every kSpan tiles, as in
 // tree_attn.cu.
 //
@@ -74,7 +80,10 @@ namespace {
 __device__ unsigned g_flags_tree_int8;
 
 constexpr int kCodeBytes = kTileKeys * kHeadDim; // 16 KB of K or V codes
-constexpr float kRise = 8.f;  // rise of a row's scores (base 2) that moves its reference
+constexpr float kTop = 7.f;   // a row's largest term, in base 2, when its reference is set
+constexpr float kRise = 8.f;  // its rise that moves the reference
+constexpr float kLeastScale = -80.f, kMostScale = 60.f;   // V scales in units of F, in base 2
+constexpr float kLeastVf = 0x1p-80f, kMostTerm = 0x1p15f; // 2^kLeastScale, 2^(kTop + kRise)
 constexpr int kSpan = 16;     // a stream's tiles between two moves of O out of the tensor core (fp32 outputs)
 constexpr int kMaxRows = 64;  // query rows of a row group
 
@@ -144,7 +153,7 @@ template <int kRows> struct __align__(1024) TreeInt8Smem {
     // a stream's rows
     float neg_m[2][Sh::kOwn]; // minus the reference
     float f_l[2][Sh::kOwn], f_o[2][Sh::kOwn], g_sums[2][Sh::kOwn];
-    float warp_part[2][4][Sh::kOwn], warp_vs[2][4];
+    float warp_part[2][4][Sh::kOwn], warp_common[2][4], warp_vs[2][4];
     float m_end[2][Sh::kOwn], l_end[2][Sh::kOwn], inv_f[2];
     float weight[2][2][Sh::kOwn]; // by the stream that writes; of stream 0's and 1's O
     uint32_t warp_over[2][4];
@@ -798,7 +807,7 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
 #pragma unroll
         for (int j = 0; j < kOwn; ++j)
             l[j] = 0.f;
-        float f = 1.f, vs_limit = 0.f; // F, and the V scale that needs a smaller one
+        float f = 0.f;                 // F; 0 until a row sees a key
         bool summed = false;           // `sums` holds earlier spans
         bool large = false;            // a reference beyond 65536
         const int first = Sh::kPair ? 0 : (unit0 ^ stream) & 1;
@@ -873,7 +882,11 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
                 tmem_wait_st();
             }
             const float mul = kScore ? 1.f : factor;
-            const float vs_size = fabsf(vs) <= FLT_MAX ? fabsf(vs) : 0.f;
+            const auto number = [&] { return fabsf(vs) <= FLT_MAX; };
+            float vf = number() ? vs * f : 0.f;
+            const auto size_of = [](float v) { // |v| < 2^size
+                return fmaxf(static_cast<float>(static_cast<int>(__float_as_uint(v) >> 23 & 0xFFu) - 126), kLeastScale);
+            };
             bool there = step == 0; // the last tile's product with V is done
             const bool span = sums && i > first && (i - first) / kTurns % kSpan == 0;
             float x[kOwn];
@@ -917,24 +930,61 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
 #pragma unroll
                 for (int g = 1; g < kGroups; ++g)
                     top = fmaxf(top, tops[g]);
-                if (!stream_any(stream, top > kRise || vs_size > vs_limit) || turn == 4)
+                if (!stream_any(stream, ex2(top) * fmaxf(fabsf(vf), kLeastVf) > kMostTerm) || turn == 4)
                     break;
                 // ---- references move in the groups that need it; F may too
                 if (!there)
                     wait(&s.o_done[stream], (step - 1) & 1);
                 there = true;
                 tc_fence_after();
-                uint32_t over = 0;
+                constexpr uint32_t kNewUnit = 1u << 31;
+                float size = size_of(vf);
+                uint32_t over = f == 0.f || size > kMostScale ? kNewUnit : 0u;
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g)
-                    over |= tops[g] > kRise ? 1u << g : 0u;
+                    over |= tops[g] + size > kTop + kRise ? 1u << g : 0u;
                 over = __reduce_or_sync(0xFFFFFFFFu, over);
-                const float warp_vs = warp_max(vs_size);
                 if (lane == 0)
-                    s.warp_over[stream][warp] = over, s.warp_vs[stream][warp] = warp_vs;
+                    s.warp_over[stream][warp] = over;
                 stream_sync(stream);
                 const uint32_t *o4 = s.warp_over[stream];
                 over = o4[0] | o4[1] | o4[2] | o4[3];
+                int moved = 0;     // F's exponent
+                bool with = false; // references and sums move along with it
+                if (over & kNewUnit) {
+                    over &= ~kNewUnit;
+                    const float vs_size = number() ? fabsf(vs) : 0.f;
+                    const int own = min(p.tile_tokens, seg.n - rg * p.tile_tokens) * p.g; // rows, may be negative
+                    const uint64_t sees = static_cast<uint64_t>(sees_hi) << 32 | sees_lo;
+                    const bool common = own <= 0 || ~sees << (64 - own) == 0; // all rows see this key
+                    const float warp_common = warp_max(common ? vs_size : 0.f), warp_vs = warp_max(vs_size);
+                    if (lane == 0)
+                        s.warp_common[stream][warp] = warp_common, s.warp_vs[stream][warp] = warp_vs;
+                    stream_sync(stream);
+                    const auto largest = [](const float *v) { return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])); };
+                    const float common_vs = largest(s.warp_common[stream]), all_vs = largest(s.warp_vs[stream]);
+                    const int of_common = __float_as_uint(common_vs) >> 23; // exponents
+                    const int of_all = __float_as_uint(all_vs) >> 23;
+                    // At first F brings the largest that all rows see to [8, 16); or, where there is
+                    // none, the largest of all to 2^50, as others' may be far smaller.
+                    const int to = common_vs > 0.f ? 130 - of_common : all_vs > 0.f ? 177 - of_all : 40;
+                    const int was = f == 0.f ? to : static_cast<int>(__float_as_uint(f) >> 23) - 127;
+                    const int e = max(-126, min(min(was, 126), static_cast<int>(kMostScale) + 126 - of_all));
+                    moved = f == 0.f ? 0 : e - was;
+                    f = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+                    vf = number() ? vs * f : 0.f;
+                    size = size_of(vf);
+                    if (moved != 0) {
+                        // A smaller F changes references and sums along with it, and no term; unless
+                        // sums are so large that they would overflow.
+                        const float limit = ex2(static_cast<float>(120 + moved));
+                        bool large_sum = false;
+#pragma unroll
+                        for (int j = 0; j < kOwn; ++j)
+                            large_sum = large_sum || l[j] > limit;
+                        with = !stream_any(stream, large_sum);
+                    }
+                }
 #pragma unroll 1
                 for (uint32_t rest = over; rest; rest &= rest - 1) {
                     const int j = 8 * (__ffs(rest) - 1);
@@ -944,34 +994,27 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
                     const uint32_t bits = seen(j);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const float most = warp_max(bits >> k & 1u ? __fmul_rn(y[k], mul) : -INFINITY);
+                        // (rounded up: however large the score, no term is past its range)
+                        const float mine = __fadd_ru(__fmul_rn(y[k], mul), size - kTop);
+                        const float most = warp_max(bits >> k & 1u ? mine : -INFINITY);
                         if (lane == k)
                             warp_part[warp][j + k] = most;
                     }
                 }
-                float fv = 1.f;
-                const float *v4 = s.warp_vs[stream];
-                const float all = fmaxf(fmaxf(v4[0], v4[1]), fmaxf(v4[2], v4[3]));
-                if (all > vs_limit) { // F all in [8, 16)
-                    const int e = min(126, max(-126, 130 - static_cast<int>(__float_as_uint(all) >> 23)));
-                    const int was = static_cast<int>(__float_as_uint(f) >> 23) - 127;
-                    fv = ex2(static_cast<float>(e - was));
-                    f = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-                    vs_limit = 64.f / f;
-                }
                 stream_sync(stream);
                 bool far = false;
                 if (key_row < kOwn) {
-                    float fm = 1.f, m = -neg_m[key_row];
+                    const float last = -neg_m[key_row];
+                    float m = with ? __fadd_ru(last, static_cast<float>(moved)) : last;
                     if (over >> (key_row >> 3) & 1u) {
                         const float most = fmaxf(fmaxf(warp_part[0][key_row], warp_part[1][key_row]),
                                                  fmaxf(warp_part[2][key_row], warp_part[3][key_row]));
-                        if (m == -INFINITY ? most > -INFINITY : most - m > kRise) {
-                            fm = m == -INFINITY ? 0.f : ex2(m - most);
-                            m = most;
-                            neg_m[key_row] = -most;
-                        }
+                        // any rise, as the group is at it: fewer rows come back for another
+                        m = most > m ? most : m;
                     }
+                    const float fm = last == m ? 1.f : last == -INFINITY ? 0.f : ex2(last - m);
+                    const float fv = ex2(static_cast<float>(moved));
+                    neg_m[key_row] = -m;
                     far = fabsf(m) > 65536.f && m > -INFINITY;
                     f_l[key_row] = fm;
                     f_o[key_row] = fm * fv;
@@ -983,7 +1026,7 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
                     l[j] *= f_l[j];
                 if (i > first) {
 #pragma unroll 1
-                    for (uint32_t rest = fv == 1.f ? over : (1u << kGroups) - 1u; rest; rest &= rest - 1) {
+                    for (uint32_t rest = moved == 0 ? over : (1u << kGroups) - 1u; rest; rest &= rest - 1) {
                         const int j = 8 * (__ffs(rest) - 1);
                         float hi[8], lo[8];
                         tmem_ld8(hi, tmem_o + j);
@@ -1028,8 +1071,6 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
                 stream_sync(stream);
             }
             // ---- weights: their sum, and with the V scale as a pair into shared memory
-            const bool number = fabsf(vs) <= FLT_MAX;
-            const float vf = number ? vs * f : 0.f;
             unsigned char *p_row = s.p16[stream] + (key_row >> 3) * (kOwn == 64 ? 2048 : 1024) + (key_row & 7) * 128;
             // lo's place: the other half of the key's row, or its second panel
             const int lo_by = kOwn == 64 ? 1024 : 0, lo_part = kOwn == 64 ? 0 : Sh::kLo / 8;
@@ -1047,7 +1088,7 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
                     make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
             // a V scale that is no number goes as it is to those who see it
-            if (!number) {
+            if (!number()) {
 #pragma unroll 1
                 for (int j = 0; j < kOwn; ++j)
                     if (seen(j) & 1u)
@@ -1093,7 +1134,7 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
                                        (warp_part[2][key_row] + warp_part[3][key_row]);
             s.m_end[stream][key_row] = -neg_m[key_row];
             if (key_row == 0)
-                s.inv_f[stream] = 1.f / f;
+                s.inv_f[stream] = f == 0.f ? 0.f : 1.f / f;
         }
         both_streams_sync();
         tc_fence_after();

@@ -1,12 +1,21 @@
 """decode_attn_paged_tree_int8 over the whole range of its inputs: queries of any size, rows and elements of very
-different sizes beside each other.
+different sizes beside each other, V scales of keys that other rows see or that hardly weigh anything.
 
 Bound on the fp32 output, u = 2^-24; as tests/tree_int8_reference.py, a relative error e_j of weight j moves the output by
-at most sum_j p_j |V_j| e_j + |out| sum_j p_j e_j, with this term besides:
+at most sum_j p_j |V_j| e_j + |out| sum_j p_j e_j, with these terms besides or in another form:
   - a query row is taken by a power of two to a largest element of at least 2^-4 and rounded to fp16, whose smallest
     step is 2^-24: an element is off by at most half of that, 2^-25 / 2^-4 = 8 u of the row's largest, and the score by
-    8 u max |q| scale sum_d |K_jd|.
+    8 u max |q| scale sum_d |K_jd|;
+  - a row's exponentials are taken relative to a reference r at which its largest contribution p_j vs_j lies in [2^6, 2^15),
+    V scales (in units F, a power of two) below 2^-80 counting as that: |x - r| in base 2 is at most the distance
+    from the row's maximum plus 15 + L, L = max(|log2 vs F|, 80 for a scale of 0) <= 84. Arguments and joins round there
+    twice each: 4 u (15 + L), with L from the keys that the row sees, relative to the prefix's largest scale, which F
+    brings to [8, 16);
+  - a key's weight times its V scale is an fp16 pair hi + lo with an absolute step of 2^-24, half of it lost, beside a
+    largest contribution of at least 2^6: 2^-31 127 max_j p_j |vs_j| a key that the row sees, whatever others see.
 """
+import math
+
 import numpy as np
 import pytest
 
@@ -56,14 +65,16 @@ def reference(c):
                     bias = sl * (kpos[seen] - (kpos[seen].min() if sl < 0 else kpos[seen].max()))
                     e += 2 * U * (np.abs(bias) + abs(sl) * 64 + np.abs(x))
                     x = x + bias
-                e += 4 * U * (np.abs(x) + abs(x.max())) + 9 * U + 2.0 ** -21
+                unit = np.abs(vs[kv, :prefix]).max(initial=0.0) or 8.0
+                spread = max(min(84.0, abs(math.log2(s / unit))) if s > 0 else 84.0 for s in size)
+                e += 4 * U * (np.abs(x) + abs(x.max())) + 9 * U + 2.0 ** -21 + 4 * U * (15 + spread)
                 e += 2 * (128 + T / 128 + 64) * U
                 p = np.exp(x - x.max())
                 p /= p.sum()
                 o = p @ v
                 out[b, i, h] = o
                 bound[b, i, h] = ((p * e) @ np.abs(v) + np.abs(o) * (p @ e) +
-                                  T * 2.0 ** -28 * 127 * size.max())
+                                  len(seen) * 2.0 ** -31 * 127 * (p * size).max())
     return out, bound
 
 
@@ -140,3 +151,95 @@ def test_a_query_that_is_no_number_stays_alone(bad, M, g):
     c.q = inputs.f32_to_bf16_bits(x.astype(np.float32))
     of = check(c)
     assert np.isnan(of[0, 1, 0]).all() and np.isnan(of[1, M - 1, 2 * g - 1]).all()
+
+
+# ------------------------------------------------------------------ V scales
+def at(c, b, j):
+    return c.table[b, j // c.P], slice(None), j % c.P
+
+
+def blind_masks(M, j):
+    """Drafted token j is seen by itself and by odd tokens behind it only."""
+    masks = []
+    for i in range(M):
+        m = (2 << i) - 1
+        masks.append(m & ~(1 << j) if i != j and i % 2 == 0 else m)
+    return masks
+
+
+@pytest.mark.parametrize("power", [12, 24, 60, 120])
+@pytest.mark.parametrize("M,g", SHAPES)
+def test_a_large_value_scale_of_a_key_that_others_see(power, M, g):
+    """One drafted token's V scale is 2^power times the others': rows that do not see it keep all of their bits."""
+    for T in (M, M + 40, 700):
+        c = Case(3500 + M, [T], M, Hq=2 * g, Hkv=2, masks=[blind_masks(M, 1)])
+        c.vs[at(c, 0, T - M + 1)] *= np.float32(2.0 ** power)
+        check(c)
+
+
+@pytest.mark.parametrize("M,g", [(3, 2), (12, 2), (64, 2)])
+def test_large_value_scales_that_others_see_over_long_runs(M, g):
+    """The same with several tiles in every CTA, and V scales of the prefix between 2^-8 and 2^8."""
+    c = Case(3550 + M, [5000] * 8, M, Hq=2 * g, Hkv=2, masks=[blind_masks(M, 1)] * 8)
+    gen = np.random.default_rng(M)
+    for b in range(8):
+        for j in range(5000):
+            c.vs[at(c, b, j)] *= np.float32(2.0 ** gen.integers(-8, 9))
+        c.vs[at(c, b, 5000 - M + 1)] *= np.float32(2.0 ** (10 * b))
+    check(c)
+
+
+@pytest.mark.parametrize("lower", [5.0, 12.0, 25.0, 60.0])
+@pytest.mark.parametrize("T", [700, 9000])
+def test_a_large_value_scale_of_a_key_that_hardly_weighs(lower, T):
+    """A key whose V scale is 2^24 times the others' and whose score lies `lower` (base 2) below all of them."""
+    c = Case(3600, [T], 2, Hq=2, Hkv=2)
+    c.q[0, 1] = c.q[0, 0]
+    c.k8[...] = np.random.default_rng(1).integers(-3, 4, c.k8.shape)
+    for h in range(2):
+        q = bf16_ref.widen(c.q[0, 0, h])
+        c.k8[at(c, 0, 40)[0], h, 40 % c.P] = np.rint(-127 * q / np.abs(q).max())
+        x = SCALE * (ref.rows_of(c.k8, c.table[0], T, c.P)[h].astype(np.float64) *
+                     ref.rows_of(c.ks, c.table[0], T, c.P)[h, :, None].astype(np.float64)) @ q
+        page, off = c.table[0, 40 // c.P], 40 % c.P
+        c.ks[page, h, off] *= np.float32((lower * math.log(2) - np.median(x)) / -x[40])
+    c.vs[at(c, 0, 40)] *= np.float32(2.0 ** 24)
+    check(c)
+
+
+@pytest.mark.parametrize("weigh", [8.0, 20.0, 30.0])
+@pytest.mark.parametrize("value", [0.0, 2.0 ** -40, 2.0 ** -12, 1.0])
+@pytest.mark.parametrize("B,M", [(1, 1), (1, 40), (12, 1), (12, 12), (8, 40)])
+def test_a_first_key_that_takes_the_weight(weigh, value, B, M):
+    """The first key's score lies `weigh` (nats) above the others, its V row is nothing or small: the output is the rest's,
+    each with a weight of e^-weigh. In a batch a CTA has many tiles."""
+    c = Case(3700, [6000] * B, M, Hq=2, Hkv=2)
+    c.q[:, :] = c.q[:, :1]
+    for b in range(B):
+        page = c.table[b, 0]
+        for h in range(2):
+            q = bf16_ref.widen(c.q[b, 0, h])
+            c.k8[page, h, 0] = np.rint(127 * q / np.abs(q).max())
+            c.ks[page, h, 0] = weigh / (SCALE * (c.k8[page, h, 0].astype(np.float64) @ q))
+        c.vs[page, :, 0] *= np.float32(value)
+    check(c)
+
+
+@pytest.mark.parametrize("power", [-70, -30, 30, 70])
+@pytest.mark.parametrize("M,g", [(3, 2), (12, 2), (64, 2)])
+def test_value_scales_of_any_size(power, M, g):
+    """All V scales small or large, and those of a drafted token of its own size besides."""
+    c = Case(3800 + M, [300, M + 200], M, Hq=2 * g, Hkv=2, masks=[blind_masks(M, 1)] * 2)
+    c.vs *= np.float32(2.0 ** power)
+    c.vs[at(c, 0, 300 - M + 1)] *= np.float32(2.0 ** 20)
+    c.vs[at(c, 1, 200 + 1)] *= np.float32(2.0 ** -20)
+    check(c)
+
+
+def test_value_scales_that_grow_past_the_first_unit():
+    """From the last tile, whose keys come first, to the first one V scales grow by 2^110."""
+    c = Case(3900, [128 * 6] * 40, 2, Hq=8, Hkv=4)
+    for b in range(40):
+        for j in range(128 * 6):
+            c.vs[at(c, b, j)] *= np.float32(2.0 ** (50 - 22 * (j // 128)))
+    check(c)
