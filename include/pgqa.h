@@ -696,7 +696,7 @@ int kv_cache_read_int8(const int8_t *k_cache8, const int8_t *v_cache8, const flo
  *   with draft_logits they were drawn one after the other, without replacement,
  *     from q = softmax(draft row / temperature); child i is accepted if accept_u[b][i]
  *     < p(t) / q(t); a rejection leaves p <- max(p - q, 0) and takes t out of p and q,
- *     both renormalised. (A child counts as given once rounding leaves nothing of q.)
+ *     both renormalised. (A child counts as given once less than 2^-119 of q is left.)
  * Where no child is left, or the path has A entries, the last token is drawn from
  * what is left of p: argmax_i p_i / noise[b][i] (an exponential race: with noise ~
  * Exp(1) and accept_u ~ U[0, 1) the new tokens are distributed as if they had been

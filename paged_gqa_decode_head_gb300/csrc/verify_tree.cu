@@ -46,6 +46,9 @@ constexpr int kVerifyThreads = 512;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxDrafted = 64;
 constexpr int kPiece = 8; // logits a thread takes at a time
+// Less than this of q left is nothing: S / Q is at most its reciprocal then, 64 of them and
+// their products with q are finite.
+constexpr float kLeastRest = 0x1p-119f;
 constexpr int kMaxDevices = 64;
 
 struct VerifyParams {
@@ -433,7 +436,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const __grid_
                 const float pt = again ? 0.f : weight(s.child_p[i], st.m, k) * inv;
                 const float qt = kDraft && !again ? weight(s.child_q[i], sq.m, k) * inv_q : 0.f;
                 const float left = kDraft ? fmaxf(fmaf(-taken, qt, pt), 0.f) : pt;
-                const bool given = !kDraft || !(rest > 0.f); // a point mass
+                const bool given = !kDraft || !(rest >= kLeastRest); // a point mass
                 if (s.accept[i] * mass * (given ? 1.f : qt) < left * (given ? 1.f : rest)) {
                     accepted = i;
                     break;

@@ -1,0 +1,57 @@
+"""verify_drafted_tree where its arithmetic or its loads could go wrong: what is left of q near the smallest numbers."""
+import numpy as np
+import pytest
+import torch
+
+import paged_gqa_decode_head_gb300 as pg
+from test_gpu_verify_tree import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _clean_flags():
+    pg.device_error_flags(clear=True)
+    yield
+    assert pg.device_error_flags() == 0
+
+
+def siblings(B, M, V, tokens, temps, target, draft):
+    """B equal sequences whose root has M - 1 children; rows of float32 logits."""
+    c = Case(7000, B, M, V, draft=True, dtype=torch.float32, temps=temps)
+    c.target = torch.from_numpy(np.broadcast_to(target, (B, M, V)).astype(np.float32).copy())
+    c.draft = torch.from_numpy(np.broadcast_to(draft, (B, M, V)).astype(np.float32).copy())
+    c.parents[:], c.parents[:, 0], c.tokens[:, 1:] = 0, -1, tokens
+    return c
+
+
+@pytest.mark.parametrize("low", [60.0, 80.0, 84.0, 86.0, 87.0])
+def test_next_to_nothing_left_of_the_draft(low):
+    """Eight children of q = 1/8 each are rejected, then one whose logit lies `low` below them: 1 / q is past the largest
+    number for the last of these. The residual is p without it."""
+    V = 40
+    target, draft = np.full(V, -np.inf), np.full(V, -np.inf)
+    target[8], target[9] = 0.0, 0.0  # p = 1/2 each: the last child's token, and one that was never drafted
+    draft[:8], draft[8] = 0.0, -low
+    c = siblings(1, 10, V, range(9), [1.0], target, draft)
+    c.u[:] = 0.9  # p' / q' = 1/2 for the last child: rejected
+    c.noise[:], c.noise[0, 8] = 1.0, 1e-3  # p itself would give token 8
+    path, plen, new, logp = c.run()
+    assert plen[0] == 1 and path[0, 0] == 0 and new[0, 0] == 9
+    assert abs(logp[0, 0] - np.log(0.5)) < 2.0 ** -16
+    c.u[0, 9] = 0.1
+    path, plen, new, _ = c.run()
+    assert plen[0] == 2 and path[0, 1] == 9 and new[0, 0] == 8
+
+
+def test_a_long_row_of_small_remainders():
+    """Rejected children of q = 1, 2^-60, 2^-110, each next to nothing beside the one before: what the residual loses to each
+    adds up to a finite number, and a token that was never drafted keeps its probability."""
+    V, ln2 = 24, np.log(2.0)
+    target, draft = np.full(V, -np.inf), np.full(V, -np.inf)
+    target[2], target[5] = 0.0, 0.0
+    draft[0], draft[1], draft[2] = 0.0, -60 * ln2, -110 * ln2
+    c = siblings(1, 4, V, [0, 1, 2], [1.0], target, draft)
+    c.u[:], c.noise[:], c.noise[0, 2] = 0.9, 1.0, 1e-3
+    path, plen, new, _ = c.run()
+    assert plen[0] == 1 and new[0, 0] == 5
