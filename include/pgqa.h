@@ -714,7 +714,7 @@ int kv_cache_read_int8(const int8_t *k_cache8, const int8_t *v_cache8, const flo
  *   parents      [B][M] int32: the parent's index, below the token's own (others are
  *                never reached); parents[b][0] is ignored
  *   draft_lens   [B] int32, nullable: n_b in [0, M] (NULL: M)
- *   temperatures [B] float >= 0
+ *   temperatures [B] float >= 0; above 2^100 (infinity too) as 2^100
  *   accept_u     [B][M] float in [0, 1)
  *   noise        [B][V] float > 0, 16-byte aligned
  *   path         [B][A] int32, 1 <= A <= M: the accepted tokens' indices, path[b][0] =

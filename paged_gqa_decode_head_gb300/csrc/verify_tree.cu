@@ -49,6 +49,9 @@ constexpr int kPiece = 8; // logits a thread takes at a time
 // Less than this of q left is nothing: S / Q is at most its reciprocal then, 64 of them and
 // their products with q are finite.
 constexpr float kLeastRest = 0x1p-119f;
+// Higher temperatures count as this one: a difference of logits past fp32's range stays no
+// weight, and is not infinity times zero.
+constexpr float kMostTemperature = 0x1p100f;
 constexpr int kMaxDevices = 64;
 
 struct VerifyParams {
@@ -322,7 +325,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const __grid_
     }
     cluster_sync(); // every block has started before one writes to another
     const bool greedy = temperature == 0.f;
-    const float k = fminf(kLog2e / (greedy ? 1.f : temperature), FLT_MAX);
+    const float k = fminf(kLog2e / (greedy ? 1.f : fminf(temperature, kMostTemperature)), FLT_MAX);
     const float *noise = p.noise + static_cast<size_t>(b) * p.V;
     int turn = 0;
     int cur = 0, count = 0;

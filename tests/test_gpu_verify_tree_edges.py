@@ -1,4 +1,5 @@
-"""verify_drafted_tree where its arithmetic or its loads could go wrong: what is left of q near the smallest numbers."""
+"""verify_drafted_tree where its arithmetic or its loads could go wrong: what is left of q near the smallest numbers, very
+high temperatures."""
 import numpy as np
 import pytest
 import torch
@@ -55,3 +56,37 @@ def test_a_long_row_of_small_remainders():
     c.u[:], c.noise[:], c.noise[0, 2] = 0.9, 1.0, 1e-3
     path, plen, new, _ = c.run()
     assert plen[0] == 1 and new[0, 0] == 5
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("draft", [False, True])
+def test_an_infinite_temperature(dtype, draft):
+    """All tokens of usual logits are equally likely."""
+    V = 500
+    c = Case(7100, 12, 6, V, draft=draft, dtype=dtype, temps=[np.inf] * 12)
+    path, plen, new, logp = c.run()
+    assert (plen >= 1).all() and (new[:, 0] >= 0).all()
+    for b in range(12):
+        assert (np.abs(logp[b, :plen[b]] + np.log(V)) < 2.0 ** -16).all()
+        if plen[b] == 1 and not draft and not (c.parents[b] == 0).any():
+            assert new[b, 0] == np.argmin(c.noise[b])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("temperature", [1e-30, 1.0, 1e30, 1e38, np.inf])
+def test_logits_at_both_ends_of_their_type(dtype, temperature):
+    """The largest number beside the lowest one: the difference is past the type, and the lowest has no weight."""
+    V, most = 300, torch.finfo(dtype).max
+    c = Case(7200, 4, 2, V, draft=False, dtype=dtype, temps=[temperature] * 4)
+    c.target[:] = -most
+    c.target[:, :, 77] = most
+    c.target[1:, :, 78] = most
+    c.target[2:, :, 3] = float("inf")
+    c.tokens[:], c.u[:], c.noise[:] = 5, 0.5, 1.0
+    path, plen, new, logp = c.run()
+    assert (plen == 1).all()
+    if dtype is torch.float32:  # +inf counts as the largest float32
+        assert new[:, 0].tolist() == [77, 77, 3, 3]
+        assert np.allclose(logp[:, 0], -np.log([1, 2, 3, 3]), atol=2.0 ** -16)
+    else:
+        assert new[:2, 0].tolist() == [77, 77] and (new[2:, 0] == 3).all()
