@@ -1,11 +1,11 @@
 """verify_drafted_tree where its arithmetic or its loads could go wrong: what is left of q near the smallest numbers, very
-high temperatures."""
+high temperatures, draft rows at another alignment than the target's, rows past 32-bit offsets."""
 import numpy as np
 import pytest
 import torch
 
 import paged_gqa_decode_head_gb300 as pg
-from test_gpu_verify_tree import Case
+from test_gpu_verify_tree import MARGIN, Case
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +90,33 @@ def test_logits_at_both_ends_of_their_type(dtype, temperature):
         assert np.allclose(logp[:, 0], -np.log([1, 2, 3, 3]), atol=2.0 ** -16)
     else:
         assert new[:2, 0].tolist() == [77, 77] and (new[2:, 0] == 3).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("target_pad,draft_pad", [(0, 1), (0, 3), (0, 5), (1, 0), (3, 2), (7, 4)])
+@pytest.mark.parametrize("V", [1000, 1001, 33000])
+def test_draft_rows_at_another_alignment(V, target_pad, draft_pad, dtype):
+    """Pieces begin on the target row's 16-byte boundaries; the draft's rows lie elsewhere."""
+    c = Case(7300 + V + draft_pad, 6, 10, V, dtype=dtype)
+    c.upload()
+    for name, pad in (("target", target_pad), ("draft", draft_pad)):
+        wide = torch.full((c.B, c.M, V + pad), 1e4, dtype=dtype, device="cuda")
+        wide[..., :V] = c.d[name]
+        c.d[name] = wide[..., :V]
+    c.upload, kept = (lambda: kept), c.d  # check() uploads
+    c.check(decided=0.5)
+
+
+def test_every_decided_walk_past_32_bit_offsets():
+    """Rows whose elements lie past 2^31 in the logits: paths, tails, lengths and log probabilities."""
+    B, M, V = 6, 64, 60000
+    wide = (1 << 31) // (B * M) * 2
+    c = Case(7400, B, M, V, draft=False, temps=[0.8, 0.0, 1.0, 0.0, 0.6, 0.0])
+    c.upload()
+    rows = torch.zeros((B, M, wide), dtype=torch.bfloat16, device="cuda")
+    rows[..., :V] = c.d["target"]
+    c.d["target"] = rows[..., :V]
+    c.upload, kept = (lambda: kept), c.d
+    sure = sum(c.expected(b)[3] >= MARGIN for b in range(B))
+    assert sure >= 4
+    c.check(decided=sure / B)
