@@ -130,6 +130,16 @@ def test_rows_of_very_different_sizes(M, g, softcap, biased):
     check(c)
 
 
+@pytest.mark.parametrize("softcap,biased", [(0.0, False), (20.0, True)])
+@pytest.mark.parametrize("M,g", [(8, 2), (33, 2)])
+def test_rows_of_very_different_sizes_over_long_runs(M, g, softcap, biased):
+    """The same with many tiles and segments in every CTA, some segments' rows alike."""
+    c = Case(3250 + M, [9000, 300, 12000, 40], M, Hq=4 * g, Hkv=4, softcap=softcap, slopes=SLOPES[:4 * g] if biased else None)
+    gen = np.random.default_rng(M + g)
+    c.q[1:] = scaled(c.q[1:], 2.0 ** gen.choice([-20.0, 0.0, 20.0], (3, M, 4 * g, 1)))
+    check(c)
+
+
 @pytest.mark.parametrize("M,g", [(3, 2), (12, 2), (64, 2)])
 def test_elements_of_very_different_sizes(M, g):
     """A large element that meets zeros in K: the small ones make the scores."""
@@ -236,10 +246,21 @@ def test_value_scales_of_any_size(power, M, g):
     check(c)
 
 
-def test_value_scales_that_grow_past_the_first_unit():
+@pytest.mark.parametrize("M,g", [(2, 2), (24, 1), (64, 1), (50, 2)])
+def test_value_scales_that_grow_past_the_first_unit(M, g):
     """From the last tile, whose keys come first, to the first one V scales grow by 2^110."""
-    c = Case(3900, [128 * 6] * 40, 2, Hq=8, Hkv=4)
-    for b in range(40):
+    c = Case(3900, [128 * 6] * 20, M, Hq=8 * g, Hkv=8)
+    for b in range(20):
         for j in range(128 * 6):
             c.vs[at(c, b, j)] *= np.float32(2.0 ** (50 - 22 * (j // 128)))
+    check(c)
+
+
+@pytest.mark.parametrize("powers", [(-100, -100), (-60, 60), (100, 100)])
+@pytest.mark.parametrize("M,g", [(3, 2), (33, 1), (64, 2)])
+def test_rows_that_have_no_key_in_common(M, g, powers):
+    """Every drafted token sees itself alone, each with a V scale of its own size: the output is its V row."""
+    c = Case(3950, [M], M, Hq=2 * g, Hkv=2, masks=[[1 << i for i in range(M)]])
+    for j in range(M):
+        c.vs[at(c, 0, j)] *= np.float32(2.0 ** (powers[0] + (powers[1] - powers[0]) * j / M))
     check(c)
