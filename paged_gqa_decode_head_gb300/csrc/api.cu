@@ -990,7 +990,7 @@ int kv_cache_read_int8(const int8_t *k_cache8, const int8_t *v_cache8, const flo
         !aligned16(k_out) || !aligned16(v_out) || !aligned4(block_table) || !aligned4(context_lens) || !aligned4(first))
         return fail(PGQA_ERR_MISALIGNED, "%s: tensors need 16-byte and index arrays 4-byte alignment", fn);
     pgqa::ReadInt8Args a{k_cache8, v_cache8, k_scale, v_scale, block_table, context_lens, first, k_out, v_out, B, N, Hkv,
-                         page_size, max_pages, num_pages, sm_count_current_device()};
+                         page_size, max_pages, num_pages};
     cudaError_t err = pgqa::launch_read_int8(a, stream);
     if (err != cudaSuccess)
         return cuda_fail(err, fn);
@@ -1234,11 +1234,11 @@ int kv_cache_commit_path_int8(int8_t *const *k_caches8, int8_t *const *v_caches8
                        stream);
 }
 
+// The kernel keeps all of its state in shared memory.
 size_t verify_drafted_tree_workspace_size(int B, int M, int V)
 {
-    if (B < 0 || M < 1 || M > 64 || V < 1)
-        return 0;
-    return pgqa::verify_tree_workspace_bytes(B, M, V, sm_count_current_device());
+    (void)B, (void)M, (void)V;
+    return 0;
 }
 
 int verify_drafted_tree(const void *target_logits, const void *draft_logits, int logits_f32, long long target_stride,
@@ -1276,11 +1276,8 @@ int verify_drafted_tree(const void *target_logits, const void *draft_logits, int
         return fail(PGQA_ERR_MISALIGNED, "%s: the small arrays need 4-byte alignment", fn);
     pgqa::VerifyTreeArgs a{target_logits, draft_logits, logits_f32 != 0, target_stride, draft_stride, tokens, parents,
                            draft_lens, temperatures, accept_u, noise, B, M, A, V, path, path_lens, new_tokens, logprobs,
-                           workspace, sm_count_current_device()};
-    const size_t need = pgqa::verify_tree_workspace_bytes(B, M, V, a.sm_count);
-    if (need > 0 && (!workspace || ws_bytes < need))
-        return fail(PGQA_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, got %zu", fn, need,
-                    workspace ? ws_bytes : static_cast<size_t>(0));
+                           sm_count_current_device()};
+    (void)ws_bytes; // none is needed
     cudaError_t err = pgqa::launch_verify_tree(a, stream);
     if (err != cudaSuccess)
         return cuda_fail(err, fn);

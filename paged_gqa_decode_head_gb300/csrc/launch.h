@@ -188,7 +188,6 @@ struct ReadInt8Args {
     const int32_t *block_table, *context_lens, *first; // first: nullable
     pgqa_bf16 *k_out, *v_out;
     int B, N, Hkv, page_size, max_pages, num_pages;
-    int sm_count;
 };
 cudaError_t launch_read_int8(const ReadInt8Args &a, cudaStream_t stream);
 cudaError_t read_flags_read_int8(unsigned *flags, bool clear);
@@ -223,10 +222,8 @@ struct VerifyTreeArgs {
     int B, M, A, V;
     int32_t *path, *path_lens, *new_tokens;
     float *logprobs; // nullable
-    void *ws;
     int sm_count;
 };
-size_t verify_tree_workspace_bytes(int B, int M, int V, int sm_count);
 cudaError_t launch_verify_tree(const VerifyTreeArgs &a, cudaStream_t stream);
 cudaError_t read_flags_verify_tree(unsigned *flags, bool clear);
 

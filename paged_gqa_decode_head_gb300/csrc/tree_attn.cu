@@ -1017,6 +1017,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     grid_dependency_wait();
     allow_dependent_launch();
     plan_run<kTreeThreads>(p, s, cta);
+    if (tid == 0)
+        s.zero = 0.f;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

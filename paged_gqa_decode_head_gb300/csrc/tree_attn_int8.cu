@@ -42,15 +42,17 @@
 //
 // Bound. The cache is read once: 264 bytes per (key, KV head), 33 KB a tile of K and V, some
 // 1440 clocks of an SM's share of the memory. Measured: 64 sequences of 16384 keys and 8 heads
-// at 8 rows 377 us, 5.9 TB/s, 0.87 of the measured copy bandwidth (pages of 64; of 16, whose
-// 16 boxes a tile one thread issues in some 1300 clocks, 408 us); at 32 rows 489 us, 4.5 TB/s,
+// at 8 rows 389 us, 5.7 TB/s, 0.84 of the measured copy bandwidth (pages of 64; of 16, whose
+// 16 boxes a tile one thread issues in some 1300 clocks, 419 us); at 32 rows 487 us, 4.5 TB/s,
 // the two softmax warpgroups' work (2300 clocks a tile: one key's rows a thread in sequence,
 // and code that the instruction caches do not hold); 512 rows per KV head, 16384 keys, 8
-// sequences 596 us, 461 TFLOP/s, the same at 64 rows.
+// sequences 610 us, 451 TFLOP/s; 64 rows 122 us. Rows of very different sizes, whose scores are
+// scaled one by one: at 32 rows 542 us, 512 rows 717 us.
 //
 // Pairs. Where a (sequence, KV head) has more than 64 rows a CTA has two groups of them, one
 // for each stream, which both take every tile: its codes are widened once for 128 rows (512
-// rows: 707 us with a CTA per group of 64, 596 us in pairs).
+// rows: 707 us with a CTA per group of 64, 596 us in pairs, before rows had units and V
+// scales a share in the references).
 //
 // CTA: one per SM, five warpgroups (four at 64 rows, whose softmax wants the registers)
 // around tensor memory and rings of three (two) tiles of K's and V's codes. Two streams take
@@ -166,7 +168,6 @@ template <int kRows> struct __align__(1024) TreeInt8Smem {
     uint32_t tmem_base;
     int start_b, start_h, start_tile, start_T, start_n, units; // this CTA's run
     int scan[Sh::kThreads / 32];
-    float zero;
 };
 template <int kRows> constexpr int kInt8Smem = sizeof(TreeInt8Smem<kRows>);
 static_assert(kInt8Smem<32> <= 232448 && kInt8Smem<64> <= 232448 && kInt8Smem<128> <= 232448, "one CTA's shared memory");
@@ -346,7 +347,10 @@ __device__ bool fetch_codes(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, con
 
 // ---------------------------------------------------------------- queries and masks
 // The square root of a row's unit 2^(16 k): the unit itself may lie past fp32's range.
-__device__ __forceinline__ float root_of_unit(int k) { return __uint_as_float(static_cast<uint32_t>(127 + 8 * k) << 23); }
+__device__ __forceinline__ float root_of_unit(int k)
+{
+    return __uint_as_float(static_cast<uint32_t>(127 + 8 * k) << 23);
+}
 
 // The larger of two pairs' elements each, by size (their signs are of no use).
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b)
@@ -362,7 +366,9 @@ __device__ __forceinline__ uint4 divided_twice(uint4 x, float root)
     const uint32_t inv = (254u << 7) - (__float_as_uint(root) >> 16), pair = inv << 16 | inv; // 1 / root
     const auto times = [pair](uint32_t v) {
         uint32_t r;
-        asm("{\n\t.reg .b32 t;\n\tmul.rn.bf16x2 t, %1, %2;\n\tmul.rn.bf16x2 %0, t, %2;\n\t}" : "=r"(r) : "r"(v), "r"(pair));
+        asm("{\n\t.reg .b32 t;\n\tmul.rn.bf16x2 t, %1, %2;\n\tmul.rn.bf16x2 %0, t, %2;\n\t}"
+            : "=r"(r)
+            : "r"(v), "r"(pair));
         return r;
     };
     return make_uint4(times(x.x), times(x.y), times(x.z), times(x.w));

@@ -6,7 +6,7 @@
 // The kernels' parameter structs (P below) hold B, M, Hq, Hkv, log2_page, max_pages,
 // context_lens, draft_lens, g, tile_tokens, row_groups, rec_rows, ctas, unit_base,
 // rec_m, rec_l, rec_acc, out_f32 and out_bf16; their shared memory (S) holds start_b,
-// start_h, start_tile, start_T, start_n, units, scan and zero.
+// start_h, start_tile, start_T, start_n, units and scan.
 #pragma once
 
 #include "common.cuh"
@@ -148,7 +148,7 @@ template <int kThreads, typename P, typename S> __device__ __forceinline__ void 
     int u0;
     const int units = run_of(p, total, cta, u0);
     if (tid == 0)
-        s.units = units, s.zero = 0.f;
+        s.units = units;
     if (mine > 0 && u0 >= before && u0 < before + mine) {
         int b = b0, at = before, tiles = mine / p.Hkv; // of one head of sequence b
         if (per > 1)
@@ -301,7 +301,8 @@ template <typename P> cudaError_t launch_tree_merge(const P &p, int ctas, cudaSt
     // pieces, 1024, 2048 and 4096 rows: 22.0 and 24.5, 21.7 and 22.3, 37.7 and 32.2; 6.3
     // pieces, 768 and 1536: 20.3 and 20.7, 27.1 and 25.9; 4.75 pieces, 1024 and 2048: 26.4
     // and 27.2, 30.7 and 28.6; 3.2 pieces, 144, 384 and 1536: 30.4 and 30.3, 24.8 and 24.5,
-    // 26.8 and 25.0; 1.2 pieces, 32768 (g = 8): 153 and 102.
+    // 26.8 and 25.0; 1.2 pieces, 32768 (g = 8): 153 and 102. (With the bf16 kernel; the INT8 one
+    // shares the rule.)
     const long long heads = static_cast<long long>(p.B) * p.Hkv, rows_in_all = static_cast<long long>(p.B) * p.M * p.Hq;
     const int parts = ctas >= 4 * heads && rows_in_all * heads <= 220ll * ctas ? 4 : 1;
     const int per_block = kMergeThreads / 32 / parts;

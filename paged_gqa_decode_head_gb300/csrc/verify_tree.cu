@@ -597,8 +597,6 @@ cudaError_t launch(const VerifyParams &p, int B, int blocks, cudaStream_t stream
 
 } // namespace
 
-size_t verify_tree_workspace_bytes(int, int, int, int) { return 0; }
-
 cudaError_t launch_verify_tree(const VerifyTreeArgs &a, cudaStream_t stream)
 {
     VerifyParams p{a.target, a.draft, a.target_stride, a.draft_stride, a.tokens, a.parents, a.draft_lens, a.temperatures,
@@ -606,7 +604,8 @@ cudaError_t launch_verify_tree(const VerifyTreeArgs &a, cudaStream_t stream)
     // As many blocks a sequence as all run at once, two an SM, and no more than have a piece
     // for each thread; a power of two. 151936 bf16 logits, 4, 8 and 16 blocks: one sequence
     // 44.2, 30.2, 23.4 us; 64 with draft logits 110.5, 103.5, 151.0 us; 24 of 32003 fp32 logits
-    // 32.8, 30.4, 34.6 us.
+    // 32.8, 30.4, 34.6 us. (64 sequences get 4: with 8 half of them start when short paths of
+    // the others have ended, which this rule cannot foresee.)
     int blocks = kMaxCluster;
     while (blocks > 1 && (a.B > 2 * a.sm_count / blocks || a.V <= blocks / 2 * kVerifyThreads * kPiece))
         blocks /= 2;
