@@ -47,7 +47,7 @@
 // the two softmax warpgroups' work (2300 clocks a tile: one key's rows a thread in sequence,
 // and code that the instruction caches do not hold); 512 rows per KV head, 16384 keys, 8
 // sequences 610 us, 451 TFLOP/s; 64 rows 122 us. Rows of very different sizes, whose scores are
-// scaled one by one: at 32 rows 542 us, 512 rows 717 us.
+// scaled one by one: at 32 rows 549 us, 512 rows 730 us.
 //
 // Pairs. Where a (sequence, KV head) has more than 64 rows a CTA has two groups of them, one
 // for each stream, which both take every tile: its codes are widened once for 128 rows (512
@@ -150,7 +150,8 @@ template <int kRows> struct __align__(1024) TreeInt8Smem {
     float slope_up[2][Sh::kSets][Sh::kOwn], slope_down[2][Sh::kSets][Sh::kOwn]; // slopes (base 2), split by sign
     int anchor[2][Sh::kSets][Sh::kOwn];
     // what the rows' queries were divided by twice; 0: each row by its own
-    float q_root[2][Sh::kSets], q_roots[2][Sh::kSets][Sh::kOwn];
+    // (behind the rows' own: scale log2 e, or scale / cap)
+    float q_root[2][Sh::kSets], q_roots[2][Sh::kSets][Sh::kOwn + 1];
     int by_sign[2][Sh::kSets]; // every row's anchor is the prefix's end, or its first key for a falling slope
     // a stream's rows
     float neg_m[2][Sh::kOwn]; // minus the reference
@@ -476,8 +477,10 @@ __device__ bool fetch_rows(const TreeInt8Params &p, TreeInt8Smem<kRows> &s, int 
             }
             least = __reduce_min_sync(0xFFFFFFFFu, least);
             most = __reduce_max_sync(0xFFFFFFFFu, most);
-            if (lane == 0)
+            if (lane == 0) {
                 s.q_root[buf][set] = most > least ? 0.f : root_of_unit(most < least ? 0 : least);
+                s.q_roots[buf][set][Sh::kOwn] = kScore & 1 ? p.cap_u : p.c;
+            }
         }
         __syncwarp();
         if (lane == 0)
@@ -760,10 +763,12 @@ __device__ __forceinline__ void form_scores(const TreeInt8Params &p, const TreeI
     }
 }
 
-// A key's scores in place, each by its factor and its row's unit (a call, as it is rarely made and
-// its code would take registers and instruction cache from the loop around it).
-__device__ __noinline__ void apply_units(uint32_t tmem_s, float factor, const float *roots, int n)
+// A key's scores in place, each by its K scale, the call's factor and its row's unit, in an order
+// in which no partial product is past fp32's range before the score itself is (a call, as it is
+// rarely made and its code would take registers and instruction cache from the loop around it).
+__device__ __noinline__ void apply_units(uint32_t tmem_s, float ks, const float *roots, int n)
 {
+    const float plain = roots[n];
 #pragma unroll 1
     for (int j = 0; j < n; j += 8) {
         float y[8];
@@ -771,7 +776,7 @@ __device__ __noinline__ void apply_units(uint32_t tmem_s, float factor, const fl
         tmem_wait_ld8(y);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            y[k] *= factor * roots[j + k] * roots[j + k];
+            y[k] = y[k] * ks * roots[j + k] * plain * roots[j + k];
         tmem_st8(tmem_s + j, y);
     }
     tmem_wait_st();
@@ -835,13 +840,13 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
         };
         load_scales();
         wait(&s.rows_full[buf], (index >> 1) & 1);
-        // scale log2 e, or scale / cap, in the unit of the rows' queries
-        const float root = s.q_root[buf][set];
-        const bool uneven = root == 0.f;
-        const float by = (kScore & 1 ? p.cap_u : p.c) * (uneven ? 1.f : root) * (uneven ? 1.f : root);
+        // scale log2 e, or scale / cap, in the unit of the rows' queries, where they have one and
+        // the product keeps well within fp32's range; 0: row by row
+        const float root = s.q_root[buf][set], in_unit = (kScore & 1 ? p.cap_u : p.c) * root * root;
+        const float by = root == 1.f || (fabsf(in_unit) > 0x1p-100f && fabsf(in_unit) < 0x1p100f) ? in_unit : 0.f;
         for (int i = first; i < tiles; i += kTurns, ++step) {
             const int key0 = (seg.seg_tile1 - 1 - i) * kTileKeys, key = key0 + key_row;
-            float factor = next_ks * by, vs = next_vs; // a score is S times the factor
+            float factor = next_ks * (by == 0.f ? 1.f : by), vs = next_vs; // a score is S times the factor
             const bool valid = next_valid;
             load_scales();
             wait(&s.s_full[stream], step & 1);
@@ -856,7 +861,7 @@ template <int kScore, int kRows> __device__ bool soften(const TreeInt8Params &p,
                     factor = vs = 0.f; // may hold anything
             }
             const auto seen = [&](int j) { return (j < 32 ? sees_lo : sees_hi) >> (j & 31); };
-            if (__builtin_expect(uneven, 0)) {
+            if (__builtin_expect(by == 0.f, 0)) {
                 apply_units(tmem_s, factor, s.q_roots[buf][set], kOwn);
                 factor = 1.f;
             }

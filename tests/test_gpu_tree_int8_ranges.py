@@ -109,6 +109,18 @@ def test_queries_of_any_size(power, M, g):
     check(c)
 
 
+@pytest.mark.parametrize("power,scale_power", [(13, 116), (13, 97), (60, 66), (-100, -20), (-60, -58), (-126, 10)])
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+@pytest.mark.parametrize("M,g", [(3, 2), (12, 2), (64, 2)])
+def test_queries_and_scales_at_the_ends_of_their_range(power, scale_power, softcap, M, g):
+    """The score is of usual size, products of two of its three factors are not; a key without a K row among them."""
+    c = Case(3050 + M, [300, M + 3], M, Hq=2 * g, Hkv=2, softcap=softcap)
+    c.q, c.scale = scaled(c.q, 2.0 ** power), SCALE * 2.0 ** scale_power
+    c.ks = np.float32(c.ks.astype(np.float64) * 2.0 ** -(power + scale_power))
+    c.k8[at(c, 0, 5)], c.ks[at(c, 0, 5)] = 0, 0
+    check(c)
+
+
 @pytest.mark.parametrize("power", [-60, -20, 20])
 @pytest.mark.parametrize("softcap,biased", [(20.0, False), (0.0, True), (20.0, True)])
 @pytest.mark.parametrize("M,g", [(3, 2), (12, 2), (64, 2)])
